@@ -11,9 +11,22 @@ sm_103 GPU the call raises.
     o, lse = fa_fwd_splitkv(q, k, v, causal=True)    # decode: (Hq/Hkv)*Lq <= 16, long Lk
     dq, dk, dv = fa_bwd(q, k, v, o, lse, do, causal=True)
     o, lse = fa_fwd_variant(q, k, v, window=(4095, 0), softcap=0.0, alibi_slopes=None)
+
+A paged KV cache held in 4 bits (pool uint8 [pages, Hkv, page_size / 16, 18 D], table int32 [slots, W], seq_lens
+int32 [slots], refs int32 [pages]; layout in include/fa_gb300.h):
+
+    pool = kv4_pool(pages, Hkv, page_size, D)
+    info = fa_kv4_reserve(new_tokens, table, seq_lens, refs, page_size)         # pages for new positions
+    fa_kv4_append(k, v, cu_seqlens, pool, table, seq_lens)                      # quantise them into the cache
+    o, lse = fa_fwd_kv4(q, pool, table, seq_lens, causal=True)                  # decode attention over it
+    k, v = fa_kv4_read(cu_seqlens, total, pool, table, seq_lens)                # back to bf16 rows
+    info = fa_kv4_fork(parents, children, pool, table, seq_lens, refs)          # share and copy pages
+    fa_kv4_release(seq_ids, table, seq_lens, refs, page_size)
+    info = fa_kv4_compact(pool, table, seq_lens, refs)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -23,7 +36,9 @@ import torch
 
 __all__ = ["fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdim", "fa_fwd_varlen_noalloc", "fa_fwd_variant", "fa_fwd_varlen_variant",
            "fa_fwd_splitkv", "fp8_prepare", "fa_fwd_fp8", "fp8_sections", "splitkv_workspace", "fa_bwd",
-           "bwd_workspace", "fa_bwd_varlen", "bwd_varlen_workspace", "fa_bwd_variant", "fa_bwd_varlen_variant", "fa_check", "fa_status_string", "fa_last_launch_count",
+           "bwd_workspace", "fa_bwd_varlen", "bwd_varlen_workspace", "fa_bwd_variant", "fa_bwd_varlen_variant",
+           "kv4_pool", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4", "kv4_workspace", "fa_kv4_reserve", "fa_kv4_fork",
+           "fa_kv4_release", "fa_kv4_compact", "kv4_pages_workspace", "fa_check", "fa_status_string", "fa_last_launch_count",
            "FAError", "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,10 +50,14 @@ FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = ran
 EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdim", "fa_fwd_varlen_noalloc", "fa_fwd_variant", "fa_fwd_varlen_variant",
                     "fa_fwd_splitkv", "fa_fwd_splitkv_workspace", "fa_bwd", "fa_bwd_workspace", "fa_bwd_varlen",
                     "fa_bwd_varlen_workspace", "fa_bwd_variant", "fa_bwd_varlen_variant", "fa_fp8_workspace",
-                    "fa_fp8_prepare", "fa_fwd_fp8", "fa_check", "fa_status_string", "fa_last_launch_count",
+                    "fa_fp8_prepare", "fa_fwd_fp8", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4",
+                    "fa_fwd_kv4_workspace", "fa_kv4_reserve", "fa_kv4_fork", "fa_kv4_release", "fa_kv4_compact",
+                    "fa_kv4_pages_workspace", "fa_check", "fa_status_string", "fa_last_launch_count",
                     "fa_test_inject_fault")
 SPLITKV_MAX_ROWS = 16  # (Hq / Hkv) * Lq limit of fa_fwd_splitkv
 NOALLOC_MAX_SEQS = 16384  # FA_NOALLOC_MAX_SEQS in include/fa_gb300.h
+KV4_MAX_ROWS = 64  # FA_KV4_MAX_ROWS: (Hq / Hkv) * Lq limit of fa_fwd_kv4
+KV4_MAX_SLOTS = 65536  # FA_KV4_MAX_SLOTS
 VARLEN_SEQS_PER_LAUNCH = 1536  # FA_VARLEN_SEQS_PER_LAUNCH (64 for head dimensions (192, 128))
 
 
@@ -46,6 +65,18 @@ class _Variant(ctypes.Structure):
     # struct fa_variant in include/fa_gb300.h
     _fields_ = [("window_left", ctypes.c_int), ("window_right", ctypes.c_int), ("softcap", ctypes.c_float),
                 ("alibi_slopes", ctypes.c_void_p)]
+
+
+class _KV4(ctypes.Structure):
+    # struct fa_kv4 in include/fa_gb300.h
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pool", "table", "seq_lens", "seq_ids", "k_scale", "v_scale")] + [
+        (n, ctypes.c_int) for n in ("num_pages", "num_slots", "table_width", "page_size", "Hkv", "D")]
+
+
+class _KV4Pages(ctypes.Structure):
+    # struct fa_kv4_pages in include/fa_gb300.h
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pool", "table", "seq_lens", "refs")] + [
+        (n, ctypes.c_int) for n in ("num_pages", "num_slots", "table_width", "page_size", "Hkv", "D", "num_layers")]
 
 
 class FAError(RuntimeError):
@@ -110,6 +141,16 @@ def load_library() -> ctypes.CDLL:
                                               f, vp, ctypes.c_size_t, vp]
         lib.fa_bwd_varlen_workspace.restype = i
         lib.fa_bwd_varlen_workspace.argtypes = [i, i, i, ctypes.POINTER(ctypes.c_size_t)]
+        c4, pg, sz = ctypes.POINTER(_KV4), ctypes.POINTER(_KV4Pages), ctypes.c_size_t
+        for name, args in (("fa_kv4_append", [vp, vp, vp, i, i, c4, vp]), ("fa_kv4_read", [vp, vp, vp, i, i, c4, vp]),
+                           ("fa_fwd_kv4", [vp, vp, vp, i, i, i, i, f, c4, vp, sz, vp]),
+                           ("fa_fwd_kv4_workspace", [i, i, i, i, i, ctypes.POINTER(sz)]),
+                           ("fa_kv4_reserve", [vp, vp, i, pg, vp, vp, sz, vp]),
+                           ("fa_kv4_fork", [vp, vp, i, pg, vp, vp, sz, vp]), ("fa_kv4_release", [vp, i, pg, vp]),
+                           ("fa_kv4_compact", [pg, vp, vp, sz, vp]),
+                           ("fa_kv4_pages_workspace", [i, i, ctypes.POINTER(sz)])):
+            getattr(lib, name).restype = i
+            getattr(lib, name).argtypes = args
         lib.fa_check.restype = i
         lib.fa_check.argtypes = [vp]
         lib.fa_status_string.restype = ctypes.c_char_p
@@ -646,6 +687,265 @@ def fa_bwd_varlen(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Te
     if st != FA_OK:
         raise FAError(st, name)
     return dq, dk, dv
+
+
+# ------------------------------------------------------------- 4-bit cache
+
+def kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, layers: int | None = None,
+             device="cuda") -> torch.Tensor:
+    """An empty (all zero) pool of a 4-bit paged KV cache: uint8 [num_pages, Hkv,
+    page_size / 16, 18 D], with ``layers`` in front when given."""
+    if page_size not in (16, 32, 64, 128, 256) or D not in (64, 128):
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and D 64 or 128")
+    shape = (num_pages, Hkv, page_size // 16, 18 * D)
+    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
+
+
+def _same_device(named, device):
+    for t, n in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} must be on {device}")
+
+
+def _device_guard(device):
+    """The device's context, or nothing where it is current already."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _check_slots(table, seq_lens):
+    _check_tensor(table, "table", torch.int32, 2)
+    _check_tensor(seq_lens, "seq_lens", torch.int32, 1)
+    if seq_lens.shape[0] != table.shape[0]:
+        raise ValueError(f"table has {table.shape[0]} slots and seq_lens {seq_lens.shape[0]}")
+
+
+def _check_pool(pool, ndim):
+    _check_tensor(pool, "pool", torch.uint8, ndim)
+    U, unit = pool.shape[-2:]
+    if unit not in (18 * 64, 18 * 128) or U not in (1, 2, 4, 8, 16):
+        raise ValueError(f"pool must be uint8 [..., pages, Hkv, page_size / 16, 18 D], got {tuple(pool.shape)}")
+
+
+def _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, num_seqs):
+    """Checked fa_kv4_t of a call with num_seqs sequences."""
+    _check_pool(pool, 4)
+    _check_slots(table, seq_lens)
+    N, H, U, unit = pool.shape
+    if seq_ids is not None:
+        _check_tensor(seq_ids, "seq_ids", torch.int32, 1)
+        if seq_ids.shape[0] != num_seqs:
+            raise ValueError(f"seq_ids must name {num_seqs} slots")
+    elif num_seqs > table.shape[0]:
+        raise ValueError(f"{num_seqs} sequences but {table.shape[0]} slots")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _check_tensor(t, n, torch.float32, 1)
+            if t.shape[0] != H:
+                raise ValueError(f"{n} must hold one scale for each of the {H} KV heads")
+    _same_device(((table, "table"), (seq_lens, "seq_lens"), (seq_ids, "seq_ids"), (k_scale, "k_scale"),
+                  (v_scale, "v_scale")), pool.device)
+    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return _KV4(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ptr(seq_ids), ptr(k_scale), ptr(v_scale), N,
+                table.shape[0], table.shape[1], 16 * U, H, unit // 18)
+
+
+def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
+                  table: torch.Tensor, seq_lens: torch.Tensor, seq_ids: torch.Tensor | None = None,
+                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise packed rows k, v [T,Hkv,D] bf16 into the cache: the rows
+    [cu_seqlens[s], cu_seqlens[s+1]) become the last positions of sequence s
+    (slot seq_ids[s], default s), which seq_lens already counts."""
+    for t, n in ((k, "k"), (v, "v")):
+        _check_tensor(t, n, torch.bfloat16, 3)
+    _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, cu_seqlens.shape[0] - 1)
+    if k.shape != v.shape or k.shape[1] != c.Hkv or k.shape[2] != c.D:
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {c.Hkv} heads of {c.D}")
+    _same_device(((k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens")), pool.device)
+    lib = load_library()
+    with _device_guard(pool.device):
+        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, k.shape[0],
+                               ctypes.byref(c), _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_append")
+
+
+def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table: torch.Tensor,
+                seq_lens: torch.Tensor, seq_ids: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
+                v_scale: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                v_out: torch.Tensor | None = None, stream=None):
+    """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as
+    packed bf16 rows (k, v), each [total,Hkv,D]: a cached prefix as the keys
+    of fa_fwd_varlen.  Rows behind the last sequence are left as they were."""
+    _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, cu_seqlens.shape[0] - 1)
+    shape = (int(total), c.Hkv, c.D)
+    if shape[0] < 0:
+        raise ValueError("total must not be negative")
+    k_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if v_out is None else v_out
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _check_tensor(t, n, torch.bfloat16, 3)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
+    _same_device(((k_out, "k_out"), (v_out, "v_out"), (cu_seqlens, "cu_seqlens")), pool.device)
+    lib = load_library()
+    with _device_guard(pool.device):
+        st = lib.fa_kv4_read(k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
+                             shape[0], ctypes.byref(c), _stream_handle(stream))
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_read")
+    return k_out, v_out
+
+
+def kv4_workspace(B: int, Hq: int, Hkv: int, Lq: int, D: int) -> int:
+    """Workspace bytes fa_fwd_kv4 needs on the current device."""
+    nbytes = ctypes.c_size_t(0)
+    st = load_library().fa_fwd_kv4_workspace(B, Hq, Hkv, Lq, D, ctypes.byref(nbytes))
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_kv4_workspace")
+    return nbytes.value
+
+
+def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor,
+               causal: bool = False, softmax_scale: float | None = None, seq_ids: torch.Tensor | None = None,
+               k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None, stream=None):
+    """Decode attention over a 4-bit paged cache.  q [B,Hq,Lq,D] bf16 CUDA with
+    (Hq/Hkv)*Lq <= 64; sequence b is slot seq_ids[b] (default b) and attends its
+    first seq_lens positions; with ``causal`` the queries are the last Lq of
+    them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
+    _check_tensor(q, "q", torch.bfloat16, 4)
+    B, Hq, Lq, D = q.shape
+    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, B)
+    if D != c.D:
+        raise ValueError(f"q has head dimension {D} and the cache {c.D}")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    _check_tensor(out, "out", torch.float32, 4)
+    _check_tensor(lse, "lse", torch.float32, 3)
+    if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Lq):
+        raise ValueError("out/lse shape mismatch")
+    _same_device(((q, "q"), (out, "out"), (lse, "lse"), (workspace, "workspace")), pool.device)
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    lib = load_library()
+    with _device_guard(q.device):
+        nbytes = kv4_workspace(B, Hq, c.Hkv, Lq, D)
+        if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        st = lib.fa_fwd_kv4(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq, int(bool(causal)),
+                            float(softmax_scale), ctypes.byref(c), workspace.data_ptr() if nbytes else None, nbytes,
+                            _stream_handle(stream))
+        if nbytes and isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)  # keep the block out of reuse until that stream is done
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_kv4")
+    return out, lse
+
+
+def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
+    """Workspace bytes fa_kv4_reserve, fa_kv4_fork and fa_kv4_compact (n = 0) need."""
+    nbytes = ctypes.c_size_t(0)
+    st = load_library().fa_kv4_pages_workspace(num_pages, n, ctypes.byref(nbytes))
+    if st != FA_OK:
+        raise FAError(st, "fa_kv4_pages_workspace")
+    return nbytes.value
+
+
+def _page_call(name, pool, page_size, table, seq_lens, refs, lists, info, workspace, stream):
+    """Checks and runs one page operation; lists: the call's int32 [n] tensors
+    (None where it names no slots); info None: the call returns none."""
+    _check_slots(table, seq_lens)
+    _check_tensor(refs, "refs", torch.int32, 1)
+    lib = load_library()
+    named = [(table, "table"), (seq_lens, "seq_lens")]
+    n = None
+    for t, what in lists:
+        if t is None:
+            continue
+        _check_tensor(t, what, torch.int32, 1)
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{what} must hold {n} entries")
+        n = t.shape[0]
+        named.append((t, what))
+    if pool is None:
+        geometry = (None, page_size, 1, 64, 1)
+    else:
+        _check_pool(pool, 5 if pool.dim() == 5 else 4)
+        N, H, U, unit = pool.shape[-4:]
+        if N != refs.shape[0]:
+            raise ValueError(f"pool has {N} pages and refs {refs.shape[0]}")
+        named.append((pool, "pool"))
+        geometry = (pool.data_ptr(), 16 * U, H, unit // 18, pool.shape[0] if pool.dim() == 5 else 1)
+    device = refs.device
+    plan = name != "fa_kv4_release"
+    if plan:
+        if info is None:
+            info = torch.empty(2, dtype=torch.int32, device=device)
+        _check_tensor(info, "info", torch.int32, 1)
+        if info.shape[0] != 2:
+            raise ValueError("info must hold 2 numbers")
+        named += [(info, "info"), (workspace, "workspace")]
+    _same_device(named, device)
+    pages = _KV4Pages(geometry[0], table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), refs.shape[0],
+                      table.shape[0], table.shape[1], *geometry[1:])
+    args = [None if t is None else t.data_ptr() for t, _ in lists] + ([n] if lists else [])
+    with _device_guard(device):
+        args.append(ctypes.byref(pages))
+        if plan:
+            nbytes = kv4_pages_workspace(refs.shape[0], n or 0)
+            if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            args += [info.data_ptr(), workspace.data_ptr(), nbytes]
+        st = getattr(lib, name)(*args, _stream_handle(stream))
+        if plan and isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
+    if st != FA_OK:
+        raise FAError(st, name)
+    return info
+
+
+def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
+                   page_size: int, seq_ids: torch.Tensor | None = None, info: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Give slot seq_ids[i] (default i) pages for new_tokens[i] more positions and
+    count them in seq_lens.  Returns info, int32 [2] on the device: free pages
+    left, and 0, or the pages that were missing (then nothing was changed), or
+    -1 for bad arguments on the device."""
+    return _page_call("fa_kv4_reserve", None, int(page_size), table, seq_lens, refs,
+                      ((seq_ids, "seq_ids"), (new_tokens, "new_tokens")), info, workspace, stream)
+
+
+def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+                seq_lens: torch.Tensor, refs: torch.Tensor, info: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Make the empty slots children[i] copies of the slots parents[i]: full pages
+    are shared, a partly filled last page is copied.  pool as for
+    fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
+    return _page_call("fa_kv4_fork", pool, None, table, seq_lens, refs,
+                      ((parents, "parents"), (children, "children")), info, workspace, stream)
+
+
+def fa_kv4_release(seq_ids: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
+                   page_size: int, stream=None) -> None:
+    """Free the slots seq_ids: their pages lose a reference each, their lengths become 0."""
+    _page_call("fa_kv4_release", None, int(page_size), table, seq_lens, refs, ((seq_ids, "seq_ids"),), None, None,
+               stream)
+
+
+def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
+                   info: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
+    return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, (), info, workspace, stream)
 
 
 def fa_check(stream=None) -> int:

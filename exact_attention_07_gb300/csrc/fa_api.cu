@@ -13,6 +13,7 @@
 #include "fa_bwd.h"
 #include "fa_decode.h"
 #include "fa_fp8.h"
+#include "fa_kv4.h"
 #include "fa_launch.h"
 #include "fa_params.h"
 
@@ -1203,6 +1204,257 @@ extern "C" fa_status_t fa_fwd_fp8(const void* prepared, float* o, float* lse, in
                                  : launch_fwd<128, false, false, kVarFp8>(mq, mk, mv, p, grid, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     g_last_launches = 1;
+    return FA_OK;
+}
+
+// ------------------------------------------------------------- 4-bit cache
+
+namespace {
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sizes that the cache and the page operations share.
+fa_status_t kv4_geometry(int num_pages, int num_slots, int table_width, int page_size, int Hkv, int D, int* page_shift)
+{
+    if (num_pages <= 0 || num_slots <= 0 || num_slots > FA_KV4_MAX_SLOTS || table_width <= 0 || page_size <= 0 ||
+        Hkv <= 0 || D <= 0)
+        return FA_ERR_INVALID_ARG;
+    if ((long long)table_width * page_size >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    int shift = 4;
+    while (shift < 8 && (1 << shift) < page_size) ++shift;
+    if ((1 << shift) != page_size) return FA_ERR_UNSUPPORTED;
+    *page_shift = shift;
+    return FA_OK;
+}
+
+// Checks a cache description for a call of num_seqs sequences and fills the kernels' form of it.
+fa_status_t kv4_cache(const fa_kv4_t* c, int num_seqs, Kv4Cache* out)
+{
+    if (!c || !c->pool || !c->table || !c->seq_lens || num_seqs <= 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(c->pool) || !aligned4(c->table) || !aligned4(c->seq_lens) || !aligned4(c->seq_ids) ||
+        !aligned4(c->k_scale) || !aligned4(c->v_scale))
+        return FA_ERR_INVALID_ARG;
+    const fa_status_t st = kv4_geometry(c->num_pages, c->num_slots, c->table_width, c->page_size, c->Hkv, c->D,
+                                        &out->page_shift);
+    if (st != FA_OK) return st;
+    if (!c->seq_ids && num_seqs > c->num_slots) return FA_ERR_INVALID_ARG;
+    out->pool = static_cast<uint8_t*>(c->pool);
+    out->table = c->table;
+    out->lens = c->seq_lens;
+    out->ids = c->seq_ids;
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->num_pages = c->num_pages;
+    out->num_slots = c->num_slots;
+    out->table_width = c->table_width;
+    out->Hkv = c->Hkv;
+    return FA_OK;
+}
+
+fa_status_t kv4_rows(const void* k, const void* v, bool write, const int* cu_seqlens, int num_seqs, int total,
+                     const fa_kv4_t* cache, cudaStream_t stream)
+{
+    g_last_launches = 0;
+    Kv4RowsParams p{};
+    fa_status_t st = kv4_cache(cache, num_seqs, &p.c);
+    if (st != FA_OK) return st;
+    if (!cu_seqlens || !aligned4(cu_seqlens) || total < 0) return FA_ERR_INVALID_ARG;
+    if (total > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
+    // threads of the launch: one per pair of positions, KV head and 16 dimensions
+    if (((long long)(total >> 1) + num_seqs) * cache->Hkv * (cache->D / 16) >= (1ll << 31) * 256)
+        return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    if (total == 0) return FA_OK;  // no rows: nothing to launch
+    p.k_in = p.k_out = static_cast<uint16_t*>(const_cast<void*>(k));
+    p.v_in = p.v_out = static_cast<uint16_t*>(const_cast<void*>(v));
+    p.cu = cu_seqlens;
+    p.num_seqs = num_seqs;
+    p.total = total;
+    p.c.err = ds->err;
+    p.c.diag = ds->diag;
+    const cudaError_t e = write ? launch_kv4_append(cache->D, p, stream) : launch_kv4_read(cache->D, p, stream);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 1;
+    return FA_OK;
+}
+
+// Shape checks of fa_fwd_kv4; items = (sequence, KV head) pairs.
+fa_status_t kv4_attn_shape(int B, int Hq, int Hkv, int Lq, int D, int* R)
+{
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Lq <= 0 || D <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    const long long rows = (long long)(Hq / Hkv) * Lq;
+    if (rows > FA_KV4_MAX_ROWS) return FA_ERR_UNSUPPORTED;
+    if ((long long)B * Hq * Lq >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    *R = (int)rows;
+    return FA_OK;
+}
+}  // namespace
+
+extern "C" fa_status_t fa_kv4_append(const void* k, const void* v, const int* cu_seqlens, int num_seqs, int total,
+                                     const fa_kv4_t* cache, cudaStream_t stream)
+{
+    return kv4_rows(k, v, true, cu_seqlens, num_seqs, total, cache, stream);
+}
+
+extern "C" fa_status_t fa_kv4_read(void* k, void* v, const int* cu_seqlens, int num_seqs, int total,
+                                   const fa_kv4_t* cache, cudaStream_t stream)
+{
+    return kv4_rows(k, v, false, cu_seqlens, num_seqs, total, cache, stream);
+}
+
+extern "C" fa_status_t fa_fwd_kv4_workspace(int B, int Hq, int Hkv, int Lq, int D, size_t* workspace_bytes)
+{
+    if (!workspace_bytes) return FA_ERR_INVALID_ARG;
+    int R = 0;
+    fa_status_t st = kv4_attn_shape(B, Hq, Hkv, Lq, D, &R);
+    if (st != FA_OK) return st;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    return kv4_attn_workspace(D, R, B * Hkv, ds->num_sms, workspace_bytes) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+extern "C" fa_status_t fa_fwd_kv4(const void* q, float* o, float* lse, int B, int Hq, int Lq, int causal,
+                                  float softmax_scale, const fa_kv4_t* cache, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream)
+{
+    g_last_launches = 0;
+    if (!q || !o || !lse || !cache) return FA_ERR_INVALID_ARG;
+    Kv4AttnParams p{};
+    fa_status_t st = kv4_attn_shape(B, Hq, cache->Hkv, Lq, cache->D, &p.R);
+    if (st != FA_OK) return st;
+    st = kv4_cache(cache, B, &p.c);
+    if (st != FA_OK) return st;
+    if (!scale_ok(softmax_scale)) return FA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    size_t need = 0;
+    if (kv4_attn_workspace(cache->D, p.R, B * cache->Hkv, ds->num_sms, &need) != cudaSuccess) return FA_ERR_CUDA;
+    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    p.q = static_cast<const uint16_t*>(q);
+    p.o = o;
+    p.lse = lse;
+    p.part = static_cast<float*>(workspace);
+    p.B = B;
+    p.Hq = Hq;
+    p.Lq = Lq;
+    p.group = Hq / cache->Hkv;
+    p.causal = causal != 0;
+    p.scale = softmax_scale;
+    p.c.err = ds->err;
+    p.c.diag = ds->diag;
+    p.fault = g_fault_next;
+    g_fault_next = 0;
+    int launches = 0;
+    if (launch_kv4_attn(cache->D, p, ds->num_sms, stream, &launches) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = launches;
+    return FA_OK;
+}
+
+namespace {
+// Checks of the page operations, and their kernel parameters.
+fa_status_t kv4_pages(const fa_kv4_pages_t* c, bool pool, const int* ids, const int* other, int n, bool plan,
+                      int* info, void* workspace, size_t workspace_bytes, Kv4PageParams* p, DeviceState** ds)
+{
+    g_last_launches = 0;
+    if (!c || !c->table || !c->seq_lens || !c->refs || n < 0) return FA_ERR_INVALID_ARG;
+    if (!aligned4(c->table) || !aligned4(c->seq_lens) || !aligned16(c->refs)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(ids) || !aligned4(other)) return FA_ERR_INVALID_ARG;
+    fa_status_t st = kv4_geometry(c->num_pages, c->num_slots, c->table_width, c->page_size, c->Hkv, c->D,
+                                  &p->page_shift);
+    if (st != FA_OK) return st;
+    if (pool && (!c->pool || !aligned16(c->pool) || c->num_layers <= 0)) return FA_ERR_INVALID_ARG;
+    if (n > FA_KV4_MAX_SLOTS) return FA_ERR_INVALID_ARG;
+    if (plan) {
+        if (!info || !aligned4(info)) return FA_ERR_INVALID_ARG;
+        if (!workspace || !aligned16(workspace) || workspace_bytes < kv4_pages_workspace(c->num_pages, n))
+            return FA_ERR_INVALID_ARG;
+    }
+    st = device_state(ds);
+    if (st != FA_OK) return st;
+    p->pool = static_cast<uint8_t*>(c->pool);
+    p->table = c->table;
+    p->lens = c->seq_lens;
+    p->refs = c->refs;
+    p->ids = ids;
+    p->other = other;
+    p->info = info;
+    p->ws = static_cast<int*>(workspace);
+    p->n = n;
+    p->num_pages = c->num_pages;
+    p->num_slots = c->num_slots;
+    p->table_width = c->table_width;
+    p->Hkv = c->Hkv;
+    p->D = c->D;
+    p->layers = c->num_layers;
+    p->err = (*ds)->err;
+    return FA_OK;
+}
+}  // namespace
+
+extern "C" fa_status_t fa_kv4_pages_workspace(int num_pages, int n, size_t* workspace_bytes)
+{
+    if (!workspace_bytes || num_pages <= 0 || n < 0 || n > FA_KV4_MAX_SLOTS) return FA_ERR_INVALID_ARG;
+    *workspace_bytes = kv4_pages_workspace(num_pages, n);
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_kv4_reserve(const int* seq_ids, const int* new_tokens, int n, const fa_kv4_pages_t* pages,
+                                      int* info, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    Kv4PageParams p{};
+    DeviceState* ds = nullptr;
+    g_last_launches = 0;
+    if (!new_tokens || n <= 0) return FA_ERR_INVALID_ARG;
+    const fa_status_t st = kv4_pages(pages, false, seq_ids, new_tokens, n, true, info, workspace, workspace_bytes, &p, &ds);
+    if (st != FA_OK) return st;
+    if (!seq_ids && n > pages->num_slots) return FA_ERR_INVALID_ARG;
+    if (launch_kv4_reserve(p, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 1;
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_kv4_fork(const int* parents, const int* children, int n, const fa_kv4_pages_t* pages,
+                                   int* info, void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    Kv4PageParams p{};
+    DeviceState* ds = nullptr;
+    g_last_launches = 0;
+    if (!parents || !children || n <= 0) return FA_ERR_INVALID_ARG;
+    const fa_status_t st = kv4_pages(pages, true, parents, children, n, true, info, workspace, workspace_bytes, &p, &ds);
+    if (st != FA_OK) return st;
+    if (launch_kv4_fork(p, ds->num_sms, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 2;
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_kv4_release(const int* seq_ids, int n, const fa_kv4_pages_t* pages, cudaStream_t stream)
+{
+    Kv4PageParams p{};
+    DeviceState* ds = nullptr;
+    g_last_launches = 0;
+    if (!seq_ids || n <= 0) return FA_ERR_INVALID_ARG;
+    const fa_status_t st = kv4_pages(pages, false, seq_ids, nullptr, n, false, nullptr, nullptr, 0, &p, &ds);
+    if (st != FA_OK) return st;
+    if (launch_kv4_release(p, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 1;
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_kv4_compact(const fa_kv4_pages_t* pages, int* info, void* workspace, size_t workspace_bytes,
+                                      cudaStream_t stream)
+{
+    Kv4PageParams p{};
+    DeviceState* ds = nullptr;
+    const fa_status_t st = kv4_pages(pages, true, nullptr, nullptr, 0, true, info, workspace, workspace_bytes, &p, &ds);
+    if (st != FA_OK) return st;
+    if (launch_kv4_compact(p, ds->num_sms, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 2;
     return FA_OK;
 }
 

@@ -1,0 +1,72 @@
+// Device helpers of the 4-bit cache kernels: codes, scales, checked lookups.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "fa_kv4.h"
+#include "ptx_sm103.cuh"
+
+namespace fa {
+
+// Two e2m1 codes of byte I of w to fp16 (low nibble in the low half): exact.
+template <int I>
+__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, a;}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 1)
+        asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, b;}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 2)
+        asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, c;}" : "=r"(r) : "r"(w));
+    else
+        asm("{.reg .b8 a, b, c, d; mov.b32 {a, b, c, d}, %1; cvt.rn.f16x2.e2m1x2 %0, d;}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// Two e4m3 scales to fp16: exact (at most 448, at least 2^-9).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t b)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(b));
+    return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h)
+{
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Slot and length of the call's sequence i; a bad slot or length is latched
+// and counts as an empty sequence.
+__device__ __forceinline__ int kv4_sequence(const Kv4Cache& c, int i, int& slot)
+{
+    slot = c.ids ? c.ids[i] : i;
+    int len = -1;
+    if (slot >= 0 && slot < c.num_slots) len = c.lens[slot];
+    if (len < 0 || (long long)len > ((long long)c.table_width << c.page_shift)) {
+        atomicOr(c.err, 2);
+        slot = 0;
+        len = 0;
+    }
+    return len;
+}
+
+// Page of a position of a sequence (position below its length); a bad page
+// number is latched and becomes page 0.
+__device__ __forceinline__ int kv4_page(const Kv4Cache& c, int slot, int pos)
+{
+    const int page = c.table[(long long)slot * c.table_width + (pos >> c.page_shift)];
+    if ((unsigned)page < (unsigned)c.num_pages) return page;
+    atomicOr(c.err, 2);
+    return 0;
+}
+
+// Byte offset of the unit of position pos of KV head h.
+__device__ __forceinline__ long long kv4_unit(const Kv4Cache& c, int D, int page, int h, int pos)
+{
+    const int units = 1 << (c.page_shift - 4);
+    return (((long long)page * c.Hkv + h) * units + ((pos >> 4) & (units - 1))) * (18 * D);
+}
+
+}  // namespace fa

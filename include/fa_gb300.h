@@ -365,6 +365,190 @@ fa_status_t fa_bwd_varlen_variant(const void* q, const void* k, const void* v, c
                                   size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Paged KV cache held in 4 bits ("kv4"; no counterpart on the pages).
+ *
+ * The cache is a pool of pages, each of page_size positions of one sequence:
+ *
+ *   pool [num_pages][Hkv][page_size / 16][18 * D] bytes
+ *
+ * The last axis is a unit: 16 consecutive positions of one KV head, 18 * D
+ * bytes (4.5 bits per value of K and V):
+ *
+ *   offset 0     K codes   [16 keys][D / 2]                 low nibble = even dimension
+ *   offset 8 D   V codes   [2][D / 16][4 key pairs][16]     key = 8 i0 + 2 pair + (0: low, 1: high nibble),
+ *                                                           dimension = 16 i1 + i3
+ *   offset 16 D  K scales  [16 keys][D / 16]
+ *   offset 17 D  V scales  [D / 16][16 keys]
+ *
+ * Codes are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), scales are e4m3,
+ * one for each 16 consecutive dimensions of a position's row.  A value is
+ * code * scale * k_scale[head] (v_scale for V).  Position p of the sequence
+ * in slot s is in page table[s * table_width + p / page_size], and
+ * seq_lens[s] positions are valid.  Bytes of positions behind that are never
+ * used, whatever they hold.
+ *
+ * fa_kv4_t is a HOST struct of DEVICE pointers:
+ *   pool      16-byte aligned
+ *   table     int32 [num_slots][table_width]; entries behind a sequence's
+ *             last page are not read
+ *   seq_lens  int32 [num_slots]
+ *   seq_ids   int32, the slot of each sequence of the call, or NULL for the
+ *             slots 0, 1, 2, ... in order
+ *   k_scale, v_scale  fp32 [Hkv], positive and finite, or NULL for 1
+ *   D 64 or 128; page_size 16, 32, 64, 128 or 256 (FA_ERR_UNSUPPORTED
+ *   otherwise); num_slots at most 65536; table_width * page_size below 2^31.
+ *
+ * Slots, lengths and page numbers are read on the device and checked there: a
+ * slot out of range, a length that is negative or above table_width *
+ * page_size, or a page number out of range latches FA_ERR_INVALID_ARG (read
+ * by fa_check).  Nothing is read or written out of range then; what that
+ * sequence's outputs hold is unspecified.  These calls allocate nothing,
+ * copy nothing to the host and may be captured into a graph.
+ */
+#define FA_KV4_MAX_SLOTS 65536
+#define FA_KV4_MAX_ROWS 64
+typedef struct fa_kv4 {
+    void* pool;
+    const int* table;
+    const int* seq_lens;
+    const int* seq_ids;
+    const float* k_scale;
+    const float* v_scale;
+    int num_pages;
+    int num_slots;
+    int table_width;
+    int page_size;
+    int Hkv;
+    int D;
+} fa_kv4_t;
+
+/*
+ * Quantises new rows into the cache.  k, v [total, Hkv, D] bf16 (DEVICE, 16-byte
+ * aligned), packed as for fa_fwd_varlen: sequence s of the call owns rows
+ * [cu_seqlens[s], cu_seqlens[s + 1]) (int32 DEVICE [num_seqs + 1], from 0, non-
+ * decreasing), which become its LAST positions: seq_lens already counts them
+ * (fa_kv4_reserve adds them).  Rows behind cu_seqlens[num_seqs] are not read.
+ *
+ * Each 16 consecutive dimensions x of a row, divided by the head's scale, get
+ * the scale s = e4m3(max|x| / 6) (at most 448) and the codes e2m1(x / s), both
+ * round to nearest even; codes beyond 6 become 6, a zero of either sign has
+ * code 0, and s = 0 (max|x| up to 6 * 2^-10) gives zeros.  A group that holds a NaN or an infinity gets a NaN
+ * scale, so that every value read from it is NaN.
+ *
+ * Bytes of other positions keep their values.  A sequence named twice in one
+ * call latches FA_ERR_INVALID_ARG, and what it then holds is unspecified.
+ * Pages written must belong to one sequence (fa_kv4_fork shares full pages
+ * only).  1 kernel.
+ */
+fa_status_t fa_kv4_append(const void* k, const void* v, const int* cu_seqlens, int num_seqs, int total,
+                          const fa_kv4_t* cache, cudaStream_t stream);
+
+/*
+ * The inverse: the last cu_seqlens[s + 1] - cu_seqlens[s] positions of each
+ * sequence as packed bf16 rows k, v [total, Hkv, D] (outputs), e.g. a whole
+ * cached prefix as the keys of fa_fwd_varlen.  Each value is rounded to bf16
+ * once (exact where the head scale is a power of two).  Rows behind
+ * cu_seqlens[num_seqs] are left as they were.  1 kernel.
+ */
+fa_status_t fa_kv4_read(void* k, void* v, const int* cu_seqlens, int num_seqs, int total, const fa_kv4_t* cache,
+                        cudaStream_t stream);
+
+/*
+ * Attention over the cache for decode: fa_fwd_splitkv's operation with the
+ * keys and values of the B sequences' caches, whose lengths may differ.
+ *
+ *   q [B, Hq, Lq, D] bf16; o [B, Hq, Lq, D] fp32; lse [B, Hq, Lq] fp32
+ *   Hq a multiple of cache->Hkv, (Hq / Hkv) * Lq at most FA_KV4_MAX_ROWS
+ *   (FA_ERR_UNSUPPORTED otherwise).  With causal != 0 the queries are the last
+ *   Lq positions of their sequence, whose keys the cache already holds.
+ *   Masked keys contribute nothing whatever their bytes hold; a row without
+ *   keys gets O = 0 and LSE = -inf.
+ *   workspace: DEVICE memory of at least fa_fwd_kv4_workspace bytes, 16-byte
+ *   aligned; calls that overlap on the GPU need separate workspaces.
+ *
+ * Codes times scales are exact in fp16, the scores, softmax statistics and O
+ * accumulate in fp32, and P enters P.V as the sum of two fp16 numbers (22
+ * bits).  The work is cut evenly over the GPU from the lengths on the device.
+ * 2 kernels.
+ */
+fa_status_t fa_fwd_kv4(const void* q, float* o, float* lse, int B, int Hq, int Lq, int causal,
+                       float softmax_scale, const fa_kv4_t* cache, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+/* Workspace bytes of fa_fwd_kv4 on the CURRENT device, written to *workspace_bytes. */
+fa_status_t fa_fwd_kv4_workspace(int B, int Hq, int Hkv, int Lq, int D, size_t* workspace_bytes);
+
+/*
+ * Pages of the cache: who holds which.  refs int32 [num_pages] counts the
+ * sequences that use a page; pages with refs = 0 are free.  The calls change
+ * table, seq_lens and refs (and, where said, copy pages of num_layers pools
+ * that lie one after the other and share table, seq_lens and refs).  Free
+ * pages are given out lowest first, so results do not depend on timing.
+ *
+ * info (DEVICE int32 [2], output): info[0] = free pages after the call;
+ * info[1] = 0 when the call was done, else nothing was changed: the number of
+ * pages that were missing, or -1 for invalid arguments on the device (a slot
+ * out of range or named twice, a length out of range, ...), which also latch
+ * FA_ERR_INVALID_ARG.
+ *
+ * workspace: DEVICE memory of at least fa_kv4_pages_workspace bytes, 16-byte
+ * aligned; calls that overlap on the GPU need separate workspaces, and calls
+ * on the same table must be ordered.
+ */
+typedef struct fa_kv4_pages {
+    void* pool; /* [num_layers][num_pages][Hkv][page_size / 16][18 * D] bytes */
+    int* table;
+    int* seq_lens;
+    int* refs;
+    int num_pages;
+    int num_slots;
+    int table_width;
+    int page_size;
+    int Hkv;
+    int D;
+    int num_layers;
+} fa_kv4_pages_t;
+
+/*
+ * Makes room for new_tokens[i] >= 0 (int32 DEVICE [n]) more positions in slot
+ * seq_ids[i] (NULL: slots 0 .. n - 1): gives it the pages it needs, with one
+ * reference each, and adds the tokens to seq_lens.  No slot may be named
+ * twice.  The pool is not touched and may be NULL.  1 kernel.
+ */
+fa_status_t fa_kv4_reserve(const int* seq_ids, const int* new_tokens, int n, const fa_kv4_pages_t* pages, int* info,
+                           void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Makes the empty slot children[i] a copy of slot parents[i] (int32 DEVICE
+ * [n]): full pages are shared and counted once more, a partly filled last
+ * page is copied into a page of the child's own (in every layer; only the
+ * units of 16 positions that hold valid ones, the others keep their bytes).
+ * Children must be distinct, of length 0 and no one's parent in the same
+ * call.  2 kernels.
+ */
+fa_status_t fa_kv4_fork(const int* parents, const int* children, int n, const fa_kv4_pages_t* pages, int* info,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Frees the slots seq_ids[i]: each page loses one reference, the table row
+ * becomes -1 and the length 0.  Empty slots and slots named again are left
+ * alone.  The pool is not touched and may be NULL.  1 kernel.
+ */
+fa_status_t fa_kv4_release(const int* seq_ids, int n, const fa_kv4_pages_t* pages, cudaStream_t stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with L pages in use, those
+ * at L or behind go, in order, into the free ones before L, in order, in
+ * every layer, and the tables of all slots follow.  info as above.  2 kernels.
+ */
+fa_status_t fa_kv4_compact(const fa_kv4_pages_t* pages, int* info, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* Workspace bytes of the three calls above for num_pages pages and n sequences
+ * (n = 0 for fa_kv4_compact), written to *workspace_bytes. */
+fa_status_t fa_kv4_pages_workspace(int num_pages, int n, size_t* workspace_bytes);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side error latch
  * of the current device: FA_ERR_TIMEOUT or FA_ERR_INVALID_ARG from an earlier
  * launch, or FA_ERR_CUDA when a kernel found its launch configuration unusable
