@@ -1218,7 +1218,7 @@ fa_status_t kv4_geometry(int num_pages, int num_slots, int table_width, int page
     if (num_pages <= 0 || num_slots <= 0 || num_slots > FA_KV4_MAX_SLOTS || table_width <= 0 || page_size <= 0 ||
         Hkv <= 0 || D <= 0)
         return FA_ERR_INVALID_ARG;
-    if ((long long)table_width * page_size >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    if ((long long)table_width * page_size > (1ll << 30)) return FA_ERR_INVALID_ARG;
     if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
     int shift = 4;
     while (shift < 8 && (1 << shift) < page_size) ++shift;

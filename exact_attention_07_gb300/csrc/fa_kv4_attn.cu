@@ -1,5 +1,41 @@
-// Attention over the 4-bit cache (decode): first form, one CTA per query row.
+// Attention over the 4-bit cache (decode): few query rows per KV head, a long
+// key range, keys and values as e2m1 codes with e4m3 scales.
+//
+//   s_ij = scale * sum_d q_id K_jd,  p_ij = 2^(s_ij log2 e - m_i),
+//   O_i = sum_j p_ij V_j / sum_j p_ij
+//
+// Bound: the cache's bytes are read once, 18 D / 16 per (key, KV head).  At
+// 6.8 TB/s that is 23 bytes, 41 values, per clock and SM, so the arithmetic
+// between HBM and the tensor cores decides: a value costs half a conversion
+// (e2m1x2 -> f16x2, 64 lanes a clock and SM), half a product with its scale
+// (64 a clock) and its share of an MMA.  Staging dequantised tiles in shared
+// memory for tcgen05 would add 2 bytes written and 2 read per value, 164
+// bytes a clock and SM where shared memory gives 128; so the codes go from
+// shared memory straight into the registers that are the operand fragments
+// of mma.sync (1024 multiply-adds a clock and SM, 330 to 660 needed), and the
+// cache's layout is the one in which each lane's fragments are 16 contiguous
+// bytes:
+//
+//   S^T [16 keys x 8 rows] = K (A, from codes) Q^T (B, registers)
+//   O^T [16 dims x 8 rows] += V^T (A, from codes) P^T (B, S^T after the
+//   exponential, turned by movmatrix)
+//
+// Codes times scales are exact in fp16 (2 + 4 significant bits, 2^-10 to
+// 2688).  q becomes fp16 after a power of two per row (its row's largest
+// magnitude in [1, 2)): exact down to 2^-17 of that.  P is the sum of two
+// fp16 numbers, hi = fp16(p) and lo = fp16(p - hi): with up to 4 rows the two
+// fill the 8 columns of one MMA, with up to 8 they take two.
+//
+// Each warp streams tiles of 32 keys through a ring of its own with
+// cp.async.bulk (no block-wide step in the loop), keeps its own maximum, sum
+// and O^T, and raises the maximum only when a score exceeds it by 2^8, so
+// that the rescaling and its shuffles are rare.  The tiles of all (sequence,
+// KV head) items form one list, cut evenly over the blocks from the lengths
+// on the device; an item that lies in several blocks is joined by a second
+// kernel.
+#include <cfloat>
 #include <cmath>
+#include <utility>
 
 #include "kv4_common.cuh"
 
@@ -7,87 +43,688 @@ namespace fa {
 
 namespace {
 
-constexpr int kAttnThreads = 128;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTileKeys = 32;
+constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
 
-template <int D>
-__global__ void __launch_bounds__(kAttnThreads) fa_kv4_attn_kernel(const Kv4AttnParams p)
+// MODE 0: up to 4 rows; 1: up to 8; 2: up to 16 (more rows: several items).
+template <int D, int MODE>
+struct Cfg {
+    static constexpr int UNIT = 18 * D;
+    static constexpr int STAGE = 2 * UNIT;
+    static constexpr int STAGES = D == 128 ? 2 : 4;  // per warp
+    static constexpr int ROWS = 4 << MODE;
+    static constexpr int NT = MODE == 2 ? 2 : 1;  // column tiles of 8
+    static constexpr int KS = D / 16;             // MMA steps over D, and 16-row tiles of O^T
+    static constexpr int OSTRIDE = D + (D == 128 ? 4 : 2);  // floats per column in the joining buffer
+    static constexpr int RING = kWarps * STAGES * STAGE;
+    static constexpr int OBUF = kWarps * 8 * OSTRIDE * 4;
+    static constexpr int QBUF = MODE == 2 ? 32 * KS * NT * 8 : 0;  // fragments of Q
+    static constexpr int ML = kWarps * ROWS * 8;
+    static constexpr int BARS = RING + OBUF + QBUF + ML;
+    static constexpr int SMEM = BARS + kWarps * STAGES * 8 + 64;
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
 {
-    constexpr int G = D / 16;
-    __shared__ float qs[D], ps[kAttnThreads], red[kAttnThreads / 32];
-    const int tid = threadIdx.x;
-    const long long row = blockIdx.x;  // (b * Hq + hq) * Lq + i
-    const int i = (int)(row % p.Lq), hq = (int)(row / p.Lq % p.Hq), b = (int)(row / p.Lq / p.Hq);
-    const int h = hq / p.group;
-    int slot;
-    const int len = kv4_sequence(p.c, b, slot);
-    const float gk = p.c.k_scale ? p.c.k_scale[h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
-    for (int d = tid; d < D; d += kAttnThreads) qs[d] = __uint_as_float((uint32_t)p.q[row * D + d] << 16);
-    const int lim = p.causal ? min(len, i + len - p.Lq + 1) : len;
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int j0 = 0; j0 < lim; j0 += kAttnThreads) {
-        __syncthreads();
-        const int j = j0 + tid;
-        float s = -INFINITY;
-        if (j < lim) {
-            const uint8_t* u = p.c.pool + kv4_unit(p.c, D, kv4_page(p.c, slot, j), h, j);
-            s = 0.f;
-            for (int g = 0; g < G; ++g) {
-                const float sc = f16x2_to_f32(e4m3x2_to_f16x2(u[16 * D + (j & 15) * G + g])).x;
-                float x = 0.f;
-                for (int e = 0; e < 8; ++e) {
-                    const float2 c = f16x2_to_f32(e2m1x2_to_f16x2<0>(u[(j & 15) * (D / 2) + g * 8 + e]));
-                    x += c.x * qs[g * 16 + 2 * e] + c.y * qs[g * 16 + 2 * e + 1];
-                }
-                s += x * sc;
-            }
-            s *= p.scale * gk;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint2 lds8(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds_u8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Codes 2 i, 2 i + 1 (in bytes) of a lane's run as fp16 pairs.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(const uint32_t* w)
+{
+    return e2m1x2_to_f16x2<(I & 3)>(w[I >> 2]);
+}
+
+// step(0), step(1), ... with the index as a constant.
+template <typename F, int... I>
+__device__ __forceinline__ void for_steps(F& step, std::integer_sequence<int, I...>)
+{
+    (step(std::integral_constant<int, I>{}), ...);
+}
+
+// NaN halves of a pair of scales (bit 0: low, bit 1: high).
+__device__ __forceinline__ uint32_t nan_halves(uint32_t s)
+{
+    return ((s & 0x7fffu) > 0x7c00u ? 1u : 0u) | ((s >> 16 & 0x7fffu) > 0x7c00u ? 2u : 0u);
+}
+
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTileKeys - 1) / kTileKeys : 1; }
+
+// Where the kernels keep what they share in the workspace.
+struct Parts {
+    float* o;   // [blocks][2][ROWS][D]
+    float2* ml; // [blocks][2][ROWS]: maximum (log2 units) and sum
+    int4* join; // [blocks]: sequence, head and chunk, last block, 1; or w = 0
+};
+
+template <int D, int MODE>
+__host__ __device__ inline Parts parts_of(float* ws, int blocks)
+{
+    constexpr int ROWS = Cfg<D, MODE>::ROWS;
+    Parts p;
+    p.join = reinterpret_cast<int4*>(ws);
+    p.ml = reinterpret_cast<float2*>(p.join + blocks);
+    p.o = reinterpret_cast<float*>(p.ml + (size_t)blocks * 2 * ROWS);
+    return p;
+}
+
+// A walk over the tile list: tile t of item hc (KV head and chunk of rows) of sequence b.
+struct Walk {
+    int b, hc, t, nt, len, slot;
+};
+
+__device__ __forceinline__ void walk_sequence(const Kv4AttnParams& p, Walk& w)
+{
+    w.len = 0;
+    w.slot = 0;
+    if (w.b < p.B) w.len = kv4_sequence(p.c, w.b, w.slot);
+    w.nt = tiles_of(w.len);
+}
+
+// n tiles on; items = KV heads x chunks of a sequence.
+__device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, int items)
+{
+    w.t += n;
+    while (w.t >= w.nt && w.b < p.B) {
+        w.t -= w.nt;
+        if (++w.hc == items) {
+            w.hc = 0;
+            ++w.b;
+            walk_sequence(p, w);
         }
-        float t = s;
-        for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-        if ((tid & 31) == 0) red[tid >> 5] = t;
-        __syncthreads();
-        for (int w = 0; w < kAttnThreads / 32; ++w) t = fmaxf(t, red[w]);
-        const float mn = fmaxf(m, t), use = mn == -INFINITY ? 0.f : mn;
-        const float a = expf(m - use);
-        ps[tid] = j < lim ? expf(s - use) : 0.f;
-        m = mn;
-        l *= a;
-        acc *= a;
-        __syncthreads();
-        const int n = min(kAttnThreads, lim - j0);
-        for (int k = 0; k < n; ++k) {
-            l += ps[k];
-            if (tid < D) {
-                const int jj = j0 + k, kk = jj & 15;
-                const uint8_t* u = p.c.pool + kv4_unit(p.c, D, kv4_page(p.c, slot, jj), h, jj);
-                const float sc = f16x2_to_f32(e4m3x2_to_f16x2(u[17 * D + (tid >> 4) * 16 + kk])).x;
-                const float2 c = f16x2_to_f32(e2m1x2_to_f16x2<0>(
-                    u[8 * D + (kk >> 3) * 4 * D + (tid >> 4) * 64 + ((kk & 7) >> 1) * 16 + (tid & 15)]));
-                acc += ps[k] * ((kk & 1) ? c.y : c.x) * sc;
+    }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnParams p, const int chunks)
+{
+    using C = Cfg<D, MODE>;
+    constexpr int NT = C::NT, KS = C::KS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ long long s_sum[kWarps], s_total, s_base;
+    __shared__ int s_b;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const uint32_t base = smem_u32(smem);
+    const uint32_t ring = base + warp * (C::STAGES * C::STAGE);
+    const uint32_t bars = base + C::BARS + warp * (C::STAGES * 8);
+    float* obuf = reinterpret_cast<float*>(smem + C::RING);
+    float2* mlbuf = reinterpret_cast<float2*>(smem + C::RING + C::OBUF + C::QBUF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BARS + kWarps * C::STAGES * 8);
+    const WaitFailure wf{p.c.err, p.c.diag};
+    const int items = p.c.Hkv * chunks;  // of one sequence
+
+    if (lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) mbar_init(bars + 8 * s, 1);
+        mbar_init_fence();
+    }
+    if (tid == 0) *abort_flag = 0;
+
+    // This block's share of the tile list, from the lengths: the total first,
+    // then the sequence in which the share begins.
+    long long mine = 0;
+    for (int b = tid; b < p.B; b += kThreads) {
+        int slot;
+        mine += (long long)tiles_of(kv4_sequence(p.c, b, slot)) * items;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    if (tid == 0) {
+        long long x = 0;
+        for (int w = 0; w < kWarps; ++w) x += s_sum[w];
+        s_total = x;
+    }
+    __syncthreads();
+    const long long total = s_total;
+    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
+    const long long first = share * blockIdx.x, last = min(total, first + share);
+    Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
+    if (tid == 0) parts.join[blockIdx.x].w = 0;
+    if (first >= last) return;
+    if (warp == 0) {  // warp-wide prefix, 32 sequences a step
+        long long before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            int slot;
+            const int b = b0 + lane;
+            const long long x = b < p.B ? (long long)tiles_of(kv4_sequence(p.c, b, slot)) * items : 0;
+            long long incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(~0u, incl, o);
+                if (lane >= o) incl += y;
+            }
+            if (before + incl - x <= first && first < before + incl) {
+                s_b = b;
+                s_base = before + incl - x;
+            }
+            before += __shfl_sync(~0u, incl, 31);
+            if (before > first) break;
+        }
+    }
+    __syncthreads();
+    Walk seg;  // the item in hand
+    seg.b = s_b;
+    walk_sequence(p, seg);
+    {
+        const long long off = first - s_base;
+        seg.hc = (int)(off / seg.nt);
+        seg.t = (int)(off % seg.nt);  // first tile of this block in it
+    }
+    int left = (int)(last - first);  // tiles of this block from seg.t on
+
+    // ---- the warp's loads, running ahead of its tiles
+    Walk ld = seg;
+    int ld_left = left - warp;  // > 0: a tile to load
+    walk_on(p, ld, warp, items);
+    int issued = 0, page0 = 0, page1 = 0;
+    bool skip_first = p.fault == 1;
+    const int page_keys = 1 << p.c.page_shift;
+    auto look_up = [&]() {  // skip tiles without keys, then find the pages of the next one
+        while (ld_left > 0 && ld.len == 0) {
+            walk_on(p, ld, kWarps, items);
+            ld_left -= kWarps;
+        }
+        if (ld_left > 0) {
+            const int key = ld.t * kTileKeys;
+            page0 = kv4_page(p.c, ld.slot, key);
+            if (page_keys == 16 && key + 16 < ld.len) page1 = kv4_page(p.c, ld.slot, key + 16);
+        }
+    };
+    auto issue = [&]() {
+        if (ld_left <= 0) return;
+        if (lane == 0 && !skip_first) {
+            const int key = ld.t * kTileKeys, h = ld.hc / chunks;
+            const uint32_t st = issued % C::STAGES, dst = ring + st * C::STAGE, bar = bars + 8 * st;
+            const bool two = key + 16 < ld.len;
+            mbar_arrive_expect_tx(bar, two ? 2 * C::UNIT : C::UNIT);
+            const uint8_t* src = p.c.pool + kv4_unit(p.c, D, page0, h, key);
+            if (page_keys > 16) {
+                bulk_load(dst, src, two ? 2 * C::UNIT : C::UNIT, bar);
+            } else {
+                bulk_load(dst, src, C::UNIT, bar);
+                if (two) bulk_load(dst + C::UNIT, p.c.pool + kv4_unit(p.c, D, page1, h, key + 16), C::UNIT, bar);
+            }
+        }
+        skip_first = false;
+        ++issued;
+        walk_on(p, ld, kWarps, items);
+        ld_left -= kWarps;
+        look_up();
+    };
+    look_up();
+    for (int s = 0; s < C::STAGES; ++s) issue();
+
+    int used = 0;      // stages consumed
+    int next = warp;   // the warp's next tile, counted from the block's first
+    int done = 0;      // tiles of the block before the segment in hand
+    bool failed = false;
+    while (left > 0) {
+        const int n_seg = min(left, seg.nt - seg.t);
+        const int h = seg.hc / chunks, chunk = seg.hc - h * chunks;
+        const int r0 = chunk * C::ROWS, nrows = min(C::ROWS, p.R - r0);
+        const long long row0 = ((long long)seg.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
+        const int len = seg.len;
+        // keys every row may see; behind them scores are masked one by one
+        const int all_see = p.causal ? len - p.Lq + 1 : len;
+
+        // Q fragments: lane (g, t4) holds dimensions t4 D/4 ... of rows g, 8 + g
+        uint32_t qf[MODE == 2 ? 1 : NT * KS * 2];
+        float sc[NT][2];
+        int lim[NT][2];
+        float m[NT][2], l[NT][2], acc[NT][KS][4];
+        const uint32_t qbuf = base + C::RING + C::OBUF;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = 8 * nt + g, r = MODE == 0 ? (col & 3) : col;
+            uint32_t x[KS * 2];
+            uint32_t top = 0;
+            if (r < nrows) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D + t4 * (D / 4));
+#pragma unroll
+                for (int i = 0; i < KS / 2; ++i) {
+                    const uint4 v = __ldg(src + i);
+                    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < KS * 2; ++i) x[i] = 0;
+            }
+#pragma unroll
+            for (int i = 0; i < KS * 2; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            // power of two of the row: its largest magnitude comes to [1, 2)
+            const int e = top >= 0x7f80u || top == 0 ? 0 : max((int)(top >> 7) - 127, -120);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int i = 0; i < KS * 2; ++i) {
+                const uint32_t f = f16x2(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
+                if constexpr (MODE == 2)
+                    x[i] = f;
+                else
+                    qf[nt * KS * 2 + i] = f;
+            }
+            if constexpr (MODE == 2) {  // every warp holds the same fragments: the first writes them
+                if (warp == 0) {
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qbuf + ((nt * KS + i) * 32 + lane) * 8),
+                                     "r"(x[2 * i]), "r"(x[2 * i + 1])
+                                     : "memory");
+                }
+            }
+            const float s = p.scale * 1.4426950408889634f * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
+                const int cc = 8 * nt + 2 * t4 + c, rr = r0 + (MODE == 0 ? (cc & 3) : cc);
+                lim[nt][c] = p.causal ? rr % p.Lq + all_see : len;
+                m[nt][c] = -FLT_MAX;
+                l[nt][c] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
+        }
+        if constexpr (MODE == 2) __syncthreads();
+
+        for (; next < done + n_seg && len > 0; next += kWarps) {
+            const int key0 = (seg.t + next - done) * kTileKeys;
+            const uint32_t st = used % C::STAGES, tile = ring + st * C::STAGE;
+            if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
+                failed = true;
+                break;
+            }
+            const bool border = key0 + kTileKeys > all_see;
+            const int nu = key0 + 16 < len ? 2 : 1;
+
+            // ---- S^T = K Q^T
+            float s[2][NT][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[u][nt][c] = u < nu ? 0.f : -INFINITY;
+                if (u < nu) {
+                    const uint32_t unit = tile + u * C::UNIT;
+                    uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
+                    if constexpr (D == 128) {
+                        const uint4 a = lds16(unit + g * 64 + t4 * 16), b = lds16(unit + (g + 8) * 64 + t4 * 16);
+                        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+                        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+                        const uint32_t x = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + g * 8 + t4 * 2));
+                        const uint32_t y = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + (g + 8) * 8 + t4 * 2));
+                        sa[0] = __byte_perm(x, x, 0x1010), sa[1] = __byte_perm(x, x, 0x3232);
+                        sb[0] = __byte_perm(y, y, 0x1010), sb[1] = __byte_perm(y, y, 0x3232);
+                    } else {
+                        const uint2 a = lds8(unit + g * 32 + t4 * 8), b = lds8(unit + (g + 8) * 32 + t4 * 8);
+                        ka[0] = a.x, ka[1] = a.y;
+                        kb[0] = b.x, kb[1] = b.y;
+                        const uint32_t x = lds_u8(unit + 16 * D + g * 4 + t4), y = lds_u8(unit + 16 * D + (g + 8) * 4 + t4);
+                        sa[0] = e4m3x2_to_f16x2((uint16_t)(x | x << 8));
+                        sb[0] = e4m3x2_to_f16x2((uint16_t)(y | y << 8));
+                    }
+                    auto step = [&](auto jj) {
+                        constexpr int j = decltype(jj)::value;
+                        const uint32_t a0 = hmul2(code_pair<2 * j>(ka), sa[j / 4]);
+                        const uint32_t a1 = hmul2(code_pair<2 * j>(kb), sb[j / 4]);
+                        const uint32_t a2 = hmul2(code_pair<2 * j + 1>(ka), sa[j / 4]);
+                        const uint32_t a3 = hmul2(code_pair<2 * j + 1>(kb), sb[j / 4]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (MODE == 2) {
+                                const uint2 b = lds8(qbuf + ((nt * KS + j) * 32 + lane) * 8);
+                                mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                            } else {
+                                mma_f16(s[u][nt], a0, a1, a2, a3, qf[2 * j], qf[2 * j + 1]);
+                            }
+                        }
+                    };
+                    for_steps(step, std::make_integer_sequence<int, KS>{});
+                }
+            }
+            // ---- scores in log2 units, masks, the running maximum
+            bool raise = false;
+            float mx[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        s[u][nt][c] *= sc[nt][c & 1];
+                        if (border && key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
+                    }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    mx[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+                    raise |= mx[nt][c] > m[nt][c] + kRaise;
+                }
+            }
+            if (__any_sync(~0u, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float x = mx[nt][c];
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                        x = fmaxf(x, m[nt][c]);
+                        const float a = x == m[nt][c] ? 1.f : ex2_approx(m[nt][c] - x);
+                        m[nt][c] = x;
+                        l[nt][c] *= a;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            acc[nt][i][c] *= a;
+                            acc[nt][i][c + 2] *= a;
+                        }
+                    }
+            }
+            // ---- P^T as two fp16 numbers, turned into B fragments
+            uint32_t pb[2][NT][MODE == 0 ? 1 : 2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k8 = 0; k8 < 2; ++k8) {
+                        const float p0 = ex2_approx(s[u][nt][2 * k8] - m[nt][0]);
+                        const float p1 = ex2_approx(s[u][nt][2 * k8 + 1] - m[nt][1]);
+                        l[nt][0] += p0;
+                        l[nt][1] += p1;
+                        const uint32_t hi = f16x2(p0, p1);
+                        const float2 f = f16x2_to_f32(hi);
+                        const uint32_t lo = f16x2(p0 - f.x, p1 - f.y);
+                        if constexpr (MODE == 0) {
+                            pb[u][nt][0][k8] = transpose8x8(t4 < 2 ? hi : lo);
+                        } else {
+                            pb[u][nt][0][k8] = transpose8x8(hi);
+                            pb[u][nt][1][k8] = transpose8x8(lo);
+                        }
+                    }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u >= nu) break;
+                const uint32_t unit = tile + u * C::UNIT;
+                const int grp = D == 128 ? g : g >> 1;
+                uint32_t va[KS / 2], vb[KS / 2];
+                if constexpr (D == 128) {
+                    const uint4 a = lds16(unit + 8 * D + g * 64 + t4 * 16), b = lds16(unit + 12 * D + g * 64 + t4 * 16);
+                    va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
+                    vb[0] = b.x, vb[1] = b.y, vb[2] = b.z, vb[3] = b.w;
+                } else {
+                    const uint32_t at = unit + 8 * D + grp * 64 + t4 * 16 + (g & 1) * 8;
+                    const uint2 a = lds8(at), b = lds8(at + 4 * D);
+                    va[0] = a.x, va[1] = a.y;
+                    vb[0] = b.x, vb[1] = b.y;
+                }
+                uint32_t sa = e4m3x2_to_f16x2(lds_u16(unit + 17 * D + grp * 16 + 2 * t4));
+                uint32_t sb = e4m3x2_to_f16x2(lds_u16(unit + 17 * D + grp * 16 + 8 + 2 * t4));
+                if (border) {
+                    // positions behind the end: whatever their scales hold becomes 0
+                    const int k = key0 + 16 * u + 2 * t4;
+                    if (k >= len) sa = 0;
+                    if (k + 1 >= len) sa &= 0xffffu;
+                    if (k + 8 >= len) sb = 0;
+                    if (k + 9 >= len) sb &= 0xffffu;
+                    // A NaN scale reaches only the rows that see its key: it is
+                    // taken out of the product and put into their sums.
+                    const uint32_t na = nan_halves(sa), nb = nan_halves(sb);
+                    if (__any_sync(~0u, na | nb)) {
+                        sa = (na & 1 ? 0u : sa & 0xffffu) | (na & 2 ? 0u : sa & 0xffff0000u);
+                        sb = (nb & 1 ? 0u : sb & 0xffffu) | (nb & 2 ? 0u : sb & 0xffff0000u);
+                        for (int j = 0; j < 16; ++j) {
+                            if ((lds_u8(unit + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (key0 + 16 * u + j < min(lim[nt][c], len)) {
+#pragma unroll
+                                        for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
+                                    }
+                        }
+                    }
+                }
+                auto step = [&](auto ii) {
+                    constexpr int i = decltype(ii)::value;
+                    const uint32_t a0 = hmul2(code_pair<2 * i>(va), sa), a1 = hmul2(code_pair<2 * i + 1>(va), sa);
+                    const uint32_t a2 = hmul2(code_pair<2 * i>(vb), sb), a3 = hmul2(code_pair<2 * i + 1>(vb), sb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
+                        if constexpr (MODE != 0) mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
+                    }
+                };
+                for_steps(step, std::make_integer_sequence<int, KS>{});
+            }
+            __syncwarp();  // the stage has been read
+            ++used;
+            issue();
+        }
+        if (len == 0)
+            while (next < done + n_seg) next += kWarps;
+
+        // ---- join the warps
+        const bool whole = seg.t == 0 && n_seg == seg.nt;
+        const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
+        const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = l[nt][c];
+                x += __shfl_xor_sync(~0u, x, 4);
+                x += __shfl_xor_sync(~0u, x, 8);
+                x += __shfl_xor_sync(~0u, x, 16);
+                const int col = 8 * nt + 2 * t4 + c;
+                if (g == 0 && col < C::ROWS) mlbuf[warp * C::ROWS + col] = make_float2(m[nt][c], x);
+                // the buffer holds column `col`, dimension d at a place that
+                // spreads a store's lanes over the banks
+                float* dst = obuf + (warp * 8 + 2 * t4 + c) * C::OSTRIDE;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    const int at = D == 128 ? 16 * g + ((2 * i + 2 * g) & 15) : 8 * g + 2 * i;
+                    *reinterpret_cast<float2*>(dst + at) = make_float2(acc[nt][i][c], acc[nt][i][c + 2]);
+                }
+            }
+            if (__syncthreads_or(failed)) {
+                // waits ran out: let the copies in flight land, then leave
+                for (; used < issued; ++used)
+                    if (!(p.fault == 1 && used == 0))
+                        mbar_settle(bars + 8 * (used % C::STAGES), (used / C::STAGES) & 1, wf, 51);
+                return;
+            }
+            const int cols = MODE == 0 ? 4 : 8;
+            for (int x = tid; x < cols * D; x += kThreads) {
+                const int col = x / D, d = x % D, r = 8 * nt + col;
+                if (r >= nrows) break;
+                const int at = D == 128 ? (d & ~15) | ((d + 2 * (d >> 4)) & 15) : d;
+                float mm = -FLT_MAX;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[w * C::ROWS + r].x);
+                float o = 0.f, sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float2 ml = mlbuf[w * C::ROWS + r];
+                    const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
+                    float v = obuf[(w * 8 + col) * C::OSTRIDE + at];
+                    if constexpr (MODE == 0) v += obuf[(w * 8 + col + 4) * C::OSTRIDE + at];
+                    o = fmaf(a, v, o);
+                    sum = fmaf(a, ml.y, sum);
+                }
+                if (whole) {
+                    p.o[(row0 + r) * D + d] = sum == 0.f ? 0.f : o / sum * gv;
+                    if (d == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
+                } else {
+                    parts.o[((long long)part * C::ROWS + r) * D + d] = o;
+                    if (d == 0) parts.ml[(long long)part * C::ROWS + r] = make_float2(mm, sum);
+                }
+            }
+            __syncthreads();
+        }
+        if (tid == 0 && seg.t == 0 && !whole) {
+            const long long end = first + done + seg.nt;  // of the item in the tile list
+            parts.join[blockIdx.x] = make_int4(seg.b, seg.hc, (int)((end - 1) / share), 1);
+        }
+        left -= n_seg;
+        done += n_seg;
+        if (left > 0) {
+            seg.t = 0;
+            if (++seg.hc == items) {
+                seg.hc = 0;
+                ++seg.b;
+                walk_sequence(p, seg);
             }
         }
     }
-    if (tid < D) p.o[row * D + tid] = lim > 0 ? acc / l * gv : 0.f;
-    if (tid == 0) p.lse[row] = lim > 0 ? m + logf(l) : -INFINITY;
 }
+
+// Joins the parts of the item that begins in block blockIdx.x and ends in a
+// later one: one warp per row, parts in order.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads) fa_kv4_join_kernel(const Kv4AttnParams p, const int chunks)
+{
+    constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32;
+    const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
+    const int4 j = parts.join[blockIdx.x];
+    if (j.w == 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int h = j.y / chunks, r0 = (j.y - h * chunks) * ROWS, nrows = min(ROWS, p.R - r0);
+    const long long row0 = ((long long)j.x * p.Hq + (long long)h * p.group) * p.Lq + r0;
+    const int n = j.z - (int)blockIdx.x + 1;
+    const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
+    const auto index = [&](int k, int r) {
+        return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
+    };
+    for (int r = warp; r < nrows; r += kWarps) {
+        float mm = -FLT_MAX;
+        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, parts.ml[index(k, r)].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+        float acc[V] = {}, sum = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float2 ml = parts.ml[index(k, r)];
+            const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
+            sum = fmaf(a, ml.y, sum);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(a, parts.o[index(k, r) * D + lane + 32 * e], acc[e]);
+        }
+        const float inv = sum == 0.f ? 0.f : gv / sum;
+#pragma unroll
+        for (int e = 0; e < V; ++e) p.o[(row0 + r) * D + lane + 32 * e] = acc[e] * inv;
+        if (lane == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
+    }
+}
+
+int mode_of(int R) { return R <= 4 ? 0 : R <= 8 ? 1 : 2; }
+
+template <int D, int MODE>
+cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
+{
+    using C = Cfg<D, MODE>;
+    static_assert(2 * (C::SMEM + 1024 + 256) <= 233472, "two blocks per SM");
+    const cudaError_t e = smem_limit_once<fa_kv4_attn_kernel<D, MODE>>(C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int chunks = (p.R + C::ROWS - 1) / C::ROWS;
+    fa_kv4_attn_kernel<D, MODE><<<blocks, kThreads, C::SMEM, stream>>>(p, chunks);
+    const cudaError_t f = cudaGetLastError();
+    if (f != cudaSuccess) return f;
+    fa_kv4_join_kernel<D, MODE><<<blocks, kThreads, 0, stream>>>(p, chunks);
+    return cudaGetLastError();
+}
+
+int blocks_of(int num_sms) { return 2 * num_sms; }
 
 }  // namespace
 
-cudaError_t kv4_attn_workspace(int, int, int, int, size_t* bytes)
+cudaError_t kv4_attn_workspace(int D, int R, int, int num_sms, size_t* bytes)
 {
-    *bytes = 0;
+    const size_t blocks = (size_t)blocks_of(num_sms), rows = blocks * 2 * (4u << mode_of(R));
+    *bytes = blocks * sizeof(int4) + rows * sizeof(float2) + rows * D * sizeof(float);
     return cudaSuccess;
 }
 
-cudaError_t launch_kv4_attn(int D, const Kv4AttnParams& p, int, cudaStream_t stream, int* launches)
+cudaError_t launch_kv4_attn(int D, const Kv4AttnParams& p, int num_sms, cudaStream_t stream, int* launches)
 {
-    const unsigned grid = (unsigned)(p.B * p.Hq * p.Lq);
+    *launches = 2;
+    const int blocks = blocks_of(num_sms), mode = mode_of(p.R);
     if (D == 128)
-        fa_kv4_attn_kernel<128><<<grid, kAttnThreads, 0, stream>>>(p);
-    else
-        fa_kv4_attn_kernel<64><<<grid, kAttnThreads, 0, stream>>>(p);
-    *launches = 1;
-    return cudaGetLastError();
+        return mode == 0   ? launch<128, 0>(p, blocks, stream)
+               : mode == 1 ? launch<128, 1>(p, blocks, stream)
+                           : launch<128, 2>(p, blocks, stream);
+    return mode == 0 ? launch<64, 0>(p, blocks, stream)
+           : mode == 1 ? launch<64, 1>(p, blocks, stream)
+                       : launch<64, 2>(p, blocks, stream);
 }
 
 }  // namespace fa

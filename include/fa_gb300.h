@@ -396,7 +396,7 @@ fa_status_t fa_bwd_varlen_variant(const void* q, const void* k, const void* v, c
  *             slots 0, 1, 2, ... in order
  *   k_scale, v_scale  fp32 [Hkv], positive and finite, or NULL for 1
  *   D 64 or 128; page_size 16, 32, 64, 128 or 256 (FA_ERR_UNSUPPORTED
- *   otherwise); num_slots at most 65536; table_width * page_size below 2^31.
+ *   otherwise); num_slots at most 65536; table_width * page_size at most 2^30.
  *
  * Slots, lengths and page numbers are read on the device and checked there: a
  * slot out of range, a length that is negative or above table_width *

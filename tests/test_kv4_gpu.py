@@ -605,6 +605,20 @@ def test_captured_decode_step_follows_the_cache():
     fa.fa_check()
 
 
+def test_a_load_that_never_arrives_ends_the_call_with_a_timeout():
+    rng = np.random.default_rng(12)
+    pool, table = random_cache(rng, [500, 40], 2, 64, 32)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32([500, 40]))
+    q = bf16(rng.standard_normal((2, 4, 1, 64))).to(DEV)
+    fa.load_library().fa_test_inject_fault(1)
+    fa.fa_fwd_kv4(q, *dev)
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_check()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    o, lse = run_attention(q, *dev)
+    check_attention(q, o, lse, pool, table, [0, 1], [500, 40], np.ones(2), np.ones(2), 0.125, False, "after a timeout")
+
+
 def test_two_calls_at_once_on_two_streams():
     rng = np.random.default_rng(11)
     lens = [2000, 3, 700]
