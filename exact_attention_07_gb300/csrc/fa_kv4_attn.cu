@@ -46,6 +46,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTileKeys = 32;
+// What beginning and joining an item costs a block, in tiles (the lists of
+// short sequences took 107 us where items counted only by their tiles).
+constexpr int kItemCost = 12;
 constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
 
 // MODE 0: up to 4 rows; 1: up to 8; 2: up to 16 (more rows: several items).
@@ -177,18 +180,19 @@ struct Walk {
 
 __device__ __forceinline__ void walk_sequence(const Kv4AttnParams& p, Walk& w)
 {
-    w.len = 0;
-    w.slot = 0;
-    if (w.b < p.B) w.len = kv4_sequence(p.c, w.b, w.slot);
+    w.len = kv4_sequence(p.c, w.b, w.slot);
     w.nt = tiles_of(w.len);
 }
 
-// n tiles on; items = KV heads x chunks of a sequence.
-__device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, int items)
+// n tiles on; items = KV heads x chunks of a sequence.  `left`, what remains
+// of the block's share from the tile on, pays for items entered.
+__device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, int items, int& left)
 {
     w.t += n;
-    while (w.t >= w.nt && w.b < p.B) {
+    left -= n;
+    while (w.t >= w.nt && left > 0) {
         w.t -= w.nt;
+        left -= kItemCost;
         if (++w.hc == items) {
             w.hc = 0;
             ++w.b;
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     using C = Cfg<D, MODE>;
     constexpr int NT = C::NT, KS = C::KS;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kWarps], s_total, s_base;
+    __shared__ long long s_sum[kWarps], s_base;
     __shared__ int s_b;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t base = smem_u32(smem);
@@ -221,72 +225,67 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     }
     if (tid == 0) *abort_flag = 0;
 
-    // This block's share of the tile list, from the lengths: the total first,
-    // then the sequence in which the share begins.
-    long long mine = 0;
-    for (int b = tid; b < p.B; b += kThreads) {
+    // This block's share of the list of all items, each kItemCost + its tiles
+    // long, from the lengths: thread i sums a run of sequences, the block's
+    // prefix sums give the total and the run in which the share begins.
+    const int run = (p.B + kThreads - 1) / kThreads;
+    const int run0 = min(p.B, tid * run), run1 = min(p.B, run0 + run);
+    auto cost = [&](int b) {
         int slot;
-        mine += (long long)tiles_of(kv4_sequence(p.c, b, slot)) * items;
-    }
+        return (long long)(tiles_of(kv4_sequence(p.c, b, slot)) + kItemCost) * items;
+    };
+    long long mine = 0;
+    for (int b = run0; b < run1; ++b) mine += cost(b);
+    long long upto = mine;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-        long long x = 0;
-        for (int w = 0; w < kWarps; ++w) x += s_sum[w];
-        s_total = x;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(~0u, upto, o);
+        if (lane >= o) upto += y;
     }
+    if (lane == 31) s_sum[warp] = upto;
     __syncthreads();
-    const long long total = s_total;
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) upto += total;
+        total += s_sum[w];
+    }
     const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
     const long long first = share * blockIdx.x, last = min(total, first + share);
     Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
     if (tid == 0) parts.join[blockIdx.x].w = 0;
     if (first >= last) return;
-    if (warp == 0) {  // warp-wide prefix, 32 sequences a step
-        long long before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            int slot;
-            const int b = b0 + lane;
-            const long long x = b < p.B ? (long long)tiles_of(kv4_sequence(p.c, b, slot)) * items : 0;
-            long long incl = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(~0u, incl, o);
-                if (lane >= o) incl += y;
-            }
-            if (before + incl - x <= first && first < before + incl) {
-                s_b = b;
-                s_base = before + incl - x;
-            }
-            before += __shfl_sync(~0u, incl, 31);
-            if (before > first) break;
-        }
+    if (first < upto && first >= upto - mine) {
+        long long at = upto - mine;
+        int b = run0;
+        for (long long x; at + (x = cost(b)) <= first; ++b) at += x;
+        s_b = b;
+        s_base = at;
     }
     __syncthreads();
     Walk seg;  // the item in hand
     seg.b = s_b;
     walk_sequence(p, seg);
+    int left = (int)(last - first);  // of the share, from tile seg.t on
     {
         const long long off = first - s_base;
-        seg.hc = (int)(off / seg.nt);
-        seg.t = (int)(off % seg.nt);  // first tile of this block in it
+        seg.hc = (int)(off / (seg.nt + kItemCost));
+        seg.t = (int)(off % (seg.nt + kItemCost)) - kItemCost;  // first tile of this block in it
+        if (seg.t < 0) {
+            left += seg.t;
+            seg.t = 0;
+        }
     }
-    int left = (int)(last - first);  // tiles of this block from seg.t on
 
     // ---- the warp's loads, running ahead of its tiles
     Walk ld = seg;
-    int ld_left = left - warp;  // > 0: a tile to load
-    walk_on(p, ld, warp, items);
+    int ld_left = left;  // > 0: a tile to load
+    walk_on(p, ld, warp, items, ld_left);
     int issued = 0, page0 = 0, page1 = 0;
     bool skip_first = p.fault == 1;
     const int page_keys = 1 << p.c.page_shift;
     auto look_up = [&]() {  // skip tiles without keys, then find the pages of the next one
-        while (ld_left > 0 && ld.len == 0) {
-            walk_on(p, ld, kWarps, items);
-            ld_left -= kWarps;
-        }
+        while (ld_left > 0 && ld.len == 0) walk_on(p, ld, kWarps, items, ld_left);
         if (ld_left > 0) {
             const int key = ld.t * kTileKeys;
             page0 = kv4_page(p.c, ld.slot, key);
@@ -310,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         skip_first = false;
         ++issued;
-        walk_on(p, ld, kWarps, items);
-        ld_left -= kWarps;
+        walk_on(p, ld, kWarps, items, ld_left);
         look_up();
     };
     look_up();
@@ -632,13 +630,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             __syncthreads();
         }
         if (tid == 0 && seg.t == 0 && !whole) {
-            const long long end = first + done + seg.nt;  // of the item in the tile list
+            const long long end = last - left + seg.nt;  // of the item in the list
             parts.join[blockIdx.x] = make_int4(seg.b, seg.hc, (int)((end - 1) / share), 1);
         }
         left -= n_seg;
         done += n_seg;
         if (left > 0) {
             seg.t = 0;
+            left -= kItemCost;
             if (++seg.hc == items) {
                 seg.hc = 0;
                 ++seg.b;
@@ -649,11 +648,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 }
 
 // Joins the parts of the item that begins in block blockIdx.x and ends in a
-// later one: one warp per row, parts in order.
+// later one.  Several warps share a row: each adds every WPR-th part in order,
+// then the warps' sums are added in order.
+constexpr int kJoinThreads = 1024;
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads) fa_kv4_join_kernel(const Kv4AttnParams p, const int chunks)
+__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4AttnParams p, const int chunks)
 {
-    constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32;
+    constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32, WPR = kJoinThreads / 32 / ROWS;
+    __shared__ float s_o[ROWS][WPR][D];
+    __shared__ float2 s_ml[ROWS][WPR];
     const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
     const int4 j = parts.join[blockIdx.x];
     if (j.w == 0) return;
@@ -661,28 +665,36 @@ __global__ void __launch_bounds__(kThreads) fa_kv4_join_kernel(const Kv4AttnPara
     const int h = j.y / chunks, r0 = (j.y - h * chunks) * ROWS, nrows = min(ROWS, p.R - r0);
     const long long row0 = ((long long)j.x * p.Hq + (long long)h * p.group) * p.Lq + r0;
     const int n = j.z - (int)blockIdx.x + 1;
-    const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
-    const auto index = [&](int k, int r) {
-        return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
-    };
-    for (int r = warp; r < nrows; r += kWarps) {
-        float mm = -FLT_MAX;
-        for (int k = lane; k < n; k += 32) mm = fmaxf(mm, parts.ml[index(k, r)].x);
+    const int r = warp / WPR, w = warp % WPR;
+    const auto index = [&](int k) { return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r; };
+    float mm = -FLT_MAX;
+    for (int k = lane; k < n; k += 32) mm = fmaxf(mm, parts.ml[index(k)].x);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-        float acc[V] = {}, sum = 0.f;
+    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
+    float acc[V] = {}, sum = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float2 ml = parts.ml[index(k, r)];
-            const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
-            sum = fmaf(a, ml.y, sum);
+    for (int k = w; k < n; k += WPR) {
+        const float2 ml = parts.ml[index(k)];
+        const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
+        sum = fmaf(a, ml.y, sum);
 #pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] = fmaf(a, parts.o[index(k, r) * D + lane + 32 * e], acc[e]);
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(a, parts.o[index(k) * D + lane + 32 * e], acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[r][w][lane + 32 * e] = acc[e];
+    if (lane == 0) s_ml[r][w] = make_float2(mm, sum);
+    __syncthreads();
+    const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
+    for (int x = threadIdx.x; x < nrows * D; x += kJoinThreads) {
+        const int rr = x / D, d = x % D;
+        float o = 0.f, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+            o += s_o[rr][i][d];
+            l += s_ml[rr][i].y;
         }
-        const float inv = sum == 0.f ? 0.f : gv / sum;
-#pragma unroll
-        for (int e = 0; e < V; ++e) p.o[(row0 + r) * D + lane + 32 * e] = acc[e] * inv;
-        if (lane == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
+        p.o[(row0 + rr) * D + d] = l == 0.f ? 0.f : o / l * gv;
+        if (d == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (s_ml[rr][0].x + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -699,7 +711,7 @@ cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
     fa_kv4_attn_kernel<D, MODE><<<blocks, kThreads, C::SMEM, stream>>>(p, chunks);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return f;
-    fa_kv4_join_kernel<D, MODE><<<blocks, kThreads, 0, stream>>>(p, chunks);
+    fa_kv4_join_kernel<D, MODE><<<blocks, kJoinThreads, 0, stream>>>(p, chunks);
     return cudaGetLastError();
 }
 
