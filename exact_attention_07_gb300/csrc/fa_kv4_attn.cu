@@ -45,18 +45,21 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTileKeys = 32;
 // What beginning and joining an item costs a block, in tiles (the lists of
 // short sequences took 107 us where items counted only by their tiles).
 constexpr int kItemCost = 12;
 constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
 
+// Keys of a warp's tile: 4608 bytes.
+__host__ __device__ constexpr int tile_keys(int D) { return D == 128 ? 32 : 64; }
+
 // MODE 0: up to 4 rows; 1: up to 8; 2: up to 16 (more rows: several items).
 template <int D, int MODE>
 struct Cfg {
     static constexpr int UNIT = 18 * D;
-    static constexpr int STAGE = 2 * UNIT;
-    static constexpr int STAGES = D == 128 ? 2 : 4;  // per warp
+    static constexpr int NU = tile_keys(D) / 16;  // units of a tile
+    static constexpr int STAGE = NU * UNIT;
+    static constexpr int STAGES = 2;  // per warp
     static constexpr int ROWS = 4 << MODE;
     static constexpr int NT = MODE == 2 ? 2 : 1;  // column tiles of 8
     static constexpr int KS = D / 16;             // MMA steps over D, and 16-row tiles of O^T
@@ -153,7 +156,11 @@ __device__ __forceinline__ uint32_t nan_halves(uint32_t s)
     return ((s & 0x7fffu) > 0x7c00u ? 1u : 0u) | ((s >> 16 & 0x7fffu) > 0x7c00u ? 2u : 0u);
 }
 
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTileKeys - 1) / kTileKeys : 1; }
+template <int D>
+__device__ __forceinline__ int tiles_of(int len)
+{
+    return len > 0 ? (len + tile_keys(D) - 1) / tile_keys(D) : 1;
+}
 
 // Where the kernels keep what they share in the workspace.
 struct Parts {
@@ -175,17 +182,22 @@ __host__ __device__ inline Parts parts_of(float* ws, int blocks)
 
 // A walk over the tile list: tile t of item hc (KV head and chunk of rows) of sequence b.
 struct Walk {
-    int b, hc, t, nt, len, slot;
+    int b, hc, t, nt, len;
+    const int* row;  // of the table
 };
 
+template <int D>
 __device__ __forceinline__ void walk_sequence(const Kv4AttnParams& p, Walk& w)
 {
-    w.len = kv4_sequence(p.c, w.b, w.slot);
-    w.nt = tiles_of(w.len);
+    int slot;
+    w.len = kv4_sequence(p.c, w.b, slot);
+    w.row = p.c.table + (long long)slot * p.c.table_width;
+    w.nt = tiles_of<D>(w.len);
 }
 
 // n tiles on; items = KV heads x chunks of a sequence.  `left`, what remains
 // of the block's share from the tile on, pays for items entered.
+template <int D>
 __device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, int items, int& left)
 {
     w.t += n;
@@ -196,7 +208,7 @@ __device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, 
         if (++w.hc == items) {
             w.hc = 0;
             ++w.b;
-            walk_sequence(p, w);
+            walk_sequence<D>(p, w);
         }
     }
 }
@@ -205,7 +217,7 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnParams p, const int chunks)
 {
     using C = Cfg<D, MODE>;
-    constexpr int NT = C::NT, KS = C::KS;
+    constexpr int NT = C::NT, KS = C::KS, NU = C::NU, TILE = tile_keys(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps], s_base;
     __shared__ int s_b;
@@ -219,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     const WaitFailure wf{p.c.err, p.c.diag};
     const int items = p.c.Hkv * chunks;  // of one sequence
 
+    let_dependents_launch();
     if (lane == 0) {
         for (int s = 0; s < C::STAGES; ++s) mbar_init(bars + 8 * s, 1);
         mbar_init_fence();
@@ -232,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     const int run0 = min(p.B, tid * run), run1 = min(p.B, run0 + run);
     auto cost = [&](int b) {
         int slot;
-        return (long long)(tiles_of(kv4_sequence(p.c, b, slot)) + kItemCost) * items;
+        return (long long)(tiles_of<D>(kv4_sequence(p.c, b, slot)) + kItemCost) * items;
     };
     long long mine = 0;
     for (int b = run0; b < run1; ++b) mine += cost(b);
@@ -265,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     __syncthreads();
     Walk seg;  // the item in hand
     seg.b = s_b;
-    walk_sequence(p, seg);
+    walk_sequence<D>(p, seg);
     int left = (int)(last - first);  // of the share, from tile seg.t on
     {
         const long long off = first - s_base;
@@ -277,44 +290,75 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
     }
 
-    // ---- the warp's loads, running ahead of its tiles
+    // ---- the warp's loads, running ahead of its tiles: lane i holds where the
+    // warp's i-th tile from `ld` on lies and copies it when its turn comes
     Walk ld = seg;
     int ld_left = left;  // > 0: a tile to load
-    walk_on(p, ld, warp, items, ld_left);
-    int issued = 0, page0 = 0, page1 = 0;
-    bool skip_first = p.fault == 1;
-    const int page_keys = 1 << p.c.page_shift;
-    auto look_up = [&]() {  // skip tiles without keys, then find the pages of the next one
-        while (ld_left > 0 && ld.len == 0) walk_on(p, ld, kWarps, items, ld_left);
-        if (ld_left > 0) {
-            const int key = ld.t * kTileKeys;
-            page0 = kv4_page(p.c, ld.slot, key);
-            if (page_keys == 16 && key + 16 < ld.len) page1 = kv4_page(p.c, ld.slot, key + 16);
-        }
-    };
-    auto issue = [&]() {
-        if (ld_left <= 0) return;
-        if (lane == 0 && !skip_first) {
-            const int key = ld.t * kTileKeys, h = ld.hc / chunks;
-            const uint32_t st = issued % C::STAGES, dst = ring + st * C::STAGE, bar = bars + 8 * st;
-            const bool two = key + 16 < ld.len;
-            mbar_arrive_expect_tx(bar, two ? 2 * C::UNIT : C::UNIT);
-            const uint8_t* src = p.c.pool + kv4_unit(p.c, D, page0, h, key);
-            if (page_keys > 16) {
-                bulk_load(dst, src, two ? 2 * C::UNIT : C::UNIT, bar);
-            } else {
-                bulk_load(dst, src, C::UNIT, bar);
-                if (two) bulk_load(dst + C::UNIT, p.c.pool + kv4_unit(p.c, D, page1, h, key + 16), C::UNIT, bar);
+    walk_on<D>(p, ld, warp, items, ld_left);
+    const int shift = p.c.page_shift, units = 1 << (shift - 4);
+    const int span = min(1 << shift, TILE);  // keys of a tile in one page
+    const uint32_t head_bytes = (uint32_t)units * C::UNIT;
+    const long long page_bytes = (long long)p.c.Hkv * head_bytes;
+    int my_page[NU], my_units = 0;
+    uint32_t my_off = 0, turn = 0;  // turn: lanes that have a tile to copy
+    auto refill = [&]() {
+        Walk w = ld;
+        int w_left = ld_left;
+        walk_on<D>(p, w, kWarps * lane, items, w_left);
+        const int key0 = w.t * TILE;
+        my_units = w_left > 0 ? min(NU, (w.len - key0 + 15) >> 4) : 0;  // 0 without keys
+        my_off = (uint32_t)(w.hc / chunks) * head_bytes + ((key0 >> 4) & (units - 1)) * C::UNIT;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+            my_page[i] = 0;
+            if (i * (span >> 4) < my_units) {
+                my_page[i] = w.row[(key0 >> shift) + i];
+                if ((unsigned)my_page[i] >= (unsigned)p.c.num_pages) {
+                    atomicOr(p.c.err, 2);
+                    my_page[i] = 0;
+                }
             }
         }
-        skip_first = false;
-        ++issued;
-        walk_on(p, ld, kWarps, items, ld_left);
-        look_up();
+        turn = __ballot_sync(~0u, my_units > 0);
+        // the next batch begins one step behind lane 31's tile
+        ld.b = __shfl_sync(~0u, w.b, 31);
+        ld.hc = __shfl_sync(~0u, w.hc, 31);
+        ld.t = __shfl_sync(~0u, w.t, 31);
+        ld.nt = __shfl_sync(~0u, w.nt, 31);
+        ld.len = __shfl_sync(~0u, w.len, 31);
+        ld.row = reinterpret_cast<const int*>(__shfl_sync(~0u, reinterpret_cast<long long>(w.row), 31));
+        ld_left = __shfl_sync(~0u, w_left, 31);
+        walk_on<D>(p, ld, kWarps, items, ld_left);
     };
-    look_up();
+    int issued = 0;
+    auto issue = [&]() {
+        if (turn == 0) return;
+        if (lane == __ffs(turn) - 1 && !(p.fault == 1 && issued == 0)) {
+            const int st = issued % C::STAGES;
+            const uint32_t dst = ring + st * C::STAGE, bar = bars + 8 * st;
+            const uint8_t* src = p.c.pool + my_off;
+            mbar_arrive_expect_tx(bar, my_units * C::UNIT);
+            if (span == TILE) {
+                bulk_load(dst, src + my_page[0] * page_bytes, my_units * C::UNIT, bar);
+            } else {  // pages shorter than the tile: it starts at a page's first unit
+#pragma unroll
+                for (int i = 0; i < NU; ++i) {
+                    const int u0 = i * (span >> 4);
+                    if (u0 < my_units)
+                        bulk_load(dst + u0 * C::UNIT, src + my_page[i] * page_bytes,
+                                  min(span >> 4, my_units - u0) * C::UNIT, bar);
+                }
+            }
+        }
+        turn &= turn - 1;
+        ++issued;
+        while (turn == 0 && ld_left > 0) refill();
+    };
+    while (turn == 0 && ld_left > 0) refill();
     for (int s = 0; s < C::STAGES; ++s) issue();
 
+    // MODE 0: what a lane's columns take of hi, 0 (columns 0 .. 3) or -1
+    const uint64_t part2 = t4 < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);
     int used = 0;      // stages consumed
     int next = warp;   // the warp's next tile, counted from the block's first
     int done = 0;      // tiles of the block before the segment in hand
@@ -392,19 +436,19 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         if constexpr (MODE == 2) __syncthreads();
 
         for (; next < done + n_seg && len > 0; next += kWarps) {
-            const int key0 = (seg.t + next - done) * kTileKeys;
+            const int key0 = (seg.t + next - done) * TILE;
             const uint32_t st = used % C::STAGES, tile = ring + st * C::STAGE;
             if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
                 failed = true;
                 break;
             }
-            const bool border = key0 + kTileKeys > all_see;
-            const int nu = key0 + 16 < len ? 2 : 1;
+            const bool border = key0 + TILE > all_see;
+            const int nu = min(NU, (len - key0 + 15) >> 4);
 
             // ---- S^T = K Q^T
-            float s[2][NT][4];
+            float s[NU][NT][4];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < NU; ++u) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -447,24 +491,28 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     for_steps(step, std::make_integer_sequence<int, KS>{});
                 }
             }
-            // ---- scores in log2 units, masks, the running maximum
+            // ---- masks, the running maximum in log2 units
+            if (border) {
+#pragma unroll
+                for (int u = 0; u < NU; ++u)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
+            }
             bool raise = false;
             float mx[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        s[u][nt][c] *= sc[nt][c & 1];
-                        if (border && key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
-                    }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    mx[nt][c] = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
+                    float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+#pragma unroll
+                    for (int u = 1; u < NU; ++u) x = fmaxf(x, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
+                    mx[nt][c] = x * sc[nt][c];
                     raise |= mx[nt][c] > m[nt][c] + kRaise;
                 }
-            }
             if (__any_sync(~0u, raise)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -486,30 +534,35 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     }
             }
             // ---- P^T as two fp16 numbers, turned into B fragments
-            uint32_t pb[2][NT][MODE == 0 ? 1 : 2][2];
+            uint32_t pb[NU][NT][MODE == 0 ? 1 : 2][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint64_t sc2 = f2_pack(sc[nt][0], sc[nt][1]), m2 = f2_pack(-m[nt][0], -m[nt][1]);
+                uint64_t l2 = f2_pack(l[nt][0], l[nt][1]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int u = 0; u < NU; ++u)
 #pragma unroll
                     for (int k8 = 0; k8 < 2; ++k8) {
-                        const float p0 = ex2_approx(s[u][nt][2 * k8] - m[nt][0]);
-                        const float p1 = ex2_approx(s[u][nt][2 * k8 + 1] - m[nt][1]);
-                        l[nt][0] += p0;
-                        l[nt][1] += p1;
-                        const uint32_t hi = f16x2(p0, p1);
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(s[u][nt][2 * k8], s[u][nt][2 * k8 + 1]), sc2, m2), x0, x1);
+                        const uint64_t p2 = f2_pack(x0 = ex2_approx(x0), x1 = ex2_approx(x1));
+                        l2 = f2_add(l2, p2);
+                        const uint32_t hi = f16x2(x0, x1);
                         const float2 f = f16x2_to_f32(hi);
-                        const uint32_t lo = f16x2(p0 - f.x, p1 - f.y);
                         if constexpr (MODE == 0) {
-                            pb[u][nt][0][k8] = transpose8x8(t4 < 2 ? hi : lo);
+                            // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take p - hi
+                            f2_unpack(f2_fma(f2_pack(f.x, f.y), part2, p2), x0, x1);
+                            pb[u][nt][0][k8] = transpose8x8(f16x2(x0, x1));
                         } else {
                             pb[u][nt][0][k8] = transpose8x8(hi);
-                            pb[u][nt][1][k8] = transpose8x8(lo);
+                            pb[u][nt][1][k8] = transpose8x8(f16x2(x0 - f.x, x1 - f.y));
                         }
                     }
+                f2_unpack(l2, l[nt][0], l[nt][1]);
+            }
             // ---- O^T += V^T P^T
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < NU; ++u) {
                 if (u >= nu) break;
                 const uint32_t unit = tile + u * C::UNIT;
                 const int grp = D == 128 ? g : g >> 1;
@@ -641,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             if (++seg.hc == items) {
                 seg.hc = 0;
                 ++seg.b;
-                walk_sequence(p, seg);
+                walk_sequence<D>(p, seg);
             }
         }
     }
@@ -659,6 +712,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
     __shared__ float s_o[ROWS][WPR][D];
     __shared__ float2 s_ml[ROWS][WPR];
     const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
+    wait_for_primary();
     const int4 j = parts.join[blockIdx.x];
     if (j.w == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -711,8 +765,7 @@ cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
     fa_kv4_attn_kernel<D, MODE><<<blocks, kThreads, C::SMEM, stream>>>(p, chunks);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return f;
-    fa_kv4_join_kernel<D, MODE><<<blocks, kJoinThreads, 0, stream>>>(p, chunks);
-    return cudaGetLastError();
+    return launch_dependent(fa_kv4_join_kernel<D, MODE>, blocks, kJoinThreads, stream, p, chunks);
 }
 
 int blocks_of(int num_sms) { return 2 * num_sms; }

@@ -69,4 +69,25 @@ __device__ __forceinline__ long long kv4_unit(const Kv4Cache& c, int D, int page
     return (((long long)page * c.Hkv + h) * units + ((pos >> 4) & (units - 1))) * (18 * D);
 }
 
+// A second kernel that is launched while the first still runs (programmatic
+// dependent launch): its launch latency is hidden, and wait_for_primary()
+// returns once the first has ended and its writes are visible.
+__device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), int blocks, int threads, cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 }  // namespace fa
