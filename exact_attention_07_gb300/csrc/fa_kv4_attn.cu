@@ -80,6 +80,28 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+__device__ __forceinline__ uint32_t low_twice(uint32_t a)
+{
+    uint32_t r;
+    asm("{.reg .b16 x, y; mov.b32 {x, y}, %1; mov.b32 %0, {x, x};}" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t high_twice(uint32_t a)
+{
+    uint32_t r;
+    asm("{.reg .b16 x, y; mov.b32 {x, y}, %1; mov.b32 %0, {y, y};}" : "=r"(r) : "r"(a));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
@@ -115,7 +137,7 @@ __device__ __forceinline__ uint2 lds8(uint32_t a)
     return v;
 }
 
-__device__ __forceinline__ uint32_t lds_u16(uint32_t a)
+__device__ __forceinline__ uint16_t lds_u16(uint32_t a)
 {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
@@ -443,53 +465,59 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 break;
             }
             const bool border = key0 + TILE > all_see;
-            const int nu = min(NU, (len - key0 + 15) >> 4);
 
-            // ---- S^T = K Q^T
+            // ---- S^T = K Q^T.  Units behind the sequence's end hold old
+            // bytes: their scores are masked, their V scales zeroed.
             float s[NU][NT][4];
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) s[u][nt][c] = u < nu ? 0.f : -INFINITY;
-                if (u < nu) {
-                    const uint32_t unit = tile + u * C::UNIT;
-                    uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
-                    if constexpr (D == 128) {
-                        const uint4 a = lds16(unit + g * 64 + t4 * 16), b = lds16(unit + (g + 8) * 64 + t4 * 16);
-                        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
-                        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
-                        const uint32_t x = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + g * 8 + t4 * 2));
-                        const uint32_t y = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + (g + 8) * 8 + t4 * 2));
-                        sa[0] = __byte_perm(x, x, 0x1010), sa[1] = __byte_perm(x, x, 0x3232);
-                        sb[0] = __byte_perm(y, y, 0x1010), sb[1] = __byte_perm(y, y, 0x3232);
-                    } else {
-                        const uint2 a = lds8(unit + g * 32 + t4 * 8), b = lds8(unit + (g + 8) * 32 + t4 * 8);
-                        ka[0] = a.x, ka[1] = a.y;
-                        kb[0] = b.x, kb[1] = b.y;
-                        const uint32_t x = lds_u8(unit + 16 * D + g * 4 + t4), y = lds_u8(unit + 16 * D + (g + 8) * 4 + t4);
-                        sa[0] = e4m3x2_to_f16x2((uint16_t)(x | x << 8));
-                        sb[0] = e4m3x2_to_f16x2((uint16_t)(y | y << 8));
-                    }
-                    auto step = [&](auto jj) {
-                        constexpr int j = decltype(jj)::value;
-                        const uint32_t a0 = hmul2(code_pair<2 * j>(ka), sa[j / 4]);
-                        const uint32_t a1 = hmul2(code_pair<2 * j>(kb), sb[j / 4]);
-                        const uint32_t a2 = hmul2(code_pair<2 * j + 1>(ka), sa[j / 4]);
-                        const uint32_t a3 = hmul2(code_pair<2 * j + 1>(kb), sb[j / 4]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (MODE == 2) {
-                                const uint2 b = lds8(qbuf + ((nt * KS + j) * 32 + lane) * 8);
-                                mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
-                            } else {
-                                mma_f16(s[u][nt], a0, a1, a2, a3, qf[2 * j], qf[2 * j + 1]);
-                            }
-                        }
-                    };
-                    for_steps(step, std::make_integer_sequence<int, KS>{});
+                const uint32_t unit = tile + u * C::UNIT;
+                uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
+                if constexpr (D == 128) {
+                    const uint4 a = lds16(unit + g * 64 + t4 * 16), b = lds16(unit + (g + 8) * 64 + t4 * 16);
+                    ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+                    kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+                    const uint32_t x = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + g * 8 + t4 * 2));
+                    const uint32_t y = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + (g + 8) * 8 + t4 * 2));
+                    sa[0] = low_twice(x), sa[1] = high_twice(x);
+                    sb[0] = low_twice(y), sb[1] = high_twice(y);
+                } else {
+                    const uint2 a = lds8(unit + g * 32 + t4 * 8), b = lds8(unit + (g + 8) * 32 + t4 * 8);
+                    ka[0] = a.x, ka[1] = a.y;
+                    kb[0] = b.x, kb[1] = b.y;
+                    const uint32_t x = lds_u8(unit + 16 * D + g * 4 + t4), y = lds_u8(unit + 16 * D + (g + 8) * 4 + t4);
+                    sa[0] = low_twice(e4m3x2_to_f16x2((uint16_t)x));
+                    sb[0] = low_twice(e4m3x2_to_f16x2((uint16_t)y));
                 }
+                auto step = [&](auto jj) {
+                    constexpr int j = decltype(jj)::value;
+                    const uint32_t a0 = hmul2(code_pair<2 * j>(ka), sa[j / 4]);
+                    const uint32_t a1 = hmul2(code_pair<2 * j>(kb), sb[j / 4]);
+                    const uint32_t a2 = hmul2(code_pair<2 * j + 1>(ka), sa[j / 4]);
+                    const uint32_t a3 = hmul2(code_pair<2 * j + 1>(kb), sb[j / 4]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 b;
+                        if constexpr (MODE == 2)
+                            b = lds8(qbuf + ((nt * KS + j) * 32 + lane) * 8);
+                        else
+                            b = make_uint2(qf[2 * j], qf[2 * j + 1]);
+                        if constexpr (j == 0)
+                            mma_f16_first(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                        else
+                            mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                    }
+                };
+                for_steps(step, std::make_integer_sequence<int, KS>{});
+            }
+            // V's scales, with what a border tile must not use taken out
+            const int grp = D == 128 ? g : g >> 1;
+            uint32_t va_s[NU], vb_s[NU];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+                const uint32_t at = tile + u * C::UNIT + 17 * D + grp * 16 + 2 * t4;
+                va_s[u] = e4m3x2_to_f16x2(lds_u16(at));
+                vb_s[u] = e4m3x2_to_f16x2(lds_u16(at + 8));
             }
             // ---- masks, the running maximum in log2 units
             if (border) {
@@ -500,6 +528,34 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             if (key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                    // positions behind the end: whatever their scales hold becomes 0
+                    const int k = key0 + 16 * u + 2 * t4;
+                    uint32_t &x = va_s[u], &y = vb_s[u];
+                    if (k >= len) x = 0;
+                    if (k + 1 >= len) x &= 0xffffu;
+                    if (k + 8 >= len) y = 0;
+                    if (k + 9 >= len) y &= 0xffffu;
+                    // A NaN scale reaches only the rows that see its key: it is
+                    // taken out of the product and put into their sums.
+                    const uint32_t nx = nan_halves(x), ny = nan_halves(y);
+                    if (__any_sync(~0u, nx | ny)) {
+                        x = (nx & 1 ? 0u : x & 0xffffu) | (nx & 2 ? 0u : x & 0xffff0000u);
+                        y = (ny & 1 ? 0u : y & 0xffffu) | (ny & 2 ? 0u : y & 0xffff0000u);
+                        for (int j = 0; j < 16; ++j) {
+                            if ((lds_u8(tile + u * C::UNIT + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (key0 + 16 * u + j < min(lim[nt][c], len)) {
+#pragma unroll
+                                        for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
+                                    }
+                        }
+                    }
+                }
             }
             bool raise = false;
             float mx[NT][2];
@@ -563,9 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-                if (u >= nu) break;
                 const uint32_t unit = tile + u * C::UNIT;
-                const int grp = D == 128 ? g : g >> 1;
                 uint32_t va[KS / 2], vb[KS / 2];
                 if constexpr (D == 128) {
                     const uint4 a = lds16(unit + 8 * D + g * 64 + t4 * 16), b = lds16(unit + 12 * D + g * 64 + t4 * 16);
@@ -577,34 +631,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     va[0] = a.x, va[1] = a.y;
                     vb[0] = b.x, vb[1] = b.y;
                 }
-                uint32_t sa = e4m3x2_to_f16x2(lds_u16(unit + 17 * D + grp * 16 + 2 * t4));
-                uint32_t sb = e4m3x2_to_f16x2(lds_u16(unit + 17 * D + grp * 16 + 8 + 2 * t4));
-                if (border) {
-                    // positions behind the end: whatever their scales hold becomes 0
-                    const int k = key0 + 16 * u + 2 * t4;
-                    if (k >= len) sa = 0;
-                    if (k + 1 >= len) sa &= 0xffffu;
-                    if (k + 8 >= len) sb = 0;
-                    if (k + 9 >= len) sb &= 0xffffu;
-                    // A NaN scale reaches only the rows that see its key: it is
-                    // taken out of the product and put into their sums.
-                    const uint32_t na = nan_halves(sa), nb = nan_halves(sb);
-                    if (__any_sync(~0u, na | nb)) {
-                        sa = (na & 1 ? 0u : sa & 0xffffu) | (na & 2 ? 0u : sa & 0xffff0000u);
-                        sb = (nb & 1 ? 0u : sb & 0xffffu) | (nb & 2 ? 0u : sb & 0xffff0000u);
-                        for (int j = 0; j < 16; ++j) {
-                            if ((lds_u8(unit + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    if (key0 + 16 * u + j < min(lim[nt][c], len)) {
-#pragma unroll
-                                        for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
-                                    }
-                        }
-                    }
-                }
+                const uint32_t sa = va_s[u], sb = vb_s[u];
                 auto step = [&](auto ii) {
                     constexpr int i = decltype(ii)::value;
                     const uint32_t a0 = hmul2(code_pair<2 * i>(va), sa), a1 = hmul2(code_pair<2 * i + 1>(va), sa);
