@@ -28,8 +28,10 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -44,6 +46,7 @@ __all__ = ["fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdim", "fa_f
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libfa_gb300.so")
 _lock = threading.Lock()
+_no_guard = contextlib.nullcontext()
 _lib = None
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
@@ -141,7 +144,8 @@ def load_library() -> ctypes.CDLL:
                                               f, vp, ctypes.c_size_t, vp]
         lib.fa_bwd_varlen_workspace.restype = i
         lib.fa_bwd_varlen_workspace.argtypes = [i, i, i, ctypes.POINTER(ctypes.c_size_t)]
-        c4, pg, sz = ctypes.POINTER(_KV4), ctypes.POINTER(_KV4Pages), ctypes.c_size_t
+        c4 = pg = ctypes.c_void_p  # a packed struct (bytes) or byref of a _KV4 or _KV4Pages
+        sz = ctypes.c_size_t
         for name, args in (("fa_kv4_append", [vp, vp, vp, i, i, c4, vp]), ("fa_kv4_read", [vp, vp, vp, i, i, c4, vp]),
                            ("fa_fwd_kv4", [vp, vp, vp, i, i, i, i, f, c4, vp, sz, vp]),
                            ("fa_fwd_kv4_workspace", [i, i, i, i, i, ctypes.POINTER(sz)]),
@@ -701,20 +705,33 @@ def kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, layers: int | Non
     return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.uint8, device=device)
 
 
-def _same_device(named, device):
-    for t, n in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{n} must be on {device}")
+# A decode step makes one such call per layer, a few microseconds of kernel
+# each, so the checks below take their time only on the way to an error.
+
+_pack_kv4 = struct.Struct("6P6i").pack    # struct fa_kv4
+_pack_pages = struct.Struct("4P7i").pack  # struct fa_kv4_pages
 
 
-def _device_guard(device):
+def _want(t, name, dtype, ndim, device):
+    """_check_tensor, and that t is on `device` (a device index)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous()):
+        _check_tensor(t, name, dtype, ndim)
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
+
+
+def _device_guard(index):
     """The device's context, or nothing where it is current already."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _no_guard if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _check_slots(table, seq_lens):
-    _check_tensor(table, "table", torch.int32, 2)
-    _check_tensor(seq_lens, "seq_lens", torch.int32, 1)
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
+
+
+def _check_slots(table, seq_lens, device):
+    _want(table, "table", torch.int32, 2, device)
+    _want(seq_lens, "seq_lens", torch.int32, 1, device)
     if seq_lens.shape[0] != table.shape[0]:
         raise ValueError(f"table has {table.shape[0]} slots and seq_lens {seq_lens.shape[0]}")
 
@@ -727,26 +744,37 @@ def _check_pool(pool, ndim):
 
 
 def _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, num_seqs):
-    """Checked fa_kv4_t of a call with num_seqs sequences."""
+    """Checks the cache of a call with num_seqs sequences.  Returns (fa_kv4_t as bytes, device index, Hkv, D)."""
     _check_pool(pool, 4)
-    _check_slots(table, seq_lens)
+    device = pool.get_device()
+    _check_slots(table, seq_lens, device)
     N, H, U, unit = pool.shape
+    slots, width = table.shape
+    ids = ks = vs = 0
     if seq_ids is not None:
-        _check_tensor(seq_ids, "seq_ids", torch.int32, 1)
+        _want(seq_ids, "seq_ids", torch.int32, 1, device)
         if seq_ids.shape[0] != num_seqs:
             raise ValueError(f"seq_ids must name {num_seqs} slots")
-    elif num_seqs > table.shape[0]:
-        raise ValueError(f"{num_seqs} sequences but {table.shape[0]} slots")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            _check_tensor(t, n, torch.float32, 1)
-            if t.shape[0] != H:
-                raise ValueError(f"{n} must hold one scale for each of the {H} KV heads")
-    _same_device(((table, "table"), (seq_lens, "seq_lens"), (seq_ids, "seq_ids"), (k_scale, "k_scale"),
-                  (v_scale, "v_scale")), pool.device)
-    ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return _KV4(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ptr(seq_ids), ptr(k_scale), ptr(v_scale), N,
-                table.shape[0], table.shape[1], 16 * U, H, unit // 18)
+        ids = seq_ids.data_ptr()
+    elif num_seqs > slots:
+        raise ValueError(f"{num_seqs} sequences but {slots} slots")
+    if k_scale is not None:
+        _want(k_scale, "k_scale", torch.float32, 1, device)
+        ks = k_scale.data_ptr()
+    if v_scale is not None:
+        _want(v_scale, "v_scale", torch.float32, 1, device)
+        vs = v_scale.data_ptr()
+    if ks and k_scale.shape[0] != H or vs and v_scale.shape[0] != H:
+        raise ValueError(f"k_scale and v_scale must hold one scale for each of the {H} KV heads")
+    c = _pack_kv4(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ids, ks, vs, N, slots, width, 16 * U, H,
+                  unit // 18)
+    return c, device, H, unit // 18
+
+
+def _num_seqs(cu_seqlens):
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    return cu_seqlens.shape[0] - 1
 
 
 def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
@@ -755,19 +783,17 @@ def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, po
     """Quantise packed rows k, v [T,Hkv,D] bf16 into the cache: the rows
     [cu_seqlens[s], cu_seqlens[s+1]) become the last positions of sequence s
     (slot seq_ids[s], default s), which seq_lens already counts."""
-    for t, n in ((k, "k"), (v, "v")):
-        _check_tensor(t, n, torch.bfloat16, 3)
-    _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    if cu_seqlens.shape[0] < 2:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
-    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, cu_seqlens.shape[0] - 1)
-    if k.shape != v.shape or k.shape[1] != c.Hkv or k.shape[2] != c.D:
-        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {c.Hkv} heads of {c.D}")
-    _same_device(((k, "k"), (v, "v"), (cu_seqlens, "cu_seqlens")), pool.device)
-    lib = load_library()
-    with _device_guard(pool.device):
-        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1, k.shape[0],
-                               ctypes.byref(c), _stream_handle(stream))
+    n = _num_seqs(cu_seqlens)
+    c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
+    _want(k, "k", torch.bfloat16, 3, device)
+    _want(v, "v", torch.bfloat16, 3, device)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    if k.shape != v.shape or k.shape[1:] != (H, D):
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {H} heads of {D}")
+    lib = _lib or load_library()
+    with _device_guard(device):
+        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), n, k.shape[0], c,
+                               _raw_stream(stream, device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_append")
 
@@ -779,24 +805,26 @@ def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table:
     """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as
     packed bf16 rows (k, v), each [total,Hkv,D]: a cached prefix as the keys
     of fa_fwd_varlen.  Rows behind the last sequence are left as they were."""
-    _check_tensor(cu_seqlens, "cu_seqlens", torch.int32, 1)
-    if cu_seqlens.shape[0] < 2:
-        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
-    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, cu_seqlens.shape[0] - 1)
-    shape = (int(total), c.Hkv, c.D)
+    n = _num_seqs(cu_seqlens)
+    c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    shape = (int(total), H, D)
     if shape[0] < 0:
         raise ValueError("total must not be negative")
-    k_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device) if v_out is None else v_out
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _check_tensor(t, n, torch.bfloat16, 3)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{n} must be {shape}, got {tuple(t.shape)}")
-    _same_device(((k_out, "k_out"), (v_out, "v_out"), (cu_seqlens, "cu_seqlens")), pool.device)
-    lib = load_library()
-    with _device_guard(pool.device):
-        st = lib.fa_kv4_read(k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), cu_seqlens.shape[0] - 1,
-                             shape[0], ctypes.byref(c), _stream_handle(stream))
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+    else:
+        _want(k_out, "k_out", torch.bfloat16, 3, device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=pool.device)
+    else:
+        _want(v_out, "v_out", torch.bfloat16, 3, device)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"k_out and v_out must be {shape}, got {tuple(k_out.shape)} and {tuple(v_out.shape)}")
+    lib = _lib or load_library()
+    with _device_guard(device):
+        st = lib.fa_kv4_read(k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), n, shape[0], c,
+                             _raw_stream(stream, device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_read")
     return k_out, v_out
@@ -822,35 +850,46 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
     _check_tensor(q, "q", torch.bfloat16, 4)
     B, Hq, Lq, D = q.shape
-    c = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, B)
-    if D != c.D:
-        raise ValueError(f"q has head dimension {D} and the cache {c.D}")
+    c, device, H, cache_d = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, B)
+    if D != cache_d:
+        raise ValueError(f"q has head dimension {D} and the cache {cache_d}")
+    if q.get_device() != device:
+        raise ValueError(f"q must be on {pool.device}, got {q.device}")
     if out is None:
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    else:
+        _want(out, "out", torch.float32, 4, device)
     if lse is None:
         lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
-    _check_tensor(out, "out", torch.float32, 4)
-    _check_tensor(lse, "lse", torch.float32, 3)
-    if out.shape != q.shape or tuple(lse.shape) != (B, Hq, Lq):
+    else:
+        _want(lse, "lse", torch.float32, 3, device)
+    if out.shape != q.shape or lse.shape != (B, Hq, Lq):
         raise ValueError("out/lse shape mismatch")
-    _same_device(((q, "q"), (out, "out"), (lse, "lse"), (workspace, "workspace")), pool.device)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
-    lib = load_library()
-    with _device_guard(q.device):
-        nbytes = kv4_workspace(B, Hq, c.Hkv, Lq, D)
-        if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
+    lib = _lib or load_library()
+    with _device_guard(device):
+        nbytes = _attn_workspace(device, Hq, H, Lq, D)
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        st = lib.fa_fwd_kv4(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq, int(bool(causal)),
-                            float(softmax_scale), ctypes.byref(c), workspace.data_ptr() if nbytes else None, nbytes,
-                            _stream_handle(stream))
-        if nbytes and isinstance(stream, torch.cuda.Stream):
+        elif workspace.get_device() != device:
+            raise ValueError(f"workspace must be on {q.device}, got {workspace.device}")
+        st = lib.fa_fwd_kv4(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq, 1 if causal else 0, softmax_scale,
+                            c, workspace.data_ptr(), nbytes, _raw_stream(stream, device))
+        if isinstance(stream, torch.cuda.Stream):
             workspace.record_stream(stream)  # keep the block out of reuse until that stream is done
     if st != FA_OK:
         raise FAError(st, "fa_fwd_kv4")
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(device, Hq, Hkv, Lq, D):
+    """kv4_workspace on the current device, whose index is `device`."""
+    return kv4_workspace(1, Hq, Hkv, Lq, D)
+
+
+@functools.lru_cache(maxsize=256)
 def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
     """Workspace bytes fa_kv4_reserve, fa_kv4_fork and fa_kv4_compact (n = 0) need."""
     nbytes = ctypes.c_size_t(0)
@@ -860,54 +899,44 @@ def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
     return nbytes.value
 
 
-def _page_call(name, pool, page_size, table, seq_lens, refs, lists, info, workspace, stream):
-    """Checks and runs one page operation; lists: the call's int32 [n] tensors
-    (None where it names no slots); info None: the call returns none."""
-    _check_slots(table, seq_lens)
-    _check_tensor(refs, "refs", torch.int32, 1)
-    lib = load_library()
-    named = [(table, "table"), (seq_lens, "seq_lens")]
-    n = None
-    for t, what in lists:
-        if t is None:
-            continue
-        _check_tensor(t, what, torch.int32, 1)
-        if n is not None and t.shape[0] != n:
-            raise ValueError(f"{what} must hold {n} entries")
-        n = t.shape[0]
-        named.append((t, what))
+def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, info, workspace, stream, device):
+    """Runs one page operation.  first, second: device addresses of its lists
+    of n entries (None: the operation has no such list)."""
+    _check_slots(table, seq_lens, device)
+    slots, width = table.shape
+    N = refs.shape[0]
     if pool is None:
-        geometry = (None, page_size, 1, 64, 1)
+        pages = _pack_pages(0, table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width, page_size, 1,
+                            64, 1)
     else:
         _check_pool(pool, 5 if pool.dim() == 5 else 4)
-        N, H, U, unit = pool.shape[-4:]
-        if N != refs.shape[0]:
-            raise ValueError(f"pool has {N} pages and refs {refs.shape[0]}")
-        named.append((pool, "pool"))
-        geometry = (pool.data_ptr(), 16 * U, H, unit // 18, pool.shape[0] if pool.dim() == 5 else 1)
-    device = refs.device
-    plan = name != "fa_kv4_release"
-    if plan:
-        if info is None:
-            info = torch.empty(2, dtype=torch.int32, device=device)
-        _check_tensor(info, "info", torch.int32, 1)
-        if info.shape[0] != 2:
-            raise ValueError("info must hold 2 numbers")
-        named += [(info, "info"), (workspace, "workspace")]
-    _same_device(named, device)
-    pages = _KV4Pages(geometry[0], table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), refs.shape[0],
-                      table.shape[0], table.shape[1], *geometry[1:])
-    args = [None if t is None else t.data_ptr() for t, _ in lists] + ([n] if lists else [])
+        P, H, U, unit = pool.shape[-4:]
+        if P != N:
+            raise ValueError(f"pool has {P} pages and refs {N}")
+        if pool.get_device() != device:
+            raise ValueError(f"pool must be on cuda:{device}, got {pool.device}")
+        pages = _pack_pages(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width,
+                            16 * U, H, unit // 18, pool.shape[0] if pool.dim() == 5 else 1)
+    lib = _lib or load_library()
     with _device_guard(device):
-        args.append(ctypes.byref(pages))
-        if plan:
-            nbytes = kv4_pages_workspace(refs.shape[0], n or 0)
+        if name == "fa_kv4_release":
+            st = lib.fa_kv4_release(first, n, pages, _raw_stream(stream, device))
+        else:
+            nbytes = kv4_pages_workspace(N, n)
+            if info is None:
+                info = torch.empty(2, dtype=torch.int32, device=refs.device)
+            else:
+                _want(info, "info", torch.int32, 1, device)
+                if info.shape[0] != 2:
+                    raise ValueError("info must hold 2 numbers")
             if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            args += [info.data_ptr(), workspace.data_ptr(), nbytes]
-        st = getattr(lib, name)(*args, _stream_handle(stream))
-        if plan and isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
+            elif workspace.get_device() != device:
+                raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
+            tail = (pages, info.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(stream, device))
+            st = lib.fa_kv4_compact(*tail) if first is second is None else getattr(lib, name)(first, second, n, *tail)
+            if isinstance(stream, torch.cuda.Stream):
+                workspace.record_stream(stream)
     if st != FA_OK:
         raise FAError(st, name)
     return info
@@ -920,8 +949,17 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
     count them in seq_lens.  Returns info, int32 [2] on the device: free pages
     left, and 0, or the pages that were missing (then nothing was changed), or
     -1 for bad arguments on the device."""
-    return _page_call("fa_kv4_reserve", None, int(page_size), table, seq_lens, refs,
-                      ((seq_ids, "seq_ids"), (new_tokens, "new_tokens")), info, workspace, stream)
+    _check_tensor(refs, "refs", torch.int32, 1)
+    device = refs.get_device()
+    _want(new_tokens, "new_tokens", torch.int32, 1, device)
+    n = new_tokens.shape[0]
+    if seq_ids is not None:
+        _want(seq_ids, "seq_ids", torch.int32, 1, device)
+        if seq_ids.shape[0] != n:
+            raise ValueError(f"seq_ids must name {n} slots")
+    return _page_call("fa_kv4_reserve", None, page_size, table, seq_lens, refs,
+                      None if seq_ids is None else seq_ids.data_ptr(), new_tokens.data_ptr(), n, info, workspace,
+                      stream, device)
 
 
 def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
@@ -930,22 +968,34 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     """Make the empty slots children[i] copies of the slots parents[i]: full pages
     are shared, a partly filled last page is copied.  pool as for
     fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
-    return _page_call("fa_kv4_fork", pool, None, table, seq_lens, refs,
-                      ((parents, "parents"), (children, "children")), info, workspace, stream)
+    _check_tensor(refs, "refs", torch.int32, 1)
+    device = refs.get_device()
+    _want(parents, "parents", torch.int32, 1, device)
+    _want(children, "children", torch.int32, 1, device)
+    n = parents.shape[0]
+    if children.shape[0] != n:
+        raise ValueError(f"{n} parents but {children.shape[0]} children")
+    return _page_call("fa_kv4_fork", pool, None, table, seq_lens, refs, parents.data_ptr(), children.data_ptr(), n,
+                      info, workspace, stream, device)
 
 
 def fa_kv4_release(seq_ids: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
                    page_size: int, stream=None) -> None:
     """Free the slots seq_ids: their pages lose a reference each, their lengths become 0."""
-    _page_call("fa_kv4_release", None, int(page_size), table, seq_lens, refs, ((seq_ids, "seq_ids"),), None, None,
-               stream)
+    _check_tensor(refs, "refs", torch.int32, 1)
+    device = refs.get_device()
+    _want(seq_ids, "seq_ids", torch.int32, 1, device)
+    _page_call("fa_kv4_release", None, page_size, table, seq_lens, refs, seq_ids.data_ptr(), None, seq_ids.shape[0],
+               None, None, stream, device)
 
 
 def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
                    info: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
-    return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, (), info, workspace, stream)
+    _check_tensor(refs, "refs", torch.int32, 1)
+    return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace, stream,
+                      refs.get_device())
 
 
 def fa_check(stream=None) -> int:
