@@ -1260,9 +1260,8 @@ fa_status_t kv4_rows(const void* k, const void* v, bool write, const int* cu_seq
     if (st != FA_OK) return st;
     if (!cu_seqlens || !aligned4(cu_seqlens) || total < 0) return FA_ERR_INVALID_ARG;
     if (total > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
-    // threads of the launch: one per pair of positions, KV head and 16 dimensions
-    if (((long long)(total >> 1) + num_seqs) * cache->Hkv * (cache->D / 16) >= (1ll << 31) * 256)
-        return FA_ERR_INVALID_ARG;
+    // warps of the launch: one per 16 positions and KV head
+    if (((long long)(total >> 4) + 2ll * num_seqs) * cache->Hkv >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != FA_OK) return st;
@@ -1272,6 +1271,7 @@ fa_status_t kv4_rows(const void* k, const void* v, bool write, const int* cu_seq
     p.cu = cu_seqlens;
     p.num_seqs = num_seqs;
     p.total = total;
+    p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
     p.c.err = ds->err;
     p.c.diag = ds->diag;
     const cudaError_t e = write ? launch_kv4_append(cache->D, p, stream) : launch_kv4_read(cache->D, p, stream);

@@ -35,6 +35,7 @@ struct Kv4RowsParams {  // append and read
     uint16_t* v_out;
     const int* cu;
     int num_seqs, total;
+    bool wide;  // the bf16 rows are 32-byte aligned
     Kv4Cache c;
 };
 

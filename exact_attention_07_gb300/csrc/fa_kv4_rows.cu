@@ -3,10 +3,14 @@
 // are bound by HBM: 4 D bytes of bf16 and 18 D / 16 bytes of cache per
 // (position, KV head).
 //
-// One thread handles one group of 16 dimensions of one KV head at the two
-// positions 2 i and 2 i + 1, which share the bytes of V (one nibble each): K
-// and V of both are eight independent 16-byte loads (or stores) of bf16, and
-// the cache's side is 16 bytes of V codes and 8 + 8 bytes of K codes.
+// One warp handles one unit: 16 positions of one KV head, 18 D contiguous
+// bytes of the cache.  A lane's piece is a group of 16 dimensions: of one
+// position for K, of two neighbouring ones for V, whose codes share bytes.
+// The order of the pieces is that of the cache's bytes, so that a warp reads
+// or writes them in contiguous runs, and the bf16 side goes in whole 32-byte
+// sectors (one 32-byte access per lane where the caller's rows are so
+// aligned).  All loads of a unit are issued before the first is used: 256
+// bytes per lane.
 #include "kv4_common.cuh"
 
 namespace fa {
@@ -15,47 +19,58 @@ namespace {
 
 constexpr int kRowsThreads = 256;
 
-// Slots of position pairs: sequence s of the call starts at pair slot
-// cu[s] / 2 + s, which leaves it at least the n / 2 + 1 pairs that n positions
-// may touch, so a grid of total / 2 + num_seqs slots needs no prefix sums.
-__device__ __forceinline__ int pair_slot(const int* cu, int s) { return (cu[s] >> 1) + s; }
+// Slots of units: sequence s of the call starts at unit slot cu[s] / 16 + 2 s,
+// which leaves it at least the (n + 14) / 16 + 1 units that n positions may
+// touch, so a grid of total / 16 + 2 num_seqs slots needs no prefix sums.
+__device__ __forceinline__ int unit_slot(const int* cu, int s) { return (cu[s] >> 4) + 2 * s; }
 
-struct PairTask {
-    int slot;        // slot of the sequence
-    int pos;         // even position of the pair
-    long long row;   // packed row of `pos` (of pos + 1: row + 1)
-    bool even, odd;  // which of the two are the call's
+struct UnitTask {
+    uint8_t* unit;      // its bytes in the cache; null for a bad page
+    int lo, hi;         // rows lo .. hi - 1 of the unit are the call's
+    long long row;      // packed row of the unit's row 0
+    int h;
 };
 
-// False when the pair slot holds nothing to do.
-__device__ __forceinline__ bool find_pair(const Kv4RowsParams& p, int u, PairTask& t)
+// False when the warp has nothing to do.
+template <int D>
+__device__ __forceinline__ bool find_unit(const Kv4RowsParams& p, UnitTask& t)
 {
-    int lo = 0, hi = p.num_seqs - 1;  // the last sequence whose first slot is <= u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pair_slot(p.cu, mid) <= u)
-            lo = mid;
+    const unsigned w = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
+    const unsigned u = w / (unsigned)p.c.Hkv;
+    t.h = (int)(w - u * (unsigned)p.c.Hkv);
+    if (u >= (unsigned)(p.total >> 4) + 2u * (unsigned)p.num_seqs) return false;
+    int s = 0, end = p.num_seqs - 1;  // the last sequence whose first slot is <= u
+    while (s < end) {
+        const int mid = (s + end + 1) >> 1;
+        if (unit_slot(p.cu, mid) <= (int)u)
+            s = mid;
         else
-            hi = mid - 1;
+            end = mid - 1;
     }
-    const int c0 = p.cu[lo], c1 = p.cu[lo + 1];
-    if (c0 < 0 || c1 < c0 || c1 > p.total || (lo == 0 && c0 != 0)) {
+    const int c0 = p.cu[s], c1 = p.cu[s + 1];
+    if (c0 < 0 || c1 < c0 || c1 > p.total || (s == 0 && c0 != 0)) {
         atomicOr(p.c.err, 2);
         return false;
     }
-    const int len = kv4_sequence(p.c, lo, t.slot), n = c1 - c0;
-    if (n > len) {
-        if (n > 0) atomicOr(p.c.err, 2);
+    int slot;
+    const int len = kv4_sequence(p.c, s, slot), n = c1 - c0, first = len - n;
+    if (first < 0) {
+        atomicOr(p.c.err, 2);
         return false;
     }
-    const int first = len - n;
-    const long long pos = 2ll * ((first >> 1) + (u - pair_slot(p.cu, lo)));
+    const long long pos = 16ll * ((first >> 4) + ((int)u - unit_slot(p.cu, s)));
     if (pos < 0 || pos >= len) return false;
-    t.pos = (int)pos;
-    t.even = t.pos >= first;
-    t.odd = t.pos + 1 < len && t.pos + 1 >= first;
-    t.row = (long long)c0 + t.pos - first;
-    return t.even || t.odd;
+    t.lo = max(0, first - (int)pos);
+    t.hi = min(16, len - (int)pos);
+    if (t.lo >= t.hi) return false;
+    t.row = c0 + (pos - first);
+    const int page = p.c.table[(long long)slot * p.c.table_width + (pos >> p.c.page_shift)];
+    if ((unsigned)page >= (unsigned)p.c.num_pages) {
+        atomicOr(p.c.err, 2);
+        return false;
+    }
+    t.unit = p.c.pool + kv4_unit(p.c, D, page, t.h, (int)pos);
+    return true;
 }
 
 // ------------------------------------------------------------------ append
@@ -64,14 +79,17 @@ struct Group {
     uint32_t w[8];  // 16 bf16
 };
 
-__device__ __forceinline__ Group load_group(const uint16_t* src, bool on)
+__device__ __forceinline__ Group load_group(const uint16_t* src, bool on, bool wide)
 {
-    Group x;
-    if (on) {
+    Group x = {{0, 0, 0, 0, 0, 0, 0, 0}};
+    if (on && wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3]), "=r"(x.w[4]), "=r"(x.w[5]),
+                       "=r"(x.w[6]), "=r"(x.w[7])
+                     : "l"(src));
+    } else if (on) {
         const uint4 a = __ldcs(reinterpret_cast<const uint4*>(src)), b = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
         x = {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
-    } else {
-        x = {{0, 0, 0, 0, 0, 0, 0, 0}};
     }
     return x;
 }
@@ -123,7 +141,7 @@ __device__ __forceinline__ uint32_t e2m1_word(float x0, float x1, float x2, floa
 template <int D>
 __global__ void __launch_bounds__(kRowsThreads) fa_kv4_append_kernel(const Kv4RowsParams p)
 {
-    constexpr int G = D / 16;
+    constexpr int G = D / 16, KI = D / 32, VI = D / 64;
     // the last block looks for slots that the call names twice
     if (p.c.ids && blockIdx.x == gridDim.x - 1) {
         __shared__ uint32_t seen[kKv4MaxSlots / 32];
@@ -137,55 +155,59 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_append_kernel(const Kv4Ro
         }
         return;
     }
-    const long long flat = (long long)blockIdx.x * kRowsThreads + threadIdx.x;
-    const int per = p.c.Hkv * G;
-    const long long u = flat / per;
-    if (u >= (long long)(p.total >> 1) + p.num_seqs) return;
-    PairTask t;
-    if (!find_pair(p, (int)u, t)) return;
-    const int hg = (int)(flat - u * per), h = hg / G, g = hg % G;
-    const int page = p.c.table[(long long)t.slot * p.c.table_width + (t.pos >> p.c.page_shift)];
-    if ((unsigned)page >= (unsigned)p.c.num_pages) {
-        atomicOr(p.c.err, 2);
-        return;
-    }
-    const long long src = (t.row * p.c.Hkv + h) * D + g * 16, row = (long long)p.c.Hkv * D;
-    const Group ka = load_group(p.k_in + src, t.even), kb = load_group(p.k_in + src + row, t.odd);
-    const Group va = load_group(p.v_in + src, t.even), vb = load_group(p.v_in + src + row, t.odd);
-    uint8_t* unit = p.c.pool + kv4_unit(p.c, D, page, h, t.pos);
-    const int key = t.pos & 15;
-    const float gk = p.c.k_scale ? p.c.k_scale[h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
-
+    UnitTask t;
+    if (!find_unit<D>(p, t)) return;
+    const int lane = threadIdx.x & 31;
+    const long long pitch = (long long)p.c.Hkv * D, base = t.row * pitch + t.h * D;
+    const auto mine = [&](int r) { return r >= t.lo && r < t.hi; };
+    Group k[KI], v[VI][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (i ? t.odd : t.even) {
-            float y[16];
-            const uint32_t s = quantise_group(i ? kb : ka, gk, y);
-            *reinterpret_cast<uint2*>(unit + (key + i) * (D / 2) + g * 8) =
-                make_uint2(e2m1_word(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]),
-                           e2m1_word(y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]));
-            unit[16 * D + (key + i) * G + g] = (uint8_t)s;
-        }
+    for (int i = 0; i < KI; ++i) {
+        const int x = 32 * i + lane, r = x / G, g = x % G;
+        k[i] = load_group(p.k_in + base + r * pitch + g * 16, mine(r), p.wide);
     }
-    {
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            v[i][e] = load_group(p.v_in + base + (r + e) * pitch + g * 16, mine(r + e), p.wide);
+    }
+    const float gk = p.c.k_scale ? p.c.k_scale[t.h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[t.h] : 1.f;
+#pragma unroll
+    for (int i = 0; i < KI; ++i) {
+        const int x = 32 * i + lane;
+        if (!mine(x / G)) continue;
+        float y[16];
+        const uint32_t s = quantise_group(k[i], gk, y);
+        *reinterpret_cast<uint2*>(t.unit + x * 8) =
+            make_uint2(e2m1_word(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]),
+                       e2m1_word(y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]));
+        t.unit[16 * D + x] = (uint8_t)s;
+    }
+#pragma unroll
+    for (int i = 0; i < VI; ++i) {
+        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+        const bool even = mine(r), odd = mine(r + 1);
+        if (!even && !odd) continue;
         float ya[16], yb[16];
-        const uint32_t sa = quantise_group(va, gv, ya), sb = quantise_group(vb, gv, yb);
-        uint4* codes = reinterpret_cast<uint4*>(unit + 8 * D + (key >> 3) * (4 * D) + g * 64 + ((key & 7) >> 1) * 16);
+        const uint32_t sa = quantise_group(v[i][0], gv, ya), sb = quantise_group(v[i][1], gv, yb);
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             w[e] = e2m1_word(ya[4 * e], yb[4 * e], ya[4 * e + 1], yb[4 * e + 1], ya[4 * e + 2], yb[4 * e + 2],
                              ya[4 * e + 3], yb[4 * e + 3]);
-        uint8_t* scales = unit + 17 * D + g * 16 + key;
-        if (t.even && t.odd) {
+        uint4* codes = reinterpret_cast<uint4*>(t.unit + 8 * D + x * 16);
+        uint8_t* scales = t.unit + 17 * D + g * 16 + r;
+        if (even && odd) {
             *codes = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(sa | sb << 8);
         } else {  // the pair's other position keeps its nibbles
-            const uint32_t mine = t.even ? 0x0f0f0f0fu : 0xf0f0f0f0u;
+            const uint32_t own = even ? 0x0f0f0f0fu : 0xf0f0f0f0u;
             const uint4 old = *codes;
-            *codes = make_uint4((old.x & ~mine) | (w[0] & mine), (old.y & ~mine) | (w[1] & mine),
-                                (old.z & ~mine) | (w[2] & mine), (old.w & ~mine) | (w[3] & mine));
-            scales[t.even ? 0 : 1] = (uint8_t)(t.even ? sa : sb);
+            *codes = make_uint4((old.x & ~own) | (w[0] & own), (old.y & ~own) | (w[1] & own),
+                                (old.z & ~own) | (w[2] & own), (old.w & ~own) | (w[3] & own));
+            scales[even ? 0 : 1] = (uint8_t)(even ? sa : sb);
         }
     }
 }
@@ -206,80 +228,94 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ void store_group(uint16_t* dst, const uint32_t (&w)[8])
+__device__ __forceinline__ void store_group(uint16_t* dst, const uint32_t (&w)[8], bool on, bool wide)
 {
-    __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
-    __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    if (on && wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else if (on) {
+        __stcs(reinterpret_cast<uint4*>(dst), make_uint4(w[0], w[1], w[2], w[3]));
+        __stcs(reinterpret_cast<uint4*>(dst) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kRowsThreads) fa_kv4_read_kernel(const Kv4RowsParams p)
 {
-    constexpr int G = D / 16;
-    const long long flat = (long long)blockIdx.x * kRowsThreads + threadIdx.x;
-    const int per = p.c.Hkv * G;
-    const long long u = flat / per;
-    if (u >= (long long)(p.total >> 1) + p.num_seqs) return;
-    PairTask t;
-    if (!find_pair(p, (int)u, t)) return;
-    const int hg = (int)(flat - u * per), h = hg / G, g = hg % G;
-    const int page = kv4_page(p.c, t.slot, t.pos);
-    const uint8_t* unit = p.c.pool + kv4_unit(p.c, D, page, h, t.pos);
-    const int key = t.pos & 15;
-    const uint4 vc =
-        *reinterpret_cast<const uint4*>(unit + 8 * D + (key >> 3) * (4 * D) + g * 64 + ((key & 7) >> 1) * 16);
-    const uint32_t vs = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(unit + 17 * D + g * 16 + key));
-    const float gk = p.c.k_scale ? p.c.k_scale[h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
-    const long long dst = (t.row * p.c.Hkv + h) * D + g * 16, row = (long long)p.c.Hkv * D;
+    constexpr int G = D / 16, KI = D / 32, VI = D / 64;
+    UnitTask t;
+    if (!find_unit<D>(p, t)) return;
+    const int lane = threadIdx.x & 31;
+    uint2 kc[KI];
+    uint4 vc[VI];
+    uint32_t ks[KI], vs[VI];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (i ? t.odd : t.even) {
-            const uint2 kc = *reinterpret_cast<const uint2*>(unit + (key + i) * (D / 2) + g * 8);
-            const uint32_t s1 = unit[16 * D + (key + i) * G + g];
-            const uint32_t s = e4m3x2_to_f16x2((uint16_t)(s1 | s1 << 8));
-            uint32_t w[8];
+    for (int i = 0; i < KI; ++i) {
+        const int x = 32 * i + lane;
+        kc[i] = __ldcs(reinterpret_cast<const uint2*>(t.unit + x * 8));
+        ks[i] = t.unit[16 * D + x];
+    }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t c = e ? kc.y : kc.x;
-                const uint32_t f[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
-                                       e2m1x2_to_f16x2<3>(c)};
+    for (int i = 0; i < VI; ++i) {
+        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+        vc[i] = __ldcs(reinterpret_cast<const uint4*>(t.unit + 8 * D + x * 16));
+        vs[i] = *reinterpret_cast<const uint16_t*>(t.unit + 17 * D + g * 16 + r);
+    }
+    const long long pitch = (long long)p.c.Hkv * D, base = t.row * pitch + t.h * D;
+    const auto mine = [&](int r) { return r >= t.lo && r < t.hi; };
+    const float gk = p.c.k_scale ? p.c.k_scale[t.h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[t.h] : 1.f;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const float2 x = f16x2_to_f32(hmul2(f[b], s));
-                    w[4 * e + b] = bf16x2(x.x * gk, x.y * gk);
-                }
+    for (int i = 0; i < KI; ++i) {
+        const int x = 32 * i + lane, r = x / G, g = x % G;
+        const uint32_t s = e4m3x2_to_f16x2((uint16_t)(ks[i] | ks[i] << 8));
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t c = e ? kc[i].y : kc[i].x;
+            const uint32_t f[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
+                                   e2m1x2_to_f16x2<3>(c)};
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const float2 y = f16x2_to_f32(hmul2(f[b], s));
+                w[4 * e + b] = bf16x2(y.x * gk, y.y * gk);
             }
-            store_group(p.k_out + dst + i * row, w);
         }
+        store_group(p.k_out + base + r * pitch + g * 16, w, mine(r), p.wide);
     }
-    uint32_t wa[8], wb[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t c = e == 0 ? vc.x : e == 1 ? vc.y : e == 2 ? vc.z : vc.w;
-        const uint32_t f[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
-                               e2m1x2_to_f16x2<3>(c)};
+    for (int i = 0; i < VI; ++i) {
+        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+        const uint32_t s = e4m3x2_to_f16x2((uint16_t)vs[i]);
+        uint32_t wa[8], wb[8];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const float2 x = f16x2_to_f32(hmul2(f[2 * b], vs)), y = f16x2_to_f32(hmul2(f[2 * b + 1], vs));
-            wa[2 * e + b] = bf16x2(x.x * gv, y.x * gv);
-            wb[2 * e + b] = bf16x2(x.y * gv, y.y * gv);
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t c = e == 0 ? vc[i].x : e == 1 ? vc[i].y : e == 2 ? vc[i].z : vc[i].w;
+            const uint32_t f[4] = {e2m1x2_to_f16x2<0>(c), e2m1x2_to_f16x2<1>(c), e2m1x2_to_f16x2<2>(c),
+                                   e2m1x2_to_f16x2<3>(c)};
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float2 y = f16x2_to_f32(hmul2(f[2 * b], s)), z = f16x2_to_f32(hmul2(f[2 * b + 1], s));
+                wa[2 * e + b] = bf16x2(y.x * gv, z.x * gv);
+                wb[2 * e + b] = bf16x2(y.y * gv, z.y * gv);
+            }
         }
+        store_group(p.v_out + base + r * pitch + g * 16, wa, mine(r), p.wide);
+        store_group(p.v_out + base + (r + 1) * pitch + g * 16, wb, mine(r + 1), p.wide);
     }
-    if (t.even) store_group(p.v_out + dst, wa);
-    if (t.odd) store_group(p.v_out + dst + row, wb);
 }
 
-long long rows_blocks(int D, const Kv4RowsParams& p)
+unsigned rows_blocks(const Kv4RowsParams& p)
 {
-    const long long threads = ((long long)(p.total >> 1) + p.num_seqs) * p.c.Hkv * (D / 16);
-    return (threads + kRowsThreads - 1) / kRowsThreads;
+    const long long warps = ((long long)(p.total >> 4) + 2ll * p.num_seqs) * p.c.Hkv;
+    return (unsigned)((warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32));
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)(rows_blocks(D, p) + (p.c.ids ? 1 : 0));
+    const unsigned grid = rows_blocks(p) + (p.c.ids ? 1 : 0);
     if (D == 128)
         fa_kv4_append_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else
@@ -289,7 +325,7 @@ cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream
 
 cudaError_t launch_kv4_read(int D, const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned grid = (unsigned)rows_blocks(D, p);
+    const unsigned grid = rows_blocks(p);
     if (D == 128)
         fa_kv4_read_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else

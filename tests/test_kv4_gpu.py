@@ -322,6 +322,24 @@ def test_append_and_read_match_the_oracle(H, D, P, old, new, scaled, named):
         row += c
 
 
+def test_rows_at_addresses_that_are_not_32_byte_aligned():
+    rng = np.random.default_rng(13)
+    H, D, P = 2, 64, 16
+    pool, table = random_cache(rng, [40], H, D, P)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32([40]))
+    kv = [torch.zeros(8 + 20 * H * D, dtype=torch.bfloat16, device=DEV)[8:].view(20, H, D) for _ in range(4)]
+    for t in kv[:2]:
+        t.copy_(bf16(rng.standard_normal(t.shape)))
+    assert kv[0].data_ptr() % 32 == 16
+    fa.fa_kv4_append(kv[0], kv[1], i32([0, 20]), *dev)
+    kv4.append(pool, table, [40], [0], [20], f64(kv[0]), f64(kv[1]), np.ones(H), np.ones(H))
+    same_bytes(dev[0].cpu().numpy(), pool, "append")
+    fa.fa_kv4_read(i32([0, 20]), 20, *dev, k_out=kv[2], v_out=kv[3])
+    for got, want in zip(kv[2:], kv4.rows(pool, table, 0, 40, np.ones(H), np.ones(H))):
+        assert np.array_equal(f64(got), want[:, 20:].transpose(1, 0, 2))
+    fa.fa_check()
+
+
 def test_no_rows_at_all():
     pool, table, lens = fa.kv4_pool(2, 1, 16, 64), i32([[0], [1]]), i32([3, 0])
     none = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
