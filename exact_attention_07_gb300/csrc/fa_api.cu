@@ -1260,8 +1260,8 @@ fa_status_t kv4_rows(const void* k, const void* v, bool write, const int* cu_seq
     if (st != FA_OK) return st;
     if (!cu_seqlens || !aligned4(cu_seqlens) || total < 0) return FA_ERR_INVALID_ARG;
     if (total > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return FA_ERR_INVALID_ARG;
-    // warps of the launch: one per 16 positions and KV head
-    if (((long long)(total >> 4) + 2ll * num_seqs) * cache->Hkv >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    // warps of the launch: one or two per 16 positions and KV head
+    if (((long long)(total >> 4) + 2ll * num_seqs) * cache->Hkv >= (1ll << 30)) return FA_ERR_INVALID_ARG;
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != FA_OK) return st;

@@ -4,7 +4,7 @@
 // (position, KV head).
 //
 // One warp handles one unit: 16 positions of one KV head, 18 D contiguous
-// bytes of the cache.  A lane's piece is a group of 16 dimensions: of one
+// bytes of the cache (append: one warp for its K and one for its V).  A lane's piece is a group of 16 dimensions: of one
 // position for K, of two neighbouring ones for V, whose codes share bytes.
 // The order of the pieces is that of the cache's bytes, so that a warp reads
 // or writes them in contiguous runs, and the bf16 side goes in whole 32-byte
@@ -31,11 +31,10 @@ struct UnitTask {
     int h;
 };
 
-// False when the warp has nothing to do.
+// The w-th (unit slot, KV head); false when there is nothing to do.
 template <int D>
-__device__ __forceinline__ bool find_unit(const Kv4RowsParams& p, UnitTask& t)
+__device__ __forceinline__ bool find_unit(const Kv4RowsParams& p, unsigned w, UnitTask& t)
 {
-    const unsigned w = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
     const unsigned u = w / (unsigned)p.c.Hkv;
     t.h = (int)(w - u * (unsigned)p.c.Hkv);
     if (u >= (unsigned)(p.total >> 4) + 2u * (unsigned)p.num_seqs) return false;
@@ -94,38 +93,13 @@ __device__ __forceinline__ Group load_group(const uint16_t* src, bool on, bool w
     return x;
 }
 
-// Scale byte of a group and the 16 quotients x / (head scale * scale).  The
-// maximum is taken on the magnitudes' bits, where infinities and NaN come out
-// above every number; such a group gets a NaN scale and zero codes.
-__device__ __forceinline__ uint32_t quantise_group(const Group& x, float head, float (&y)[16])
+// e2m1 codes of eight values in four packed pairs, two a byte, the first in
+// the low nibble: ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1_word(const uint64_t (&y)[4])
 {
-    uint32_t m = 0;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x.w[i] & 0x7fff7fffu);
-    const uint32_t top = max(m & 0xffffu, m >> 16);
-    const float amax = __fdiv_rn(__uint_as_float(top << 16), head);
-    uint16_t pair;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(__fdiv_rn(amax, 6.f)));
-    const bool none = top >= 0x7f80u || (pair & 0x7f) == 0;
-    const float s = none ? 0.f : f16x2_to_f32(e4m3x2_to_f16x2(pair)).x * head;
-    // Quotients with Markstein's correction (x r, then the remainder's share):
-    // the rounded quotient, so that a value exactly between two codes is seen
-    // as such; x r alone is off by an ulp there.
-    const float r = none ? 0.f : __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float v = none ? 0.f : __uint_as_float((i & 1) ? x.w[i >> 1] & 0xffff0000u : x.w[i >> 1] << 16);
-        const float q = v * r;
-        y[i] = __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
-    }
-    return top >= 0x7f80u ? 0x7fu : (pair & 0xffu);
-}
-
-// e2m1 codes of eight values, two a byte, the first in the low nibble: ties
-// to even, saturating at 6.
-__device__ __forceinline__ uint32_t e2m1_word(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
-                                              float x7)
-{
+    for (int i = 0; i < 4; ++i) f2_unpack(y[i], x[2 * i], x[2 * i + 1]);
     uint32_t r;
     asm("{.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -134,12 +108,77 @@ __device__ __forceinline__ uint32_t e2m1_word(float x0, float x1, float x2, floa
         "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
         "mov.b32 %0, {a, b, c, d};}"
         : "=r"(r)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
     return r;
 }
 
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A quotient x / y from r, 1 / y to an ulp, with Markstein's correction: the
+// product x r, then the remainder's share of it.  A quotient that is a number
+// comes out as that number, so a value exactly between two codes is seen as
+// such; x r alone is off by an ulp there.
+__device__ __forceinline__ float quotient(float x, float y, float r)
+{
+    const float q = x * r;
+    return __fmaf_rn(__fmaf_rn(-q, y, x), r, q);
+}
+
+struct Codes {
+    uint32_t w[2];  // dimensions 0 .. 7, 8 .. 15
+    uint32_t scale;
+};
+
+// Quantises a group.  head6 = 6 * head scale, r6 its reciprocal.  The maximum
+// is taken on the magnitudes' bits, where infinities and NaN come out above
+// every number; such a group gets a NaN scale and zero codes.
+__device__ __forceinline__ Codes quantise_group(const Group& x, float head, float head6, float r6)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x.w[i] & 0x7fff7fffu);
+    const uint32_t top = max(m & 0xffffu, m >> 16);
+    const bool bad = top >= 0x7f80u;
+    uint16_t pair;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(pair)
+        : "f"(0.f), "f"(bad ? 0.f : quotient(__uint_as_float(top << 16), head6, r6)));
+    Codes c;
+    c.scale = bad ? 0x7fu : (uint32_t)pair;
+    const float s = f16x2_to_f32(e4m3x2_to_f16x2(pair)).x * head;
+    const float r = pair == 0 ? 0.f : rcp_approx(s);
+    const uint64_t r2 = f2_pack(r, r), s2 = f2_pack(-s, -s);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        uint64_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // quotient(), two values at a time
+            const uint32_t w = x.w[4 * e + i];
+            const uint64_t v = f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+            const uint64_t q = f2_mul(v, r2);
+            y[i] = f2_fma(f2_fma(q, s2, v), r2, q);
+        }
+        c.w[e] = pair == 0 ? 0u : e2m1_word(y);
+    }
+    return c;
+}
+
+// Codes of two positions, eight dimensions a word, to one byte a dimension
+// (position a in the low nibble): dimensions 0 .. 3 and 4 .. 7.
+__device__ __forceinline__ uint2 pair_codes(uint32_t a, uint32_t b)
+{
+    const uint32_t even = (a & 0x0f0f0f0fu) | (b & 0x0f0f0f0fu) << 4;
+    const uint32_t odd = (a >> 4 & 0x0f0f0f0fu) | (b & 0xf0f0f0f0u);
+    return make_uint2(__byte_perm(even, odd, 0x5140), __byte_perm(even, odd, 0x7362));
+}
+
 template <int D>
-__global__ void __launch_bounds__(kRowsThreads) fa_kv4_append_kernel(const Kv4RowsParams p)
+__global__ void __launch_bounds__(kRowsThreads, 4) fa_kv4_append_kernel(const Kv4RowsParams p)
 {
     constexpr int G = D / 16, KI = D / 32, VI = D / 64;
     // the last block looks for slots that the call names twice
@@ -155,17 +194,34 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_append_kernel(const Kv4Ro
         }
         return;
     }
+    // one warp for K and one for V of a unit: with both in one the loaded
+    // rows took 88 registers and 16 warps an SM
+    const unsigned w = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
     UnitTask t;
-    if (!find_unit<D>(p, t)) return;
+    if (!find_unit<D>(p, w >> 1, t)) return;
     const int lane = threadIdx.x & 31;
     const long long pitch = (long long)p.c.Hkv * D, base = t.row * pitch + t.h * D;
     const auto mine = [&](int r) { return r >= t.lo && r < t.hi; };
-    Group k[KI], v[VI][2];
+    const float* heads = w & 1 ? p.c.v_scale : p.c.k_scale;
+    const float head = heads ? heads[t.h] : 1.f, head6 = 6.f * head, r6 = rcp_approx(head6);
+    if (!(w & 1)) {
+        Group k[KI];
 #pragma unroll
-    for (int i = 0; i < KI; ++i) {
-        const int x = 32 * i + lane, r = x / G, g = x % G;
-        k[i] = load_group(p.k_in + base + r * pitch + g * 16, mine(r), p.wide);
+        for (int i = 0; i < KI; ++i) {
+            const int x = 32 * i + lane, r = x / G, g = x % G;
+            k[i] = load_group(p.k_in + base + r * pitch + g * 16, mine(r), p.wide);
+        }
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int x = 32 * i + lane;
+            const Codes c = quantise_group(k[i], head, head6, r6);
+            if (!mine(x / G)) continue;
+            *reinterpret_cast<uint2*>(t.unit + x * 8) = make_uint2(c.w[0], c.w[1]);
+            t.unit[16 * D + x] = (uint8_t)c.scale;
+        }
+        return;
     }
+    Group v[VI][2];
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
         const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
@@ -173,41 +229,24 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_append_kernel(const Kv4Ro
         for (int e = 0; e < 2; ++e)
             v[i][e] = load_group(p.v_in + base + (r + e) * pitch + g * 16, mine(r + e), p.wide);
     }
-    const float gk = p.c.k_scale ? p.c.k_scale[t.h] : 1.f, gv = p.c.v_scale ? p.c.v_scale[t.h] : 1.f;
-#pragma unroll
-    for (int i = 0; i < KI; ++i) {
-        const int x = 32 * i + lane;
-        if (!mine(x / G)) continue;
-        float y[16];
-        const uint32_t s = quantise_group(k[i], gk, y);
-        *reinterpret_cast<uint2*>(t.unit + x * 8) =
-            make_uint2(e2m1_word(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]),
-                       e2m1_word(y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]));
-        t.unit[16 * D + x] = (uint8_t)s;
-    }
 #pragma unroll
     for (int i = 0; i < VI; ++i) {
         const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
         const bool even = mine(r), odd = mine(r + 1);
+        const Codes a = quantise_group(v[i][0], head, head6, r6), b = quantise_group(v[i][1], head, head6, r6);
         if (!even && !odd) continue;
-        float ya[16], yb[16];
-        const uint32_t sa = quantise_group(v[i][0], gv, ya), sb = quantise_group(v[i][1], gv, yb);
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = e2m1_word(ya[4 * e], yb[4 * e], ya[4 * e + 1], yb[4 * e + 1], ya[4 * e + 2], yb[4 * e + 2],
-                             ya[4 * e + 3], yb[4 * e + 3]);
+        const uint2 lo = pair_codes(a.w[0], b.w[0]), hi = pair_codes(a.w[1], b.w[1]);
         uint4* codes = reinterpret_cast<uint4*>(t.unit + 8 * D + x * 16);
         uint8_t* scales = t.unit + 17 * D + g * 16 + r;
         if (even && odd) {
-            *codes = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(sa | sb << 8);
+            *codes = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(a.scale | b.scale << 8);
         } else {  // the pair's other position keeps its nibbles
             const uint32_t own = even ? 0x0f0f0f0fu : 0xf0f0f0f0u;
             const uint4 old = *codes;
-            *codes = make_uint4((old.x & ~own) | (w[0] & own), (old.y & ~own) | (w[1] & own),
-                                (old.z & ~own) | (w[2] & own), (old.w & ~own) | (w[3] & own));
-            scales[even ? 0 : 1] = (uint8_t)(even ? sa : sb);
+            *codes = make_uint4((old.x & ~own) | (lo.x & own), (old.y & ~own) | (lo.y & own),
+                                (old.z & ~own) | (hi.x & own), (old.w & ~own) | (hi.y & own));
+            scales[even ? 0 : 1] = (uint8_t)(even ? a.scale : b.scale);
         }
     }
 }
@@ -245,7 +284,7 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_read_kernel(const Kv4Rows
 {
     constexpr int G = D / 16, KI = D / 32, VI = D / 64;
     UnitTask t;
-    if (!find_unit<D>(p, t)) return;
+    if (!find_unit<D>(p, blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5), t)) return;
     const int lane = threadIdx.x & 31;
     uint2 kc[KI];
     uint4 vc[VI];
@@ -305,9 +344,9 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_read_kernel(const Kv4Rows
     }
 }
 
-unsigned rows_blocks(const Kv4RowsParams& p)
+unsigned rows_blocks(const Kv4RowsParams& p, int warps_per_unit)
 {
-    const long long warps = ((long long)(p.total >> 4) + 2ll * p.num_seqs) * p.c.Hkv;
+    const long long warps = ((long long)(p.total >> 4) + 2ll * p.num_seqs) * p.c.Hkv * warps_per_unit;
     return (unsigned)((warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32));
 }
 
@@ -315,7 +354,7 @@ unsigned rows_blocks(const Kv4RowsParams& p)
 
 cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned grid = rows_blocks(p) + (p.c.ids ? 1 : 0);
+    const unsigned grid = rows_blocks(p, 2) + (p.c.ids ? 1 : 0);
     if (D == 128)
         fa_kv4_append_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else
@@ -325,7 +364,7 @@ cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream
 
 cudaError_t launch_kv4_read(int D, const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned grid = rows_blocks(p);
+    const unsigned grid = rows_blocks(p, 1);
     if (D == 128)
         fa_kv4_read_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else
