@@ -58,6 +58,7 @@ template <int D, int MODE>
 struct Cfg {
     static constexpr int UNIT = 18 * D;
     static constexpr int NU = tile_keys(D) / 16;  // units of a tile
+    static constexpr int UG = MODE == 2 ? NU / 2 : NU;  // units worked on at once (registers)
     static constexpr int STAGE = NU * UNIT;
     static constexpr int STAGES = 2;  // per warp
     static constexpr int ROWS = 4 << MODE;
@@ -239,10 +240,10 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnParams p, const int chunks)
 {
     using C = Cfg<D, MODE>;
-    constexpr int NT = C::NT, KS = C::KS, NU = C::NU, TILE = tile_keys(D);
+    constexpr int NT = C::NT, KS = C::KS, NU = C::NU, UG = C::UG, TILE = tile_keys(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps], s_base;
-    __shared__ int s_b;
+    __shared__ Walk s_seg;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t base = smem_u32(smem);
     const uint32_t ring = base + warp * (C::STAGES * C::STAGE);
@@ -294,13 +295,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         long long at = upto - mine;
         int b = run0;
         for (long long x; at + (x = cost(b)) <= first; ++b) at += x;
-        s_b = b;
+        s_seg.b = b;
+        walk_sequence<D>(p, s_seg);
         s_base = at;
     }
     __syncthreads();
-    Walk seg;  // the item in hand
-    seg.b = s_b;
-    walk_sequence<D>(p, seg);
+    Walk seg = s_seg;  // the item in hand
     int left = (int)(last - first);  // of the share, from tile seg.t on
     {
         const long long off = first - s_base;
@@ -311,6 +311,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             seg.t = 0;
         }
     }
+
+    // Q rows of item hc of sequence b into L2, before the tiles' loads queue up
+    auto prefetch_q = [&](int b, int hc) {
+        const int h = hc / chunks, r0 = (hc - h * chunks) * C::ROWS;
+        const long long row0 = ((long long)b * p.Hq + (long long)h * p.group) * p.Lq + r0;
+        const char* q = reinterpret_cast<const char*>(p.q + row0 * D);
+        if (lane * 128 < min(C::ROWS, p.R - r0) * D * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
+    };
+    if (warp == 0) prefetch_q(seg.b, seg.hc);
 
     // ---- the warp's loads, running ahead of its tiles: lane i holds where the
     // warp's i-th tile from `ld` on lies and copies it when its turn comes
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             // power of two of the row: its largest magnitude comes to [1, 2)
-            const int e = top >= 0x7f80u || top == 0 ? 0 : max((int)(top >> 7) - 127, -120);
+            const int e = top >= 0x7f80u || top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 126);
             const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
             for (int i = 0; i < KS * 2; ++i) {
@@ -456,193 +465,203 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
         }
         if constexpr (MODE == 2) __syncthreads();
+        if (warp == 0 && left > n_seg) {
+            const bool same = seg.hc + 1 < items;
+            if (same || seg.b + 1 < p.B) prefetch_q(same ? seg.b : seg.b + 1, same ? seg.hc + 1 : 0);
+        }
 
         for (; next < done + n_seg && len > 0; next += kWarps) {
-            const int key0 = (seg.t + next - done) * TILE;
-            const uint32_t st = used % C::STAGES, tile = ring + st * C::STAGE;
+            const int tile0 = (seg.t + next - done) * TILE;
+            const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;
             if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
                 failed = true;
                 break;
             }
-            const bool border = key0 + TILE > all_see;
+#pragma unroll 1
+            for (int v0 = 0; v0 < NU; v0 += UG) {
+                if (UG < NU && v0 > 0 && tile0 + 16 * v0 >= len) break;
+                const int key0 = tile0 + 16 * v0;
+                const uint32_t tile = stage + v0 * C::UNIT;
+                const bool border = key0 + 16 * UG > all_see;
 
-            // ---- S^T = K Q^T.  Units behind the sequence's end hold old
-            // bytes: their scores are masked, their V scales zeroed.
-            float s[NU][NT][4];
+                // ---- S^T = K Q^T.  Units behind the sequence's end hold old
+                // bytes: their scores are masked, their V scales zeroed.
+                float s[UG][NT][4];
 #pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const uint32_t unit = tile + u * C::UNIT;
-                uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
-                if constexpr (D == 128) {
-                    const uint4 a = lds16(unit + g * 64 + t4 * 16), b = lds16(unit + (g + 8) * 64 + t4 * 16);
-                    ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
-                    kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
-                    const uint32_t x = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + g * 8 + t4 * 2));
-                    const uint32_t y = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + (g + 8) * 8 + t4 * 2));
-                    sa[0] = low_twice(x), sa[1] = high_twice(x);
-                    sb[0] = low_twice(y), sb[1] = high_twice(y);
-                } else {
-                    const uint2 a = lds8(unit + g * 32 + t4 * 8), b = lds8(unit + (g + 8) * 32 + t4 * 8);
-                    ka[0] = a.x, ka[1] = a.y;
-                    kb[0] = b.x, kb[1] = b.y;
-                    const uint32_t x = lds_u8(unit + 16 * D + g * 4 + t4), y = lds_u8(unit + 16 * D + (g + 8) * 4 + t4);
-                    sa[0] = low_twice(e4m3x2_to_f16x2((uint16_t)x));
-                    sb[0] = low_twice(e4m3x2_to_f16x2((uint16_t)y));
-                }
-                auto step = [&](auto jj) {
-                    constexpr int j = decltype(jj)::value;
-                    const uint32_t a0 = hmul2(code_pair<2 * j>(ka), sa[j / 4]);
-                    const uint32_t a1 = hmul2(code_pair<2 * j>(kb), sb[j / 4]);
-                    const uint32_t a2 = hmul2(code_pair<2 * j + 1>(ka), sa[j / 4]);
-                    const uint32_t a3 = hmul2(code_pair<2 * j + 1>(kb), sb[j / 4]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint2 b;
-                        if constexpr (MODE == 2)
-                            b = lds8(qbuf + ((nt * KS + j) * 32 + lane) * 8);
-                        else
-                            b = make_uint2(qf[2 * j], qf[2 * j + 1]);
-                        if constexpr (j == 0)
-                            mma_f16_first(s[u][nt], a0, a1, a2, a3, b.x, b.y);
-                        else
-                            mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                for (int u = 0; u < UG; ++u) {
+                    const uint32_t unit = tile + u * C::UNIT;
+                    uint32_t ka[KS / 2], kb[KS / 2], sa[KS / 4], sb[KS / 4];
+                    if constexpr (D == 128) {
+                        const uint4 a = lds16(unit + g * 64 + t4 * 16), b = lds16(unit + (g + 8) * 64 + t4 * 16);
+                        ka[0] = a.x, ka[1] = a.y, ka[2] = a.z, ka[3] = a.w;
+                        kb[0] = b.x, kb[1] = b.y, kb[2] = b.z, kb[3] = b.w;
+                        const uint32_t x = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + g * 8 + t4 * 2));
+                        const uint32_t y = e4m3x2_to_f16x2(lds_u16(unit + 16 * D + (g + 8) * 8 + t4 * 2));
+                        sa[0] = low_twice(x), sa[1] = high_twice(x);
+                        sb[0] = low_twice(y), sb[1] = high_twice(y);
+                    } else {
+                        const uint2 a = lds8(unit + g * 32 + t4 * 8), b = lds8(unit + (g + 8) * 32 + t4 * 8);
+                        ka[0] = a.x, ka[1] = a.y;
+                        kb[0] = b.x, kb[1] = b.y;
+                        const uint32_t x = lds_u8(unit + 16 * D + g * 4 + t4), y = lds_u8(unit + 16 * D + (g + 8) * 4 + t4);
+                        sa[0] = low_twice(e4m3x2_to_f16x2((uint16_t)x));
+                        sb[0] = low_twice(e4m3x2_to_f16x2((uint16_t)y));
                     }
-                };
-                for_steps(step, std::make_integer_sequence<int, KS>{});
-            }
-            // V's scales, with what a border tile must not use taken out
-            const int grp = D == 128 ? g : g >> 1;
-            uint32_t va_s[NU], vb_s[NU];
+                    auto step = [&](auto jj) {
+                        constexpr int j = decltype(jj)::value;
+                        const uint32_t a0 = hmul2(code_pair<2 * j>(ka), sa[j / 4]);
+                        const uint32_t a1 = hmul2(code_pair<2 * j>(kb), sb[j / 4]);
+                        const uint32_t a2 = hmul2(code_pair<2 * j + 1>(ka), sa[j / 4]);
+                        const uint32_t a3 = hmul2(code_pair<2 * j + 1>(kb), sb[j / 4]);
 #pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const uint32_t at = tile + u * C::UNIT + 17 * D + grp * 16 + 2 * t4;
-                va_s[u] = e4m3x2_to_f16x2(lds_u16(at));
-                vb_s[u] = e4m3x2_to_f16x2(lds_u16(at + 8));
-            }
-            // ---- masks, the running maximum in log2 units
-            if (border) {
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint2 b;
+                            if constexpr (MODE == 2)
+                                b = lds8(qbuf + ((nt * KS + j) * 32 + lane) * 8);
+                            else
+                                b = make_uint2(qf[2 * j], qf[2 * j + 1]);
+                            if constexpr (j == 0)
+                                mma_f16_first(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                            else
+                                mma_f16(s[u][nt], a0, a1, a2, a3, b.x, b.y);
+                        }
+                    };
+                    for_steps(step, std::make_integer_sequence<int, KS>{});
+                }
+                // V's scales, with what a border tile must not use taken out
+                const int grp = D == 128 ? g : g >> 1;
+                uint32_t va_s[UG], vb_s[UG];
 #pragma unroll
-                for (int u = 0; u < NU; ++u)
+                for (int u = 0; u < UG; ++u) {
+                    const uint32_t at = tile + u * C::UNIT + 17 * D + grp * 16 + 2 * t4;
+                    va_s[u] = e4m3x2_to_f16x2(lds_u16(at));
+                    vb_s[u] = e4m3x2_to_f16x2(lds_u16(at + 8));
+                }
+                // ---- masks, the running maximum in log2 units
+                if (border) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int u = 0; u < UG; ++u)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            if (key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                    // positions behind the end: whatever their scales hold becomes 0
-                    const int k = key0 + 16 * u + 2 * t4;
-                    uint32_t &x = va_s[u], &y = vb_s[u];
-                    if (k >= len) x = 0;
-                    if (k + 1 >= len) x &= 0xffffu;
-                    if (k + 8 >= len) y = 0;
-                    if (k + 9 >= len) y &= 0xffffu;
-                    // A NaN scale reaches only the rows that see its key: it is
-                    // taken out of the product and put into their sums.
-                    const uint32_t nx = nan_halves(x), ny = nan_halves(y);
-                    if (__any_sync(~0u, nx | ny)) {
-                        x = (nx & 1 ? 0u : x & 0xffffu) | (nx & 2 ? 0u : x & 0xffff0000u);
-                        y = (ny & 1 ? 0u : y & 0xffffu) | (ny & 2 ? 0u : y & 0xffff0000u);
-                        for (int j = 0; j < 16; ++j) {
-                            if ((lds_u8(tile + u * C::UNIT + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
+                            for (int c = 0; c < 4; ++c)
+                                if (key0 + 16 * u + g + 8 * (c >> 1) >= lim[nt][c & 1]) s[u][nt][c] = -INFINITY;
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
+                    for (int u = 0; u < UG; ++u) {
+                        // positions behind the end: whatever their scales hold becomes 0
+                        const int k = key0 + 16 * u + 2 * t4;
+                        uint32_t &x = va_s[u], &y = vb_s[u];
+                        if (k >= len) x = 0;
+                        if (k + 1 >= len) x &= 0xffffu;
+                        if (k + 8 >= len) y = 0;
+                        if (k + 9 >= len) y &= 0xffffu;
+                        // A NaN scale reaches only the rows that see its key: it is
+                        // taken out of the product and put into their sums.
+                        const uint32_t nx = nan_halves(x), ny = nan_halves(y);
+                        if (__any_sync(~0u, nx | ny)) {
+                            x = (nx & 1 ? 0u : x & 0xffffu) | (nx & 2 ? 0u : x & 0xffff0000u);
+                            y = (ny & 1 ? 0u : y & 0xffffu) | (ny & 2 ? 0u : y & 0xffff0000u);
+                            for (int j = 0; j < 16; ++j) {
+                                if ((lds_u8(tile + u * C::UNIT + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
 #pragma unroll
-                                for (int c = 0; c < 2; ++c)
-                                    if (key0 + 16 * u + j < min(lim[nt][c], len)) {
+                                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                        for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
-                                    }
+                                    for (int c = 0; c < 2; ++c)
+                                        if (key0 + 16 * u + j < min(lim[nt][c], len)) {
+#pragma unroll
+                                            for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
+                                        }
+                            }
                         }
                     }
                 }
-            }
-            bool raise = false;
-            float mx[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-#pragma unroll
-                    for (int u = 1; u < NU; ++u) x = fmaxf(x, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
-                    mx[nt][c] = x * sc[nt][c];
-                    raise |= mx[nt][c] > m[nt][c] + kRaise;
-                }
-            if (__any_sync(~0u, raise)) {
+                bool raise = false;
+                float mx[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float x = mx[nt][c];
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                        x = fmaxf(x, m[nt][c]);
-                        const float a = x == m[nt][c] ? 1.f : ex2_approx(m[nt][c] - x);
-                        m[nt][c] = x;
-                        l[nt][c] *= a;
+                        float x = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
 #pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            acc[nt][i][c] *= a;
-                            acc[nt][i][c + 2] *= a;
-                        }
+                        for (int u = 1; u < UG; ++u) x = fmaxf(x, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
+                        mx[nt][c] = x * sc[nt][c];
+                        raise |= mx[nt][c] > m[nt][c] + kRaise;
                     }
-            }
-            // ---- P^T as two fp16 numbers, turned into B fragments
-            uint32_t pb[NU][NT][MODE == 0 ? 1 : 2][2];
+                if (__any_sync(~0u, raise)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint64_t sc2 = f2_pack(sc[nt][0], sc[nt][1]), m2 = f2_pack(-m[nt][0], -m[nt][1]);
-                uint64_t l2 = f2_pack(l[nt][0], l[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int u = 0; u < NU; ++u)
+                        for (int c = 0; c < 2; ++c) {
+                            float x = mx[nt][c];
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                            x = fmaxf(x, m[nt][c]);
+                            const float a = x == m[nt][c] ? 1.f : ex2_approx(m[nt][c] - x);
+                            m[nt][c] = x;
+                            l[nt][c] *= a;
 #pragma unroll
-                    for (int k8 = 0; k8 < 2; ++k8) {
-                        float x0, x1;
-                        f2_unpack(f2_fma(f2_pack(s[u][nt][2 * k8], s[u][nt][2 * k8 + 1]), sc2, m2), x0, x1);
-                        const uint64_t p2 = f2_pack(x0 = ex2_approx(x0), x1 = ex2_approx(x1));
-                        l2 = f2_add(l2, p2);
-                        const uint32_t hi = f16x2(x0, x1);
-                        const float2 f = f16x2_to_f32(hi);
-                        if constexpr (MODE == 0) {
-                            // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take p - hi
-                            f2_unpack(f2_fma(f2_pack(f.x, f.y), part2, p2), x0, x1);
-                            pb[u][nt][0][k8] = transpose8x8(f16x2(x0, x1));
-                        } else {
-                            pb[u][nt][0][k8] = transpose8x8(hi);
-                            pb[u][nt][1][k8] = transpose8x8(f16x2(x0 - f.x, x1 - f.y));
+                            for (int i = 0; i < KS; ++i) {
+                                acc[nt][i][c] *= a;
+                                acc[nt][i][c + 2] *= a;
+                            }
                         }
-                    }
-                f2_unpack(l2, l[nt][0], l[nt][1]);
-            }
-            // ---- O^T += V^T P^T
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-                const uint32_t unit = tile + u * C::UNIT;
-                uint32_t va[KS / 2], vb[KS / 2];
-                if constexpr (D == 128) {
-                    const uint4 a = lds16(unit + 8 * D + g * 64 + t4 * 16), b = lds16(unit + 12 * D + g * 64 + t4 * 16);
-                    va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
-                    vb[0] = b.x, vb[1] = b.y, vb[2] = b.z, vb[3] = b.w;
-                } else {
-                    const uint32_t at = unit + 8 * D + grp * 64 + t4 * 16 + (g & 1) * 8;
-                    const uint2 a = lds8(at), b = lds8(at + 4 * D);
-                    va[0] = a.x, va[1] = a.y;
-                    vb[0] = b.x, vb[1] = b.y;
                 }
-                const uint32_t sa = va_s[u], sb = vb_s[u];
-                auto step = [&](auto ii) {
-                    constexpr int i = decltype(ii)::value;
-                    const uint32_t a0 = hmul2(code_pair<2 * i>(va), sa), a1 = hmul2(code_pair<2 * i + 1>(va), sa);
-                    const uint32_t a2 = hmul2(code_pair<2 * i>(vb), sb), a3 = hmul2(code_pair<2 * i + 1>(vb), sb);
+                // ---- P^T as two fp16 numbers, turned into B fragments
+                uint32_t pb[UG][NT][MODE == 0 ? 1 : 2][2];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
-                        if constexpr (MODE != 0) mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint64_t sc2 = f2_pack(sc[nt][0], sc[nt][1]), m2 = f2_pack(-m[nt][0], -m[nt][1]);
+                    uint64_t l2 = f2_pack(l[nt][0], l[nt][1]);
+#pragma unroll
+                    for (int u = 0; u < UG; ++u)
+#pragma unroll
+                        for (int k8 = 0; k8 < 2; ++k8) {
+                            float x0, x1;
+                            f2_unpack(f2_fma(f2_pack(s[u][nt][2 * k8], s[u][nt][2 * k8 + 1]), sc2, m2), x0, x1);
+                            const uint64_t p2 = f2_pack(x0 = ex2_approx(x0), x1 = ex2_approx(x1));
+                            l2 = f2_add(l2, p2);
+                            const uint32_t hi = f16x2(x0, x1);
+                            const float2 f = f16x2_to_f32(hi);
+                            if constexpr (MODE == 0) {
+                                // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take p - hi
+                                f2_unpack(f2_fma(f2_pack(f.x, f.y), part2, p2), x0, x1);
+                                pb[u][nt][0][k8] = transpose8x8(f16x2(x0, x1));
+                            } else {
+                                pb[u][nt][0][k8] = transpose8x8(hi);
+                                pb[u][nt][1][k8] = transpose8x8(f16x2(x0 - f.x, x1 - f.y));
+                            }
+                        }
+                    f2_unpack(l2, l[nt][0], l[nt][1]);
+                }
+                // ---- O^T += V^T P^T
+#pragma unroll
+                for (int u = 0; u < UG; ++u) {
+                    const uint32_t unit = tile + u * C::UNIT;
+                    uint32_t va[KS / 2], vb[KS / 2];
+                    if constexpr (D == 128) {
+                        const uint4 a = lds16(unit + 8 * D + g * 64 + t4 * 16), b = lds16(unit + 12 * D + g * 64 + t4 * 16);
+                        va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
+                        vb[0] = b.x, vb[1] = b.y, vb[2] = b.z, vb[3] = b.w;
+                    } else {
+                        const uint32_t at = unit + 8 * D + grp * 64 + t4 * 16 + (g & 1) * 8;
+                        const uint2 a = lds8(at), b = lds8(at + 4 * D);
+                        va[0] = a.x, va[1] = a.y;
+                        vb[0] = b.x, vb[1] = b.y;
                     }
-                };
-                for_steps(step, std::make_integer_sequence<int, KS>{});
+                    const uint32_t sa = va_s[u], sb = vb_s[u];
+                    auto step = [&](auto ii) {
+                        constexpr int i = decltype(ii)::value;
+                        const uint32_t a0 = hmul2(code_pair<2 * i>(va), sa), a1 = hmul2(code_pair<2 * i + 1>(va), sa);
+                        const uint32_t a2 = hmul2(code_pair<2 * i>(vb), sb), a3 = hmul2(code_pair<2 * i + 1>(vb), sb);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
+                            if constexpr (MODE != 0) mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
+                        }
+                    };
+                    for_steps(step, std::make_integer_sequence<int, KS>{});
+                }
             }
             __syncwarp();  // the stage has been read
             ++used;
@@ -728,54 +747,82 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 }
 
 // Joins the parts of the item that begins in block blockIdx.x and ends in a
-// later one.  Several warps share a row: each adds every WPR-th part in order,
-// then the warps' sums are added in order.
-constexpr int kJoinThreads = 1024;
+// later one: four rows a block, four warps a row.  A warp takes every fourth
+// part, four at a time, all loads before the first use; the warps' sums are
+// added in order.
+constexpr int kJoinRows = 4, kJoinWarps = 4, kJoinThreads = 32 * kJoinRows * kJoinWarps;
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4AttnParams p, const int chunks)
 {
-    constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32, WPR = kJoinThreads / 32 / ROWS;
-    __shared__ float s_o[ROWS][WPR][D];
-    __shared__ float2 s_ml[ROWS][WPR];
+    constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32, U = 4;
+    __shared__ float s_o[kJoinRows][kJoinWarps][D];
+    __shared__ float2 s_ml[kJoinRows][kJoinWarps];
     const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
     wait_for_primary();
     const int4 j = parts.join[blockIdx.x];
     if (j.w == 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = j.y / chunks, r0 = (j.y - h * chunks) * ROWS, nrows = min(ROWS, p.R - r0);
+    const int h = j.y / chunks, first = blockIdx.y * kJoinRows;  // of the item's rows
+    const int r0 = (j.y - h * chunks) * ROWS + first, nrows = min(kJoinRows, min(ROWS - first, p.R - r0));
+    if (nrows <= 0) return;
     const long long row0 = ((long long)j.x * p.Hq + (long long)h * p.group) * p.Lq + r0;
     const int n = j.z - (int)blockIdx.x + 1;
-    const int r = warp / WPR, w = warp % WPR;
-    const auto index = [&](int k) { return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r; };
-    float mm = -FLT_MAX;
-    for (int k = lane; k < n; k += 32) mm = fmaxf(mm, parts.ml[index(k)].x);
+    const int r = warp / kJoinWarps, w = warp % kJoinWarps;
+    float acc[V] = {}, sum = 0.f, mm = -FLT_MAX;
+    if (r < nrows) {
+        for (int k0 = w; k0 < n; k0 += U * kJoinWarps) {
+            float2 ml[U];
+            float x[U][V];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(~0u, mm, o));
-    float acc[V] = {}, sum = 0.f;
-#pragma unroll 4
-    for (int k = w; k < n; k += WPR) {
-        const float2 ml = parts.ml[index(k)];
-        const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
-        sum = fmaf(a, ml.y, sum);
+            for (int i = 0; i < U; ++i) {
+                const int k = k0 + i * kJoinWarps;
+                ml[i] = make_float2(-FLT_MAX, 0.f);
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = fmaf(a, parts.o[index(k) * D + lane + 32 * e], acc[e]);
+                for (int e = 0; e < V; ++e) x[i][e] = 0.f;
+                if (k < n) {
+                    const long long at = ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + first + r;
+                    ml[i] = parts.ml[at];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[i][e] = parts.o[at * D + lane + 32 * e];
+                }
+            }
+            float top = mm;
+#pragma unroll
+            for (int i = 0; i < U; ++i) top = fmaxf(top, ml[i].x);
+            const float down = mm == top ? 1.f : ex2_approx(mm - top);
+            mm = top;
+            sum *= down;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= down;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const float a = ml[i].x == top ? 1.f : ex2_approx(ml[i].x - top);
+                sum = fmaf(a, ml[i].y, sum);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(a, x[i][e], acc[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) s_o[r][w][lane + 32 * e] = acc[e];
+        if (lane == 0) s_ml[r][w] = make_float2(mm, sum);
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) s_o[r][w][lane + 32 * e] = acc[e];
-    if (lane == 0) s_ml[r][w] = make_float2(mm, sum);
     __syncthreads();
     const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.f;
     for (int x = threadIdx.x; x < nrows * D; x += kJoinThreads) {
         const int rr = x / D, d = x % D;
-        float o = 0.f, l = 0.f;
+        float top = -FLT_MAX, o = 0.f, l = 0.f;
 #pragma unroll
-        for (int i = 0; i < WPR; ++i) {
-            o += s_o[rr][i][d];
-            l += s_ml[rr][i].y;
+        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_ml[rr][i].x);
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            const float2 ml = s_ml[rr][i];
+            const float a = ml.x == top ? 1.f : ex2_approx(ml.x - top);
+            o = fmaf(a, s_o[rr][i][d], o);
+            l = fmaf(a, ml.y, l);
         }
         p.o[(row0 + rr) * D + d] = l == 0.f ? 0.f : o / l * gv;
-        if (d == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (s_ml[rr][0].x + log2f(l)) * 0.6931471805599453f;
+        if (d == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
     }
 }
 
@@ -792,7 +839,8 @@ cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
     fa_kv4_attn_kernel<D, MODE><<<blocks, kThreads, C::SMEM, stream>>>(p, chunks);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return f;
-    return launch_dependent(fa_kv4_join_kernel<D, MODE>, blocks, kJoinThreads, stream, p, chunks);
+    return launch_dependent(fa_kv4_join_kernel<D, MODE>, dim3(blocks, C::ROWS / kJoinRows), kJoinThreads, stream, p,
+                            chunks);
 }
 
 int blocks_of(int num_sms) { return 2 * num_sms; }

@@ -76,13 +76,13 @@ __device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepc
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int blocks, int threads, cudaStream_t stream, Args... args)
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 blocks, int threads, cudaStream_t stream, Args... args)
 {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.gridDim = blocks;
     cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cfg.attrs = &attr;
