@@ -34,6 +34,7 @@
 // on the device; an item that lies in several blocks is joined by a second
 // kernel.
 #include <cfloat>
+#include <climits>
 #include <cmath>
 #include <utility>
 
@@ -46,8 +47,9 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 // What beginning and joining an item costs a block, in tiles (the lists of
-// short sequences took 107 us where items counted only by their tiles).
-constexpr int kItemCost = 12;
+// short sequences took 107 us where items counted only by their tiles), and
+// what beginning a group of items of one warp each does.
+constexpr int kItemCost = 16, kSoloCost = 8;
 constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
 
 // Keys of a warp's tile: 4608 bytes.
@@ -67,9 +69,10 @@ struct Cfg {
     static constexpr int OSTRIDE = D + (D == 128 ? 4 : 2);  // floats per column in the joining buffer
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int OBUF = kWarps * 8 * OSTRIDE * 4;
-    static constexpr int QBUF = MODE == 2 ? 32 * KS * NT * 8 : 0;  // fragments of Q
     static constexpr int ML = kWarps * ROWS * 8;
-    static constexpr int BARS = RING + OBUF + QBUF + ML;
+    static constexpr int BARS = RING + OBUF + ML;
+    // MODE 2 keeps a warp's fragments of Q in its part of the joining buffer
+    static_assert(MODE != 2 || 32 * KS * NT * 8 <= 8 * OSTRIDE * 4, "Q fragments");
     static constexpr int SMEM = BARS + kWarps * STAGES * 8 + 64;
 };
 
@@ -152,6 +155,8 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a)
     return v;
 }
 
+__device__ __forceinline__ void prefetch_l2(const char* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -185,11 +190,18 @@ __device__ __forceinline__ int tiles_of(int len)
     return len > 0 ? (len + tile_keys(D) - 1) / tile_keys(D) : 1;
 }
 
+// The item that begins in a block and ends in a later one: its end in the
+// list of work and the blocks' share of that; item -1: none.
+struct Cut {
+    int b, item;
+    long long end, share;
+};
+
 // Where the kernels keep what they share in the workspace.
 struct Parts {
     float* o;   // [blocks][2][ROWS][D]
     float2* ml; // [blocks][2][ROWS]: maximum (log2 units) and sum
-    int4* join; // [blocks]: sequence, head and chunk, last block, 1; or w = 0
+    Cut* join;  // [blocks]
 };
 
 template <int D, int MODE>
@@ -197,44 +209,88 @@ __host__ __device__ inline Parts parts_of(float* ws, int blocks)
 {
     constexpr int ROWS = Cfg<D, MODE>::ROWS;
     Parts p;
-    p.join = reinterpret_cast<int4*>(ws);
+    p.join = reinterpret_cast<Cut*>(ws);
     p.ml = reinterpret_cast<float2*>(p.join + blocks);
     p.o = reinterpret_cast<float*>(p.ml + (size_t)blocks * 2 * ROWS);
     return p;
 }
 
-// A walk over the tile list: tile t of item hc (KV head and chunk of rows) of sequence b.
-struct Walk {
-    int b, hc, t, nt, len;
-    const int* row;  // of the table
+// The list of work.  Every sequence has `items` (KV head and chunk of rows).
+// Those of a long sequence are entries of the list one by one, kItemCost +
+// tiles long, and may be cut between blocks; the block's warps share an
+// entry's tiles.  Those of a short sequence come in groups of one item per
+// warp, which need no joining: 8 x tiles + kSoloCost long and never cut (they
+// are the block's in which their last unit lies).  A sequence is short when a
+// group of it has at most 5/4 of the tiles that a block has on average (more
+// would leave other blocks waiting), or two tiles an item.
+struct Seg {  // a block's part of an entry
+    int b, e;         // sequence, entry
+    int t, n;         // tiles t .. t + n - 1 (of each item, in a group)
+    int left;         // of the block's share, from tile t on
+    int len, nt, entries;
+    bool solo;        // a group
+    const int* row;   // of the table
+};
+
+struct Split {
+    int items, limit;  // limit: most tiles of a group
+
+    __device__ __forceinline__ bool solo(int nt) const { return items >= kWarps / 2 && kWarps * nt <= limit; }
+    __device__ __forceinline__ int entries(bool solo) const { return solo ? (items + kWarps - 1) / kWarps : items; }
+    // units in front of the part that may be cut
+    __device__ __forceinline__ int ahead(bool solo, int nt) const { return solo ? kWarps * nt + kSoloCost - 1 : kItemCost; }
+    __device__ __forceinline__ int body(bool solo, int nt) const { return solo ? 1 : nt; }
+    __device__ __forceinline__ long long cost(int nt) const
+    {
+        const bool one = solo(nt);
+        return (long long)(ahead(one, nt) + body(one, nt)) * entries(one);
+    }
 };
 
 template <int D>
-__device__ __forceinline__ void walk_sequence(const Kv4AttnParams& p, Walk& w)
+__device__ __forceinline__ void seg_open(const Kv4AttnParams& p, const Split& sp, Seg& s)
 {
     int slot;
-    w.len = kv4_sequence(p.c, w.b, slot);
-    w.row = p.c.table + (long long)slot * p.c.table_width;
-    w.nt = tiles_of<D>(w.len);
+    s.len = kv4_sequence(p.c, s.b, slot);
+    s.row = p.c.table + (long long)slot * p.c.table_width;
+    s.nt = tiles_of<D>(s.len);
+    s.solo = sp.solo(s.nt);
+    s.entries = sp.entries(s.solo);
 }
 
-// n tiles on; items = KV heads x chunks of a sequence.  `left`, what remains
-// of the block's share from the tile on, pays for items entered.
+// The block's part of the next entry; false at the end of its share.
 template <int D>
-__device__ __forceinline__ void walk_on(const Kv4AttnParams& p, Walk& w, int n, int items, int& left)
+__device__ __forceinline__ bool seg_next(const Kv4AttnParams& p, const Split& sp, Seg& s)
 {
-    w.t += n;
-    left -= n;
-    while (w.t >= w.nt && left > 0) {
-        w.t -= w.nt;
-        left -= kItemCost;
-        if (++w.hc == items) {
-            w.hc = 0;
-            ++w.b;
-            walk_sequence<D>(p, w);
-        }
+    s.left -= s.solo ? 1 : s.n;
+    if (s.left <= 0) return false;
+    if (++s.e == s.entries) {
+        s.e = 0;
+        ++s.b;
+        seg_open<D>(p, sp, s);
     }
+    s.left -= sp.ahead(s.solo, s.nt);
+    s.t = 0;
+    s.n = s.solo ? s.nt : min(s.left, s.nt);
+    return s.left > 0;
 }
+
+// KV head and chunk of rows of an item (chunk * Hkv + head; few chunks).
+__device__ __forceinline__ int2 head_and_chunk(int item, int Hkv)
+{
+    int chunk = 0;
+    for (; item >= Hkv; item -= Hkv) ++chunk;
+    return make_int2(item, chunk);
+}
+
+// Tiles of warp w in it, and its item.
+__device__ __forceinline__ int seg_item(const Seg& s, int w) { return s.solo ? kWarps * s.e + w : s.e; }
+__device__ __forceinline__ int seg_tiles(const Split& sp, const Seg& s, int w)
+{
+    if (s.len == 0) return 0;
+    return s.solo ? (seg_item(s, w) < sp.items ? s.n : 0) : max(0, (s.n - w + kWarps - 1) / kWarps);
+}
+__device__ __forceinline__ int seg_tile(const Seg& s, int w, int k) { return s.solo ? k : s.t + w + kWarps * k; }
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnParams p, const int chunks)
@@ -242,17 +298,17 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     using C = Cfg<D, MODE>;
     constexpr int NT = C::NT, KS = C::KS, NU = C::NU, UG = C::UG, TILE = tile_keys(D);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kWarps], s_base;
-    __shared__ Walk s_seg;
+    __shared__ long long s_sum[kWarps];
+    __shared__ Seg s_seg;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t base = smem_u32(smem);
     const uint32_t ring = base + warp * (C::STAGES * C::STAGE);
     const uint32_t bars = base + C::BARS + warp * (C::STAGES * 8);
     float* obuf = reinterpret_cast<float*>(smem + C::RING);
-    float2* mlbuf = reinterpret_cast<float2*>(smem + C::RING + C::OBUF + C::QBUF);
+    float2* mlbuf = reinterpret_cast<float2*>(smem + C::RING + C::OBUF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::BARS + kWarps * C::STAGES * 8);
     const WaitFailure wf{p.c.err, p.c.diag};
-    const int items = p.c.Hkv * chunks;  // of one sequence
+    Split sp{p.c.Hkv * chunks, 0};
 
     let_dependents_launch();
     if (lane == 0) {
@@ -260,18 +316,42 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         mbar_init_fence();
     }
     if (tid == 0) *abort_flag = 0;
+    {
+        // Q and (where the call names no slots) the table into L2 while the
+        // lengths are on their way, a line per thread of the grid
+        const long long line = ((long long)blockIdx.x * kThreads + tid) * 128;
+        const long long q_bytes = (long long)p.B * p.Hq * p.Lq * D * 2;
+        const long long t_bytes = p.c.ids ? 0 : (long long)p.B * p.c.table_width * 4;
+        if (line < t_bytes)
+            prefetch_l2(reinterpret_cast<const char*>(p.c.table) + line);
+        else if (line - t_bytes < q_bytes)
+            prefetch_l2(reinterpret_cast<const char*>(p.q) + (line - t_bytes));
+    }
 
-    // This block's share of the list of all items, each kItemCost + its tiles
-    // long, from the lengths: thread i sums a run of sequences, the block's
-    // prefix sums give the total and the run in which the share begins.
+    // This block's share of the list, from the lengths: thread i sums a run of
+    // sequences.  First the tiles alone, for the limit of a group, then the
+    // list's units, whose prefix sums say in which run the share begins.
     const int run = (p.B + kThreads - 1) / kThreads;
     const int run0 = min(p.B, tid * run), run1 = min(p.B, run0 + run);
-    auto cost = [&](int b) {
+    auto tiles = [&](int b) {
         int slot;
-        return (long long)(tiles_of<D>(kv4_sequence(p.c, b, slot)) + kItemCost) * items;
+        return tiles_of<D>(kv4_sequence(p.c, b, slot));
     };
-    long long mine = 0;
-    for (int b = run0; b < run1; ++b) mine += cost(b);
+    const int nt0 = run0 < run1 ? tiles(run0) : 0;  // of the run's first; most have no other
+    long long mine = nt0;
+    for (int b = run0 + 1; b < run1; ++b) mine += tiles(b);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    const float per_block = 1.f / gridDim.x;
+    sp.limit = (int)fminf(fmaxf(1.25f * per_block * (float)total * (float)sp.items, 2.f * kWarps), 1e9f);
+    __syncthreads();
+    mine = run0 < run1 ? sp.cost(nt0) : 0;
+    for (int b = run0 + 1; b < run1; ++b) mine += sp.cost(tiles(b));
     long long upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -280,52 +360,69 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     }
     if (lane == 31) s_sum[warp] = upto;
     __syncthreads();
-    long long total = 0;
+    total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w == warp) upto += total;
         total += s_sum[w];
     }
-    const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kWarps);
+    // ceil(total / blocks), or a little above
+    long long share = (long long)((float)total * per_block * 1.000002f + 0.999f);
+    share += share * gridDim.x < total;
+    share = max(share, (long long)kWarps);
     const long long first = share * blockIdx.x, last = min(total, first + share);
     Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
-    if (tid == 0) parts.join[blockIdx.x].w = 0;
+    if (tid == 0) parts.join[blockIdx.x].item = -1;
     if (first >= last) return;
     if (first < upto && first >= upto - mine) {
         long long at = upto - mine;
-        int b = run0;
-        for (long long x; at + (x = cost(b)) <= first; ++b) at += x;
-        s_seg.b = b;
-        walk_sequence<D>(p, s_seg);
-        s_base = at;
+        Seg s;
+        s.b = run0;
+        for (long long x; at + (x = sp.cost(s.b == run0 ? nt0 : tiles(s.b))) <= first; ++s.b) at += x;
+        seg_open<D>(p, sp, s);
+        const int ahead = sp.ahead(s.solo, s.nt), one = ahead + sp.body(s.solo, s.nt);
+        for (s.e = 0; at + one <= first; at += one) ++s.e;
+        s.left = (int)(last - first);
+        s.t = (int)(first - at) - ahead;
+        if (s.t < 0) {
+            s.left += s.t;
+            s.t = 0;
+        }
+        s.n = s.solo ? s.nt : min(s.left, s.nt - s.t);
+        s_seg = s;
     }
     __syncthreads();
-    Walk seg = s_seg;  // the item in hand
-    int left = (int)(last - first);  // of the share, from tile seg.t on
-    {
-        const long long off = first - s_base;
-        seg.hc = (int)(off / (seg.nt + kItemCost));
-        seg.t = (int)(off % (seg.nt + kItemCost)) - kItemCost;  // first tile of this block in it
-        if (seg.t < 0) {
-            left += seg.t;
-            seg.t = 0;
-        }
-    }
+    Seg seg = s_seg;  // in hand
+    if (seg.left <= 0) return;
 
-    // Q rows of item hc of sequence b into L2, before the tiles' loads queue up
-    auto prefetch_q = [&](int b, int hc) {
-        const int h = hc / chunks, r0 = (hc - h * chunks) * C::ROWS;
-        const long long row0 = ((long long)b * p.Hq + (long long)h * p.group) * p.Lq + r0;
-        const char* q = reinterpret_cast<const char*>(p.q + row0 * D);
-        if (lane * 128 < min(C::ROWS, p.R - r0) * D * 2) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + lane * 128));
+    // Raw Q of a part: lane (g, t4) holds dimensions t4 D/4 ... of rows g, 8 + g
+    // of the warp's item.  Those of the block's first part are asked for before
+    // its tiles, whose loads fill the memory's queues for microseconds.
+    uint32_t qraw[NT][KS * 2];
+    auto load_q = [&](const Seg& x) {
+        const int item = min(seg_item(x, warp), sp.items - 1);  // a group's last warps may have none
+        const int2 hc = head_and_chunk(item, p.c.Hkv);
+        const int r0 = hc.y * C::ROWS;
+        const long long row0 = ((long long)x.b * p.Hq + (long long)hc.x * p.group) * p.Lq + r0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = 8 * nt + g, r = MODE == 0 ? (col & 3) : col;
+            const bool on = r0 + r < p.R;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D + t4 * (D / 4));
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) {
+                const uint4 v = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                qraw[nt][4 * i] = v.x, qraw[nt][4 * i + 1] = v.y, qraw[nt][4 * i + 2] = v.z, qraw[nt][4 * i + 3] = v.w;
+            }
+        }
     };
-    if (warp == 0) prefetch_q(seg.b, seg.hc);
+    load_q(seg);
 
     // ---- the warp's loads, running ahead of its tiles: lane i holds where the
-    // warp's i-th tile from `ld` on lies and copies it when its turn comes
-    Walk ld = seg;
-    int ld_left = left;  // > 0: a tile to load
-    walk_on<D>(p, ld, warp, items, ld_left);
+    // warp's i-th tile from (ld, ld_k) on lies and copies it when its turn comes
+    Seg ld = seg;
+    int ld_k = 0;
+    bool more = true;  // there may be tiles from there on
     const int shift = p.c.page_shift, units = 1 << (shift - 4);
     const int span = min(1 << shift, TILE);  // keys of a tile in one page
     const uint32_t head_bytes = (uint32_t)units * C::UNIT;
@@ -333,12 +430,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     int my_page[NU], my_units = 0;
     uint32_t my_off = 0, turn = 0;  // turn: lanes that have a tile to copy
     auto refill = [&]() {
-        Walk w = ld;
-        int w_left = ld_left;
-        walk_on<D>(p, w, kWarps * lane, items, w_left);
-        const int key0 = w.t * TILE;
-        my_units = w_left > 0 ? min(NU, (w.len - key0 + 15) >> 4) : 0;  // 0 without keys
-        my_off = (uint32_t)(w.hc / chunks) * head_bytes + ((key0 >> 4) & (units - 1)) * C::UNIT;
+        Seg w = ld;
+        int k = ld_k + lane;
+        bool ok = true;
+        for (int c; ok && k >= (c = seg_tiles(sp, w, warp));) {
+            k -= c;
+            ok = seg_next<D>(p, sp, w);
+        }
+        const int key0 = seg_tile(w, warp, k) * TILE;
+        my_units = ok ? min(NU, (w.len - key0 + 15) >> 4) : 0;
+        my_off = (uint32_t)head_and_chunk(seg_item(w, warp), p.c.Hkv).x * head_bytes + ((key0 >> 4) & (units - 1)) * C::UNIT;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
             my_page[i] = 0;
@@ -350,19 +451,25 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 }
             }
         }
-        turn = __ballot_sync(~0u, my_units > 0);
-        // the next batch begins one step behind lane 31's tile
-        ld.b = __shfl_sync(~0u, w.b, 31);
-        ld.hc = __shfl_sync(~0u, w.hc, 31);
-        ld.t = __shfl_sync(~0u, w.t, 31);
-        ld.nt = __shfl_sync(~0u, w.nt, 31);
-        ld.len = __shfl_sync(~0u, w.len, 31);
-        ld.row = reinterpret_cast<const int*>(__shfl_sync(~0u, reinterpret_cast<long long>(w.row), 31));
-        ld_left = __shfl_sync(~0u, w_left, 31);
-        walk_on<D>(p, ld, kWarps, items, ld_left);
+        turn = __ballot_sync(~0u, ok);
+        more = __shfl_sync(~0u, ok, 31);
+        if (more) {  // the next batch begins behind lane 31's tile
+            ld.b = __shfl_sync(~0u, w.b, 31);
+            ld.e = __shfl_sync(~0u, w.e, 31);
+            ld.t = __shfl_sync(~0u, w.t, 31);
+            ld.n = __shfl_sync(~0u, w.n, 31);
+            ld.left = __shfl_sync(~0u, w.left, 31);
+            ld.len = __shfl_sync(~0u, w.len, 31);
+            ld.nt = __shfl_sync(~0u, w.nt, 31);
+            ld.entries = __shfl_sync(~0u, w.entries, 31);
+            ld.solo = __shfl_sync(~0u, w.solo, 31);
+            ld.row = reinterpret_cast<const int*>(__shfl_sync(~0u, reinterpret_cast<long long>(w.row), 31));
+            ld_k = __shfl_sync(~0u, k, 31) + 1;
+        }
     };
     int issued = 0;
     auto issue = [&]() {
+        if (turn == 0 && more) refill();
         if (turn == 0) return;
         if (lane == __ffs(turn) - 1 && !(p.fault == 1 && issued == 0)) {
             const int st = issued % C::STAGES;
@@ -383,48 +490,40 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         turn &= turn - 1;
         ++issued;
-        while (turn == 0 && ld_left > 0) refill();
     };
-    while (turn == 0 && ld_left > 0) refill();
+#pragma unroll 1
     for (int s = 0; s < C::STAGES; ++s) issue();
 
     // MODE 0: what a lane's columns take of hi, 0 (columns 0 .. 3) or -1
     const uint64_t part2 = t4 < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);
     int used = 0;      // stages consumed
-    int next = warp;   // the warp's next tile, counted from the block's first
-    int done = 0;      // tiles of the block before the segment in hand
+    auto leave = [&]() {  // waits ran out: let the copies in flight land
+        for (; used < issued; ++used)
+            if (!(p.fault == 1 && used == 0))
+                mbar_settle(bars + 8 * (used % C::STAGES), (used / C::STAGES) & 1, wf, 51);
+    };
     bool failed = false;
-    while (left > 0) {
-        const int n_seg = min(left, seg.nt - seg.t);
-        const int h = seg.hc / chunks, chunk = seg.hc - h * chunks;
-        const int r0 = chunk * C::ROWS, nrows = min(C::ROWS, p.R - r0);
+    for (bool again = true; again;) {
+        Seg behind = seg;  // the part after this one
+        again = seg_next<D>(p, sp, behind);
+        const int item = min(seg_item(seg, warp), sp.items - 1);  // a group's last warps may have none
+        const int2 hc = head_and_chunk(item, p.c.Hkv);
+        const int h = hc.x, r0 = hc.y * C::ROWS, nrows = min(C::ROWS, p.R - r0);
         const long long row0 = ((long long)seg.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
         const int len = seg.len;
         // keys every row may see; behind them scores are masked one by one
         const int all_see = p.causal ? len - p.Lq + 1 : len;
 
-        // Q fragments: lane (g, t4) holds dimensions t4 D/4 ... of rows g, 8 + g
+        // Q fragments
         uint32_t qf[MODE == 2 ? 1 : NT * KS * 2];
         float sc[NT][2];
         int lim[NT][2];
         float m[NT][2], l[NT][2], acc[NT][KS][4];
-        const uint32_t qbuf = base + C::RING + C::OBUF;
+        const uint32_t qbuf = base + C::RING + warp * (8 * C::OSTRIDE * 4);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int col = 8 * nt + g, r = MODE == 0 ? (col & 3) : col;
-            uint32_t x[KS * 2];
+            uint32_t(&x)[KS * 2] = qraw[nt];
             uint32_t top = 0;
-            if (r < nrows) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + r) * D + t4 * (D / 4));
-#pragma unroll
-                for (int i = 0; i < KS / 2; ++i) {
-                    const uint4 v = __ldg(src + i);
-                    x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < KS * 2; ++i) x[i] = 0;
-            }
 #pragma unroll
             for (int i = 0; i < KS * 2; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
             top = max(top & 0xffffu, top >> 16);
@@ -441,21 +540,19 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 else
                     qf[nt * KS * 2 + i] = f;
             }
-            if constexpr (MODE == 2) {  // every warp holds the same fragments: the first writes them
-                if (warp == 0) {
+            if constexpr (MODE == 2) {  // each lane reads back what it wrote
 #pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qbuf + ((nt * KS + i) * 32 + lane) * 8),
-                                     "r"(x[2 * i]), "r"(x[2 * i + 1])
-                                     : "memory");
-                }
+                for (int i = 0; i < KS; ++i)
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qbuf + ((nt * KS + i) * 32 + lane) * 8),
+                                 "r"(x[2 * i]), "r"(x[2 * i + 1])
+                                 : "memory");
             }
             const float s = p.scale * 1.4426950408889634f * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
                 const int cc = 8 * nt + 2 * t4 + c, rr = r0 + (MODE == 0 ? (cc & 3) : cc);
-                lim[nt][c] = p.causal ? rr % p.Lq + all_see : len;
+                lim[nt][c] = p.causal ? (p.Lq == 1 ? 0 : rr % p.Lq) + all_see : len;
                 m[nt][c] = -FLT_MAX;
                 l[nt][c] = 0.f;
             }
@@ -464,14 +561,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
         }
-        if constexpr (MODE == 2) __syncthreads();
-        if (warp == 0 && left > n_seg) {
-            const bool same = seg.hc + 1 < items;
-            if (same || seg.b + 1 < p.B) prefetch_q(same ? seg.b : seg.b + 1, same ? seg.hc + 1 : 0);
-        }
-
-        for (; next < done + n_seg && len > 0; next += kWarps) {
-            const int tile0 = (seg.t + next - done) * TILE;
+        const int count = failed ? 0 : seg_tiles(sp, seg, warp);
+        for (int k = 0; k < count; ++k) {
+            const int tile0 = seg_tile(seg, warp, k) * TILE;
             const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;
             if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
                 failed = true;
@@ -667,13 +759,39 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             ++used;
             issue();
         }
-        if (len == 0)
-            while (next < done + n_seg) next += kWarps;
-
-        // ---- join the warps
-        const bool whole = seg.t == 0 && n_seg == seg.nt;
-        const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
         const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
+        if (seg.solo) {  // ---- the warp's own item: straight to the output
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x = l[nt][c];
+                    x += __shfl_xor_sync(~0u, x, 4);
+                    x += __shfl_xor_sync(~0u, x, 8);
+                    x += __shfl_xor_sync(~0u, x, 16);
+                    const int r = 8 * nt + 2 * t4 + c;
+                    const bool on = r < nrows && seg_item(seg, warp) < sp.items;
+                    const float inv = x == 0.f ? 0.f : gv / x;
+                    float* dst = p.o + (row0 + r) * D + (D / 8) * g;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        float y = acc[nt][i][c], z = acc[nt][i][c + 2];
+                        if constexpr (MODE == 0) {  // hi's share and lo's
+                            y += __shfl_xor_sync(~0u, y, 2);
+                            z += __shfl_xor_sync(~0u, z, 2);
+                        }
+                        if (on) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(y * inv, z * inv);
+                    }
+                    if (on && g == 0)
+                        p.lse[row0 + r] = x == 0.f ? -INFINITY : (m[nt][c] + log2f(x)) * 0.6931471805599453f;
+                }
+            seg = behind;
+            if (again) load_q(seg);
+            continue;
+        }
+        // ---- join the warps
+        const bool whole = seg.t == 0 && seg.n == seg.nt;
+        const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -694,13 +812,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 }
             }
             if (__syncthreads_or(failed)) {
-                // waits ran out: let the copies in flight land, then leave
-                for (; used < issued; ++used)
-                    if (!(p.fault == 1 && used == 0))
-                        mbar_settle(bars + 8 * (used % C::STAGES), (used / C::STAGES) & 1, wf, 51);
+                leave();
                 return;
             }
             const int cols = MODE == 0 ? 4 : 8;
+#pragma unroll 1
             for (int x = tid; x < cols * D; x += kThreads) {
                 const int col = x / D, d = x % D, r = 8 * nt + col;
                 if (r >= nrows) break;
@@ -729,21 +845,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             __syncthreads();
         }
         if (tid == 0 && seg.t == 0 && !whole) {
-            const long long end = last - left + seg.nt;  // of the item in the list
-            parts.join[blockIdx.x] = make_int4(seg.b, seg.hc, (int)((end - 1) / share), 1);
+            parts.join[blockIdx.x] = Cut{seg.b, item, last - seg.left + seg.nt, share};
         }
-        left -= n_seg;
-        done += n_seg;
-        if (left > 0) {
-            seg.t = 0;
-            left -= kItemCost;
-            if (++seg.hc == items) {
-                seg.hc = 0;
-                ++seg.b;
-                walk_sequence<D>(p, seg);
-            }
-        }
+        seg = behind;
+        if (again) load_q(seg);
     }
+    if (failed) leave();
 }
 
 // Joins the parts of the item that begins in block blockIdx.x and ends in a
@@ -760,14 +867,15 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
     __shared__ float2 s_ml[kJoinRows][kJoinWarps];
     const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
     wait_for_primary();
-    const int4 j = parts.join[blockIdx.x];
-    if (j.w == 0) return;
+    const Cut j = parts.join[blockIdx.x];
+    if (j.item < 0) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = j.y / chunks, first = blockIdx.y * kJoinRows;  // of the item's rows
-    const int r0 = (j.y - h * chunks) * ROWS + first, nrows = min(kJoinRows, min(ROWS - first, p.R - r0));
+    const int2 hc = head_and_chunk(j.item, p.c.Hkv);
+    const int h = hc.x, first = blockIdx.y * kJoinRows;  // of the item's rows
+    const int r0 = hc.y * ROWS + first, nrows = min(kJoinRows, min(ROWS - first, p.R - r0));
     if (nrows <= 0) return;
-    const long long row0 = ((long long)j.x * p.Hq + (long long)h * p.group) * p.Lq + r0;
-    const int n = j.z - (int)blockIdx.x + 1;
+    const long long row0 = ((long long)j.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
+    const int n = (int)((j.end - 1) / j.share) - (int)blockIdx.x + 1;
     const int r = warp / kJoinWarps, w = warp % kJoinWarps;
     float acc[V] = {}, sum = 0.f, mm = -FLT_MAX;
     if (r < nrows) {
@@ -850,7 +958,7 @@ int blocks_of(int num_sms) { return 2 * num_sms; }
 cudaError_t kv4_attn_workspace(int D, int R, int, int num_sms, size_t* bytes)
 {
     const size_t blocks = (size_t)blocks_of(num_sms), rows = blocks * 2 * (4u << mode_of(R));
-    *bytes = blocks * sizeof(int4) + rows * sizeof(float2) + rows * D * sizeof(float);
+    *bytes = blocks * sizeof(Cut) + rows * sizeof(float2) + rows * D * sizeof(float);
     return cudaSuccess;
 }
 
