@@ -197,6 +197,12 @@ struct Cut {
     long long end, share;
 };
 
+__device__ __forceinline__ uint32_t without_nan(uint32_t s)
+{
+    const uint32_t n = nan_halves(s);
+    return (n & 1 ? 0u : s & 0xffffu) | (n & 2 ? 0u : s & 0xffff0000u);
+}
+
 // Where the kernels keep what they share in the workspace.
 struct Parts {
     float* o;   // [blocks][2][ROWS][D]
@@ -279,6 +285,7 @@ __device__ __forceinline__ bool seg_next(const Kv4AttnParams& p, const Split& sp
 __device__ __forceinline__ int2 head_and_chunk(int item, int Hkv)
 {
     int chunk = 0;
+#pragma unroll 1
     for (; item >= Hkv; item -= Hkv) ++chunk;
     return make_int2(item, chunk);
 }
@@ -339,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     };
     const int nt0 = run0 < run1 ? tiles(run0) : 0;  // of the run's first; most have no other
     long long mine = nt0;
+#pragma unroll 1
     for (int b = run0 + 1; b < run1; ++b) mine += tiles(b);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
@@ -351,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     sp.limit = (int)fminf(fmaxf(1.25f * per_block * (float)total * (float)sp.items, 2.f * kWarps), 1e9f);
     __syncthreads();
     mine = run0 < run1 ? sp.cost(nt0) : 0;
+#pragma unroll 1
     for (int b = run0 + 1; b < run1; ++b) mine += sp.cost(tiles(b));
     long long upto = mine;
 #pragma unroll
@@ -378,9 +387,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         long long at = upto - mine;
         Seg s;
         s.b = run0;
+#pragma unroll 1
         for (long long x; at + (x = sp.cost(s.b == run0 ? nt0 : tiles(s.b))) <= first; ++s.b) at += x;
         seg_open<D>(p, sp, s);
         const int ahead = sp.ahead(s.solo, s.nt), one = ahead + sp.body(s.solo, s.nt);
+#pragma unroll 1
         for (s.e = 0; at + one <= first; at += one) ++s.e;
         s.left = (int)(last - first);
         s.t = (int)(first - at) - ahead;
@@ -433,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         Seg w = ld;
         int k = ld_k + lane;
         bool ok = true;
+#pragma unroll 1
         for (int c; ok && k >= (c = seg_tiles(sp, w, warp));) {
             k -= c;
             ok = seg_next<D>(p, sp, w);
@@ -491,9 +503,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         turn &= turn - 1;
         ++issued;
     };
-#pragma unroll 1
-    for (int s = 0; s < C::STAGES; ++s) issue();
-
     // MODE 0: what a lane's columns take of hi, 0 (columns 0 .. 3) or -1
     const uint64_t part2 = t4 < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);
     int used = 0;      // stages consumed
@@ -502,24 +511,23 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             if (!(p.fault == 1 && used == 0))
                 mbar_settle(bars + 8 * (used % C::STAGES), (used / C::STAGES) & 1, wf, 51);
     };
+    uint32_t qf[MODE == 2 ? 1 : NT * KS * 2];  // fragments of Q
+    float sc[NT][2];
+    int lim[NT][2];
+    float m[NT][2], l[NT][2], acc[NT][KS][4];
+    const uint32_t qbuf = base + C::RING + warp * (8 * C::OSTRIDE * 4);
     bool failed = false;
-    for (bool again = true; again;) {
-        Seg behind = seg;  // the part after this one
-        again = seg_next<D>(p, sp, behind);
+    // One loop over the beginning of each part, the warp's tiles in it and its
+    // end, so that the code of the copies, which is long, exists once.
+    for (int k = 0, count = -1;;) {
+        while (issued < used + C::STAGES && (turn != 0 || more)) issue();
         const int item = min(seg_item(seg, warp), sp.items - 1);  // a group's last warps may have none
         const int2 hc = head_and_chunk(item, p.c.Hkv);
-        const int h = hc.x, r0 = hc.y * C::ROWS, nrows = min(C::ROWS, p.R - r0);
-        const long long row0 = ((long long)seg.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
+        const int h = hc.x, r0 = hc.y * C::ROWS;
         const int len = seg.len;
         // keys every row may see; behind them scores are masked one by one
         const int all_see = p.causal ? len - p.Lq + 1 : len;
-
-        // Q fragments
-        uint32_t qf[MODE == 2 ? 1 : NT * KS * 2];
-        float sc[NT][2];
-        int lim[NT][2];
-        float m[NT][2], l[NT][2], acc[NT][KS][4];
-        const uint32_t qbuf = base + C::RING + warp * (8 * C::OSTRIDE * 4);
+        if (count < 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             uint32_t(&x)[KS * 2] = qraw[nt];
@@ -561,13 +569,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
         }
-        const int count = failed ? 0 : seg_tiles(sp, seg, warp);
-        for (int k = 0; k < count; ++k) {
+            k = 0;
+            count = failed ? 0 : seg_tiles(sp, seg, warp);
+        }
+        if (k < count) {
             const int tile0 = seg_tile(seg, warp, k) * TILE;
             const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;
             if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
                 failed = true;
-                break;
+                count = k;
+                continue;
             }
 #pragma unroll 1
             for (int v0 = 0; v0 < NU; v0 += UG) {
@@ -647,24 +658,34 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                         if (k + 1 >= len) x &= 0xffffu;
                         if (k + 8 >= len) y = 0;
                         if (k + 9 >= len) y &= 0xffffu;
-                        // A NaN scale reaches only the rows that see its key: it is
-                        // taken out of the product and put into their sums.
-                        const uint32_t nx = nan_halves(x), ny = nan_halves(y);
-                        if (__any_sync(~0u, nx | ny)) {
-                            x = (nx & 1 ? 0u : x & 0xffffu) | (nx & 2 ? 0u : x & 0xffff0000u);
-                            y = (ny & 1 ? 0u : y & 0xffffu) | (ny & 2 ? 0u : y & 0xffff0000u);
+                    }
+                    // A NaN scale reaches only the rows that see its key: it is
+                    // taken out of the product and put into their sums.
+                    uint32_t nans = 0;
+#pragma unroll
+                    for (int u = 0; u < UG; ++u) nans |= nan_halves(va_s[u]) | nan_halves(vb_s[u]);
+                    if (__any_sync(~0u, nans)) {
+                        bool hit[NT][2] = {};
+#pragma unroll
+                        for (int u = 0; u < UG; ++u) {
+                            va_s[u] = without_nan(va_s[u]);
+                            vb_s[u] = without_nan(vb_s[u]);
+#pragma unroll 1
                             for (int j = 0; j < 16; ++j) {
                                 if ((lds_u8(tile + u * C::UNIT + 17 * D + grp * 16 + j) & 0x7f) != 0x7f) continue;
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c)
-                                        if (key0 + 16 * u + j < min(lim[nt][c], len)) {
-#pragma unroll
-                                            for (int i = 0; i < KS; ++i) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
-                                        }
+                                    for (int c = 0; c < 2; ++c) hit[nt][c] |= key0 + 16 * u + j < min(lim[nt][c], len);
                             }
                         }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int i = 0; i < KS; ++i)
+                                    if (hit[nt][c]) acc[nt][i][c] = acc[nt][i][c + 2] = NAN;
                     }
                 }
                 bool raise = false;
@@ -757,8 +778,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             }
             __syncwarp();  // the stage has been read
             ++used;
-            issue();
+            ++k;
+            continue;
         }
+        const int nrows = min(C::ROWS, p.R - r0);
+        const long long row0 = ((long long)seg.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
         const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
         if (seg.solo) {  // ---- the warp's own item: straight to the output
 #pragma unroll
@@ -771,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     x += __shfl_xor_sync(~0u, x, 16);
                     const int r = 8 * nt + 2 * t4 + c;
                     const bool on = r < nrows && seg_item(seg, warp) < sp.items;
-                    const float inv = x == 0.f ? 0.f : gv / x;
+                    const float inv = x == 0.f ? 0.f : __fdividef(gv, x);
                     float* dst = p.o + (row0 + r) * D + (D / 8) * g;
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
@@ -783,72 +807,70 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                         if (on) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(y * inv, z * inv);
                     }
                     if (on && g == 0)
-                        p.lse[row0 + r] = x == 0.f ? -INFINITY : (m[nt][c] + log2f(x)) * 0.6931471805599453f;
+                        p.lse[row0 + r] = x == 0.f ? -INFINITY : (m[nt][c] + __log2f(x)) * 0.6931471805599453f;
                 }
-            seg = behind;
-            if (again) load_q(seg);
-            continue;
-        }
-        // ---- join the warps
-        const bool whole = seg.t == 0 && seg.n == seg.nt;
-        const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
+        } else {  // ---- join the warps
+            const bool whole = seg.t == 0 && seg.n == seg.nt;
+            const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x = l[nt][c];
-                x += __shfl_xor_sync(~0u, x, 4);
-                x += __shfl_xor_sync(~0u, x, 8);
-                x += __shfl_xor_sync(~0u, x, 16);
-                const int col = 8 * nt + 2 * t4 + c;
-                if (g == 0 && col < C::ROWS) mlbuf[warp * C::ROWS + col] = make_float2(m[nt][c], x);
-                // the buffer holds column `col`, dimension d at a place that
-                // spreads a store's lanes over the banks
-                float* dst = obuf + (warp * 8 + 2 * t4 + c) * C::OSTRIDE;
+                for (int c = 0; c < 2; ++c) {
+                    float x = l[nt][c];
+                    x += __shfl_xor_sync(~0u, x, 4);
+                    x += __shfl_xor_sync(~0u, x, 8);
+                    x += __shfl_xor_sync(~0u, x, 16);
+                    const int col = 8 * nt + 2 * t4 + c;
+                    if (g == 0 && col < C::ROWS) mlbuf[warp * C::ROWS + col] = make_float2(m[nt][c], x);
+                    // the buffer holds column `col`, dimension d at a place that
+                    // spreads a store's lanes over the banks
+                    float* dst = obuf + (warp * 8 + 2 * t4 + c) * C::OSTRIDE;
 #pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const int at = D == 128 ? 16 * g + ((2 * i + 2 * g) & 15) : 8 * g + 2 * i;
-                    *reinterpret_cast<float2*>(dst + at) = make_float2(acc[nt][i][c], acc[nt][i][c + 2]);
+                    for (int i = 0; i < KS; ++i) {
+                        const int at = D == 128 ? 16 * g + ((2 * i + 2 * g) & 15) : 8 * g + 2 * i;
+                        *reinterpret_cast<float2*>(dst + at) = make_float2(acc[nt][i][c], acc[nt][i][c + 2]);
+                    }
                 }
-            }
-            if (__syncthreads_or(failed)) {
-                leave();
-                return;
-            }
-            const int cols = MODE == 0 ? 4 : 8;
+                if (__syncthreads_or(failed)) {
+                    leave();
+                    return;
+                }
+                const int cols = MODE == 0 ? 4 : 8;
 #pragma unroll 1
-            for (int x = tid; x < cols * D; x += kThreads) {
-                const int col = x / D, d = x % D, r = 8 * nt + col;
-                if (r >= nrows) break;
-                const int at = D == 128 ? (d & ~15) | ((d + 2 * (d >> 4)) & 15) : d;
-                float mm = -FLT_MAX;
+                for (int x = tid; x < cols * D; x += kThreads) {
+                    const int col = x / D, d = x % D, r = 8 * nt + col;
+                    if (r >= nrows) break;
+                    const int at = D == 128 ? (d & ~15) | ((d + 2 * (d >> 4)) & 15) : d;
+                    float mm = -FLT_MAX;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[w * C::ROWS + r].x);
-                float o = 0.f, sum = 0.f;
+                    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, mlbuf[w * C::ROWS + r].x);
+                    float o = 0.f, sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float2 ml = mlbuf[w * C::ROWS + r];
-                    const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
-                    float v = obuf[(w * 8 + col) * C::OSTRIDE + at];
-                    if constexpr (MODE == 0) v += obuf[(w * 8 + col + 4) * C::OSTRIDE + at];
-                    o = fmaf(a, v, o);
-                    sum = fmaf(a, ml.y, sum);
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float2 ml = mlbuf[w * C::ROWS + r];
+                        const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
+                        float v = obuf[(w * 8 + col) * C::OSTRIDE + at];
+                        if constexpr (MODE == 0) v += obuf[(w * 8 + col + 4) * C::OSTRIDE + at];
+                        o = fmaf(a, v, o);
+                        sum = fmaf(a, ml.y, sum);
+                    }
+                    if (whole) {
+                        p.o[(row0 + r) * D + d] = sum == 0.f ? 0.f : o * __fdividef(gv, sum);
+                        if (d == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (mm + __log2f(sum)) * 0.6931471805599453f;
+                    } else {
+                        parts.o[((long long)part * C::ROWS + r) * D + d] = o;
+                        if (d == 0) parts.ml[(long long)part * C::ROWS + r] = make_float2(mm, sum);
+                    }
                 }
-                if (whole) {
-                    p.o[(row0 + r) * D + d] = sum == 0.f ? 0.f : o / sum * gv;
-                    if (d == 0) p.lse[row0 + r] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * 0.6931471805599453f;
-                } else {
-                    parts.o[((long long)part * C::ROWS + r) * D + d] = o;
-                    if (d == 0) parts.ml[(long long)part * C::ROWS + r] = make_float2(mm, sum);
-                }
+                __syncthreads();
             }
-            __syncthreads();
+            if (tid == 0 && seg.t == 0 && !whole) {
+                parts.join[blockIdx.x] = Cut{seg.b, item, last - seg.left + seg.nt, share};
+            }
         }
-        if (tid == 0 && seg.t == 0 && !whole) {
-            parts.join[blockIdx.x] = Cut{seg.b, item, last - seg.left + seg.nt, share};
-        }
-        seg = behind;
-        if (again) load_q(seg);
+        if (!seg_next<D>(p, sp, seg)) break;
+        load_q(seg);
+        count = -1;
     }
     if (failed) leave();
 }
@@ -929,8 +951,8 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4Attn
             o = fmaf(a, s_o[rr][i][d], o);
             l = fmaf(a, ml.y, l);
         }
-        p.o[(row0 + rr) * D + d] = l == 0.f ? 0.f : o / l * gv;
-        if (d == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+        p.o[(row0 + rr) * D + d] = l == 0.f ? 0.f : o * __fdividef(gv, l);
+        if (d == 0) p.lse[row0 + rr] = l == 0.f ? -INFINITY : (top + __log2f(l)) * 0.6931471805599453f;
     }
 }
 
