@@ -623,6 +623,34 @@ def test_captured_decode_step_follows_the_cache():
     fa.fa_check()
 
 
+def test_calls_of_several_threads_at_once():
+    """Threads that share a stream, whose launches may interleave, and one with its own."""
+    import threading
+    rng = np.random.default_rng(14)
+    lens = [3000, 10, 700]
+    pool, table = random_cache(rng, lens, 2, 64, 64)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32(lens))
+    qs = [bf16(rng.standard_normal((3, 8, 1, 64))).to(DEV) for _ in range(4)]
+    want = [fa.fa_fwd_kv4(q, *dev, causal=True) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.current_stream()] * 3 + [torch.cuda.Stream()]
+    got = [[] for _ in qs]
+
+    def work(i):
+        with torch.cuda.stream(streams[i]):
+            for _ in range(50):
+                got[i].append(fa.fa_fwd_kv4(qs[i], *dev, causal=True))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert len(g) == 50 and all(torch.equal(o, w[0]) and torch.equal(lse, w[1]) for o, lse in g)
+
+
 def test_a_load_that_never_arrives_ends_the_call_with_a_timeout():
     rng = np.random.default_rng(12)
     pool, table = random_cache(rng, [500, 40], 2, 64, 32)
