@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     constexpr int NT = C::NT, KS = C::KS, NU = C::NU, UG = C::UG, TILE = tile_keys(D);
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long s_sum[kWarps];
-    __shared__ Seg s_seg;
+    // a warp's part in hand and the part of its next copies: looked at once in
+    // a while, and not to take registers from the tiles
+    __shared__ Seg s_seg, s_now[kWarps], s_ld[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t base = smem_u32(smem);
     const uint32_t ring = base + warp * (C::STAGES * C::STAGE);
@@ -403,8 +405,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         s_seg = s;
     }
     __syncthreads();
-    Seg seg = s_seg;  // in hand
-    if (seg.left <= 0) return;
+    if (s_seg.left <= 0) return;
+    if (lane == 0) s_now[warp] = s_ld[warp] = s_seg;
+    __syncwarp();
 
     // Raw Q of a part: lane (g, t4) holds dimensions t4 D/4 ... of rows g, 8 + g
     // of the warp's item.  Those of the block's first part are asked for before
@@ -427,11 +430,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             }
         }
     };
-    load_q(seg);
+    load_q(s_seg);
 
     // ---- the warp's loads, running ahead of its tiles: lane i holds where the
-    // warp's i-th tile from (ld, ld_k) on lies and copies it when its turn comes
-    Seg ld = seg;
+    // warp's i-th tile from (s_ld, ld_k) on lies and copies it when its turn comes
     int ld_k = 0;
     bool more = true;  // there may be tiles from there on
     const int shift = p.c.page_shift, units = 1 << (shift - 4);
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     int my_page[NU], my_units = 0;
     uint32_t my_off = 0, turn = 0;  // turn: lanes that have a tile to copy
     auto refill = [&]() {
-        Seg w = ld;
+        Seg w = s_ld[warp];
         int k = ld_k + lane;
         bool ok = true;
 #pragma unroll 1
@@ -465,19 +467,11 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         turn = __ballot_sync(~0u, ok);
         more = __shfl_sync(~0u, ok, 31);
-        if (more) {  // the next batch begins behind lane 31's tile
-            ld.b = __shfl_sync(~0u, w.b, 31);
-            ld.e = __shfl_sync(~0u, w.e, 31);
-            ld.t = __shfl_sync(~0u, w.t, 31);
-            ld.n = __shfl_sync(~0u, w.n, 31);
-            ld.left = __shfl_sync(~0u, w.left, 31);
-            ld.len = __shfl_sync(~0u, w.len, 31);
-            ld.nt = __shfl_sync(~0u, w.nt, 31);
-            ld.entries = __shfl_sync(~0u, w.entries, 31);
-            ld.solo = __shfl_sync(~0u, w.solo, 31);
-            ld.row = reinterpret_cast<const int*>(__shfl_sync(~0u, reinterpret_cast<long long>(w.row), 31));
-            ld_k = __shfl_sync(~0u, k, 31) + 1;
-        }
+        // the next batch begins behind lane 31's tile
+        ld_k = __shfl_sync(~0u, k, 31) + 1;
+        __syncwarp();
+        if (lane == 31) s_ld[warp] = w;
+        __syncwarp();
     };
     int issued = 0;
     auto issue = [&]() {
@@ -519,15 +513,19 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     bool failed = false;
     // One loop over the beginning of each part, the warp's tiles in it and its
     // end, so that the code of the copies, which is long, exists once.
-    for (int k = 0, count = -1;;) {
+    int len = 0, all_see = 0;   // all_see: keys every row may see; behind them scores are masked one by one
+    int key = 0, key_step = 0;  // first key of the warp's next tile, and from one to the next
+    for (int count = -1;;) {    // count: tiles left
         while (issued < used + C::STAGES && (turn != 0 || more)) issue();
-        const int item = min(seg_item(seg, warp), sp.items - 1);  // a group's last warps may have none
-        const int2 hc = head_and_chunk(item, p.c.Hkv);
-        const int h = hc.x, r0 = hc.y * C::ROWS;
-        const int len = seg.len;
-        // keys every row may see; behind them scores are masked one by one
-        const int all_see = p.causal ? len - p.Lq + 1 : len;
         if (count < 0) {
+            const Seg& seg = s_now[warp];
+            len = seg.len;
+            all_see = p.causal ? len - p.Lq + 1 : len;
+            key = seg_tile(seg, warp, 0) * TILE;
+            key_step = seg.solo ? TILE : kWarps * TILE;
+            count = failed ? 0 : seg_tiles(sp, seg, warp);
+            const int2 hc = head_and_chunk(min(seg_item(seg, warp), sp.items - 1), p.c.Hkv);
+            const int h = hc.x, r0 = hc.y * C::ROWS;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             uint32_t(&x)[KS * 2] = qraw[nt];
@@ -569,21 +567,18 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
                 for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
         }
-            k = 0;
-            count = failed ? 0 : seg_tiles(sp, seg, warp);
         }
-        if (k < count) {
-            const int tile0 = seg_tile(seg, warp, k) * TILE;
+        if (count > 0) {
             const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;
             if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
                 failed = true;
-                count = k;
+                count = 0;
                 continue;
             }
 #pragma unroll 1
             for (int v0 = 0; v0 < NU; v0 += UG) {
-                if (UG < NU && v0 > 0 && tile0 + 16 * v0 >= len) break;
-                const int key0 = tile0 + 16 * v0;
+                if (UG < NU && v0 > 0 && key + 16 * v0 >= len) break;
+                const int key0 = key + 16 * v0;
                 const uint32_t tile = stage + v0 * C::UNIT;
                 const bool border = key0 + 16 * UG > all_see;
 
@@ -778,10 +773,14 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             }
             __syncwarp();  // the stage has been read
             ++used;
-            ++k;
+            --count;
+            key += key_step;
             continue;
         }
-        const int nrows = min(C::ROWS, p.R - r0);
+        Seg seg = s_now[warp];
+        const int item = min(seg_item(seg, warp), sp.items - 1);  // a group's last warps may have none
+        const int2 hc = head_and_chunk(item, p.c.Hkv);
+        const int h = hc.x, r0 = hc.y * C::ROWS, nrows = min(C::ROWS, p.R - r0);
         const long long row0 = ((long long)seg.b * p.Hq + (long long)h * p.group) * p.Lq + r0;
         const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.f;
         if (seg.solo) {  // ---- the warp's own item: straight to the output
@@ -870,6 +869,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         if (!seg_next<D>(p, sp, seg)) break;
         load_q(seg);
+        __syncwarp();
+        if (lane == 0) s_now[warp] = seg;
+        __syncwarp();
         count = -1;
     }
     if (failed) leave();
@@ -962,7 +964,7 @@ template <int D, int MODE>
 cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
 {
     using C = Cfg<D, MODE>;
-    static_assert(2 * (C::SMEM + 1024 + 256) <= 233472, "two blocks per SM");
+    static_assert(2 * (C::SMEM + 1024 + 1024) <= 233472, "two blocks per SM");
     const cudaError_t e = smem_limit_once<fa_kv4_attn_kernel<D, MODE>>(C::SMEM);
     if (e != cudaSuccess) return e;
     const int chunks = (p.R + C::ROWS - 1) / C::ROWS;
