@@ -70,7 +70,8 @@ struct Cfg {
     static constexpr int RING = kWarps * STAGES * STAGE;
     static constexpr int OBUF = kWarps * 8 * OSTRIDE * 4;
     static constexpr int ML = kWarps * ROWS * 8;
-    static constexpr int BARS = RING + OBUF + ML;
+    static constexpr int DESC = kWarps * 32 * NU * 8;  // the copies to come
+    static constexpr int BARS = RING + OBUF + ML + DESC;
     // MODE 2 keeps a warp's fragments of Q in its part of the joining buffer
     static_assert(MODE != 2 || 32 * KS * NT * 8 <= 8 * OSTRIDE * 4, "Q fragments");
     static constexpr int SMEM = BARS + kWarps * STAGES * 8 + 64;
@@ -157,7 +158,7 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t a)
 
 __device__ __forceinline__ void prefetch_l2(const char* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar)
+__device__ __forceinline__ void bulk_load(uint32_t dst, uint64_t src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -436,12 +437,10 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     // warp's i-th tile from (s_ld, ld_k) on lies and copies it when its turn comes
     int ld_k = 0;
     bool more = true;  // there may be tiles from there on
-    const int shift = p.c.page_shift, units = 1 << (shift - 4);
-    const int span = min(1 << shift, TILE);  // keys of a tile in one page
-    const uint32_t head_bytes = (uint32_t)units * C::UNIT;
-    const long long page_bytes = (long long)p.c.Hkv * head_bytes;
-    int my_page[NU], my_units = 0;
-    uint32_t my_off = 0, turn = 0;  // turn: lanes that have a tile to copy
+    // sources of the lane's tile, one per page it lies in; the first with the
+    // number of its units in the low bits
+    uint64_t* desc = reinterpret_cast<uint64_t*>(smem + C::RING + C::OBUF + C::ML) + (warp * 32 + lane) * NU;
+    uint32_t turn = 0;  // lanes that have a tile to copy
     auto refill = [&]() {
         Seg w = s_ld[warp];
         int k = ld_k + lane;
@@ -451,18 +450,22 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             k -= c;
             ok = seg_next<D>(p, sp, w);
         }
-        const int key0 = seg_tile(w, warp, k) * TILE;
-        my_units = ok ? min(NU, (w.len - key0 + 15) >> 4) : 0;
-        my_off = (uint32_t)head_and_chunk(seg_item(w, warp), p.c.Hkv).x * head_bytes + ((key0 >> 4) & (units - 1)) * C::UNIT;
+        if (ok) {
+            const int shift = p.c.page_shift, units = 1 << (shift - 4);
+            const int key0 = seg_tile(w, warp, k) * TILE, n = min(NU, (w.len - key0 + 15) >> 4);
+            const uint32_t head_bytes = (uint32_t)units * C::UNIT;
+            const uint8_t* src = p.c.pool + (uint32_t)head_and_chunk(seg_item(w, warp), p.c.Hkv).x * head_bytes +
+                                 ((key0 >> 4) & (units - 1)) * C::UNIT;
 #pragma unroll
-        for (int i = 0; i < NU; ++i) {
-            my_page[i] = 0;
-            if (i * (span >> 4) < my_units) {
-                my_page[i] = w.row[(key0 >> shift) + i];
-                if ((unsigned)my_page[i] >= (unsigned)p.c.num_pages) {
+            for (int i = 0; i < NU; ++i) {
+                if (i * units >= n) break;
+                int page = w.row[(key0 >> shift) + i];
+                if ((unsigned)page >= (unsigned)p.c.num_pages) {
                     atomicOr(p.c.err, 2);
-                    my_page[i] = 0;
+                    page = 0;
                 }
+                const uint64_t from = reinterpret_cast<uint64_t>(src + page * ((long long)p.c.Hkv * head_bytes));
+                desc[i] = i == 0 ? from + n : from;
             }
         }
         turn = __ballot_sync(~0u, ok);
@@ -480,19 +483,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         if (lane == __ffs(turn) - 1 && !(p.fault == 1 && issued == 0)) {
             const int st = issued % C::STAGES;
             const uint32_t dst = ring + st * C::STAGE, bar = bars + 8 * st;
-            const uint8_t* src = p.c.pool + my_off;
-            mbar_arrive_expect_tx(bar, my_units * C::UNIT);
-            if (span == TILE) {
-                bulk_load(dst, src + my_page[0] * page_bytes, my_units * C::UNIT, bar);
-            } else {  // pages shorter than the tile: it starts at a page's first unit
+            const uint64_t from = desc[0];
+            const int n = (int)(from & 15), per = 1 << (p.c.page_shift - 4);
+            mbar_arrive_expect_tx(bar, n * C::UNIT);
+            bulk_load(dst, from & ~15ull, min(per, n) * C::UNIT, bar);
 #pragma unroll
-                for (int i = 0; i < NU; ++i) {
-                    const int u0 = i * (span >> 4);
-                    if (u0 < my_units)
-                        bulk_load(dst + u0 * C::UNIT, src + my_page[i] * page_bytes,
-                                  min(span >> 4, my_units - u0) * C::UNIT, bar);
-                }
-            }
+            for (int i = 1; i < NU; ++i)  // pages shorter than the tile
+                if (i * per < n) bulk_load(dst + i * per * C::UNIT, desc[i], min(per, n - i * per) * C::UNIT, bar);
         }
         turn &= turn - 1;
         ++issued;
@@ -507,7 +504,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     };
     uint32_t qf[MODE == 2 ? 1 : NT * KS * 2];  // fragments of Q
     float sc[NT][2];
-    int lim[NT][2];
     float m[NT][2], l[NT][2], acc[NT][KS][4];
     const uint32_t qbuf = base + C::RING + warp * (8 * C::OSTRIDE * 4);
     bool failed = false;
@@ -557,8 +553,6 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
-                const int cc = 8 * nt + 2 * t4 + c, rr = r0 + (MODE == 0 ? (cc & 3) : cc);
-                lim[nt][c] = p.causal ? (p.Lq == 1 ? 0 : rr % p.Lq) + all_see : len;
                 m[nt][c] = -FLT_MAX;
                 l[nt][c] = 0.f;
             }
@@ -637,6 +631,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 }
                 // ---- masks, the running maximum in log2 units
                 if (border) {
+                    int lim[NT][2];  // keys that the columns' rows see
+                    const int r0 = head_and_chunk(min(seg_item(s_now[warp], warp), sp.items - 1), p.c.Hkv).y * C::ROWS;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int col = 8 * nt + 2 * t4 + c, r = r0 + (MODE == 0 ? (col & 3) : col);
+                            lim[nt][c] = p.causal && p.Lq > 1 ? r % p.Lq + all_see : len;
+                        }
 #pragma unroll
                     for (int u = 0; u < UG; ++u)
 #pragma unroll
@@ -742,34 +745,50 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                         }
                     f2_unpack(l2, l[nt][0], l[nt][1]);
                 }
-                // ---- O^T += V^T P^T
+                // ---- O^T += V^T P^T.  The MMA adds to its accumulator without
+                // rounding to nearest, a bias that grows with the number of
+                // additions (9e-7 of O after 54 of them, 3e-7 so), so each
+                // group starts from 0 and is added here.
+                uint32_t va[UG][KS / 2], vb[UG][KS / 2];
 #pragma unroll
                 for (int u = 0; u < UG; ++u) {
                     const uint32_t unit = tile + u * C::UNIT;
-                    uint32_t va[KS / 2], vb[KS / 2];
                     if constexpr (D == 128) {
                         const uint4 a = lds16(unit + 8 * D + g * 64 + t4 * 16), b = lds16(unit + 12 * D + g * 64 + t4 * 16);
-                        va[0] = a.x, va[1] = a.y, va[2] = a.z, va[3] = a.w;
-                        vb[0] = b.x, vb[1] = b.y, vb[2] = b.z, vb[3] = b.w;
+                        va[u][0] = a.x, va[u][1] = a.y, va[u][2] = a.z, va[u][3] = a.w;
+                        vb[u][0] = b.x, vb[u][1] = b.y, vb[u][2] = b.z, vb[u][3] = b.w;
                     } else {
                         const uint32_t at = unit + 8 * D + grp * 64 + t4 * 16 + (g & 1) * 8;
                         const uint2 a = lds8(at), b = lds8(at + 4 * D);
-                        va[0] = a.x, va[1] = a.y;
-                        vb[0] = b.x, vb[1] = b.y;
+                        va[u][0] = a.x, va[u][1] = a.y;
+                        vb[u][0] = b.x, vb[u][1] = b.y;
                     }
-                    const uint32_t sa = va_s[u], sb = vb_s[u];
-                    auto step = [&](auto ii) {
-                        constexpr int i = decltype(ii)::value;
-                        const uint32_t a0 = hmul2(code_pair<2 * i>(va), sa), a1 = hmul2(code_pair<2 * i + 1>(va), sa);
-                        const uint32_t a2 = hmul2(code_pair<2 * i>(vb), sb), a3 = hmul2(code_pair<2 * i + 1>(vb), sb);
+                }
+                auto step = [&](auto ii) {
+                    constexpr int i = decltype(ii)::value;
+                    float part[NT][4];
+#pragma unroll
+                    for (int u = 0; u < UG; ++u) {
+                        const uint32_t sa = va_s[u], sb = vb_s[u];
+                        const uint32_t a0 = hmul2(code_pair<2 * i>(va[u]), sa), a1 = hmul2(code_pair<2 * i + 1>(va[u]), sa);
+                        const uint32_t a2 = hmul2(code_pair<2 * i>(vb[u]), sb), a3 = hmul2(code_pair<2 * i + 1>(vb[u]), sb);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
-                            if constexpr (MODE != 0) mma_f16(acc[nt][i], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
+                            if (u == 0)
+                                mma_f16_first(part[nt], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
+                            else
+                                mma_f16(part[nt], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
+                            if constexpr (MODE != 0) mma_f16(part[nt], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
                         }
-                    };
-                    for_steps(step, std::make_integer_sequence<int, KS>{});
-                }
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float(&o)[4] = acc[nt][i];
+                        f2_unpack(f2_add(f2_pack(o[0], o[1]), f2_pack(part[nt][0], part[nt][1])), o[0], o[1]);
+                        f2_unpack(f2_add(f2_pack(o[2], o[3]), f2_pack(part[nt][2], part[nt][3])), o[2], o[3]);
+                    }
+                };
+                for_steps(step, std::make_integer_sequence<int, KS>{});
             }
             __syncwarp();  // the stage has been read
             ++used;
