@@ -26,7 +26,6 @@ int32 [slots], refs int32 [pages]; layout in include/fa_gb300.h):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -46,7 +45,6 @@ __all__ = ["fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdim", "fa_f
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libfa_gb300.so")
 _lock = threading.Lock()
-_no_guard = contextlib.nullcontext()
 _lib = None
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(5)
@@ -709,6 +707,7 @@ def kv4_pool(num_pages: int, Hkv: int, page_size: int, D: int, layers: int | Non
 # each, so the checks below take their time only on the way to an error.
 
 _pack_kv4 = struct.Struct("6P6i").pack    # struct fa_kv4
+_KV4_UNITS, _KV4_PAGES = (18 * 64, 18 * 128), (1, 2, 4, 8, 16)  # bytes of a unit, units of a page
 _pack_pages = struct.Struct("4P7i").pack  # struct fa_kv4_pages
 
 
@@ -720,9 +719,12 @@ def _want(t, name, dtype, ndim, device):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-def _device_guard(index):
-    """The device's context, or nothing where it is current already."""
-    return _no_guard if torch.cuda.current_device() == index else torch.cuda.device(index)
+def _on_device(index, fn, *args):
+    """fn(*args) with the device current."""
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _raw_stream(stream, index):
@@ -739,17 +741,25 @@ def _check_slots(table, seq_lens, device):
 def _check_pool(pool, ndim):
     _check_tensor(pool, "pool", torch.uint8, ndim)
     U, unit = pool.shape[-2:]
-    if unit not in (18 * 64, 18 * 128) or U not in (1, 2, 4, 8, 16):
+    if unit not in _KV4_UNITS or U not in _KV4_PAGES:
         raise ValueError(f"pool must be uint8 [..., pages, Hkv, page_size / 16, 18 D], got {tuple(pool.shape)}")
 
 
 def _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, num_seqs):
     """Checks the cache of a call with num_seqs sequences.  Returns (fa_kv4_t as bytes, device index, Hkv, D)."""
-    _check_pool(pool, 4)
     device = pool.get_device()
-    _check_slots(table, seq_lens, device)
+    if not (pool.dtype is torch.uint8 and pool.dim() == 4 and pool.is_contiguous() and device >= 0
+            and table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous()
+            and table.get_device() == device and seq_lens.dtype is torch.int32 and seq_lens.dim() == 1
+            and seq_lens.is_contiguous() and seq_lens.get_device() == device):
+        _check_pool(pool, 4)
+        _check_slots(table, seq_lens, device)
     N, H, U, unit = pool.shape
     slots, width = table.shape
+    if unit not in _KV4_UNITS or U not in _KV4_PAGES:
+        _check_pool(pool, 4)
+    if seq_lens.shape[0] != slots:
+        _check_slots(table, seq_lens, device)
     ids = ks = vs = 0
     if seq_ids is not None:
         _want(seq_ids, "seq_ids", torch.int32, 1, device)
@@ -791,9 +801,8 @@ def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, po
     if k.shape != v.shape or k.shape[1:] != (H, D):
         raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {H} heads of {D}")
     lib = _lib or load_library()
-    with _device_guard(device):
-        st = lib.fa_kv4_append(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), n, k.shape[0], c,
-                               _raw_stream(stream, device))
+    st = _on_device(device, lib.fa_kv4_append, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), n, k.shape[0], c,
+                    _raw_stream(stream, device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_append")
 
@@ -822,9 +831,8 @@ def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table:
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"k_out and v_out must be {shape}, got {tuple(k_out.shape)} and {tuple(v_out.shape)}")
     lib = _lib or load_library()
-    with _device_guard(device):
-        st = lib.fa_kv4_read(k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), n, shape[0], c,
-                             _raw_stream(stream, device))
+    st = _on_device(device, lib.fa_kv4_read, k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), n, shape[0], c,
+                    _raw_stream(stream, device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_read")
     return k_out, v_out
@@ -848,7 +856,8 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     (Hq/Hkv)*Lq <= 64; sequence b is slot seq_ids[b] (default b) and attends its
     first seq_lens positions; with ``causal`` the queries are the last Lq of
     them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
-    _check_tensor(q, "q", torch.bfloat16, 4)
+    if not (q.dtype is torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.is_cuda):
+        _check_tensor(q, "q", torch.bfloat16, 4)
     B, Hq, Lq, D = q.shape
     c, device, H, cache_d = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, B)
     if D != cache_d:
@@ -868,16 +877,15 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     lib = _lib or load_library()
-    with _device_guard(device):
-        nbytes = _attn_workspace(device, Hq, H, Lq, D)
-        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        elif workspace.get_device() != device:
-            raise ValueError(f"workspace must be on {q.device}, got {workspace.device}")
-        st = lib.fa_fwd_kv4(q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq, 1 if causal else 0, softmax_scale,
-                            c, workspace.data_ptr(), nbytes, _raw_stream(stream, device))
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)  # keep the block out of reuse until that stream is done
+    nbytes = _attn_workspace(device, Hq, H, Lq, D)
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device:
+        raise ValueError(f"workspace must be on {q.device}, got {workspace.device}")
+    st = _on_device(device, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq,
+                    1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(stream, device))
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
+        workspace.record_stream(stream)  # keep the block out of reuse until that stream is done
     if st != FA_OK:
         raise FAError(st, "fa_fwd_kv4")
     return out, lse
@@ -885,8 +893,8 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
 
 @functools.lru_cache(maxsize=256)
 def _attn_workspace(device, Hq, Hkv, Lq, D):
-    """kv4_workspace on the current device, whose index is `device`."""
-    return kv4_workspace(1, Hq, Hkv, Lq, D)
+    """kv4_workspace on device `device`."""
+    return _on_device(device, kv4_workspace, 1, Hq, Hkv, Lq, D)
 
 
 @functools.lru_cache(maxsize=256)
@@ -918,25 +926,27 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
         pages = _pack_pages(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width,
                             16 * U, H, unit // 18, pool.shape[0] if pool.dim() == 5 else 1)
     lib = _lib or load_library()
-    with _device_guard(device):
-        if name == "fa_kv4_release":
-            st = lib.fa_kv4_release(first, n, pages, _raw_stream(stream, device))
+    if name == "fa_kv4_release":
+        st = _on_device(device, lib.fa_kv4_release, first, n, pages, _raw_stream(stream, device))
+    else:
+        nbytes = kv4_pages_workspace(N, n)
+        if info is None:
+            info = torch.empty(2, dtype=torch.int32, device=refs.device)
         else:
-            nbytes = kv4_pages_workspace(N, n)
-            if info is None:
-                info = torch.empty(2, dtype=torch.int32, device=refs.device)
-            else:
-                _want(info, "info", torch.int32, 1, device)
-                if info.shape[0] != 2:
-                    raise ValueError("info must hold 2 numbers")
-            if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
-            elif workspace.get_device() != device:
-                raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
-            tail = (pages, info.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(stream, device))
-            st = lib.fa_kv4_compact(*tail) if first is second is None else getattr(lib, name)(first, second, n, *tail)
-            if isinstance(stream, torch.cuda.Stream):
-                workspace.record_stream(stream)
+            _want(info, "info", torch.int32, 1, device)
+            if info.shape[0] != 2:
+                raise ValueError("info must hold 2 numbers")
+        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
+        elif workspace.get_device() != device:
+            raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
+        tail = (pages, info.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(stream, device))
+        if name == "fa_kv4_compact":
+            st = _on_device(device, lib.fa_kv4_compact, *tail)
+        else:
+            st = _on_device(device, getattr(lib, name), first, second, n, *tail)
+        if stream is not None and isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)
     if st != FA_OK:
         raise FAError(st, name)
     return info
