@@ -907,17 +907,33 @@ def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
     return nbytes.value
 
 
+def _slots_of(table, seq_lens, device):
+    """Shape of a call's table, after the checks of _check_slots."""
+    if not (table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous() and table.get_device() == device
+            and seq_lens.dtype is torch.int32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
+            and seq_lens.get_device() == device and seq_lens.shape[0] == table.shape[0]):
+        _check_slots(table, seq_lens, device)
+    return table.shape
+
+
+def _refs_device(refs):
+    if not (refs.dtype is torch.int32 and refs.dim() == 1 and refs.is_cuda and refs.is_contiguous()):
+        _check_tensor(refs, "refs", torch.int32, 1)
+    return refs.get_device()
+
+
 def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, info, workspace, stream, device):
     """Runs one page operation.  first, second: device addresses of its lists
     of n entries (None: the operation has no such list)."""
-    _check_slots(table, seq_lens, device)
-    slots, width = table.shape
+    slots, width = _slots_of(table, seq_lens, device)
     N = refs.shape[0]
     if pool is None:
         pages = _pack_pages(0, table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width, page_size, 1,
                             64, 1)
     else:
-        _check_pool(pool, 5 if pool.dim() == 5 else 4)
+        if not (pool.dtype is torch.uint8 and pool.dim() in (4, 5) and pool.is_contiguous()
+                and pool.shape[-1] in _KV4_UNITS and pool.shape[-2] in _KV4_PAGES):
+            _check_pool(pool, 5 if pool.dim() == 5 else 4)
         P, H, U, unit = pool.shape[-4:]
         if P != N:
             raise ValueError(f"pool has {P} pages and refs {N}")
@@ -959,8 +975,7 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
     count them in seq_lens.  Returns info, int32 [2] on the device: free pages
     left, and 0, or the pages that were missing (then nothing was changed), or
     -1 for bad arguments on the device."""
-    _check_tensor(refs, "refs", torch.int32, 1)
-    device = refs.get_device()
+    device = _refs_device(refs)
     _want(new_tokens, "new_tokens", torch.int32, 1, device)
     n = new_tokens.shape[0]
     if seq_ids is not None:
@@ -978,8 +993,7 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     """Make the empty slots children[i] copies of the slots parents[i]: full pages
     are shared, a partly filled last page is copied.  pool as for
     fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
-    _check_tensor(refs, "refs", torch.int32, 1)
-    device = refs.get_device()
+    device = _refs_device(refs)
     _want(parents, "parents", torch.int32, 1, device)
     _want(children, "children", torch.int32, 1, device)
     n = parents.shape[0]
@@ -992,8 +1006,7 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
 def fa_kv4_release(seq_ids: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
                    page_size: int, stream=None) -> None:
     """Free the slots seq_ids: their pages lose a reference each, their lengths become 0."""
-    _check_tensor(refs, "refs", torch.int32, 1)
-    device = refs.get_device()
+    device = _refs_device(refs)
     _want(seq_ids, "seq_ids", torch.int32, 1, device)
     _page_call("fa_kv4_release", None, page_size, table, seq_lens, refs, seq_ids.data_ptr(), None, seq_ids.shape[0],
                None, None, stream, device)
@@ -1003,9 +1016,8 @@ def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tens
                    info: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
-    _check_tensor(refs, "refs", torch.int32, 1)
     return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace, stream,
-                      refs.get_device())
+                      _refs_device(refs))
 
 
 def fa_check(stream=None) -> int:

@@ -8,8 +8,7 @@
 #include <algorithm>
 #include <climits>
 
-#include "fa_kv4.h"
-#include "ptx_sm103.cuh"
+#include "kv4_common.cuh"
 
 namespace fa {
 
@@ -227,6 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4P
 
 __global__ void __launch_bounds__(kPlanThreads) fa_kv4_fork_plan_kernel(const Kv4PageParams p)
 {
+    let_dependents_launch();
     __shared__ PlanSmem sm;
     const int tid = threadIdx.x, page_size = 1 << p.page_shift;
     int* moves = p.ws + kWsBase;
@@ -312,6 +312,7 @@ __device__ __forceinline__ void copy_moves(const Kv4PageParams& p, int count, co
 
 __global__ void __launch_bounds__(256) fa_kv4_fork_kernel(const Kv4PageParams p)
 {
+    wait_for_primary();
     if (!p.ws[kWsDone]) return;
     for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int s = p.ids[i], len = p.lens[s], full = len >> p.page_shift;
@@ -374,6 +375,7 @@ __global__ void __launch_bounds__(128) fa_kv4_release_kernel(const Kv4PageParams
 // workspace: header | map [num_pages] | sources | targets
 __global__ void __launch_bounds__(kPlanThreads) fa_kv4_compact_plan_kernel(const Kv4PageParams p)
 {
+    let_dependents_launch();
     __shared__ PlanSmem sm;
     const int tid = threadIdx.x, n = p.num_pages;
     int* map = p.ws + kWsBase;
@@ -412,6 +414,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_compact_plan_kernel(const
 
 __global__ void __launch_bounds__(256) fa_kv4_compact_kernel(const Kv4PageParams p)
 {
+    wait_for_primary();
     const int count = p.ws[kWsCount];
     if (!p.ws[kWsDone] || count == 0) return;
     const int live = p.ws[2];
@@ -453,8 +456,7 @@ cudaError_t launch_kv4_fork(const Kv4PageParams& p, int num_sms, cudaStream_t st
     if (e != cudaSuccess) return e;
     const long long warps = (long long)p.n * p.layers * p.Hkv;
     const int grid = (int)std::min(8ll * num_sms, std::max((long long)p.n, (warps + 7) / 8));
-    fa_kv4_fork_kernel<<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(fa_kv4_fork_kernel, dim3(grid), 256, stream, p);
 }
 
 cudaError_t launch_kv4_release(const Kv4PageParams& p, cudaStream_t stream)
@@ -470,8 +472,7 @@ cudaError_t launch_kv4_compact(const Kv4PageParams& p, int num_sms, cudaStream_t
     if (e != cudaSuccess) return e;
     const long long warps = (long long)(p.num_pages + 1) / 2 * p.layers * p.Hkv;
     const int grid = (int)std::min(8ll * num_sms, std::max((long long)p.num_slots, (warps + 7) / 8));
-    fa_kv4_compact_kernel<<<grid, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(fa_kv4_compact_kernel, dim3(grid), 256, stream, p);
 }
 
 }  // namespace fa
