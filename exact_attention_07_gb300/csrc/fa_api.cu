@@ -1314,7 +1314,8 @@ extern "C" fa_status_t fa_fwd_kv4_workspace(int B, int Hq, int Hkv, int Lq, int 
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != FA_OK) return st;
-    return kv4_attn_workspace(D, R, B * Hkv, ds->num_sms, workspace_bytes) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    *workspace_bytes = kv4_attn_workspace(D, R, ds->num_sms);
+    return FA_OK;
 }
 
 extern "C" fa_status_t fa_fwd_kv4(const void* q, float* o, float* lse, int B, int Hq, int Lq, int causal,
@@ -1333,9 +1334,8 @@ extern "C" fa_status_t fa_fwd_kv4(const void* q, float* o, float* lse, int B, in
     DeviceState* ds = nullptr;
     st = device_state(&ds);
     if (st != FA_OK) return st;
-    size_t need = 0;
-    if (kv4_attn_workspace(cache->D, p.R, B * cache->Hkv, ds->num_sms, &need) != cudaSuccess) return FA_ERR_CUDA;
-    if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return FA_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < kv4_attn_workspace(cache->D, p.R, ds->num_sms))
+        return FA_ERR_INVALID_ARG;
     p.q = static_cast<const uint16_t*>(q);
     p.o = o;
     p.lse = lse;

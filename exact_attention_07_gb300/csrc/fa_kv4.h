@@ -66,9 +66,9 @@ struct Kv4PageParams {
 cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv4_read(int D, const Kv4RowsParams& p, cudaStream_t stream);
 
-// Workspace bytes of the attention on the current device, and its launches
-// (*launches kernels).
-cudaError_t kv4_attn_workspace(int D, int R, int items, int num_sms, size_t* bytes);
+// Workspace bytes of the attention on a device with num_sms SMs, and its
+// launches (*launches kernels).
+size_t kv4_attn_workspace(int D, int R, int num_sms);
 cudaError_t launch_kv4_attn(int D, const Kv4AttnParams& p, int num_sms, cudaStream_t stream, int* launches);
 
 size_t kv4_pages_workspace(int num_pages, int n);

@@ -7,17 +7,17 @@
 // Bound: the cache's bytes are read once, 18 D / 16 per (key, KV head).  At
 // 6.8 TB/s that is 23 bytes, 41 values, per clock and SM, so the arithmetic
 // between HBM and the tensor cores decides: a value costs half a conversion
-// (e2m1x2 -> f16x2, 64 lanes a clock and SM), half a product with its scale
-// (64 a clock) and its share of an MMA.  Staging dequantised tiles in shared
-// memory for tcgen05 would add 2 bytes written and 2 read per value, 164
+// (e2m1x2 -> f16x2, measured 64 lanes a clock and SM), half a product with its
+// scale (64 a clock) and its share of an MMA.  Staging dequantised tiles in
+// shared memory for tcgen05 would write and read 2 bytes per value more, 164
 // bytes a clock and SM where shared memory gives 128; so the codes go from
 // shared memory straight into the registers that are the operand fragments
-// of mma.sync (1024 multiply-adds a clock and SM, 330 to 660 needed), and the
-// cache's layout is the one in which each lane's fragments are 16 contiguous
-// bytes:
+// of mma.sync (measured 1024 multiply-adds a clock and SM; 330 needed with up
+// to 4 rows, 490 with up to 8), and the cache's layout is the one in which
+// each lane's fragments are contiguous:
 //
 //   S^T [16 keys x 8 rows] = K (A, from codes) Q^T (B, registers)
-//   O^T [16 dims x 8 rows] += V^T (A, from codes) P^T (B, S^T after the
+//   O^T [16 dims x 8 rows] += V^T (A, from codes) P^T (B: S^T after the
 //   exponential, turned by movmatrix)
 //
 // Codes times scales are exact in fp16 (2 + 4 significant bits, 2^-10 to
@@ -26,13 +26,20 @@
 // fp16 numbers, hi = fp16(p) and lo = fp16(p - hi): with up to 4 rows the two
 // fill the 8 columns of one MMA, with up to 8 they take two.
 //
-// Each warp streams tiles of 32 keys through a ring of its own with
+// Each warp streams tiles of 4608 bytes through a ring of its own with
 // cp.async.bulk (no block-wide step in the loop), keeps its own maximum, sum
 // and O^T, and raises the maximum only when a score exceeds it by 2^8, so
-// that the rescaling and its shuffles are rare.  The tiles of all (sequence,
-// KV head) items form one list, cut evenly over the blocks from the lengths
-// on the device; an item that lies in several blocks is joined by a second
-// kernel.
+// that the rescaling and its shuffles are rare.  The work of all sequences is
+// one list, cut evenly over the blocks (two an SM, 128 registers a thread)
+// from the lengths on the device; an item that lies in several blocks is
+// joined by a second kernel.
+//
+// Measured (device time): 8 sequences of 32768 keys, 32 x 8 heads, D = 128,
+// 60 us, 74 % of the copy bandwidth; a warp issues about 560
+// instructions a tile, 288 of them conversions, products and MMAs, and the
+// schedulers are 58 % busy: latencies between dependent instructions of the
+// four warps a scheduler has bound it, next to 7 us of beginning and joining.
+// 12 warps of 168 registers took 66 us.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -49,7 +56,7 @@ constexpr int kThreads = 32 * kWarps;
 // What beginning and joining an item costs a block, in tiles (the lists of
 // short sequences took 107 us where items counted only by their tiles), and
 // what beginning a group of items of one warp each does.
-constexpr int kItemCost = 16, kSoloCost = 8;
+constexpr int kItemCost = 24, kSoloCost = 16;
 constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
 
 // Keys of a warp's tile: 4608 bytes.
@@ -454,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             const int shift = p.c.page_shift, units = 1 << (shift - 4);
             const int key0 = seg_tile(w, warp, k) * TILE, n = min(NU, (w.len - key0 + 15) >> 4);
             const uint32_t head_bytes = (uint32_t)units * C::UNIT;
-            const uint8_t* src = p.c.pool + (uint32_t)head_and_chunk(seg_item(w, warp), p.c.Hkv).x * head_bytes +
+            const uint8_t* src = p.c.pool + (long long)head_and_chunk(seg_item(w, warp), p.c.Hkv).x * head_bytes +
                                  ((key0 >> 4) & (units - 1)) * C::UNIT;
 #pragma unroll
             for (int i = 0; i < NU; ++i) {
@@ -903,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 constexpr int kJoinRows = 4, kJoinWarps = 4, kJoinThreads = 32 * kJoinRows * kJoinWarps;
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4AttnParams p, const int chunks)
+__global__ void __launch_bounds__(kJoinThreads) fa_kv4_join_kernel(const Kv4AttnParams p)
 {
     constexpr int ROWS = Cfg<D, MODE>::ROWS, V = D / 32, U = 4;
     __shared__ float s_o[kJoinRows][kJoinWarps][D];
@@ -990,19 +997,17 @@ cudaError_t launch(const Kv4AttnParams& p, int blocks, cudaStream_t stream)
     fa_kv4_attn_kernel<D, MODE><<<blocks, kThreads, C::SMEM, stream>>>(p, chunks);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return f;
-    return launch_dependent(fa_kv4_join_kernel<D, MODE>, dim3(blocks, C::ROWS / kJoinRows), kJoinThreads, stream, p,
-                            chunks);
+    return launch_dependent(fa_kv4_join_kernel<D, MODE>, dim3(blocks, C::ROWS / kJoinRows), kJoinThreads, stream, p);
 }
 
 int blocks_of(int num_sms) { return 2 * num_sms; }
 
 }  // namespace
 
-cudaError_t kv4_attn_workspace(int D, int R, int, int num_sms, size_t* bytes)
+size_t kv4_attn_workspace(int D, int R, int num_sms)
 {
     const size_t blocks = (size_t)blocks_of(num_sms), rows = blocks * 2 * (4u << mode_of(R));
-    *bytes = blocks * sizeof(Cut) + rows * sizeof(float2) + rows * D * sizeof(float);
-    return cudaSuccess;
+    return blocks * sizeof(Cut) + rows * sizeof(float2) + rows * D * sizeof(float);
 }
 
 cudaError_t launch_kv4_attn(int D, const Kv4AttnParams& p, int num_sms, cudaStream_t stream, int* launches)

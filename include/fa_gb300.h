@@ -563,14 +563,15 @@ const char* fa_status_string(fa_status_t status);
  * Number of kernels the last successful forward call on this host thread
  * launched (1 for dense, 2 for varlen: schedule + attention; 1 or 2 for
  * split-KV: partials, then the merge when there is more than one partition;
- * 2 for backward).
+ * 2 for backward; for the 4-bit cache's calls as documented with each, 0 for
+ * an append or read of no rows).
  */
 int fa_last_launch_count(void);
 
 /*
  * Test hook (no counterpart on the pages).  kind = 1 makes the next fa_fwd
- * (or fa_fwd_splitkv, fa_bwd or fa_fwd_fp8) call on this host thread drop the first K
- * tile load (split-KV, backward: the first K/V tile) of every CTA: the bounded wait for it runs out (about 1 s), every thread of
+ * (or fa_fwd_splitkv, fa_bwd, fa_fwd_fp8 or fa_fwd_kv4) call on this host thread drop the first K
+ * tile load (split-KV, backward: the first K/V tile) of every CTA (fa_fwd_kv4: of every warp): the bounded wait for it runs out (about 1 s), every thread of
  * the kernel retires, and fa_check then reports FA_ERR_TIMEOUT with the CUDA
  * context still usable.  kind = 0 clears a pending request.  Results of the faulted
  * call are undefined.
