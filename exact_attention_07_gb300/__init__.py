@@ -58,6 +58,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdi
 SPLITKV_MAX_ROWS = 16  # (Hq / Hkv) * Lq limit of fa_fwd_splitkv
 NOALLOC_MAX_SEQS = 16384  # FA_NOALLOC_MAX_SEQS in include/fa_gb300.h
 KV4_MAX_ROWS = 64  # FA_KV4_MAX_ROWS: (Hq / Hkv) * Lq limit of fa_fwd_kv4
+KV4_RESERVE_NO_WORKSPACE = 2048  # FA_KV4_RESERVE_NO_WORKSPACE
 KV4_MAX_SLOTS = 65536  # FA_KV4_MAX_SLOTS
 VARLEN_SEQS_PER_LAUNCH = 1536  # FA_VARLEN_SEQS_PER_LAUNCH (64 for head dimensions (192, 128))
 
@@ -945,23 +946,24 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
     if name == "fa_kv4_release":
         st = _on_device(device, lib.fa_kv4_release, first, n, pages, _raw_stream(stream, device))
     else:
-        nbytes = kv4_pages_workspace(N, n)
+        # few sequences: a reserve needs no workspace
+        nbytes = 0 if pool is None and n <= KV4_RESERVE_NO_WORKSPACE else kv4_pages_workspace(N, n)
         if info is None:
             info = torch.empty(2, dtype=torch.int32, device=refs.device)
         else:
             _want(info, "info", torch.int32, 1, device)
             if info.shape[0] != 2:
                 raise ValueError("info must hold 2 numbers")
-        if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
-        elif workspace.get_device() != device:
+        if workspace is not None and workspace.get_device() != device:
             raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
-        tail = (pages, info.data_ptr(), workspace.data_ptr(), nbytes, _raw_stream(stream, device))
+        if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
+        tail = (pages, info.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(stream, device))
         if name == "fa_kv4_compact":
             st = _on_device(device, lib.fa_kv4_compact, *tail)
         else:
             st = _on_device(device, getattr(lib, name), first, second, n, *tail)
-        if stream is not None and isinstance(stream, torch.cuda.Stream):
+        if nbytes and isinstance(stream, torch.cuda.Stream):
             workspace.record_stream(stream)
     if st != FA_OK:
         raise FAError(st, name)

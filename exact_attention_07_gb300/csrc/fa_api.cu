@@ -1372,7 +1372,9 @@ fa_status_t kv4_pages(const fa_kv4_pages_t* c, bool pool, const int* ids, const 
     if (n > FA_KV4_MAX_SLOTS) return FA_ERR_INVALID_ARG;
     if (plan) {
         if (!info || !aligned4(info)) return FA_ERR_INVALID_ARG;
-        if (!workspace || !aligned16(workspace) || workspace_bytes < kv4_pages_workspace(c->num_pages, n))
+        // a reserve (no pool) of few sequences keeps its prefix sums in shared memory
+        if ((pool || n > kKv4ReserveShared) &&
+            (!workspace || !aligned16(workspace) || workspace_bytes < kv4_pages_workspace(c->num_pages, n)))
             return FA_ERR_INVALID_ARG;
     }
     st = device_state(ds);

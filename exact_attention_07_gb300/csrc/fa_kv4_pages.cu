@@ -167,8 +167,10 @@ __device__ __forceinline__ bool refused(const Kv4PageParams& p, bool bad, int fr
     if (threadIdx.x == 0) {
         p.info[0] = free_pages;
         p.info[1] = bad ? -1 : (int)min(need - free_pages, (long long)INT_MAX);
-        p.ws[kWsCount] = 0;
-        p.ws[kWsDone] = 0;
+        if (p.ws) {
+            p.ws[kWsCount] = 0;
+            p.ws[kWsDone] = 0;
+        }
         if (bad) atomicOr(p.err, 2);
     }
     return true;
@@ -179,8 +181,9 @@ __device__ __forceinline__ bool refused(const Kv4PageParams& p, bool bad, int fr
 __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4PageParams p)
 {
     __shared__ PlanSmem sm;
+    __shared__ int s_prefix[kKv4ReserveShared];
     const int tid = threadIdx.x;
-    int* prefix = p.ws + kWsBase;
+    int* prefix = p.n <= kKv4ReserveShared ? s_prefix : p.ws + kWsBase;
     plan_begin(sm);
     long long need = 0;
     for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4P
         if (i < p.n) {
             const int s = p.ids ? p.ids[i] : i;
             const int add = p.other[i];
-            if (add < 0 || !slot_ok(p, s) || mark(sm, s)) {
+            if (add < 0 || !slot_ok(p, s) || (add > 0 && mark(sm, s))) {
                 sm.bad = 1;
             } else {
                 const int len = p.lens[s];
@@ -215,7 +218,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4P
         p.refs[page] = 1;
     });
     __syncthreads();
-    for (int i = tid; i < p.n; i += kPlanThreads) p.lens[p.ids ? p.ids[i] : i] += p.other[i];
+    for (int i = tid; i < p.n; i += kPlanThreads)
+        if (p.other[i]) p.lens[p.ids ? p.ids[i] : i] += p.other[i];  // a slot named again adds nothing
     if (tid == 0) {
         p.info[0] = free_pages - (int)need;
         p.info[1] = 0;

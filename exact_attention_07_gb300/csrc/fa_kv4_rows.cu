@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowsThreads, 4) fa_kv4_append_kernel(const Kv
         __syncthreads();
         for (int i = threadIdx.x; i < p.num_seqs; i += kRowsThreads) {
             const int s = p.c.ids[i];
-            if (s < 0 || s >= p.c.num_slots) continue;
+            if (s < 0 || s >= p.c.num_slots || p.cu[i + 1] <= p.cu[i]) continue;  // no rows: a padded batch
             const uint32_t bit = 1u << (s & 31);
             if (atomicOr(&seen[s >> 5], bit) & bit) atomicOr(p.c.err, 2);
         }

@@ -403,7 +403,8 @@ fa_status_t fa_bwd_varlen_variant(const void* q, const void* k, const void* v, c
  * page_size, or a page number out of range latches FA_ERR_INVALID_ARG (read
  * by fa_check).  Nothing is read or written out of range then; what that
  * sequence's outputs hold is unspecified.  These calls allocate nothing,
- * copy nothing to the host and may be captured into a graph.
+ * copy nothing to the host and may be captured into a graph.  A batch is
+ * padded by naming an empty slot, as often as needed, with no rows.
  */
 #define FA_KV4_MAX_SLOTS 65536
 #define FA_KV4_MAX_ROWS 64
@@ -435,8 +436,9 @@ typedef struct fa_kv4 {
  * code 0, and s = 0 (max|x| up to 6 * 2^-10) gives zeros.  A group that holds a NaN or an infinity gets a NaN
  * scale, so that every value read from it is NaN.
  *
- * Bytes of other positions keep their values.  A sequence named twice in one
- * call latches FA_ERR_INVALID_ARG, and what it then holds is unspecified.
+ * Bytes of other positions keep their values.  A slot named twice in one call
+ * (each time with rows) latches FA_ERR_INVALID_ARG, and what it then holds is
+ * unspecified.
  * Pages written must belong to one sequence (fa_kv4_fork shares full pages
  * only).  1 kernel.
  */
@@ -512,9 +514,11 @@ typedef struct fa_kv4_pages {
 /*
  * Makes room for new_tokens[i] >= 0 (int32 DEVICE [n]) more positions in slot
  * seq_ids[i] (NULL: slots 0 .. n - 1): gives it the pages it needs, with one
- * reference each, and adds the tokens to seq_lens.  No slot may be named
- * twice.  The pool is not touched and may be NULL.  1 kernel.
+ * reference each, and adds the tokens to seq_lens.  A slot may be named again
+ * only with 0 tokens.  The pool is not touched and may be NULL, and up to
+ * FA_KV4_RESERVE_NO_WORKSPACE sequences so may the workspace.  1 kernel.
  */
+#define FA_KV4_RESERVE_NO_WORKSPACE 2048
 fa_status_t fa_kv4_reserve(const int* seq_ids, const int* new_tokens, int n, const fa_kv4_pages_t* pages, int* info,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 

@@ -140,7 +140,8 @@ class Pages:
 
     def reserve(self, slots, new):
         free = self._free()
-        bad = (len(set(slots)) < len(slots) or any(not 0 <= s < len(self.lens) for s in slots)
+        used = [s for s, a in zip(slots, new) if a]  # a slot may be named again with 0 tokens
+        bad = (len(set(used)) < len(used) or any(not 0 <= s < len(self.lens) for s in slots)
                or any(a < 0 for a in new))
         bad = bad or any(self.lens[s] + a > self.P * self.width for s, a in zip(slots, new))
         if bad:

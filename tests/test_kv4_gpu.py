@@ -402,6 +402,26 @@ def test_page_operations_follow_the_sequential_model(N, slots, width, P, H, D, l
     assert {k[0] for k in done} == {"reserve", "fork", "release", "compact"}
 
 
+def test_reserve_and_release_of_more_sequences_than_fit_in_shared_memory():
+    rng = np.random.default_rng(17)
+    S, P = 5000, 16
+    m = kv4.Pages(9000, S, 3, P)
+    dev = _page_state(m, np.zeros((1, 1, 1, 1, 18 * 64), np.uint8))
+    for n in (2048, 2049, 5000, 3000):
+        ids = [int(x) for x in rng.permutation(S)[:n]]
+        new = [int(x) for x in rng.integers(0, 17, n)]
+        want = m.reserve(ids, new)  # the last ones are refused: beyond the table's rows
+        assert tuple(fa.fa_kv4_reserve(i32(new), *dev[1:], P, seq_ids=i32(ids)).tolist()) == want
+        if want[1] < 0:
+            with pytest.raises(fa.FAError, match="invalid argument"):
+                fa.fa_check()
+        out = [int(x) for x in rng.permutation(S)[:n // 3]]
+        fa.fa_kv4_release(i32(out), *dev[1:], P)
+        m.release(out)
+        fa.fa_check()
+        assert dev[1].tolist() == m.table and dev[2].tolist() == m.lens and dev[3].tolist() == m.refs
+
+
 def test_page_operations_refuse_and_change_nothing():
     P = 16
     m = kv4.Pages(12, 6, 4, P)
@@ -576,6 +596,65 @@ def test_a_served_batch_from_prompt_to_beams():
     m.fork([2], [0], pool[None])
     decode([0, 2], 2)
     fa.fa_check()
+
+
+def test_padded_batch_names_an_empty_slot_again_and_again():
+    rng = np.random.default_rng(15)
+    H, D, P = 2, 64, 16
+    m = kv4.Pages(20, 4, 4, P)
+    m.reserve([0, 2], [20, 31])
+    pool = np.full((20, H, 1, 18 * D), 255, np.uint8)
+    k, v = rng.standard_normal((2, 51, H, D))
+    kv4.append(pool, m.table, m.lens, [0, 2], [20, 31], k, v, np.ones(H), np.ones(H))
+    dev = _page_state(m, pool)
+    ids, new = [2, 3, 0, 3, 3, 0], [1, 0, 2, 0, 0, 0]
+    assert fa.fa_kv4_reserve(i32(new), *dev[1:], P, seq_ids=i32(ids)).tolist() == list(m.reserve(ids, new))
+    k, v = bf16(rng.standard_normal((2, 3, H, D))).to(DEV)
+    fa.fa_kv4_append(k, v, i32([0, 1, 1, 3, 3, 3, 3]), *dev[:3], seq_ids=i32(ids))
+    kv4.append(pool, m.table, m.lens, ids, new, f64(k), f64(v), np.ones(H), np.ones(H))
+    fa.fa_check()
+    _same_state(m, pool, dev, "padded")
+    q = bf16(rng.standard_normal((6, 4, 1, D))).to(DEV)
+    o, lse = run_attention(q, *dev[:3], causal=True, seq_ids=i32(ids))
+    check_attention(q, o, lse, pool, m.table, ids, m.lens, np.ones(H), np.ones(H), 1 / math.sqrt(D), True, "padded")
+    fa.fa_kv4_release(i32([3, 2, 3, 2]), *dev[1:], P)
+    m.release([3, 2, 3, 2])
+    fa.fa_check()
+    _same_state(m, pool, dev, "released")
+
+
+def test_two_graphs_replayed_at_once():
+    rng = np.random.default_rng(16)
+    lens = [2500, 0, 400]
+    pool, table = random_cache(rng, lens, 2, 128, 32)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32(lens))
+    qs = [bf16(rng.standard_normal((3, 8, 1, 128))).to(DEV) for _ in range(2)]
+    want = [fa.fa_fwd_kv4(q, *dev, causal=True) for q in qs]
+    torch.cuda.synchronize()
+    graphs, got, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q in qs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            got.append(fa.fa_fwd_kv4(q, *dev, causal=True))
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_too_small_a_workspace_is_refused():
+    lib = fa.load_library()
+    pool, table, lens = fa.kv4_pool(4, 2, 16, 64), i32([[0, 1], [2, 3]]), i32([3, 4])
+    q, o = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 4, 1, 64, device=DEV)
+    c = fa._kv4(pool, table, lens, None, None, None, 2)[0]
+    need = fa.kv4_workspace(2, 4, 2, 1, 64)
+    ws = torch.zeros(need, dtype=torch.uint8, device=DEV)
+    for ptr, n in ((ws.data_ptr(), need - 1), (None, need), (ws.data_ptr() + 8, need)):
+        assert lib.fa_fwd_kv4(q.data_ptr(), o.data_ptr(), o.data_ptr(), 2, 4, 1, 0, 0.1, c, ptr, n,
+                              None) == fa.FA_ERR_INVALID_ARG
 
 
 def test_captured_decode_step_follows_the_cache():

@@ -92,8 +92,9 @@ def test_page_calls_are_refused(lib):
     assert lib.fa_kv4_reserve(None, None, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_reserve(None, 16, 0, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_reserve(None, 16, 2, p, None, 16, big, None) == INV
-    assert lib.fa_kv4_reserve(None, 16, 2, p, 16, None, big, None) == INV
-    assert lib.fa_kv4_reserve(None, 16, 2, p, 16, 16, 8, None) == INV      # workspace too small
+    n = fa.KV4_RESERVE_NO_WORKSPACE + 1
+    assert lib.fa_kv4_reserve(16, 16, n, p, 16, None, big, None) == INV    # up to 2048 sequences it needs none
+    assert lib.fa_kv4_reserve(16, 16, n, p, 16, 16, 8, None) == INV        # workspace too small
     assert lib.fa_kv4_fork(None, 16, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_fork(16, None, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_fork(16, 16, 65537, p, 16, 16, big, None) == INV
