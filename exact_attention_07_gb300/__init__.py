@@ -728,8 +728,22 @@ def _on_device(index, fn, *args):
         return fn(*args)
 
 
-def _raw_stream(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream_handle(stream)
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _on_stream(stream, fn, *args):
+    """fn(*args) with `stream` (a torch stream or a raw handle) current, so that what it allocates belongs to that
+    stream; the results may then be used on the caller's stream once that waits for it."""
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        got = fn(*args)
+    for t in got if isinstance(got, tuple) else (got,):
+        if t is not None:
+            t.record_stream(here)
+    return got
 
 
 def _check_slots(table, seq_lens, device):
@@ -748,8 +762,9 @@ def _check_pool(pool, ndim):
 
 def _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, num_seqs):
     """Checks the cache of a call with num_seqs sequences.  Returns (fa_kv4_t as bytes, device index, Hkv, D)."""
-    device = pool.get_device()
-    if not (pool.dtype is torch.uint8 and pool.dim() == 4 and pool.is_contiguous() and device >= 0
+    device = pool.get_device() if isinstance(pool, torch.Tensor) else -1
+    if not (device >= 0 and isinstance(table, torch.Tensor) and isinstance(seq_lens, torch.Tensor)
+            and pool.dtype is torch.uint8 and pool.dim() == 4 and pool.is_contiguous()
             and table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous()
             and table.get_device() == device and seq_lens.dtype is torch.int32 and seq_lens.dim() == 1
             and seq_lens.is_contiguous() and seq_lens.get_device() == device):
@@ -783,6 +798,8 @@ def _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, num_seqs):
 
 
 def _num_seqs(cu_seqlens):
+    if not isinstance(cu_seqlens, torch.Tensor):
+        raise TypeError("cu_seqlens must be a torch.Tensor")
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
     return cu_seqlens.shape[0] - 1
@@ -794,6 +811,8 @@ def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, po
     """Quantise packed rows k, v [T,Hkv,D] bf16 into the cache: the rows
     [cu_seqlens[s], cu_seqlens[s+1]) become the last positions of sequence s
     (slot seq_ids[s], default s), which seq_lens already counts."""
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_append, k, v, cu_seqlens, pool, table, seq_lens, seq_ids, k_scale, v_scale)
     n = _num_seqs(cu_seqlens)
     c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
     _want(k, "k", torch.bfloat16, 3, device)
@@ -803,7 +822,7 @@ def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, po
         raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {H} heads of {D}")
     lib = _lib or load_library()
     st = _on_device(device, lib.fa_kv4_append, k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), n, k.shape[0], c,
-                    _raw_stream(stream, device))
+                    _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_append")
 
@@ -815,6 +834,9 @@ def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table:
     """The last cu_seqlens[s+1] - cu_seqlens[s] positions of each sequence as
     packed bf16 rows (k, v), each [total,Hkv,D]: a cached prefix as the keys
     of fa_fwd_varlen.  Rows behind the last sequence are left as they were."""
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_read, cu_seqlens, total, pool, table, seq_lens, seq_ids, k_scale, v_scale, k_out,
+                          v_out)
     n = _num_seqs(cu_seqlens)
     c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
     _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
@@ -833,7 +855,7 @@ def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table:
         raise ValueError(f"k_out and v_out must be {shape}, got {tuple(k_out.shape)} and {tuple(v_out.shape)}")
     lib = _lib or load_library()
     st = _on_device(device, lib.fa_kv4_read, k_out.data_ptr(), v_out.data_ptr(), cu_seqlens.data_ptr(), n, shape[0], c,
-                    _raw_stream(stream, device))
+                    _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, "fa_kv4_read")
     return k_out, v_out
@@ -857,7 +879,10 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     (Hq/Hkv)*Lq <= 64; sequence b is slot seq_ids[b] (default b) and attends its
     first seq_lens positions; with ``causal`` the queries are the last Lq of
     them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
-    if not (q.dtype is torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.is_cuda):
+    if stream is not None:
+        return _on_stream(stream, fa_fwd_kv4, q, pool, table, seq_lens, causal, softmax_scale, seq_ids, k_scale, v_scale, out,
+                          lse, workspace)
+    if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.is_cuda):
         _check_tensor(q, "q", torch.bfloat16, 4)
     B, Hq, Lq, D = q.shape
     c, device, H, cache_d = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, B)
@@ -884,9 +909,7 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     elif workspace.get_device() != device:
         raise ValueError(f"workspace must be on {q.device}, got {workspace.device}")
     st = _on_device(device, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq,
-                    1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(stream, device))
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        workspace.record_stream(stream)  # keep the block out of reuse until that stream is done
+                    1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, "fa_fwd_kv4")
     return out, lse
@@ -910,7 +933,8 @@ def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
 
 def _slots_of(table, seq_lens, device):
     """Shape of a call's table, after the checks of _check_slots."""
-    if not (table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous() and table.get_device() == device
+    if not (isinstance(table, torch.Tensor) and isinstance(seq_lens, torch.Tensor)
+            and table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous() and table.get_device() == device
             and seq_lens.dtype is torch.int32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
             and seq_lens.get_device() == device and seq_lens.shape[0] == table.shape[0]):
         _check_slots(table, seq_lens, device)
@@ -918,23 +942,23 @@ def _slots_of(table, seq_lens, device):
 
 
 def _refs_device(refs):
-    if not (refs.dtype is torch.int32 and refs.dim() == 1 and refs.is_cuda and refs.is_contiguous()):
+    if not (isinstance(refs, torch.Tensor) and refs.dtype is torch.int32 and refs.dim() == 1 and refs.is_cuda and refs.is_contiguous()):
         _check_tensor(refs, "refs", torch.int32, 1)
     return refs.get_device()
 
 
-def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, info, workspace, stream, device):
+def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, info, workspace, device):
     """Runs one page operation.  first, second: device addresses of its lists
     of n entries (None: the operation has no such list)."""
     slots, width = _slots_of(table, seq_lens, device)
     N = refs.shape[0]
-    if pool is None:
-        pages = _pack_pages(0, table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width, page_size, 1,
-                            64, 1)
+    if page_size is not None:  # a call on the tables alone
+        pages = _pack_pages(0, table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), N, slots, width,
+                            int(page_size), 1, 64, 1)
     else:
-        if not (pool.dtype is torch.uint8 and pool.dim() in (4, 5) and pool.is_contiguous()
+        if not (isinstance(pool, torch.Tensor) and pool.dtype is torch.uint8 and pool.dim() in (4, 5) and pool.is_contiguous()
                 and pool.shape[-1] in _KV4_UNITS and pool.shape[-2] in _KV4_PAGES):
-            _check_pool(pool, 5 if pool.dim() == 5 else 4)
+            _check_pool(pool, 5 if isinstance(pool, torch.Tensor) and pool.dim() == 5 else 4)
         P, H, U, unit = pool.shape[-4:]
         if P != N:
             raise ValueError(f"pool has {P} pages and refs {N}")
@@ -944,7 +968,7 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
                             16 * U, H, unit // 18, pool.shape[0] if pool.dim() == 5 else 1)
     lib = _lib or load_library()
     if name == "fa_kv4_release":
-        st = _on_device(device, lib.fa_kv4_release, first, n, pages, _raw_stream(stream, device))
+        st = _on_device(device, lib.fa_kv4_release, first, n, pages, _raw_stream(device))
     else:
         # few sequences: a reserve needs no workspace
         nbytes = 0 if pool is None and n <= KV4_RESERVE_NO_WORKSPACE else kv4_pages_workspace(N, n)
@@ -958,13 +982,11 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
             raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
         if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
-        tail = (pages, info.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(stream, device))
+        tail = (pages, info.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(device))
         if name == "fa_kv4_compact":
             st = _on_device(device, lib.fa_kv4_compact, *tail)
         else:
             st = _on_device(device, getattr(lib, name), first, second, n, *tail)
-        if nbytes and isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)
     if st != FA_OK:
         raise FAError(st, name)
     return info
@@ -977,6 +999,8 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
     count them in seq_lens.  Returns info, int32 [2] on the device: free pages
     left, and 0, or the pages that were missing (then nothing was changed), or
     -1 for bad arguments on the device."""
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_reserve, new_tokens, table, seq_lens, refs, page_size, seq_ids, info, workspace)
     device = _refs_device(refs)
     _want(new_tokens, "new_tokens", torch.int32, 1, device)
     n = new_tokens.shape[0]
@@ -985,8 +1009,7 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
         if seq_ids.shape[0] != n:
             raise ValueError(f"seq_ids must name {n} slots")
     return _page_call("fa_kv4_reserve", None, page_size, table, seq_lens, refs,
-                      None if seq_ids is None else seq_ids.data_ptr(), new_tokens.data_ptr(), n, info, workspace,
-                      stream, device)
+                      None if seq_ids is None else seq_ids.data_ptr(), new_tokens.data_ptr(), n, info, workspace, device)
 
 
 def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
@@ -995,6 +1018,8 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     """Make the empty slots children[i] copies of the slots parents[i]: full pages
     are shared, a partly filled last page is copied.  pool as for
     fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_fork, parents, children, pool, table, seq_lens, refs, info, workspace)
     device = _refs_device(refs)
     _want(parents, "parents", torch.int32, 1, device)
     _want(children, "children", torch.int32, 1, device)
@@ -1002,23 +1027,27 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     if children.shape[0] != n:
         raise ValueError(f"{n} parents but {children.shape[0]} children")
     return _page_call("fa_kv4_fork", pool, None, table, seq_lens, refs, parents.data_ptr(), children.data_ptr(), n,
-                      info, workspace, stream, device)
+                      info, workspace, device)
 
 
 def fa_kv4_release(seq_ids: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
                    page_size: int, stream=None) -> None:
     """Free the slots seq_ids: their pages lose a reference each, their lengths become 0."""
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_release, seq_ids, table, seq_lens, refs, page_size)
     device = _refs_device(refs)
     _want(seq_ids, "seq_ids", torch.int32, 1, device)
     _page_call("fa_kv4_release", None, page_size, table, seq_lens, refs, seq_ids.data_ptr(), None, seq_ids.shape[0],
-               None, None, stream, device)
+               None, None, device)
 
 
 def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tensor, refs: torch.Tensor,
                    info: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
-    return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace, stream,
+    if stream is not None:
+        return _on_stream(stream, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace)
+    return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace,
                       _refs_device(refs))
 
 

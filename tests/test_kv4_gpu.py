@@ -522,6 +522,14 @@ def test_binding_refuses_wrong_tensors():
     refs = torch.ones(4, dtype=torch.int32, device=DEV)
     for err, call in [
         (TypeError, lambda: fa.fa_fwd_kv4(q.half(), pool, table, lens)),
+        (TypeError, lambda: fa.fa_fwd_kv4(None, pool, table, lens)),
+        (TypeError, lambda: fa.fa_fwd_kv4(q, None, table, lens)),
+        (TypeError, lambda: fa.fa_fwd_kv4(q, pool, [[0, 1], [2, 3]], lens)),
+        (TypeError, lambda: fa.fa_fwd_kv4(q, pool, table, 3)),
+        (TypeError, lambda: fa.fa_kv4_append(kv, kv, [0, 1, 2], pool, table, lens)),
+        (TypeError, lambda: fa.fa_kv4_compact(pool, table, lens, None)),
+        (TypeError, lambda: fa.fa_kv4_compact(None, table, lens, refs)),
+        (TypeError, lambda: fa.fa_kv4_release([0], table, lens, refs, 16)),
         (ValueError, lambda: fa.fa_fwd_kv4(q[:, :, 0], pool, table, lens)),
         (ValueError, lambda: fa.fa_fwd_kv4(q.repeat(1, 1, 2, 1)[:, :, ::2], pool, table, lens)),  # not contiguous
         (ValueError, lambda: fa.fa_fwd_kv4(q.repeat(2, 1, 1, 1), pool, table, lens)),  # more sequences than slots
@@ -766,3 +774,18 @@ def test_two_calls_at_once_on_two_streams():
     fa.fa_fwd_kv4(qs[0], *dev, causal=True, out=out, lse=lse, stream=streams[0])  # on a stream that is not current
     streams[0].synchronize()
     assert torch.equal(out, want[0][0])
+    for stream in (streams[1], streams[1].cuda_stream, 0):  # all that the call allocates is that stream's
+        o, lse = fa.fa_fwd_kv4(qs[1], *dev, causal=True, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[1][0]) and torch.equal(lse, want[1][1])
+        k, v = fa.fa_kv4_read(i32([0, 5, 5, 9]), 9, *dev, stream=stream)
+        torch.cuda.synchronize()
+        rk, rv = kv4.rows(pool, table, 2, 700, np.ones(2), np.ones(2))
+        assert np.array_equal(f64(k[5:]).transpose(1, 0, 2), rk[:, -4:])
+    refs = torch.zeros(pool.shape[0], dtype=torch.int32, device=DEV)
+    refs[torch.tensor(np.concatenate([table[s, :-(-n // 64)] for s, n in enumerate(lens)]), device=DEV).long()] = 1
+    fa.fa_kv4_release(i32([1]), dev[1], dev[2], refs, 64, stream=streams[0])
+    info = fa.fa_kv4_reserve(i32([70]), dev[1], dev[2], refs, 64, seq_ids=i32([1]), stream=streams[0])
+    streams[0].synchronize()
+    assert dev[2].tolist() == [2000, 70, 700] and info.tolist() == [int((refs == 0).sum()), 0]
+    fa.fa_check()
