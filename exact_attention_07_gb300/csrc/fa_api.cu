@@ -1274,7 +1274,7 @@ fa_status_t kv4_rows(const void* k, const void* v, bool write, const int* cu_seq
     p.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
     p.c.err = ds->err;
     p.c.diag = ds->diag;
-    const cudaError_t e = write ? launch_kv4_append(cache->D, p, stream) : launch_kv4_read(cache->D, p, stream);
+    const cudaError_t e = write ? launch_kv4_append(cache->D, p, ds->num_sms, stream) : launch_kv4_read(cache->D, p, stream);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     g_last_launches = 1;
     return FA_OK;

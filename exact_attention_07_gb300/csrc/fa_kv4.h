@@ -37,6 +37,7 @@ struct Kv4RowsParams {  // append and read
     const int* cu;
     int num_seqs, total;
     bool wide;  // the bf16 rows are 32-byte aligned
+    int heads;  // append: KV heads of a warp
     Kv4Cache c;
 };
 
@@ -64,7 +65,7 @@ struct Kv4PageParams {
     int* err;
 };
 
-cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream);
+cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_kv4_read(int D, const Kv4RowsParams& p, cudaStream_t stream);
 
 // Workspace bytes of the attention on a device with num_sms SMs, and its

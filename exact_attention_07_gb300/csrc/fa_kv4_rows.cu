@@ -4,13 +4,17 @@
 // (position, KV head).
 //
 // One warp handles one unit: 16 positions of one KV head, 18 D contiguous
-// bytes of the cache (append: one warp for its K and one for its V).  A lane's piece is a group of 16 dimensions: of one
-// position for K, of two neighbouring ones for V, whose codes share bytes.
-// The order of the pieces is that of the cache's bytes, so that a warp reads
-// or writes them in contiguous runs, and the bf16 side goes in whole 32-byte
-// sectors (one 32-byte access per lane where the caller's rows are so
-// aligned).  All loads of a unit are issued before the first is used: 256
-// bytes per lane.
+// bytes of the cache (append: one warp for its K and one for its V).  A lane's
+// piece is a group of 16 dimensions: of one position for K, of two
+// neighbouring ones for V, whose codes share bytes.  The order of the pieces
+// is that of the cache's bytes, so that a warp reads or writes them in
+// contiguous runs, and the bf16 side goes in whole 32-byte sectors (one
+// 32-byte access per lane where the caller's rows are so aligned).  All loads
+// of a warp's piece are issued before the first is used.  Read: 67 us for
+// 80757 positions of 8 heads, D = 128, 93 % of the copy bandwidth (91 us with
+// a thread per group of two positions and 16-byte accesses).
+#include <algorithm>
+
 #include "kv4_common.cuh"
 
 namespace fa {
@@ -31,12 +35,14 @@ struct UnitTask {
     int h;
 };
 
-// The w-th (unit slot, KV head); false when there is nothing to do.
+// The w-th (unit slot, group of `heads` KV heads); false when there is nothing
+// to do.  The task's unit is that of the group's first head; the other heads'
+// follow one page_size / 16 units apart.
 template <int D>
-__device__ __forceinline__ bool find_unit(const Kv4RowsParams& p, unsigned w, UnitTask& t)
+__device__ __forceinline__ bool find_unit(const Kv4RowsParams& p, unsigned w, int heads, UnitTask& t)
 {
-    const unsigned u = w / (unsigned)p.c.Hkv;
-    t.h = (int)(w - u * (unsigned)p.c.Hkv);
+    const unsigned groups = (unsigned)((p.c.Hkv + heads - 1) / heads), u = w / groups;
+    t.h = (int)(w - u * groups) * heads;
     if (u >= (unsigned)(p.total >> 4) + 2u * (unsigned)p.num_seqs) return false;
     int s = 0, end = p.num_seqs - 1;  // the last sequence whose first slot is <= u
     while (s < end) {
@@ -129,6 +135,14 @@ __device__ __forceinline__ float quotient(float x, float y, float r)
     return __fmaf_rn(__fmaf_rn(-q, y, x), r, q);
 }
 
+// max(a, |x|) of two bf16 each; a NaN stays one.
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t x)
+{
+    uint32_t r;
+    asm("{.reg .b32 t; abs.bf16x2 t, %2; max.NaN.bf16x2 %0, %1, t;}" : "=r"(r) : "r"(a), "r"(x));
+    return r;
+}
+
 struct Codes {
     uint32_t w[2];  // dimensions 0 .. 7, 8 .. 15
     uint32_t scale;
@@ -141,7 +155,7 @@ __device__ __forceinline__ Codes quantise_group(const Group& x, float head, floa
 {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = __vmaxu2(m, x.w[i] & 0x7fff7fffu);
+    for (int i = 0; i < 8; ++i) m = max_magnitude(m, x.w[i]);
     const uint32_t top = max(m & 0xffffu, m >> 16);
     const bool bad = top >= 0x7f80u;
     uint16_t pair;
@@ -194,59 +208,65 @@ __global__ void __launch_bounds__(kRowsThreads, 4) fa_kv4_append_kernel(const Kv
         }
         return;
     }
-    // one warp for K and one for V of a unit: with both in one the loaded
-    // rows took 88 registers and 16 warps an SM
+    // One warp for K and one for V of a unit: with both in one the loaded rows
+    // took 88 registers and left 16 warps an SM (46 us for 8 prompts of 32916
+    // tokens in all, 8 heads, D = 128; so 36 us, 4.8 TB/s).
     const unsigned w = blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5);
     UnitTask t;
-    if (!find_unit<D>(p, w >> 1, t)) return;
+    if (!find_unit<D>(p, w >> 1, p.heads, t)) return;
     const int lane = threadIdx.x & 31;
-    const long long pitch = (long long)p.c.Hkv * D, base = t.row * pitch + t.h * D;
+    const long long pitch = (long long)p.c.Hkv * D;
     const auto mine = [&](int r) { return r >= t.lo && r < t.hi; };
-    const float* heads = w & 1 ? p.c.v_scale : p.c.k_scale;
-    const float head = heads ? heads[t.h] : 1.f, head6 = 6.f * head, r6 = rcp_approx(head6);
-    if (!(w & 1)) {
-        Group k[KI];
+    const float* scales = w & 1 ? p.c.v_scale : p.c.k_scale;
+    const int end = min(t.h + p.heads, p.c.Hkv);
+#pragma unroll 1
+    for (int h = t.h; h < end; ++h, t.unit += (18 * D) << (p.c.page_shift - 4)) {
+        const long long base = t.row * pitch + h * D;
+        const float head = scales ? scales[h] : 1.f, head6 = 6.f * head, r6 = rcp_approx(head6);
+        if (!(w & 1)) {
+            Group k[KI];
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-            const int x = 32 * i + lane, r = x / G, g = x % G;
-            k[i] = load_group(p.k_in + base + r * pitch + g * 16, mine(r), p.wide);
+            for (int i = 0; i < KI; ++i) {
+                const int x = 32 * i + lane, r = x / G, g = x % G;
+                k[i] = load_group(p.k_in + base + r * pitch + g * 16, mine(r), p.wide);
+            }
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int x = 32 * i + lane;
+                const Codes c = quantise_group(k[i], head, head6, r6);
+                if (!mine(x / G)) continue;
+                *reinterpret_cast<uint2*>(t.unit + x * 8) = make_uint2(c.w[0], c.w[1]);
+                t.unit[16 * D + x] = (uint8_t)c.scale;
+            }
+            continue;
+        }
+        Group v[VI][2];
+#pragma unroll
+        for (int i = 0; i < VI; ++i) {
+            const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                v[i][e] = load_group(p.v_in + base + (r + e) * pitch + g * 16, mine(r + e), p.wide);
         }
 #pragma unroll
-        for (int i = 0; i < KI; ++i) {
-            const int x = 32 * i + lane;
-            const Codes c = quantise_group(k[i], head, head6, r6);
-            if (!mine(x / G)) continue;
-            *reinterpret_cast<uint2*>(t.unit + x * 8) = make_uint2(c.w[0], c.w[1]);
-            t.unit[16 * D + x] = (uint8_t)c.scale;
-        }
-        return;
-    }
-    Group v[VI][2];
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            v[i][e] = load_group(p.v_in + base + (r + e) * pitch + g * 16, mine(r + e), p.wide);
-    }
-#pragma unroll
-    for (int i = 0; i < VI; ++i) {
-        const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
-        const bool even = mine(r), odd = mine(r + 1);
-        const Codes a = quantise_group(v[i][0], head, head6, r6), b = quantise_group(v[i][1], head, head6, r6);
-        if (!even && !odd) continue;
-        const uint2 lo = pair_codes(a.w[0], b.w[0]), hi = pair_codes(a.w[1], b.w[1]);
-        uint4* codes = reinterpret_cast<uint4*>(t.unit + 8 * D + x * 16);
-        uint8_t* scales = t.unit + 17 * D + g * 16 + r;
-        if (even && odd) {
-            *codes = make_uint4(lo.x, lo.y, hi.x, hi.y);
-            *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(a.scale | b.scale << 8);
-        } else {  // the pair's other position keeps its nibbles
-            const uint32_t own = even ? 0x0f0f0f0fu : 0xf0f0f0f0u;
-            const uint4 old = *codes;
-            *codes = make_uint4((old.x & ~own) | (lo.x & own), (old.y & ~own) | (lo.y & own),
-                                (old.z & ~own) | (hi.x & own), (old.w & ~own) | (hi.y & own));
-            scales[even ? 0 : 1] = (uint8_t)(even ? a.scale : b.scale);
+        for (int i = 0; i < VI; ++i) {
+            const int x = 32 * i + lane, g = x / 4 % G, r = x / (4 * G) * 8 + x % 4 * 2;
+            const bool even = mine(r), odd = mine(r + 1);
+            const Codes a = quantise_group(v[i][0], head, head6, r6), b = quantise_group(v[i][1], head, head6, r6);
+            if (!even && !odd) continue;
+            const uint2 lo = pair_codes(a.w[0], b.w[0]), hi = pair_codes(a.w[1], b.w[1]);
+            uint4* codes = reinterpret_cast<uint4*>(t.unit + 8 * D + x * 16);
+            uint8_t* to = t.unit + 17 * D + g * 16 + r;
+            if (even && odd) {
+                *codes = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                *reinterpret_cast<uint16_t*>(to) = (uint16_t)(a.scale | b.scale << 8);
+            } else {  // the pair's other position keeps its nibbles
+                const uint32_t own = even ? 0x0f0f0f0fu : 0xf0f0f0f0u;
+                const uint4 old = *codes;
+                *codes = make_uint4((old.x & ~own) | (lo.x & own), (old.y & ~own) | (lo.y & own),
+                                    (old.z & ~own) | (hi.x & own), (old.w & ~own) | (hi.y & own));
+                to[even ? 0 : 1] = (uint8_t)(even ? a.scale : b.scale);
+            }
         }
     }
 }
@@ -284,7 +304,7 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_read_kernel(const Kv4Rows
 {
     constexpr int G = D / 16, KI = D / 32, VI = D / 64;
     UnitTask t;
-    if (!find_unit<D>(p, blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5), t)) return;
+    if (!find_unit<D>(p, blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5), 1, t)) return;
     const int lane = threadIdx.x & 31;
     uint2 kc[KI];
     uint4 vc[VI];
@@ -344,17 +364,23 @@ __global__ void __launch_bounds__(kRowsThreads) fa_kv4_read_kernel(const Kv4Rows
     }
 }
 
-unsigned rows_blocks(const Kv4RowsParams& p, int warps_per_unit)
-{
-    const long long warps = ((long long)(p.total >> 4) + 2ll * p.num_seqs) * p.c.Hkv * warps_per_unit;
-    return (unsigned)((warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32));
-}
+long long unit_slots(const Kv4RowsParams& p) { return (long long)(p.total >> 4) + 2ll * p.num_seqs; }
+
+unsigned rows_blocks(long long warps) { return (unsigned)((warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32)); }
 
 }  // namespace
 
-cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream)
+cudaError_t launch_kv4_append(int D, const Kv4RowsParams& params, int num_sms, cudaStream_t stream)
 {
-    const unsigned grid = rows_blocks(p, 2) + (p.c.ids ? 1 : 0);
+    // A warp finds its unit through five dependent loads and some 150
+    // instructions.  Where there are more warps than run at once (32 an SM), one
+    // takes several heads of the unit and pays for them once (8 prompts appended
+    // and read back 64 -> 62 us), while a decode step's few tokens want a warp
+    // per head.
+    Kv4RowsParams p = params;
+    const long long warps = 2 * unit_slots(p) * p.c.Hkv;
+    p.heads = (int)std::max(1ll, std::min({4ll, (long long)p.c.Hkv, warps / (32ll * num_sms)}));
+    const unsigned grid = rows_blocks(2 * unit_slots(p) * ((p.c.Hkv + p.heads - 1) / p.heads)) + (p.c.ids ? 1 : 0);
     if (D == 128)
         fa_kv4_append_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else
@@ -364,7 +390,7 @@ cudaError_t launch_kv4_append(int D, const Kv4RowsParams& p, cudaStream_t stream
 
 cudaError_t launch_kv4_read(int D, const Kv4RowsParams& p, cudaStream_t stream)
 {
-    const unsigned grid = rows_blocks(p, 1);
+    const unsigned grid = rows_blocks(unit_slots(p) * p.c.Hkv);
     if (D == 128)
         fa_kv4_read_kernel<128><<<grid, kRowsThreads, 0, stream>>>(p);
     else
