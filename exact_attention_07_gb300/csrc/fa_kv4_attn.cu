@@ -35,11 +35,11 @@
 // joined by a second kernel.
 //
 // Measured (device time): 8 sequences of 32768 keys, 32 x 8 heads, D = 128,
-// 60 us, 74 % of the copy bandwidth; a warp issues about 560
-// instructions a tile, 288 of them conversions, products and MMAs, and the
-// schedulers are 58 % busy: latencies between dependent instructions of the
-// four warps a scheduler has bound it, next to 7 us of beginning and joining.
-// 12 warps of 168 registers took 66 us.
+// 58 us, 76 % of the copy bandwidth; of 131072 keys 193 us, 92 %: about 14 us
+// go into finding the share, the first copies, the last warps and the join.
+// What the tile loop has in registers decides: 90 bytes spilled in place of 38
+// took 212 us there, 12 warps of 168 registers in place of 16 took 66 us
+// here.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -211,6 +211,10 @@ __device__ __forceinline__ uint32_t without_nan(uint32_t s)
     return (n & 1 ? 0u : s & 0xffffu) | (n & 2 ? 0u : s & 0xffff0000u);
 }
 
+struct List {
+    long long last, share;  // end of the block's share, and its length
+};
+
 // Where the kernels keep what they share in the workspace.
 struct Parts {
     float* o;   // [blocks][2][ROWS][D]
@@ -313,10 +317,12 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     using C = Cfg<D, MODE>;
     constexpr int NT = C::NT, KS = C::KS, NU = C::NU, UG = C::UG, TILE = tile_keys(D);
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long s_sum[kWarps];
     // a warp's part in hand and the part of its next copies: looked at once in
     // a while, and not to take registers from the tiles
-    __shared__ Seg s_seg, s_now[kWarps], s_ld[kWarps];
+    __shared__ Seg s_now[kWarps], s_ld[kWarps];
+    __shared__ int s_ld_k[kWarps];
+    __shared__ List s_list;
+    __shared__ long long s_sum[kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t base = smem_u32(smem);
     const uint32_t ring = base + warp * (C::STAGES * C::STAGE);
@@ -345,30 +351,35 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             prefetch_l2(reinterpret_cast<const char*>(p.q) + (line - t_bytes));
     }
 
-    // This block's share of the list, from the lengths: thread i sums a run of
-    // sequences.  First the tiles alone, for the limit of a group, then the
-    // list's units, whose prefix sums say in which run the share begins.
-    const int run = (p.B + kThreads - 1) / kThreads;
-    const int run0 = min(p.B, tid * run), run1 = min(p.B, run0 + run);
+    // This block's share of the list, from the lengths: thread i (lane i where
+    // there are no more than 32 sequences: then every warp finds the share for
+    // itself) sums a run of sequences.  First the tiles alone, only for the
+    // limit of a group, then the list's units, whose prefix sums say in which
+    // run the share begins.
+    const bool few = p.B <= 32;
+    const int run = (p.B + kThreads - 1) / kThreads, me = few ? lane : tid;
+    const int run0 = min(p.B, me * run), run1 = min(p.B, run0 + run);
     auto tiles = [&](int b) {
         int slot;
         return tiles_of<D>(kv4_sequence(p.c, b, slot));
     };
     const int nt0 = run0 < run1 ? tiles(run0) : 0;  // of the run's first; most have no other
-    long long mine = nt0;
+    float all = (float)nt0;
 #pragma unroll 1
-    for (int b = run0 + 1; b < run1; ++b) mine += tiles(b);
+    for (int b = run0 + 1; b < run1; ++b) all += (float)tiles(b);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
-    __syncthreads();
-    long long total = 0;
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(~0u, all, o);
+    if (!few) {
+        if (lane == 0) s_sum[warp] = __float_as_int(all);
+        __syncthreads();
+        all = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+        for (int w = 0; w < kWarps; ++w) all += __int_as_float((int)s_sum[w]);
+        __syncthreads();
+    }
     const float per_block = 1.f / gridDim.x;
-    sp.limit = (int)fminf(fmaxf(1.25f * per_block * (float)total * (float)sp.items, 2.f * kWarps), 1e9f);
-    __syncthreads();
-    mine = run0 < run1 ? sp.cost(nt0) : 0;
+    sp.limit = (int)fminf(fmaxf(1.25f * per_block * all * (float)sp.items, 2.f * kWarps), 1e9f);
+    long long mine = run0 < run1 ? sp.cost(nt0) : 0;
 #pragma unroll 1
     for (int b = run0 + 1; b < run1; ++b) mine += sp.cost(tiles(b));
     long long upto = mine;
@@ -377,21 +388,23 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         const long long y = __shfl_up_sync(~0u, upto, o);
         if (lane >= o) upto += y;
     }
-    if (lane == 31) s_sum[warp] = upto;
-    __syncthreads();
-    total = 0;
+    long long total = __shfl_sync(~0u, upto, 31);
+    if (!few) {
+        if (lane == 0) s_sum[warp] = total;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w == warp) upto += total;
-        total += s_sum[w];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == warp) upto += total;
+            total += s_sum[w];
+        }
     }
     // ceil(total / blocks), or a little above
     long long share = (long long)((float)total * per_block * 1.000002f + 0.999f);
     share += share * gridDim.x < total;
     share = max(share, (long long)kWarps);
     const long long first = share * blockIdx.x, last = min(total, first + share);
-    Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
-    if (tid == 0) parts.join[blockIdx.x].item = -1;
+    if (tid == 0) parts_of<D, MODE>(p.part, gridDim.x).join[blockIdx.x].item = -1;
     if (first >= last) return;
     if (first < upto && first >= upto - mine) {
         long long at = upto - mine;
@@ -410,12 +423,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             s.t = 0;
         }
         s.n = s.solo ? s.nt : min(s.left, s.nt - s.t);
-        s_seg = s;
+        for (int w = 0; w < kWarps; ++w)
+            if (!few || w == warp) {
+                s_now[w] = s_ld[w] = s;
+                s_ld_k[w] = 0;
+            }
+        if (!few || warp == 0) s_list = List{last, share};
     }
-    __syncthreads();
-    if (s_seg.left <= 0) return;
-    if (lane == 0) s_now[warp] = s_ld[warp] = s_seg;
-    __syncwarp();
+    __syncthreads();  // and the abort flag's initial value
+    if (s_now[warp].left <= 0) return;
 
     // Raw Q of a part: lane (g, t4) holds dimensions t4 D/4 ... of rows g, 8 + g
     // of the warp's item.  Those of the block's first part are asked for before
@@ -438,19 +454,17 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             }
         }
     };
-    load_q(s_seg);
+    load_q(s_now[warp]);
 
     // ---- the warp's loads, running ahead of its tiles: lane i holds where the
-    // warp's i-th tile from (s_ld, ld_k) on lies and copies it when its turn comes
-    int ld_k = 0;
-    bool more = true;  // there may be tiles from there on
+    // warp's i-th tile from (s_ld, s_ld_k) on; -1: none lies and copies it when its turn comes
     // sources of the lane's tile, one per page it lies in; the first with the
     // number of its units in the low bits
     uint64_t* desc = reinterpret_cast<uint64_t*>(smem + C::RING + C::OBUF + C::ML) + (warp * 32 + lane) * NU;
     uint32_t turn = 0;  // lanes that have a tile to copy
     auto refill = [&]() {
         Seg w = s_ld[warp];
-        int k = ld_k + lane;
+        int k = s_ld_k[warp] + lane;
         bool ok = true;
 #pragma unroll 1
         for (int c; ok && k >= (c = seg_tiles(sp, w, warp));) {
@@ -476,17 +490,20 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             }
         }
         turn = __ballot_sync(~0u, ok);
-        more = __shfl_sync(~0u, ok, 31);
-        // the next batch begins behind lane 31's tile
-        ld_k = __shfl_sync(~0u, k, 31) + 1;
         __syncwarp();
-        if (lane == 31) s_ld[warp] = w;
+        if (lane == 31) {  // the next batch begins behind this tile, if there is one
+            s_ld[warp] = w;
+            s_ld_k[warp] = ok ? k + 1 : -1;
+        }
         __syncwarp();
     };
     int issued = 0;
     auto issue = [&]() {
-        if (turn == 0 && more) refill();
-        if (turn == 0) return;
+        if (turn == 0) {
+            if (s_ld_k[warp] < 0) return false;
+            refill();
+            if (turn == 0) return false;
+        }
         if (lane == __ffs(turn) - 1 && !(p.fault == 1 && issued == 0)) {
             const int st = issued % C::STAGES;
             const uint32_t dst = ring + st * C::STAGE, bar = bars + 8 * st;
@@ -500,9 +517,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         turn &= turn - 1;
         ++issued;
+        return true;
     };
-    // MODE 0: what a lane's columns take of hi, 0 (columns 0 .. 3) or -1
-    const uint64_t part2 = t4 < 2 ? f2_pack(0.f, 0.f) : f2_pack(-1.f, -1.f);
     int used = 0;      // stages consumed
     auto leave = [&]() {  // waits ran out: let the copies in flight land
         for (; used < issued; ++used)
@@ -516,14 +532,13 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
     bool failed = false;
     // One loop over the beginning of each part, the warp's tiles in it and its
     // end, so that the code of the copies, which is long, exists once.
-    int len = 0, all_see = 0;   // all_see: keys every row may see; behind them scores are masked one by one
+    int len = 0;
     int key = 0, key_step = 0;  // first key of the warp's next tile, and from one to the next
     for (int count = -1;;) {    // count: tiles left
-        while (issued < used + C::STAGES && (turn != 0 || more)) issue();
+        while (issued < used + C::STAGES && issue()) {}
         if (count < 0) {
             const Seg& seg = s_now[warp];
             len = seg.len;
-            all_see = p.causal ? len - p.Lq + 1 : len;
             key = seg_tile(seg, warp, 0) * TILE;
             key_step = seg.solo ? TILE : kWarps * TILE;
             count = failed ? 0 : seg_tiles(sp, seg, warp);
@@ -581,7 +596,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 if (UG < NU && v0 > 0 && key + 16 * v0 >= len) break;
                 const int key0 = key + 16 * v0;
                 const uint32_t tile = stage + v0 * C::UNIT;
-                const bool border = key0 + 16 * UG > all_see;
+                const int all_see = p.causal ? len - p.Lq + 1 : len;  // keys every row may see
+                const bool border = key0 + 16 * UG > all_see;          // behind them scores are masked one by one
 
                 // ---- S^T = K Q^T.  Units behind the sequence's end hold old
                 // bytes: their scores are masked, their V scales zeroed.
@@ -743,7 +759,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                             const float2 f = f16x2_to_f32(hi);
                             if constexpr (MODE == 0) {
                                 // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take p - hi
-                                f2_unpack(f2_fma(f2_pack(f.x, f.y), part2, p2), x0, x1);
+                                const float take = t4 < 2 ? 0.f : -1.f;
+                                f2_unpack(f2_fma(f2_pack(f.x, f.y), f2_pack(take, take), p2), x0, x1);
                                 pb[u][nt][0][k8] = transpose8x8(f16x2(x0, x1));
                             } else {
                                 pb[u][nt][0][k8] = transpose8x8(hi);
@@ -837,6 +854,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         } else {  // ---- join the warps
             const bool whole = seg.t == 0 && seg.n == seg.nt;
             const int part = (int)blockIdx.x * 2 + (seg.t == 0 ? 1 : 0);
+            const Parts parts = parts_of<D, MODE>(p.part, gridDim.x);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -890,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 __syncthreads();
             }
             if (tid == 0 && seg.t == 0 && !whole) {
-                parts.join[blockIdx.x] = Cut{seg.b, item, last - seg.left + seg.nt, share};
+                parts.join[blockIdx.x] = Cut{seg.b, item, s_list.last - seg.left + seg.nt, s_list.share};
             }
         }
         if (!seg_next<D>(p, sp, seg)) break;
