@@ -58,7 +58,7 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdi
 SPLITKV_MAX_ROWS = 16  # (Hq / Hkv) * Lq limit of fa_fwd_splitkv
 NOALLOC_MAX_SEQS = 16384  # FA_NOALLOC_MAX_SEQS in include/fa_gb300.h
 KV4_MAX_ROWS = 64  # FA_KV4_MAX_ROWS: (Hq / Hkv) * Lq limit of fa_fwd_kv4
-KV4_RESERVE_NO_WORKSPACE = 2048  # FA_KV4_RESERVE_NO_WORKSPACE
+KV4_SEQS_WITHOUT_WORKSPACE = 2048  # FA_KV4_SEQS_WITHOUT_WORKSPACE: reserve and fork up to here
 KV4_MAX_SLOTS = 65536  # FA_KV4_MAX_SLOTS
 VARLEN_SEQS_PER_LAUNCH = 1536  # FA_VARLEN_SEQS_PER_LAUNCH (64 for head dimensions (192, 128))
 
@@ -923,7 +923,7 @@ def _attn_workspace(device, Hq, Hkv, Lq, D):
 
 @functools.lru_cache(maxsize=256)
 def kv4_pages_workspace(num_pages: int, n: int = 0) -> int:
-    """Workspace bytes fa_kv4_reserve, fa_kv4_fork and fa_kv4_compact (n = 0) need."""
+    """Workspace bytes fa_kv4_reserve, fa_kv4_fork (both above 2048 sequences) and fa_kv4_compact (n = 0) need."""
     nbytes = ctypes.c_size_t(0)
     st = load_library().fa_kv4_pages_workspace(num_pages, n, ctypes.byref(nbytes))
     if st != FA_OK:
@@ -970,8 +970,7 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
     if name == "fa_kv4_release":
         st = _on_device(device, lib.fa_kv4_release, first, n, pages, _raw_stream(device))
     else:
-        # few sequences: a reserve needs no workspace
-        nbytes = 0 if pool is None and n <= KV4_RESERVE_NO_WORKSPACE else kv4_pages_workspace(N, n)
+        nbytes = 0 if 0 < n <= KV4_SEQS_WITHOUT_WORKSPACE else kv4_pages_workspace(N, n)
         if info is None:
             info = torch.empty(2, dtype=torch.int32, device=refs.device)
         else:

@@ -1372,8 +1372,8 @@ fa_status_t kv4_pages(const fa_kv4_pages_t* c, bool pool, const int* ids, const 
     if (n > FA_KV4_MAX_SLOTS) return FA_ERR_INVALID_ARG;
     if (plan) {
         if (!info || !aligned4(info)) return FA_ERR_INVALID_ARG;
-        // a reserve (no pool) of few sequences keeps its prefix sums in shared memory
-        if ((pool || n > kKv4ReserveShared) &&
+        // reserve and fork (which name sequences) of few keep their prefix sums in shared memory
+        if ((n == 0 || n > kKv4SharedSeqs) &&
             (!workspace || !aligned16(workspace) || workspace_bytes < kv4_pages_workspace(c->num_pages, n)))
             return FA_ERR_INVALID_ARG;
     }

@@ -12,7 +12,7 @@ namespace fa {
 constexpr int kKv4Unit = 16;      // positions of one unit
 constexpr int kKv4MaxRows = 64;   // query rows that share a KV head
 constexpr int kKv4MaxSlots = 65536;
-constexpr int kKv4ReserveShared = 2048;  // sequences of a reserve that needs no workspace
+constexpr int kKv4SharedSeqs = 2048;  // sequences of a reserve or fork that needs no workspace
 
 // What every kernel on the cache reads.
 struct Kv4Cache {

@@ -17,9 +17,10 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
-// workspace, in int32: header | moves (source, target, units) or lists
+// workspace of compact, in int32: header | map | sources | targets; of
+// reserve and fork, where it has any: prefix sums
 constexpr int kWsCount = 0;  // page moves
-constexpr int kWsDone = 1;   // 1 = the call is carried out
+constexpr int kWsLive = 1;   // pages in use
 constexpr int kWsBase = 16;  // first entry behind the header
 
 __device__ __forceinline__ int pages_of(int len, int shift) { return (int)(((long long)len + (1 << shift) - 1) >> shift); }
@@ -160,17 +161,14 @@ __device__ __forceinline__ bool mark(PlanSmem& sm, int s)
     return (atomicOr(&sm.seen[s >> 5], bit) & bit) != 0;
 }
 
-// Refusal: info, and the latch for bad arguments.
+// Refusal: info, which also tells a second kernel, and the latch for bad
+// arguments.
 __device__ __forceinline__ bool refused(const Kv4PageParams& p, bool bad, int free_pages, long long need)
 {
     if (!bad && need <= free_pages) return false;
     if (threadIdx.x == 0) {
         p.info[0] = free_pages;
         p.info[1] = bad ? -1 : (int)min(need - free_pages, (long long)INT_MAX);
-        if (p.ws) {
-            p.ws[kWsCount] = 0;
-            p.ws[kWsDone] = 0;
-        }
         if (bad) atomicOr(p.err, 2);
     }
     return true;
@@ -181,9 +179,9 @@ __device__ __forceinline__ bool refused(const Kv4PageParams& p, bool bad, int fr
 __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4PageParams p)
 {
     __shared__ PlanSmem sm;
-    __shared__ int s_prefix[kKv4ReserveShared];
+    __shared__ int s_prefix[kKv4SharedSeqs];
     const int tid = threadIdx.x;
-    int* prefix = p.n <= kKv4ReserveShared ? s_prefix : p.ws + kWsBase;
+    int* prefix = p.n <= kKv4SharedSeqs ? s_prefix : p.ws;
     plan_begin(sm);
     long long need = 0;
     for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
@@ -232,9 +230,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_fork_plan_kernel(const Kv
 {
     let_dependents_launch();
     __shared__ PlanSmem sm;
+    __shared__ int s_prefix[kKv4SharedSeqs];
     const int tid = threadIdx.x, page_size = 1 << p.page_shift;
-    int* moves = p.ws + kWsBase;
-    int* prefix = moves + 3 * p.n;
+    int* prefix = p.n <= kKv4SharedSeqs ? s_prefix : p.ws;
     plan_begin(sm);
     for (int i = tid; i < p.n; i += kPlanThreads) {
         const int c = p.other[i];
@@ -266,58 +264,54 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_fork_plan_kernel(const Kv
     if (refused(p, sm.bad != 0, free_pages, need)) return;
     for_pages(p.refs, p.num_pages, rank, need, [](int, int r) { return r == 0; }, [&](int k, int page) {
         const int i = find_entry(prefix, p.n, k);
-        const int s = p.ids[i], len = p.lens[s], at = len >> p.page_shift;
-        moves[3 * k] = p.table[(long long)s * p.table_width + at];
-        moves[3 * k + 1] = page;
-        moves[3 * k + 2] = ((len & (page_size - 1)) + 15) >> 4;
-        p.table[(long long)p.other[i] * p.table_width + at] = page;
+        p.table[(long long)p.other[i] * p.table_width + (p.lens[p.ids[i]] >> p.page_shift)] = page;
         p.refs[page] = 1;
     });
     __syncthreads();
     for (int i = tid; i < p.n; i += kPlanThreads) p.lens[p.other[i]] = p.lens[p.ids[i]];
     if (tid == 0) {
-        p.ws[kWsCount] = need;
-        p.ws[kWsDone] = 1;
         p.info[0] = free_pages - need;
         p.info[1] = 0;
     }
 }
 
-// One warp copies the first units of one KV head's block of a page in one
-// layer; moves are {source, target, units} triples.
-__device__ __forceinline__ void copy_moves(const Kv4PageParams& p, int count, const int* src, const int* dst,
-                                           const int* units, int step)
+// One warp copies the first units of one KV head's block of a page in one layer.
+__device__ __forceinline__ void copy_block(const Kv4PageParams& p, int layer, int h, int src, int dst, int units)
 {
     constexpr int U = 6;  // 16-byte loads in flight per lane
-    const int lane = threadIdx.x & 31;
     const long long block = (long long)(18 * p.D) << (p.page_shift - 4);  // bytes of a head's block
-    const long long layer = block * p.Hkv * p.num_pages;
+    uint8_t* base = p.pool + (layer * (long long)p.num_pages * p.Hkv + h) * block;
+    const uint4* from = reinterpret_cast<const uint4*>(base + src * (block * p.Hkv));
+    uint4* to = reinterpret_cast<uint4*>(base + dst * (block * p.Hkv));
+    const int n = units * (18 * p.D / 16);
+    for (int v = threadIdx.x & 31; v < n; v += 32 * U) {
+        uint4 x[U];
+#pragma unroll
+        for (int e = 0; e < U; ++e)
+            if (v + 32 * e < n) x[e] = __ldcs(from + v + 32 * e);
+#pragma unroll
+        for (int e = 0; e < U; ++e)
+            if (v + 32 * e < n) __stcs(to + v + 32 * e, x[e]);
+    }
+}
+
+// Calls use(layer, k, head) for the warp's part of layers x count x heads.
+template <typename Use>
+__device__ __forceinline__ void for_blocks(const Kv4PageParams& p, int count, Use use)
+{
     const long long tasks = (long long)count * p.layers * p.Hkv;
     const long long stride = (long long)gridDim.x * (blockDim.x >> 5);
     for (long long t = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); t < tasks; t += stride) {
         const int h = (int)(t % p.Hkv);
         const long long r = t / p.Hkv;
-        const int k = (int)(r % count), l = (int)(r / count);
-        const int n = (units ? units[k * step] : 1 << (p.page_shift - 4)) * (18 * p.D / 16);
-        uint8_t* base = p.pool + l * layer + h * block;
-        const uint4* from = reinterpret_cast<const uint4*>(base + src[k * step] * (block * p.Hkv));
-        uint4* to = reinterpret_cast<uint4*>(base + dst[k * step] * (block * p.Hkv));
-        for (int v = lane; v < n; v += 32 * U) {
-            uint4 x[U];
-#pragma unroll
-            for (int e = 0; e < U; ++e)
-                if (v + 32 * e < n) x[e] = __ldcs(from + v + 32 * e);
-#pragma unroll
-            for (int e = 0; e < U; ++e)
-                if (v + 32 * e < n) __stcs(to + v + 32 * e, x[e]);
-        }
+        use((int)(r / count), (int)(r % count), h);
     }
 }
 
 __global__ void __launch_bounds__(256) fa_kv4_fork_kernel(const Kv4PageParams p)
 {
     wait_for_primary();
-    if (!p.ws[kWsDone]) return;
+    if (p.info[1] != 0) return;  // refused
     for (int i = blockIdx.x; i < p.n; i += gridDim.x) {
         const int s = p.ids[i], len = p.lens[s], full = len >> p.page_shift;
         const int own = (len & ((1 << p.page_shift) - 1)) ? full : -1;  // written by the plan
@@ -336,8 +330,12 @@ __global__ void __launch_bounds__(256) fa_kv4_fork_kernel(const Kv4PageParams p)
             to[j] = page;
         }
     }
-    const int* moves = p.ws + kWsBase;
-    copy_moves(p, p.ws[kWsCount], moves, moves + 1, moves + 2, 3);
+    for_blocks(p, p.n, [&](int layer, int i, int h) {  // the partly filled pages; the plan has checked both
+        const int s = p.ids[i], len = p.lens[s], at = len >> p.page_shift, rest = len & ((1 << p.page_shift) - 1);
+        if (rest)
+            copy_block(p, layer, h, p.table[(long long)s * p.table_width + at],
+                       p.table[(long long)p.other[i] * p.table_width + at], (rest + 15) >> 4);
+    });
 }
 
 // ------------------------------------------------------------------ release
@@ -409,8 +407,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_compact_plan_kernel(const
     }
     if (tid == 0) {
         p.ws[kWsCount] = movers;
-        p.ws[kWsDone] = 1;
-        p.ws[2] = live;
+        p.ws[kWsLive] = live;
         p.info[0] = n - live;
         p.info[1] = 0;
     }
@@ -419,9 +416,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_compact_plan_kernel(const
 __global__ void __launch_bounds__(256) fa_kv4_compact_kernel(const Kv4PageParams p)
 {
     wait_for_primary();
-    const int count = p.ws[kWsCount];
-    if (!p.ws[kWsDone] || count == 0) return;
-    const int live = p.ws[2];
+    if (p.info[1] != 0) return;  // refused
+    const int count = p.ws[kWsCount], live = p.ws[kWsLive];
+    if (count == 0) return;
     const int* map = p.ws + kWsBase;
     const int* src = map + p.num_pages;
     for (int s = blockIdx.x; s < p.num_slots; s += gridDim.x) {
@@ -437,14 +434,17 @@ __global__ void __launch_bounds__(256) fa_kv4_compact_kernel(const Kv4PageParams
                 atomicOr(p.err, 2);  // not a page in use
         }
     }
-    copy_moves(p, count, src, src + (p.num_pages + 1) / 2, nullptr, 1);
+    const int* dst = src + (p.num_pages + 1) / 2;
+    for_blocks(p, count, [&](int layer, int k, int h) {
+        copy_block(p, layer, h, src[k], dst[k], 1 << (p.page_shift - 4));
+    });
 }
 
 }  // namespace
 
 size_t kv4_pages_workspace(int num_pages, int n)
 {
-    return 4 * ((size_t)kWsBase + 2 * (size_t)num_pages + 2 + 4 * (size_t)n);
+    return 4 * ((size_t)kWsBase + 2 * (size_t)num_pages + 2 + (size_t)n);
 }
 
 cudaError_t launch_kv4_reserve(const Kv4PageParams& p, cudaStream_t stream)

@@ -495,8 +495,10 @@ fa_status_t fa_fwd_kv4_workspace(int B, int Hq, int Hkv, int Lq, int D, size_t* 
  *
  * workspace: DEVICE memory of at least fa_kv4_pages_workspace bytes, 16-byte
  * aligned; calls that overlap on the GPU need separate workspaces, and calls
- * on the same table must be ordered.
+ * on the same table must be ordered.  A reserve or fork of up to
+ * FA_KV4_SEQS_WITHOUT_WORKSPACE sequences needs none (NULL).
  */
+#define FA_KV4_SEQS_WITHOUT_WORKSPACE 2048
 typedef struct fa_kv4_pages {
     void* pool; /* [num_layers][num_pages][Hkv][page_size / 16][18 * D] bytes */
     int* table;
@@ -515,10 +517,8 @@ typedef struct fa_kv4_pages {
  * Makes room for new_tokens[i] >= 0 (int32 DEVICE [n]) more positions in slot
  * seq_ids[i] (NULL: slots 0 .. n - 1): gives it the pages it needs, with one
  * reference each, and adds the tokens to seq_lens.  A slot may be named again
- * only with 0 tokens.  The pool is not touched and may be NULL, and up to
- * FA_KV4_RESERVE_NO_WORKSPACE sequences so may the workspace.  1 kernel.
+ * only with 0 tokens.  The pool is not touched and may be NULL.  1 kernel.
  */
-#define FA_KV4_RESERVE_NO_WORKSPACE 2048
 fa_status_t fa_kv4_reserve(const int* seq_ids, const int* new_tokens, int n, const fa_kv4_pages_t* pages, int* info,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
 

@@ -420,6 +420,16 @@ def test_reserve_and_release_of_more_sequences_than_fit_in_shared_memory():
         m.release(out)
         fa.fa_check()
         assert dev[1].tolist() == m.table and dev[2].tolist() == m.lens and dev[3].tolist() == m.refs
+    empty = [s for s in range(S) if m.lens[s] == 0]
+    held = [s for s in range(S) if m.lens[s]]
+    kids = empty[:2049]
+    parents = [int(x) for x in rng.choice(held, len(kids))]
+    pool = rng.integers(0, 256, (1, 9000, 1, 1, 18 * 64), dtype=np.uint8)
+    dpool = torch.tensor(pool, device=DEV)
+    assert len(kids) == 2049
+    assert tuple(fa.fa_kv4_fork(i32(parents), i32(kids), dpool, *dev[1:]).tolist()) == m.fork(parents, kids, pool)
+    fa.fa_check()
+    _same_state(m, pool, (dpool, *dev[1:]), "fork of many")
 
 
 def test_page_operations_refuse_and_change_nothing():

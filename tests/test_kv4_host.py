@@ -92,9 +92,11 @@ def test_page_calls_are_refused(lib):
     assert lib.fa_kv4_reserve(None, None, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_reserve(None, 16, 0, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_reserve(None, 16, 2, p, None, 16, big, None) == INV
-    n = fa.KV4_RESERVE_NO_WORKSPACE + 1
+    n = fa.KV4_SEQS_WITHOUT_WORKSPACE + 1
     assert lib.fa_kv4_reserve(16, 16, n, p, 16, None, big, None) == INV    # up to 2048 sequences it needs none
     assert lib.fa_kv4_reserve(16, 16, n, p, 16, 16, 8, None) == INV        # workspace too small
+    assert lib.fa_kv4_fork(16, 16, n, p, 16, None, big, None) == INV
+    assert lib.fa_kv4_compact(p, 16, None, big, None) == INV
     assert lib.fa_kv4_fork(None, 16, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_fork(16, None, 2, p, 16, 16, big, None) == INV
     assert lib.fa_kv4_fork(16, 16, 65537, p, 16, 16, big, None) == INV
@@ -106,7 +108,7 @@ def test_page_calls_are_refused(lib):
     n = ctypes.c_size_t()
     assert lib.fa_kv4_pages_workspace(0, 1, ctypes.byref(n)) == INV
     assert lib.fa_kv4_pages_workspace(4, -1, ctypes.byref(n)) == INV
-    assert lib.fa_kv4_pages_workspace(1000, 10, ctypes.byref(n)) == fa.FA_OK and n.value >= 4 * (2 * 1000 + 4 * 10)
+    assert lib.fa_kv4_pages_workspace(1000, 10, ctypes.byref(n)) == fa.FA_OK and n.value >= 4 * (2 * 1000 + 10)
 
 
 def test_binding_checks_shapes_before_the_library():
