@@ -9,8 +9,6 @@
 
 namespace fa {
 
-constexpr int kKv4Unit = 16;      // positions of one unit
-constexpr int kKv4MaxRows = 64;   // query rows that share a KV head
 constexpr int kKv4MaxSlots = 65536;
 constexpr int kKv4SharedSeqs = 2048;  // sequences of a reserve or fork that needs no workspace
 

@@ -545,44 +545,44 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
             const int2 hc = head_and_chunk(min(seg_item(seg, warp), sp.items - 1), p.c.Hkv);
             const int h = hc.x, r0 = hc.y * C::ROWS;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint32_t(&x)[KS * 2] = qraw[nt];
-            uint32_t top = 0;
+            for (int nt = 0; nt < NT; ++nt) {
+                uint32_t(&x)[KS * 2] = qraw[nt];
+                uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < KS * 2; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            // power of two of the row: its largest magnitude comes to [1, 2)
-            const int e = top >= 0x7f80u || top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 126);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+                for (int i = 0; i < KS * 2; ++i) top = __vmaxu2(top, x[i] & 0x7fff7fffu);
+                top = max(top & 0xffffu, top >> 16);
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                // power of two of the row: its largest magnitude comes to [1, 2)
+                const int e = top >= 0x7f80u || top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 126);
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-            for (int i = 0; i < KS * 2; ++i) {
-                const uint32_t f = f16x2(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
-                if constexpr (MODE == 2)
-                    x[i] = f;
-                else
-                    qf[nt * KS * 2 + i] = f;
-            }
-            if constexpr (MODE == 2) {  // each lane reads back what it wrote
+                for (int i = 0; i < KS * 2; ++i) {
+                    const uint32_t f = f16x2(__uint_as_float(x[i] << 16) * down, __uint_as_float(x[i] & 0xffff0000u) * down);
+                    if constexpr (MODE == 2)
+                        x[i] = f;
+                    else
+                        qf[nt * KS * 2 + i] = f;
+                }
+                if constexpr (MODE == 2) {  // each lane reads back what it wrote
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qbuf + ((nt * KS + i) * 32 + lane) * 8),
+                                     "r"(x[2 * i]), "r"(x[2 * i + 1])
+                                     : "memory");
+                }
+                const float s = p.scale * 1.4426950408889634f * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
+                    m[nt][c] = -FLT_MAX;
+                    l[nt][c] = 0.f;
+                }
 #pragma unroll
                 for (int i = 0; i < KS; ++i)
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(qbuf + ((nt * KS + i) * 32 + lane) * 8),
-                                 "r"(x[2 * i]), "r"(x[2 * i + 1])
-                                 : "memory");
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
             }
-            const float s = p.scale * 1.4426950408889634f * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
-                m[nt][c] = -FLT_MAX;
-                l[nt][c] = 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[nt][i][c] = 0.f;
-        }
         }
         if (count > 0) {
             const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;

@@ -52,16 +52,6 @@ __device__ __forceinline__ int kv4_sequence(const Kv4Cache& c, int i, int& slot)
     return len;
 }
 
-// Page of a position of a sequence (position below its length); a bad page
-// number is latched and becomes page 0.
-__device__ __forceinline__ int kv4_page(const Kv4Cache& c, int slot, int pos)
-{
-    const int page = c.table[(long long)slot * c.table_width + (pos >> c.page_shift)];
-    if ((unsigned)page < (unsigned)c.num_pages) return page;
-    atomicOr(c.err, 2);
-    return 0;
-}
-
 // Byte offset of the unit of position pos of KV head h.
 __device__ __forceinline__ long long kv4_unit(const Kv4Cache& c, int D, int page, int h, int pos)
 {
