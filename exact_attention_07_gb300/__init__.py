@@ -995,7 +995,8 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
                    page_size: int, seq_ids: torch.Tensor | None = None, info: torch.Tensor | None = None,
                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Give slot seq_ids[i] (default i) pages for new_tokens[i] more positions and
-    count them in seq_lens.  Returns info, int32 [2] on the device: free pages
+    count them in seq_lens, or take its last -new_tokens[i] positions back where
+    that is negative (rejected drafts).  Returns info, int32 [2] on the device: free pages
     left, and 0, or the pages that were missing (then nothing was changed), or
     -1 for bad arguments on the device."""
     if stream is not None:

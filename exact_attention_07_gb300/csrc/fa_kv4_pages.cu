@@ -174,6 +174,21 @@ __device__ __forceinline__ bool refused(const Kv4PageParams& p, bool bad, int fr
     return true;
 }
 
+// Takes a reference from a page; 1 when that was the last.
+__device__ __forceinline__ int drop_page(const Kv4PageParams& p, int page)
+{
+    if ((unsigned)page >= (unsigned)p.num_pages) {
+        atomicOr(p.err, 2);
+        return 0;
+    }
+    const int held = atomicSub(p.refs + page, 1);
+    if (held <= 0) {  // no one held it
+        atomicAdd(p.refs + page, 1);
+        atomicOr(p.err, 2);
+    }
+    return held == 1;
+}
+
 // ------------------------------------------------------------------ reserve
 
 __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4PageParams p)
@@ -190,14 +205,19 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4P
         if (i < p.n) {
             const int s = p.ids ? p.ids[i] : i;
             const int add = p.other[i];
-            if (add < 0 || !slot_ok(p, s) || (add > 0 && mark(sm, s))) {
+            if (!slot_ok(p, s) || (add != 0 && mark(sm, s))) {
                 sm.bad = 1;
             } else {
                 const int len = p.lens[s];
-                if ((long long)len + add > ((long long)p.table_width << p.page_shift))
+                const long long to = (long long)len + add;
+                if (to < 0 || to > ((long long)p.table_width << p.page_shift))
                     sm.bad = 1;
-                else
-                    want = pages_of(len + add, p.page_shift) - pages_of(len, p.page_shift);
+                else if (add >= 0)
+                    want = pages_of((int)to, p.page_shift) - pages_of(len, p.page_shift);
+                else if (to & ((1 << p.page_shift) - 1)) {  // what becomes the partly filled page must be its own
+                    const int page = p.table[(long long)s * p.table_width + (to >> p.page_shift)];
+                    if ((unsigned)page >= (unsigned)p.num_pages || p.refs[page] != 1) sm.bad = 1;
+                }
             }
         }
         long long total;  // far more pages may be asked for than there are
@@ -216,10 +236,26 @@ __global__ void __launch_bounds__(kPlanThreads) fa_kv4_reserve_kernel(const Kv4P
         p.refs[page] = 1;
     });
     __syncthreads();
+    int freed = 0;  // by the warp's sequences that give tokens back
+    for (int i = tid >> 5; i < p.n; i += kPlanWarps) {
+        if (p.other[i] >= 0) continue;
+        const int s = p.ids ? p.ids[i] : i;
+        const int from = pages_of(p.lens[s] + p.other[i], p.page_shift), to = pages_of(p.lens[s], p.page_shift);
+        int* row = p.table + (long long)s * p.table_width;
+        for (int j = from + (tid & 31); j < to; j += 32) {
+            freed += drop_page(p, row[j]);
+            row[j] = -1;
+        }
+    }
+    freed = __reduce_add_sync(~0u, freed);
+    if ((tid & 31) == 0) sm.part[tid >> 5] = freed;
+    __syncthreads();
     for (int i = tid; i < p.n; i += kPlanThreads)
         if (p.other[i]) p.lens[p.ids ? p.ids[i] : i] += p.other[i];  // a slot named again adds nothing
     if (tid == 0) {
-        p.info[0] = free_pages - (int)need;
+        freed = 0;
+        for (int w = 0; w < kPlanWarps; ++w) freed += sm.part[w];
+        p.info[0] = free_pages - (int)need + freed;
         p.info[1] = 0;
     }
 }
@@ -358,15 +394,7 @@ __global__ void __launch_bounds__(128) fa_kv4_release_kernel(const Kv4PageParams
     __syncthreads();  // everyone has read the length
     const int n = pages_of(len, p.page_shift);
     int* row = p.table + (long long)s * p.table_width;
-    for (int j = threadIdx.x; j < n; j += blockDim.x) {
-        const int page = row[j];
-        if ((unsigned)page >= (unsigned)p.num_pages) {
-            atomicOr(p.err, 2);
-        } else if (atomicSub(p.refs + page, 1) <= 0) {  // no one held it
-            atomicAdd(p.refs + page, 1);
-            atomicOr(p.err, 2);
-        }
-    }
+    for (int j = threadIdx.x; j < n; j += blockDim.x) drop_page(p, row[j]);
     __syncthreads();
     for (int j = threadIdx.x; j < p.table_width; j += blockDim.x) row[j] = -1;
     if (threadIdx.x == 0) p.lens[s] = 0;

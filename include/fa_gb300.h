@@ -433,8 +433,9 @@ typedef struct fa_kv4 {
  * Each 16 consecutive dimensions x of a row, divided by the head's scale, get
  * the scale s = e4m3(max|x| / 6) (at most 448) and the codes e2m1(x / s), both
  * round to nearest even; codes beyond 6 become 6, a zero of either sign has
- * code 0, and s = 0 (max|x| up to 6 * 2^-10) gives zeros.  A group that holds a NaN or an infinity gets a NaN
- * scale, so that every value read from it is NaN.
+ * code 0, and s = 0 (max|x| up to 6 * 2^-10) gives zeros.  A group that holds
+ * a NaN or an infinity gets a NaN scale, so that every value read from it is
+ * NaN.
  *
  * Bytes of other positions keep their values.  A slot named twice in one call
  * (each time with rows) latches FA_ERR_INVALID_ARG, and what it then holds is
@@ -514,10 +515,14 @@ typedef struct fa_kv4_pages {
 } fa_kv4_pages_t;
 
 /*
- * Makes room for new_tokens[i] >= 0 (int32 DEVICE [n]) more positions in slot
+ * Makes room for new_tokens[i] (int32 DEVICE [n]) more positions in slot
  * seq_ids[i] (NULL: slots 0 .. n - 1): gives it the pages it needs, with one
- * reference each, and adds the tokens to seq_lens.  A slot may be named again
- * only with 0 tokens.  The pool is not touched and may be NULL.  1 kernel.
+ * reference each, and adds the tokens to seq_lens.  A negative number takes the
+ * last positions back (rejected drafts) and drops the pages behind the new
+ * end; the page that the end then lies in must be the sequence's own (a
+ * reference count of 1), else the call is refused.  Pages dropped are free for
+ * the next call.  A slot may be named again only with 0 tokens.  The pool is
+ * not touched and may be NULL.  1 kernel.
  */
 fa_status_t fa_kv4_reserve(const int* seq_ids, const int* new_tokens, int n, const fa_kv4_pages_t* pages, int* info,
                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
@@ -548,8 +553,8 @@ fa_status_t fa_kv4_release(const int* seq_ids, int n, const fa_kv4_pages_t* page
 fa_status_t fa_kv4_compact(const fa_kv4_pages_t* pages, int* info, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
-/* Workspace bytes of the three calls above for num_pages pages and n sequences
- * (n = 0 for fa_kv4_compact), written to *workspace_bytes. */
+/* Workspace bytes of reserve, fork and compact for num_pages pages and n
+ * sequences (n = 0 for fa_kv4_compact), written to *workspace_bytes. */
 fa_status_t fa_kv4_pages_workspace(int num_pages, int n, size_t* workspace_bytes);
 
 /*

@@ -141,12 +141,16 @@ class Pages:
     def reserve(self, slots, new):
         free = self._free()
         used = [s for s, a in zip(slots, new) if a]  # a slot may be named again with 0 tokens
-        bad = (len(set(used)) < len(used) or any(not 0 <= s < len(self.lens) for s in slots)
-               or any(a < 0 for a in new))
-        bad = bad or any(self.lens[s] + a > self.P * self.width for s, a in zip(slots, new))
-        if bad:
+        if len(set(used)) < len(used) or any(not 0 <= s < len(self.lens) for s in slots):
             return len(free), -1
-        need = [self._pages(self.lens[s] + a) - self._pages(self.lens[s]) for s, a in zip(slots, new)]
+        for s, a in zip(slots, new):
+            end = self.lens[s] + a
+            if not 0 <= end <= self.P * self.width:
+                return len(free), -1
+            # positions taken back: the page that the end comes to lie in must be the sequence's own
+            if a < 0 and end % self.P and self.refs[self.table[s][end // self.P]] != 1:
+                return len(free), -1
+        need = [max(0, self._pages(self.lens[s] + a) - self._pages(self.lens[s])) for s, a in zip(slots, new)]
         if sum(need) > len(free):
             return len(free), sum(need) - len(free)
         for s, a, c in zip(slots, new, need):
@@ -155,8 +159,11 @@ class Pages:
                 page = free.pop(0)
                 self.table[s][at + j] = page
                 self.refs[page] = 1
+            for j in range(self._pages(self.lens[s] + a), at):
+                self.refs[self.table[s][j]] -= 1
+                self.table[s][j] = -1
             self.lens[s] += a
-        return len(free), 0
+        return len(self._free()), 0
 
     def fork(self, parents, children, pool=None):
         free = self._free()

@@ -402,6 +402,39 @@ def test_page_operations_follow_the_sequential_model(N, slots, width, P, H, D, l
     assert {k[0] for k in done} == {"reserve", "fork", "release", "compact"}
 
 
+def test_positions_taken_back():
+    """Drafted tokens are rejected: pages behind the new end are dropped, a page that others use is left alone."""
+    rng = np.random.default_rng(18)
+    P = 16
+    m = kv4.Pages(40, 6, 6, P)
+    pool = rng.integers(0, 256, (1, 40, 1, 1, 18 * 64), dtype=np.uint8)
+    dev = _page_state(m, pool)
+
+    def both(ids, new):
+        want = m.reserve(ids, new)
+        assert tuple(fa.fa_kv4_reserve(i32(new), *dev[1:], P, seq_ids=i32(ids)).tolist()) == want
+        if want[1] < 0:
+            with pytest.raises(fa.FAError, match="invalid argument"):
+                fa.fa_check()
+        fa.fa_check()
+        _same_state(m, pool, dev, (ids, new))
+        return want[1]
+
+    assert both([0, 1], [50, 32]) == 0
+    fa.fa_kv4_fork(i32([0, 1]), i32([2, 3]), *dev)
+    m.fork([0, 1], [2, 3], pool)
+    assert both([0, 2, 4], [-1, 30, 5]) == 0        # within its own last page, growth beside it
+    assert both([0], [-2]) == -1                    # 47: a page shared with slot 2
+    assert both([0, 2], [-1, -32]) == 0             # 48 and 48: on the edge of shared pages
+    assert both([0, 2], [-16, -16]) == 0            # whole shared pages: a reference less each
+    assert both([3, 3, 0, 5], [-32, 0, 7, 0]) == 0  # nothing left of slot 3
+    assert both([1, 1], [-1, -1]) == -1             # a slot twice
+    assert both([1], [-1]) == 0                     # its page is its own again
+    for _ in range(60):
+        ids = [int(x) for x in rng.permutation(6)[:rng.integers(1, 7)]]
+        both(ids, [int(max(-m.lens[s], min(96 - m.lens[s], rng.integers(-40, 41)))) for s in ids])
+
+
 def test_reserve_and_release_of_more_sequences_than_fit_in_shared_memory():
     rng = np.random.default_rng(17)
     S, P = 5000, 16
@@ -454,7 +487,8 @@ def test_page_operations_refuse_and_change_nothing():
     reserve([0, 0], [1, 1])                     # a slot twice
     reserve([6], [1])
     reserve([-1], [1])
-    reserve([2], [-1])
+    reserve([2], [-1])                          # more than it has
+    reserve([0], [-41])
     reserve([2], [65])                          # beyond the table row
     reserve([2, 3, 4], [64, 64, 64], latched=False, info=4)
     reserve([2, 3], [2 ** 31 - 1, 2 ** 31 - 1])
