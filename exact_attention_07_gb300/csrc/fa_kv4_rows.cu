@@ -143,6 +143,23 @@ __device__ __forceinline__ uint32_t max_magnitude(uint32_t a, uint32_t x)
     return r;
 }
 
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Two bf16 each, brought into -bound .. bound.
+__device__ __forceinline__ uint32_t clamp_pair(uint32_t x, uint32_t bound)
+{
+    uint32_t r;
+    asm("{.reg .b32 t; min.bf16x2 t, %1, %2; max.bf16x2 %0, t, %3;}"
+        : "=r"(r)
+        : "r"(x), "r"(bound), "r"(bound ^ 0x80008000u));
+    return r;
+}
+
 struct Codes {
     uint32_t w[2];  // dimensions 0 .. 7, 8 .. 15
     uint32_t scale;
@@ -150,8 +167,10 @@ struct Codes {
 
 // Quantises a group.  head6 = 6 * head scale, r6 its reciprocal.  The maximum
 // is taken on the magnitudes' bits, where infinities and NaN come out above
-// every number; such a group gets a NaN scale and zero codes.
-__device__ __forceinline__ Codes quantise_group(const Group& x, float head, float head6, float r6)
+// every number; such a group gets a NaN scale and zero codes.  Quotients that
+// could overflow are brought to 512 (the scale) and 8 (values of a group that
+// the largest scale does not reach), which round as anything above them.
+__device__ __forceinline__ Codes quantise_group(Group& x, float head, float head6, float r6)
 {
     uint32_t m = 0;
 #pragma unroll
@@ -161,12 +180,17 @@ __device__ __forceinline__ Codes quantise_group(const Group& x, float head, floa
     uint16_t pair;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
         : "=h"(pair)
-        : "f"(0.f), "f"(bad ? 0.f : quotient(__uint_as_float(top << 16), head6, r6)));
+        : "f"(0.f), "f"(bad ? 0.f : quotient(fminf(__uint_as_float(top << 16), 512.f * head6), head6, r6)));
     Codes c;
     c.scale = bad ? 0x7fu : (uint32_t)pair;
     const float s = f16x2_to_f32(e4m3x2_to_f16x2(pair)).x * head;
     const float r = pair == 0 ? 0.f : rcp_approx(s);
     const uint64_t r2 = f2_pack(r, r), s2 = f2_pack(-s, -s);
+    if (pair == 0x7e) {
+        const uint32_t bound = bf16x2(8.f * s, 8.f * s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x.w[i] = clamp_pair(x.w[i], bound);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         uint64_t y[4];
@@ -277,13 +301,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 

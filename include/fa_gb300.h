@@ -394,7 +394,8 @@ fa_status_t fa_bwd_varlen_variant(const void* q, const void* k, const void* v, c
  *   seq_lens  int32 [num_slots]
  *   seq_ids   int32, the slot of each sequence of the call, or NULL for the
  *             slots 0, 1, 2, ... in order
- *   k_scale, v_scale  fp32 [Hkv], positive and finite, or NULL for 1
+ *   k_scale, v_scale  fp32 [Hkv], from 2^-64 to 2^64, or NULL for 1 (beyond
+ *             that range a head's values are unspecified)
  *   D 64 or 128; page_size 16, 32, 64, 128 or 256 (FA_ERR_UNSUPPORTED
  *   otherwise); num_slots at most 65536; table_width * page_size at most 2^30.
  *

@@ -340,6 +340,26 @@ def test_rows_at_addresses_that_are_not_32_byte_aligned():
     fa.fa_check()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_of_rows_of_every_magnitude(D):
+    """Groups from the smallest to the largest bf16 numbers under the smallest and largest head scales: what is above
+    6 * 448 of them takes the largest scale and codes.  Scales are powers of two, so every byte is the oracle's."""
+    rng = np.random.default_rng(20 + D)
+    H, P, T = 4, 32, 90
+    heads = np.array([2.0 ** -64, 2.0 ** -3, 1.0, 2.0 ** 64], np.float32)
+    pool, table = random_cache(rng, [T + 5], H, D, P)
+    x = rng.standard_normal((2, T, H, D // 16, 16)) * 10.0 ** rng.uniform(-38, 37.9, (2, T, H, D // 16, 1))
+    x[:, :6] = np.sign(x[:, :6]) * 10.0 ** rng.uniform(36, 38.5, (2, 6, H, D // 16, 16))
+    k, v = (bf16(t.reshape(T, H, D)).to(DEV) for t in x)
+    assert k.isfinite().all() and v.isfinite().all()
+    scales = torch.tensor(heads, device=DEV)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32([T + 5]))
+    fa.fa_kv4_append(k, v, i32([0, T]), *dev, k_scale=scales, v_scale=scales)
+    fa.fa_check()
+    kv4.append(pool, table, [T + 5], [0], [T], f64(k), f64(v), heads.astype(float), heads.astype(float))
+    same_bytes(dev[0].cpu().numpy(), pool, "append")
+
+
 def test_no_rows_at_all():
     pool, table, lens = fa.kv4_pool(2, 1, 16, 64), i32([[0], [1]]), i32([3, 0])
     none = torch.zeros(0, 1, 64, dtype=torch.bfloat16, device=DEV)
