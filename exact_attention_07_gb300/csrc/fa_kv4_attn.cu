@@ -574,7 +574,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 const float s = p.scale * 1.4426950408889634f * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.f);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    sc[nt][c] = s * __shfl_sync(~0u, up, (2 * t4 + c) * 4);
+                    // kept off 0 and infinity, whose product with a masked score
+                    // (-infinity) or a score of 0 would be NaN
+                    sc[nt][c] = fminf(fmaxf(s * __shfl_sync(~0u, up, (2 * t4 + c) * 4), FLT_MIN), FLT_MAX);
                     m[nt][c] = -FLT_MAX;
                     l[nt][c] = 0.f;
                 }

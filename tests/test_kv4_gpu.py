@@ -224,6 +224,23 @@ def test_queries_of_every_magnitude():
     check_attention(q, o, lse, pool, table, [0], [300], np.ones(1), np.ones(1), float(scale), False, "magnitudes")
 
 
+@pytest.mark.parametrize("scale,head,mult", [(2.0 ** -30, 2.0 ** -64, 2.0 ** -100), (2.0 ** 60, 2.0 ** 64, 2.0 ** 100)])
+def test_factors_beyond_the_range_of_fp32_leave_masked_keys_out(scale, head, mult):
+    """softmax_scale, a head scale and a row's power of two whose product underflows (all scores are 0) or overflows
+    (against keys that are 0, so that all scores are 0 again): each row's mean of the values that it sees."""
+    rng = np.random.default_rng(21)
+    Hq, Lq, D, P, L = 2, 3, 64, 32, 75
+    pool, table = random_cache(rng, [L], 1, D, P)
+    if mult > 1:
+        used = table[0, :-(-L // P)]
+        pool[used, :, :, :8 * D] = 0
+        pool[used, :, :, 16 * D:17 * D] = 0
+    q = bf16(rng.standard_normal((1, Hq, Lq, D)) * mult).to(DEV)
+    o, lse = run_attention(q, torch.tensor(pool, device=DEV), i32(table), i32([L]), causal=True, softmax_scale=scale,
+                           k_scale=torch.tensor([head], dtype=torch.float32, device=DEV))
+    check_attention(q, o, lse, pool, table, [0], [L], np.array([head]), np.ones(1), scale, True, "factors")
+
+
 def test_long_cache_with_offsets_beyond_32_bits():
     H, D, P = 2, 128, 256
     page_bytes = H * P // 16 * 18 * D
