@@ -906,8 +906,8 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     nbytes = _attn_workspace(device, Hq, H, Lq, D)
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != device:
-        raise ValueError(f"workspace must be on {q.device}, got {workspace.device}")
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {q.device}, got {workspace.device}")
     st = _on_device(device, lib.fa_fwd_kv4, q.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Lq,
                     1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(device))
     if st != FA_OK:
@@ -977,8 +977,8 @@ def _page_call(name, pool, page_size, table, seq_lens, refs, first, second, n, i
             _want(info, "info", torch.int32, 1, device)
             if info.shape[0] != 2:
                 raise ValueError("info must hold 2 numbers")
-        if workspace is not None and workspace.get_device() != device:
-            raise ValueError(f"workspace must be on {refs.device}, got {workspace.device}")
+        if workspace is not None and (workspace.get_device() != device or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous and on {refs.device}, got {workspace.device}")
         if nbytes and (workspace is None or workspace.numel() * workspace.element_size() < nbytes):
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=refs.device)
         tail = (pages, info.data_ptr(), workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(device))

@@ -746,6 +746,16 @@ def test_too_small_a_workspace_is_refused():
                               None) == fa.FA_ERR_INVALID_ARG
 
 
+def test_a_workspace_that_covers_less_memory_than_it_has_elements_is_refused():
+    pool, table, lens, refs = fa.kv4_pool(4, 2, 16, 64), i32([[0, 1], [2, 3]]), i32([3, 4]), i32([1, 0, 1, 0])
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV)
+    wide = torch.zeros(1, dtype=torch.uint8, device=DEV).expand(fa.kv4_workspace(2, 4, 2, 1, 64))
+    with pytest.raises(ValueError, match="contiguous"):
+        fa.fa_fwd_kv4(q, pool, table, lens, workspace=wide)
+    with pytest.raises(ValueError, match="contiguous"):
+        fa.fa_kv4_compact(pool, table, lens, refs, workspace=wide)
+
+
 def test_captured_decode_step_follows_the_cache():
     """reserve, append and attention captured once and replayed: each replay is one more token."""
     rng = np.random.default_rng(10)
