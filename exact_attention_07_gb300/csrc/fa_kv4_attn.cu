@@ -588,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
         }
         if (count > 0) {
             const uint32_t st = used % C::STAGES, stage = ring + st * C::STAGE;
-            if (!mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used)) {
+            // each lane polls for itself: the warp goes one way, together, whatever its lanes saw
+            const bool ok = mbar_wait(bars + 8 * st, (used / C::STAGES) & 1, abort_flag, wf, 50, used);
+            if (!__all_sync(~0u, ok)) {
                 failed = true;
                 count = 0;
                 continue;

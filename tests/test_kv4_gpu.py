@@ -843,6 +843,25 @@ def test_a_load_that_never_arrives_ends_the_call_with_a_timeout():
     check_attention(q, o, lse, pool, table, [0, 1], [500, 40], np.ones(2), np.ones(2), 0.125, False, "after a timeout")
 
 
+@pytest.mark.parametrize("Hq,Hkv,Lq,D", [(8, 2, 1, 128), (7, 1, 1, 128), (16, 1, 1, 128), (10, 1, 4, 64), (16, 2, 1, 64)])
+def test_a_timeout_ends_all_warps_of_every_form(Hq, Hkv, Lq, D):
+    """Warps that wait on different tiles of long sequences, beside short ones of a warp each: some lanes see the time
+    limit and some the flag of another warp, and the block leaves as one."""
+    rng = np.random.default_rng(30 + Hq + D)
+    lens = [9000, 4000] + [60] * 30
+    pool, table = random_cache(rng, lens, Hkv, D, 64)
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32(lens))
+    q = bf16(rng.standard_normal((len(lens), Hq, Lq, D))).to(DEV)
+    want = run_attention(q, *dev, causal=True)
+    fa.load_library().fa_test_inject_fault(1)
+    fa.fa_fwd_kv4(q, *dev, causal=True)
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_check()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    got = run_attention(q, *dev, causal=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_two_calls_at_once_on_two_streams():
     rng = np.random.default_rng(11)
     lens = [2000, 3, 700]
