@@ -23,12 +23,12 @@
 // Codes times scales are exact in fp16 (2 + 4 significant bits, 2^-10 to
 // 2688).  q becomes fp16 after a power of two per row (its row's largest
 // magnitude in [1, 2)): exact down to 2^-17 of that.  P is the sum of two
-// fp16 numbers, hi = fp16(p) and lo = fp16(p - hi): with up to 4 rows the two
-// fill the 8 columns of one MMA, with up to 8 they take two.
+// fp16 numbers, hi and 2^-11 lo (kHead, below): with up to 4 rows the two fill
+// the 8 columns of one MMA, with up to 8 they take two.
 //
 // Each warp streams tiles of 4608 bytes through a ring of its own with
 // cp.async.bulk (no block-wide step in the loop), keeps its own maximum, sum
-// and O^T, and raises the maximum only when a score exceeds it by 2^8, so
+// and O^T, and raises the maximum only when a score exceeds it by 2^3, so
 // that the rescaling and its shuffles are rare.  The work of all sequences is
 // one list, cut evenly over the blocks (two an SM, 128 registers a thread)
 // from the lengths on the device; an item that lies in several blocks is
@@ -57,7 +57,14 @@ constexpr int kThreads = 32 * kWarps;
 // short sequences took 107 us where items counted only by their tiles), and
 // what beginning a group of items of one warp each does.
 constexpr int kItemCost = 24, kSoloCost = 16;
-constexpr float kRaise = 8.f;  // log2 of how far a score may exceed the running maximum
+// P is held as two fp16 numbers, hi = fp16(p) and lo = fp16(2^11 (p - hi)): to
+// 22 bits, or to 2^-36.  p is 2^kHead where a score equals the maximum, which
+// is raised when a score exceeds it by 2^kRaise.  A key so has its 22 bits
+// where it weighs 2^-19 of the heaviest that its warp has seen, and is lost
+// below 2^-41 of that.  p stays below 2^8 where fp16 ends at 2^16: the rest is
+// for scores so large that their own ulp is up to 8.
+constexpr float kHead = 5.f, kRaise = 3.f;
+constexpr float kLoUp = 2048.f, kLoDown = 1.f / kLoUp;
 
 // Keys of a warp's tile: 4608 bytes.
 __host__ __device__ constexpr int tile_keys(int D) { return D == 128 ? 32 : 64; }
@@ -656,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     va_s[u] = e4m3x2_to_f16x2(lds_u16(at));
                     vb_s[u] = e4m3x2_to_f16x2(lds_u16(at + 8));
                 }
-                // ---- masks, the running maximum in log2 units
+                // ---- masks, the running maximum less kHead, in log2 units
                 if (border) {
                     int lim[NT][2];  // keys that the columns' rows see
                     const int r0 = head_and_chunk(min(seg_item(s_now[warp], warp), sp.items - 1), p.c.Hkv).y * C::ROWS;
@@ -723,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
 #pragma unroll
                         for (int u = 1; u < UG; ++u) x = fmaxf(x, fmaxf(s[u][nt][c], s[u][nt][c + 2]));
                         mx[nt][c] = x * sc[nt][c];
-                        raise |= mx[nt][c] > m[nt][c] + kRaise;
+                        raise |= mx[nt][c] > m[nt][c] + (kHead + kRaise);
                     }
                 if (__any_sync(~0u, raise)) {
 #pragma unroll
@@ -734,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                            x = fmaxf(x, m[nt][c]);
+                            x = fmaxf(x - kHead, m[nt][c]);
                             const float a = x == m[nt][c] ? 1.f : ex2_approx(m[nt][c] - x);
                             m[nt][c] = x;
                             l[nt][c] *= a;
@@ -762,13 +769,16 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                             const uint32_t hi = f16x2(x0, x1);
                             const float2 f = f16x2_to_f32(hi);
                             if constexpr (MODE == 0) {
-                                // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take p - hi
-                                const float take = t4 < 2 ? 0.f : -1.f;
-                                f2_unpack(f2_fma(f2_pack(f.x, f.y), f2_pack(take, take), p2), x0, x1);
+                                // lanes of columns 0 .. 3 keep p, which rounds to hi; those of 4 .. 7 take lo
+                                const float take = t4 < 2 ? 0.f : -1.f, up = t4 < 2 ? 1.f : kLoUp;
+                                const uint64_t y2 = f2_fma(f2_pack(f.x, f.y), f2_pack(take, take), p2);
+                                f2_unpack(f2_mul(y2, f2_pack(up, up)), x0, x1);
                                 pb[u][nt][0][k8] = transpose8x8(f16x2(x0, x1));
                             } else {
+                                const uint64_t y2 = f2_fma(f2_pack(f.x, f.y), f2_pack(-1.f, -1.f), p2);
+                                f2_unpack(f2_mul(y2, f2_pack(kLoUp, kLoUp)), x0, x1);
                                 pb[u][nt][0][k8] = transpose8x8(hi);
-                                pb[u][nt][1][k8] = transpose8x8(f16x2(x0 - f.x, x1 - f.y));
+                                pb[u][nt][1][k8] = transpose8x8(f16x2(x0, x1));
                             }
                         }
                     f2_unpack(l2, l[nt][0], l[nt][1]);
@@ -794,24 +804,64 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 }
                 auto step = [&](auto ii) {
                     constexpr int i = decltype(ii)::value;
-                    float part[NT][4];
+                    // lo's share comes down by 2^-11: with up to 8 rows from an
+                    // accumulator of its own, with more, where registers are
+                    // short, before hi's is added to the same one (8 rows at 8 x
+                    // 32768 keys, D = 128: 66.3 us against 70.7; 16 rows of 6
+                    // sequences of 900 .. 9001, D = 64: 15.1 against 14.8)
+                    float part[NT][4], low[4];
+                    if constexpr (MODE == 2) {
+                        const uint64_t down = f2_pack(kLoDown, kLoDown);
+                        uint32_t a[UG][4];
 #pragma unroll
-                    for (int u = 0; u < UG; ++u) {
-                        const uint32_t sa = va_s[u], sb = vb_s[u];
-                        const uint32_t a0 = hmul2(code_pair<2 * i>(va[u]), sa), a1 = hmul2(code_pair<2 * i + 1>(va[u]), sa);
-                        const uint32_t a2 = hmul2(code_pair<2 * i>(vb[u]), sb), a3 = hmul2(code_pair<2 * i + 1>(vb[u]), sb);
+                        for (int u = 0; u < UG; ++u) {
+                            a[u][0] = hmul2(code_pair<2 * i>(va[u]), va_s[u]);
+                            a[u][1] = hmul2(code_pair<2 * i + 1>(va[u]), va_s[u]);
+                            a[u][2] = hmul2(code_pair<2 * i>(vb[u]), vb_s[u]);
+                            a[u][3] = hmul2(code_pair<2 * i + 1>(vb[u]), vb_s[u]);
+                        }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
+                        for (int half = 1; half >= 0; --half)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                                for (int u = 0; u < UG; ++u) {
+                                    const uint32_t(&b)[2] = pb[u][nt][half];
+                                    if (half == 1 && u == 0)
+                                        mma_f16_first(part[nt], a[u][0], a[u][1], a[u][2], a[u][3], b[0], b[1]);
+                                    else
+                                        mma_f16(part[nt], a[u][0], a[u][1], a[u][2], a[u][3], b[0], b[1]);
+                                }
+                                if (half == 0) continue;
+                                f2_unpack(f2_mul(f2_pack(part[nt][0], part[nt][1]), down), part[nt][0], part[nt][1]);
+                                f2_unpack(f2_mul(f2_pack(part[nt][2], part[nt][3]), down), part[nt][2], part[nt][3]);
+                            }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < UG; ++u) {
+                            const uint32_t sa = va_s[u], sb = vb_s[u];
+                            const uint32_t a0 = hmul2(code_pair<2 * i>(va[u]), sa), a1 = hmul2(code_pair<2 * i + 1>(va[u]), sa);
+                            const uint32_t a2 = hmul2(code_pair<2 * i>(vb[u]), sb), a3 = hmul2(code_pair<2 * i + 1>(vb[u]), sb);
                             if (u == 0)
-                                mma_f16_first(part[nt], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
+                                mma_f16_first(part[0], a0, a1, a2, a3, pb[u][0][0][0], pb[u][0][0][1]);
                             else
-                                mma_f16(part[nt], a0, a1, a2, a3, pb[u][nt][0][0], pb[u][nt][0][1]);
-                            if constexpr (MODE != 0) mma_f16(part[nt], a0, a1, a2, a3, pb[u][nt][1][0], pb[u][nt][1][1]);
+                                mma_f16(part[0], a0, a1, a2, a3, pb[u][0][0][0], pb[u][0][0][1]);
+                            if constexpr (MODE == 1) {
+                                if (u == 0)
+                                    mma_f16_first(low, a0, a1, a2, a3, pb[u][0][1][0], pb[u][0][1][1]);
+                                else
+                                    mma_f16(low, a0, a1, a2, a3, pb[u][0][1][0], pb[u][0][1][1]);
+                            }
                         }
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float(&o)[4] = acc[nt][i];
+                        if constexpr (MODE == 1) {
+                            const uint64_t down = f2_pack(kLoDown, kLoDown);
+                            f2_unpack(f2_fma(f2_pack(low[0], low[1]), down, f2_pack(o[0], o[1])), o[0], o[1]);
+                            f2_unpack(f2_fma(f2_pack(low[2], low[3]), down, f2_pack(o[2], o[3])), o[2], o[3]);
+                        }
                         f2_unpack(f2_add(f2_pack(o[0], o[1]), f2_pack(part[nt][0], part[nt][1])), o[0], o[1]);
                         f2_unpack(f2_add(f2_pack(o[2], o[3]), f2_pack(part[nt][2], part[nt][3])), o[2], o[3]);
                     }
@@ -847,8 +897,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                     for (int i = 0; i < KS; ++i) {
                         float y = acc[nt][i][c], z = acc[nt][i][c + 2];
                         if constexpr (MODE == 0) {  // hi's share and lo's
-                            y += __shfl_xor_sync(~0u, y, 2);
-                            z += __shfl_xor_sync(~0u, z, 2);
+                            y = fmaf(__shfl_xor_sync(~0u, y, 2), kLoDown, y);
+                            z = fmaf(__shfl_xor_sync(~0u, z, 2), kLoDown, z);
                         }
                         if (on) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(y * inv, z * inv);
                     }
@@ -897,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                         const float2 ml = mlbuf[w * C::ROWS + r];
                         const float a = ml.x == mm ? 1.f : ex2_approx(ml.x - mm);
                         float v = obuf[(w * 8 + col) * C::OSTRIDE + at];
-                        if constexpr (MODE == 0) v += obuf[(w * 8 + col + 4) * C::OSTRIDE + at];
+                        if constexpr (MODE == 0) v = fmaf(obuf[(w * 8 + col + 4) * C::OSTRIDE + at], kLoDown, v);
                         o = fmaf(a, v, o);
                         sum = fmaf(a, ml.y, sum);
                     }

@@ -470,9 +470,12 @@ fa_status_t fa_kv4_read(void* k, void* v, const int* cu_seqlens, int num_seqs, i
  *   workspace: DEVICE memory of at least fa_fwd_kv4_workspace bytes, 16-byte
  *   aligned; calls that overlap on the GPU need separate workspaces.
  *
- * Codes times scales are exact in fp16, the scores, softmax statistics and O
- * accumulate in fp32, and P enters P.V as the sum of two fp16 numbers (22
- * bits).  The work is cut evenly over the GPU from the lengths on the device.
+ * Codes times scales are exact in fp16, and the scores, softmax statistics and
+ * O accumulate in fp32.  P enters P.V as the sum of two fp16 numbers: a key
+ * that weighs 2^-19 of its row's heaviest and more has 22 bits, a lighter one
+ * an error of at most 2^-41 of the heaviest.  Scores (softmax_scale q.k log2 e)
+ * are to stay below 2^26 in magnitude; O and LSE are unspecified beyond.
+ * The work is cut evenly over the GPU from the lengths on the device.
  * 2 kernels.
  */
 fa_status_t fa_fwd_kv4(const void* q, float* o, float* lse, int B, int Hq, int Lq, int causal,

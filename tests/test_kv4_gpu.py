@@ -241,6 +241,41 @@ def test_factors_beyond_the_range_of_fp32_leave_masked_keys_out(scale, head, mul
     check_attention(q, o, lse, pool, table, [0], [L], np.array([head]), np.ones(1), scale, True, "factors")
 
 
+@pytest.mark.parametrize("Hq,Lq,D", [(16, 1, 128), (28, 1, 128), (16, 3, 128), (8, 1, 64), (16, 2, 64), (80, 1, 64)])
+@pytest.mark.parametrize("B", [1024, 3])
+def test_keys_far_below_a_heavy_one_keep_their_weight(Hq, Lq, D, B):
+    """The first key weighs e^2 to e^20 times as much as each other one and its value is 0, so O is what the others
+    carry.  All keys of a row but the first have one score, so a rounding of P does not average out.  With 1024
+    sequences a warp takes a whole one, with 3 they are cut.
+
+    P is good to 2^-22, or to 2^-41 of the heaviest key.  Scores are single products here: the factor of the scores has
+    three roundings and the exponent's argument, up to 20 / ln 2 + 5, one, together 35 * 2^-22 * ln 2 = 5.8e-6 of a
+    weight; 2^x and the division are good to 2^-22 each; all values have one sign, so 25 tiles, two steps of a product
+    and 8 warps lose at most 25 * 2^-24 + 2 * 2^-23 + 8 * 2^-24 = 2.2e-6 of their sum.  Together below 2^-16."""
+    rng = np.random.default_rng(40 + Hq + Lq + D)
+    H, P, L = 4, 64, 777
+    need = -(-L // P)
+    pool, row = np.zeros((need, H, P // 16, 18 * D), np.uint8), list(range(need))
+    k, v = rng.standard_normal((2, L, H, D))
+    k[..., :16], v = 0, np.abs(v)
+    k[0, :, 0], v[0] = 6, 0
+    one = np.ones(H)
+    kv4.append(pool, [row], [L], [0], [L], k, v, one, one)
+    lens = [int(x) for x in rng.integers(2, L + 1, B)] if B > 3 else [2, 600, L]
+    scale = 1 / math.sqrt(D)
+    x = np.zeros((B, Hq, Lq, D))
+    x[..., 0] = rng.uniform(2, 20, (B, Hq, Lq)) / (6 * scale)
+    q = bf16(x).to(DEV)
+    gap = f64(q)[..., 0] * 6 * scale
+    o, lse = run_attention(q, torch.tensor(pool, device=DEV), i32([row] * B), i32(lens))
+    go, gl = f64(o), f64(lse)
+    for b in range(0, B, 37) if B > 3 else range(B):
+        ro, rl = kv4.attention(f64(q[b]), *kv4.rows(pool, [row], 0, lens[b], one, one), scale, False)
+        bound = 2.0 ** -16 + 2.0 ** -41 * np.exp(gap[b])
+        assert (np.abs(go[b] - ro) <= ro * bound[..., None]).all(), (b, lens[b], np.abs(go[b] - ro).max())
+        assert (np.abs(gl[b] - rl) <= 2.0 ** -16 + 2.0 ** -22 * np.abs(rl)).all()
+
+
 def test_long_cache_with_offsets_beyond_32_bits():
     H, D, P = 2, 128, 256
     page_bytes = H * P // 16 * 18 * D
