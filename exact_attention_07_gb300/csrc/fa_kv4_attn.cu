@@ -21,10 +21,11 @@
 //   exponential, turned by movmatrix)
 //
 // Codes times scales are exact in fp16 (2 + 4 significant bits, 2^-10 to
-// 2688).  q becomes fp16 after a power of two per row (its row's largest
-// magnitude in [1, 2)): exact down to 2^-17 of that.  P is the sum of two
-// fp16 numbers, hi and 2^-11 lo (kHead, below): with up to 4 rows the two fill
-// the 8 columns of one MMA, with up to 8 they take two.
+// 2688).  q becomes fp16 after a power of two per row, which brings the row's
+// largest magnitude to the top of fp16's range, [2^15, 2^16): exact down to
+// 2^-32 of that.  P is the sum of two fp16 numbers, hi and 2^-11 lo (kHead,
+// below): with up to 4 rows the two fill the 8 columns of one MMA, with up to
+// 8 they take two.
 //
 // Each warp streams tiles of 4608 bytes through a ring of its own with
 // cp.async.bulk (no block-wide step in the loop), keeps its own maximum, sum
@@ -560,8 +561,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa_kv4_attn_kernel(const Kv4AttnP
                 top = max(top & 0xffffu, top >> 16);
                 top = max(top, __shfl_xor_sync(~0u, top, 1));
                 top = max(top, __shfl_xor_sync(~0u, top, 2));
-                // power of two of the row: its largest magnitude comes to [1, 2)
-                const int e = top >= 0x7f80u || top == 0 ? 0 : min(max((int)(top >> 7) - 127, -120), 126);
+                // power of two of the row: its largest magnitude comes to [2^15, 2^16),
+                // or as near as a normal power of two brings it
+                const int e = top >= 0x7f80u || top == 0 ? 0 : max((int)(top >> 7) - (127 + 15), -126);
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
                 for (int i = 0; i < KS * 2; ++i) {

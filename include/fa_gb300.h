@@ -471,7 +471,9 @@ fa_status_t fa_kv4_read(void* k, void* v, const int* cu_seqlens, int num_seqs, i
  *   aligned; calls that overlap on the GPU need separate workspaces.
  *
  * Codes times scales are exact in fp16, and the scores, softmax statistics and
- * O accumulate in fp32.  P enters P.V as the sum of two fp16 numbers: a key
+ * O accumulate in fp32.  q enters q.k as fp16 with a power of two per row:
+ * exact down to 2^-32 of the row's largest magnitude, below that to 2^-40 of
+ * it.  P enters P.V as the sum of two fp16 numbers: a key
  * that weighs 2^-19 of its row's heaviest and more has 22 bits, a lighter one
  * an error of at most 2^-41 of the heaviest.  Scores (softmax_scale q.k log2 e)
  * are to stay below 2^26 in magnitude; O and LSE are unspecified beyond.

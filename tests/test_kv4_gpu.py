@@ -224,6 +224,28 @@ def test_queries_of_every_magnitude():
     check_attention(q, o, lse, pool, table, [0], [300], np.ones(1), np.ones(1), float(scale), False, "magnitudes")
 
 
+@pytest.mark.parametrize("Hq,Lq,D", [(4, 1, 128), (8, 1, 64), (16, 1, 128), (8, 2, 64), (40, 1, 128), (16, 2, 64)])
+def test_small_elements_of_a_query_beside_large_ones(Hq, Lq, D):
+    """Rows whose first elements, which meet keys of 0 there, are 2^16 or 2^24 times the others: the scores are those of
+    the others.  Where the row's largest magnitude is below 2^27, elements from 2^-6 on are exact and those below, one
+    or two of 112, are off by 2^-14 at most: against keys of normal numbers 2^-14 sqrt(1.4 / 3) / sqrt(128) < 2^-17 of
+    a weight in the mean.  fp32 adds 2^-18 (as in the test of the mean error)."""
+    rng = np.random.default_rng(60 + Hq + Lq + D)
+    H, P, lens = 4 if Hq == 4 else 2, 64, [300, 41, 777]
+    pool, table = random_cache(rng, lens, H, D, P)
+    pool[..., :8 * D].reshape(*pool.shape[:3], 16, D // 2)[..., :8] = 0  # K codes of the dimensions 0 .. 15
+    x = rng.standard_normal((len(lens), Hq, Lq, D))
+    x[..., :16] *= 2.0 ** 16
+    x[:, ::2, :, :16] *= 2.0 ** 8
+    q = bf16(x).to(DEV)
+    o, lse = run_attention(q, torch.tensor(pool, device=DEV), i32(table), i32(lens), causal=True)
+    for b, n in enumerate(lens):
+        ro, rl = kv4.attention(f64(q[b]), *kv4.rows(pool, table, b, n, np.ones(H), np.ones(H)), 1 / math.sqrt(D), True)
+        err = math.sqrt(np.square(f64(o[b]) - ro).mean() / np.square(ro).mean())
+        assert err < 2.0 ** -17 + 2.0 ** -18, (b, err)
+        assert np.abs(f64(lse[b]) - rl).max() < 2.0 ** -15
+
+
 @pytest.mark.parametrize("scale,head,mult", [(2.0 ** -30, 2.0 ** -64, 2.0 ** -100), (2.0 ** 60, 2.0 ** 64, 2.0 ** 100)])
 def test_factors_beyond_the_range_of_fp32_leave_masked_keys_out(scale, head, mult):
     """softmax_scale, a head scale and a row's power of two whose product underflows (all scores are 0) or overflows
