@@ -732,12 +732,19 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _on_stream(stream, fn, *args):
-    """fn(*args) with `stream` (a torch stream or a raw handle) current, so that what it allocates belongs to that
-    stream; the results may then be used on the caller's stream once that waits for it."""
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    here = torch.cuda.current_stream(stream.device)
+def _on_stream(stream, like, fn, *args):
+    """fn(*args) with `stream` current: a torch stream, or a raw handle, of the device that `like`, a tensor of the
+    call, is on.  What the call allocates belongs to that stream; the results may then be used on the caller's stream
+    once that waits for it."""
+    device = like.get_device() if isinstance(like, torch.Tensor) else -1
+    if device < 0:
+        return fn(*args)  # which refuses it
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    if stream.device.index != device:
+        raise ValueError(f"stream must be of cuda:{device}, got one of {stream.device}")
+    here = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
         got = fn(*args)
     for t in got if isinstance(got, tuple) else (got,):
@@ -812,7 +819,8 @@ def fa_kv4_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, po
     [cu_seqlens[s], cu_seqlens[s+1]) become the last positions of sequence s
     (slot seq_ids[s], default s), which seq_lens already counts."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_append, k, v, cu_seqlens, pool, table, seq_lens, seq_ids, k_scale, v_scale)
+        return _on_stream(stream, pool, fa_kv4_append, k, v, cu_seqlens, pool, table, seq_lens, seq_ids, k_scale,
+                          v_scale)
     n = _num_seqs(cu_seqlens)
     c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
     _want(k, "k", torch.bfloat16, 3, device)
@@ -835,8 +843,8 @@ def fa_kv4_read(cu_seqlens: torch.Tensor, total: int, pool: torch.Tensor, table:
     packed bf16 rows (k, v), each [total,Hkv,D]: a cached prefix as the keys
     of fa_fwd_varlen.  Rows behind the last sequence are left as they were."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_read, cu_seqlens, total, pool, table, seq_lens, seq_ids, k_scale, v_scale, k_out,
-                          v_out)
+        return _on_stream(stream, pool, fa_kv4_read, cu_seqlens, total, pool, table, seq_lens, seq_ids, k_scale,
+                          v_scale, k_out, v_out)
     n = _num_seqs(cu_seqlens)
     c, device, H, D = _kv4(pool, table, seq_lens, seq_ids, k_scale, v_scale, n)
     _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
@@ -880,8 +888,8 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     first seq_lens positions; with ``causal`` the queries are the last Lq of
     them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
     if stream is not None:
-        return _on_stream(stream, fa_fwd_kv4, q, pool, table, seq_lens, causal, softmax_scale, seq_ids, k_scale, v_scale, out,
-                          lse, workspace)
+        return _on_stream(stream, pool, fa_fwd_kv4, q, pool, table, seq_lens, causal, softmax_scale, seq_ids,
+                          k_scale, v_scale, out, lse, workspace)
     if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.is_cuda):
         _check_tensor(q, "q", torch.bfloat16, 4)
     B, Hq, Lq, D = q.shape
@@ -1000,7 +1008,8 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
     left, and 0, or the pages that were missing (then nothing was changed), or
     -1 for bad arguments on the device."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_reserve, new_tokens, table, seq_lens, refs, page_size, seq_ids, info, workspace)
+        return _on_stream(stream, refs, fa_kv4_reserve, new_tokens, table, seq_lens, refs, page_size, seq_ids, info,
+                          workspace)
     device = _refs_device(refs)
     _want(new_tokens, "new_tokens", torch.int32, 1, device)
     n = new_tokens.shape[0]
@@ -1019,7 +1028,8 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     are shared, a partly filled last page is copied.  pool as for
     fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_fork, parents, children, pool, table, seq_lens, refs, info, workspace)
+        return _on_stream(stream, refs, fa_kv4_fork, parents, children, pool, table, seq_lens, refs, info,
+                          workspace)
     device = _refs_device(refs)
     _want(parents, "parents", torch.int32, 1, device)
     _want(children, "children", torch.int32, 1, device)
@@ -1034,7 +1044,7 @@ def fa_kv4_release(seq_ids: torch.Tensor, table: torch.Tensor, seq_lens: torch.T
                    page_size: int, stream=None) -> None:
     """Free the slots seq_ids: their pages lose a reference each, their lengths become 0."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_release, seq_ids, table, seq_lens, refs, page_size)
+        return _on_stream(stream, refs, fa_kv4_release, seq_ids, table, seq_lens, refs, page_size)
     device = _refs_device(refs)
     _want(seq_ids, "seq_ids", torch.int32, 1, device)
     _page_call("fa_kv4_release", None, page_size, table, seq_lens, refs, seq_ids.data_ptr(), None, seq_ids.shape[0],
@@ -1046,7 +1056,7 @@ def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tens
                    stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
     if stream is not None:
-        return _on_stream(stream, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace)
+        return _on_stream(stream, refs, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace)
     return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace,
                       _refs_device(refs))
 

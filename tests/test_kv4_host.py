@@ -1,4 +1,5 @@
 """Refusals of the 4-bit cache's entry points that need no GPU."""
+import contextlib
 import ctypes
 
 import pytest
@@ -120,3 +121,92 @@ def test_binding_checks_shapes_before_the_library():
     with pytest.raises(ValueError, match="CUDA tensor"):
         fa.fa_fwd_kv4(torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16), pool[0], torch.zeros(1, 2, dtype=i32),
                       torch.zeros(1, dtype=i32))
+
+
+class FakeStream:
+    def __init__(self, device, handle):
+        self.device, self.cuda_stream = torch.device("cuda", device), handle
+
+
+class OnCuda1(torch.Tensor):
+    """A host tensor that says it is on cuda:1 and keeps the streams it is recorded on."""
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+    def record_stream(self, stream):
+        self.__dict__.setdefault("recorded", []).append(stream.cuda_stream)
+
+
+@pytest.fixture
+def two_gpus(monkeypatch):
+    """Two devices of the CUDA runtime's host side, cuda:0 current, and a library that keeps (call, device, stream)."""
+    now, current, calls = [0], {0: FakeStream(0, 100), 1: FakeStream(1, 200)}, []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, now[0] = now[0], torch.device("cuda", index).index if isinstance(index, int) else index.index
+        yield
+        now[0] = before
+
+    @contextlib.contextmanager
+    def stream(s):
+        before, current[s.device.index] = current[s.device.index], s
+        with device(s.device):
+            yield
+        current[s.device.index] = before
+
+    def index_of(device):
+        return now[0] if device is None else torch.device("cuda", device).index if isinstance(device, int) else device.index
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: calls.append((name, now[0], args[-1])) or fa.FA_OK
+
+    monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: FakeStream(index_of(device), handle))
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: FakeStream(index_of(device), 0))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[index_of(device)])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: now[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: current[index].cuda_stream)
+    monkeypatch.setattr(fa, "_lib", Library())
+    monkeypatch.setattr(fa, "_attn_workspace", lambda *args: 64)
+    monkeypatch.setattr(fa, "kv4_pages_workspace", lambda *args: 64)
+    return calls
+
+
+def kv4_calls():
+    """Every call that takes a stream, on tensors of cuda:1, and the workspace it is given (or None)."""
+    def there(*shape, dtype=torch.int32):
+        return torch.zeros(shape, dtype=dtype).as_subclass(OnCuda1)
+
+    pool, table, lens, refs = there(4, 2, 1, 18 * 64, dtype=torch.uint8), there(2, 2), there(2), there(4)
+    q, kv, cu = there(2, 4, 1, 64, dtype=torch.bfloat16), there(3, 2, 64, dtype=torch.bfloat16), there(3)
+    o, lse, info = there(2, 4, 1, 64, dtype=torch.float32), there(2, 4, 1, dtype=torch.float32), there(2)
+    ws = [there(64, dtype=torch.uint8) for _ in range(4)]
+    return [
+        ("fa_kv4_append", lambda s: fa.fa_kv4_append(kv, kv, cu, pool, table, lens, stream=s), None),
+        ("fa_kv4_read", lambda s: fa.fa_kv4_read(cu, 3, pool, table, lens, k_out=kv, v_out=kv, stream=s), None),
+        ("fa_fwd_kv4", lambda s: fa.fa_fwd_kv4(q, pool, table, lens, out=o, lse=lse, workspace=ws[0], stream=s), ws[0]),
+        ("fa_kv4_reserve", lambda s: fa.fa_kv4_reserve(lens, table, lens, refs, 16, info=info, workspace=ws[1], stream=s),
+         ws[1]),
+        ("fa_kv4_fork", lambda s: fa.fa_kv4_fork(lens, lens, pool, table, lens, refs, info=info, workspace=ws[2], stream=s),
+         ws[2]),
+        ("fa_kv4_release", lambda s: fa.fa_kv4_release(lens, table, lens, refs, 16, stream=s), None),
+        ("fa_kv4_compact", lambda s: fa.fa_kv4_compact(pool, table, lens, refs, info=info, workspace=ws[3], stream=s), ws[3]),
+    ]
+
+
+def test_a_stream_is_one_of_the_tensors_device(two_gpus):
+    for name, call, _ in kv4_calls():
+        for stream, handle in ((7, 7), (0, 0), (FakeStream(1, 55), 55), (None, 200)):
+            two_gpus.clear()
+            call(stream)
+            assert two_gpus == [(name, 1, handle)]
+        two_gpus.clear()
+        with pytest.raises(ValueError, match="stream"):
+            call(FakeStream(0, 66))
+        assert two_gpus == []
