@@ -732,21 +732,26 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _on_stream(stream, like, fn, *args):
-    """fn(*args) with `stream` current: a torch stream, or a raw handle, of the device that `like`, a tensor of the
-    call, is on.  What the call allocates belongs to that stream; the results may then be used on the caller's stream
-    once that waits for it."""
+def _on_stream(stream, like, fn, *args, **scratch):
+    """fn(*args, **scratch) with `stream` current: a torch stream, or a raw handle, of the device that `like`, a tensor
+    of the call, is on.  What the call allocates belongs to that stream; the results may then be used on the caller's
+    stream once that waits for it.  A caller's workspace (`scratch`) is kept out of reuse until a torch stream is done
+    with it."""
     device = like.get_device() if isinstance(like, torch.Tensor) else -1
     if device < 0:
-        return fn(*args)  # which refuses it
-    if not isinstance(stream, torch.cuda.Stream):
+        return fn(*args, **scratch)  # which refuses it
+    named = isinstance(stream, torch.cuda.Stream)
+    if not named:
         handle = _stream_handle(stream)
         stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     if stream.device.index != device:
         raise ValueError(f"stream must be of cuda:{device}, got one of {stream.device}")
     here = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        got = fn(*args)
+        got = fn(*args, **scratch)
+    for t in scratch.values():
+        if named and t is not None and t.get_device() == device:
+            t.record_stream(stream)
     for t in got if isinstance(got, tuple) else (got,):
         if t is not None:
             t.record_stream(here)
@@ -889,7 +894,7 @@ def fa_fwd_kv4(q: torch.Tensor, pool: torch.Tensor, table: torch.Tensor, seq_len
     them.  Returns (o [B,Hq,Lq,D] fp32, lse [B,Hq,Lq] fp32)."""
     if stream is not None:
         return _on_stream(stream, pool, fa_fwd_kv4, q, pool, table, seq_lens, causal, softmax_scale, seq_ids,
-                          k_scale, v_scale, out, lse, workspace)
+                          k_scale, v_scale, out, lse, workspace=workspace)
     if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.dim() == 4 and q.is_contiguous() and q.is_cuda):
         _check_tensor(q, "q", torch.bfloat16, 4)
     B, Hq, Lq, D = q.shape
@@ -1009,7 +1014,7 @@ def fa_kv4_reserve(new_tokens: torch.Tensor, table: torch.Tensor, seq_lens: torc
     -1 for bad arguments on the device."""
     if stream is not None:
         return _on_stream(stream, refs, fa_kv4_reserve, new_tokens, table, seq_lens, refs, page_size, seq_ids, info,
-                          workspace)
+                          workspace=workspace)
     device = _refs_device(refs)
     _want(new_tokens, "new_tokens", torch.int32, 1, device)
     n = new_tokens.shape[0]
@@ -1029,7 +1034,7 @@ def fa_kv4_fork(parents: torch.Tensor, children: torch.Tensor, pool: torch.Tenso
     fa_kv4_append, or with the layers in front.  Returns info as fa_kv4_reserve."""
     if stream is not None:
         return _on_stream(stream, refs, fa_kv4_fork, parents, children, pool, table, seq_lens, refs, info,
-                          workspace)
+                          workspace=workspace)
     device = _refs_device(refs)
     _want(parents, "parents", torch.int32, 1, device)
     _want(children, "children", torch.int32, 1, device)
@@ -1056,7 +1061,7 @@ def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tens
                    stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool (of every layer).  Returns info as fa_kv4_reserve."""
     if stream is not None:
-        return _on_stream(stream, refs, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace)
+        return _on_stream(stream, refs, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace=workspace)
     return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace,
                       _refs_device(refs))
 

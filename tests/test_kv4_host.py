@@ -210,3 +210,10 @@ def test_a_stream_is_one_of_the_tensors_device(two_gpus):
         with pytest.raises(ValueError, match="stream"):
             call(FakeStream(0, 66))
         assert two_gpus == []
+
+
+def test_a_callers_workspace_is_kept_until_its_stream_is_done(two_gpus):
+    for name, call, ws in kv4_calls():
+        call(FakeStream(1, 55))
+        call(None)  # on the current stream, whose order protects it
+        assert ws is None or ws.recorded == [55], name
