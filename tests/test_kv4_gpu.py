@@ -416,6 +416,57 @@ def test_append_and_read_match_the_oracle(H, D, P, old, new, scaled, named):
         row += c
 
 
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_append_under_head_scales_rounds_to_the_nearest(D, P):
+    """Head 0 has a power of two for its scale: its bytes are the oracle's, as are all that the call does not own.
+    Elsewhere 6 g and s g (g the head's scale, s the group's) are rounded to fp32 before a quotient by them, which is
+    rounded itself: two relative errors of 2^-24 each.  A scale or code may so be the other neighbour where the
+    quotient lies within 2^-22 of the border between two, and nowhere else."""
+    rng = np.random.default_rng(70 + D)
+    H, old, new, slots = 5, [3, 0, 40, 17], [60, 33, 1, 14], [3, 0, 4, 1]
+    heads = {"k": np.array([0.25, 1.1, 0.7001, 3e-5, 7.3e6], np.float32), "v": np.array([8, 0.9, 1.37, 1.3e4, 2e-7], np.float32)}
+    lens = [16] * 5
+    for i, s in enumerate(slots):
+        lens[s] = old[i] + new[i]
+    pool, table = random_cache(rng, lens, H, D, P)
+    T = sum(new)
+    x = {n: f64(bf16(rng.standard_normal((T, H, D)) * np.exp(rng.standard_normal((T, H, 1)) * 2) * heads[n][:, None]))
+         for n in "kv"}
+    dev = (torch.tensor(pool, device=DEV), i32(table), i32(lens))
+    fa.fa_kv4_append(bf16(x["k"]).to(DEV), bf16(x["v"]).to(DEV), i32(np.concatenate([[0], np.cumsum(new)])), *dev,
+                     seq_ids=i32(slots), k_scale=torch.tensor(heads["k"], device=DEV),
+                     v_scale=torch.tensor(heads["v"], device=DEV))
+    fa.fa_check()
+    want, got = pool.copy(), dev[0].cpu().numpy()
+    g = {n: heads[n].astype(float) for n in "kv"}
+    kv4.append(want, table, lens, slots, new, x["k"], x["v"], g["k"], g["v"])
+    kc, ks = kv4.quantise(x["k"], g["k"])
+    vc, vs = kv4.quantise(x["v"], g["v"])
+    d, grp = np.arange(D), np.arange(D // 16)
+    row = 0
+    for i, s in enumerate(slots):
+        for pos in range(old[i], lens[s]):
+            for h in range(1, H):
+                unit, key = got[table[s][pos // P], h, pos % P // 16], pos % 16
+                k = unit[key * (D // 2):(key + 1) * (D // 2)]
+                v = unit[8 * D + key // 8 * 4 * D + d // 16 * 64 + key % 8 // 2 * 16 + d % 16]
+                have = {"k": (np.stack([k & 15, k >> 4], 1).reshape(D), unit[16 * D + key * (D // 16) + grp]),
+                        "v": (v >> 4 if key % 2 else v & 15, unit[17 * D + grp * 16 + key])}
+                for n, (codes, scales) in have.items():
+                    y = np.abs(x[n][row, h]).reshape(D // 16, 16) / g[n][h]
+                    top = y.max(1) / 6
+                    off = np.abs(top[:, None] - kv4.E4M3)
+                    assert (off[grp, scales] <= off.min(1) + 2.0 ** -22 * top).all(), (n, pos, h)
+                    e = kv4.E4M3[scales][:, None]
+                    z = np.where(e > 0, y / np.where(e > 0, e, 1), 0).reshape(D)  # a scale of 0: codes of 0
+                    off = np.abs(z[:, None] - kv4.E2M1)
+                    assert (off[d, codes & 7] <= off.min(1) + 2.0 ** -22 * z).all(), (n, pos, h)
+                    assert ((codes >> 3) == ((x[n][row, h] < 0) & (e > 0).repeat(16))).all(), (n, pos, h)
+                kv4.write_row(unit, key, D, kc[row, h], ks[row, h], vc[row, h], vs[row, h])
+            row += 1
+    same_bytes(got, want, "append")
+
+
 def test_rows_at_addresses_that_are_not_32_byte_aligned():
     rng = np.random.default_rng(13)
     H, D, P = 2, 64, 16
