@@ -35,12 +35,14 @@
 // from the lengths on the device; an item that lies in several blocks is
 // joined by a second kernel.
 //
-// Measured (device time): 8 sequences of 32768 keys, 32 x 8 heads, D = 128,
-// 58 us, 76 % of the copy bandwidth; of 131072 keys 193 us, 92 %: about 14 us
-// go into finding the share, the first copies, the last warps and the join.
-// What the tile loop has in registers decides: 90 bytes spilled in place of 38
-// took 212 us there, 12 warps of 168 registers in place of 16 took 66 us
-// here.
+// Measured (device time): 8 sequences of 32768 keys, 32 x 8 heads, D = 128, 4
+// rows, 59 us, 75 % of the copy bandwidth; of 131072 keys 196 us, 91 %: about
+// 14 us go into finding the share, the first copies, the last warps and the
+// join.  8 rows take 68 us, 16 rows 118, more go in chunks of 16.  What the
+// tile loop has in registers decides (spilled at D = 128: 38 bytes with up to
+// 4 rows, 70 with up to 8, 376 with more; at D = 64: 0, 18, 18): 90 bytes in
+// place of 38 took 10 % more at 131072 keys, 12 warps of 168 registers in
+// place of 16 took 66 us in place of 62 at 32768.
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -56,7 +58,9 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 // What beginning and joining an item costs a block, in tiles (the lists of
 // short sequences took 107 us where items counted only by their tiles), and
-// what beginning a group of items of one warp each does.
+// what beginning a group of items of one warp each does.  From a sweep with up
+// to 4 rows and D = 128; with more rows a tile costs up to twice as much and
+// the same weights serve.
 constexpr int kItemCost = 24, kSoloCost = 16;
 // P is held as two fp16 numbers, hi = fp16(p) and lo = fp16(2^11 (p - hi)): to
 // 22 bits, or to 2^-36.  p is 2^kHead where a score equals the maximum, which

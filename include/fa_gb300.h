@@ -403,9 +403,11 @@ fa_status_t fa_bwd_varlen_variant(const void* q, const void* k, const void* v, c
  * slot out of range, a length that is negative or above table_width *
  * page_size, or a page number out of range latches FA_ERR_INVALID_ARG (read
  * by fa_check).  Nothing is read or written out of range then; what that
- * sequence's outputs hold is unspecified.  These calls allocate nothing,
- * copy nothing to the host and may be captured into a graph.  A batch is
- * padded by naming an empty slot, as often as needed, with no rows.
+ * sequence's outputs hold is unspecified.  Slots, lengths and table must stay
+ * as they are while a call that reads them runs: calls that change them are
+ * ordered with it.  These calls allocate nothing, copy nothing to the host and
+ * may be captured into a graph.  A batch is padded by naming an empty slot, as
+ * often as needed, with no rows.
  */
 #define FA_KV4_MAX_SLOTS 65536
 #define FA_KV4_MAX_ROWS 64
@@ -546,8 +548,8 @@ fa_status_t fa_kv4_fork(const int* parents, const int* children, int n, const fa
 
 /*
  * Frees the slots seq_ids[i]: each page loses one reference, the table row
- * becomes -1 and the length 0.  Empty slots and slots named again are left
- * alone.  The pool is not touched and may be NULL.  1 kernel.
+ * becomes -1 and the length 0.  A slot may be empty or named again: no page
+ * loses a reference for it then.  The pool is not touched and may be NULL.  1 kernel.
  */
 fa_status_t fa_kv4_release(const int* seq_ids, int n, const fa_kv4_pages_t* pages, cudaStream_t stream);
 
