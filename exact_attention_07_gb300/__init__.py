@@ -23,6 +23,19 @@ int32 [slots], refs int32 [pages]; layout in include/fa_gb300.h):
     info = fa_kv4_fork(parents, children, pool, table, seq_lens, refs)          # share and copy pages
     fa_kv4_release(seq_ids, table, seq_lens, refs, page_size)
     info = fa_kv4_compact(pool, table, seq_lens, refs)
+
+Rotary positions, and a paged KV cache in bf16 (pool bf16 [pages, 2, Hkv, page_size, D]; table, lengths, fa_kv4_reserve
+and fa_kv4_release as above) for decoding, drafted trees and chunks of prompts:
+
+    rope = rope_plan(D, base=500000.0)                                          # frequencies, on the device
+    q, k = fa_rope(q, k, rope, positions)                                       # packed or dense rows
+    dq, dk = fa_rope_bwd(dq, dk, rope, positions, dtype=torch.bfloat16)
+    pool = kv16_pool(pages, Hkv, page_size, D)
+    mask, depth = draft_mask(parents, cu_seqlens)                               # of drafted trees
+    q = fa_kv16_append(k, v, cu_seqlens, pool, table, seq_lens, rope=rope, positions=positions, q=q)
+    o, lse = fa_fwd_kv16(q, cu_seqlens, pool, table, seq_lens, mask=mask)       # or causal=True
+    back = fa_kv16_keep(keep, counts, cu_seqlens, pool, table, seq_lens)        # accepted nodes to the front
+    info = fa_kv4_reserve(back, table, seq_lens, refs, page_size)               # the others' positions given back
 """
 from __future__ import annotations
 
@@ -32,6 +45,7 @@ import math
 import os
 import struct
 import threading
+from fractions import Fraction
 
 import torch
 
@@ -39,7 +53,8 @@ __all__ = ["fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdim", "fa_f
            "fa_fwd_splitkv", "fp8_prepare", "fa_fwd_fp8", "fp8_sections", "splitkv_workspace", "fa_bwd",
            "bwd_workspace", "fa_bwd_varlen", "bwd_varlen_workspace", "fa_bwd_variant", "fa_bwd_varlen_variant",
            "kv4_pool", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4", "kv4_workspace", "fa_kv4_reserve", "fa_kv4_fork",
-           "fa_kv4_release", "fa_kv4_compact", "kv4_pages_workspace", "fa_check", "fa_status_string", "fa_last_launch_count",
+           "fa_kv4_release", "fa_kv4_compact", "kv4_pages_workspace", "RopePlan", "rope_plan", "fa_rope", "fa_rope_bwd",
+           "kv16_pool", "fa_kv16_append", "fa_fwd_kv16", "kv16_workspace", "fa_kv16_keep", "draft_mask", "fa_check", "fa_status_string", "fa_last_launch_count",
            "FAError", "library_path", "load_library", "EXPORTED_SYMBOLS"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -53,7 +68,8 @@ EXPORTED_SYMBOLS = ("fa_fwd", "fa_fwd_varlen", "fa_fwd_hdim", "fa_fwd_varlen_hdi
                     "fa_bwd_varlen_workspace", "fa_bwd_variant", "fa_bwd_varlen_variant", "fa_fp8_workspace",
                     "fa_fp8_prepare", "fa_fwd_fp8", "fa_kv4_append", "fa_kv4_read", "fa_fwd_kv4",
                     "fa_fwd_kv4_workspace", "fa_kv4_reserve", "fa_kv4_fork", "fa_kv4_release", "fa_kv4_compact",
-                    "fa_kv4_pages_workspace", "fa_check", "fa_status_string", "fa_last_launch_count",
+                    "fa_kv4_pages_workspace", "fa_rope", "fa_rope_bwd", "fa_kv16_append", "fa_fwd_kv16",
+                    "fa_fwd_kv16_workspace", "fa_kv16_keep", "fa_check", "fa_status_string", "fa_last_launch_count",
                     "fa_test_inject_fault")
 SPLITKV_MAX_ROWS = 16  # (Hq / Hkv) * Lq limit of fa_fwd_splitkv
 NOALLOC_MAX_SEQS = 16384  # FA_NOALLOC_MAX_SEQS in include/fa_gb300.h
@@ -79,6 +95,25 @@ class _KV4Pages(ctypes.Structure):
     # struct fa_kv4_pages in include/fa_gb300.h
     _fields_ = [(n, ctypes.c_void_p) for n in ("pool", "table", "seq_lens", "refs")] + [
         (n, ctypes.c_int) for n in ("num_pages", "num_slots", "table_width", "page_size", "Hkv", "D", "num_layers")]
+
+
+class _Rope(ctypes.Structure):
+    # struct fa_rope in include/fa_gb300.h
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("start", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("mscale", ctypes.c_float)]
+
+
+class _RotaryRows(ctypes.Structure):
+    # struct fa_rotary_rows in include/fa_gb300.h
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_longlong) for n in ("x_batch", "x_token", "x_head", "y_batch", "y_token", "y_head")] + [
+        ("heads", ctypes.c_int)]
+
+
+class _KV16(ctypes.Structure):
+    # struct fa_kv16 in include/fa_gb300.h
+    _fields_ = [(n, ctypes.c_void_p) for n in ("pool", "table", "seq_lens", "seq_ids")] + [
+        (n, ctypes.c_int) for n in ("num_pages", "num_slots", "table_width", "page_size", "Hkv", "D")]
 
 
 class FAError(RuntimeError):
@@ -144,14 +179,20 @@ def load_library() -> ctypes.CDLL:
         lib.fa_bwd_varlen_workspace.restype = i
         lib.fa_bwd_varlen_workspace.argtypes = [i, i, i, ctypes.POINTER(ctypes.c_size_t)]
         c4 = pg = ctypes.c_void_p  # a packed struct (bytes) or byref of a _KV4 or _KV4Pages
-        sz = ctypes.c_size_t
+        sz, ll = ctypes.c_size_t, ctypes.c_longlong
         for name, args in (("fa_kv4_append", [vp, vp, vp, i, i, c4, vp]), ("fa_kv4_read", [vp, vp, vp, i, i, c4, vp]),
                            ("fa_fwd_kv4", [vp, vp, vp, i, i, i, i, f, c4, vp, sz, vp]),
                            ("fa_fwd_kv4_workspace", [i, i, i, i, i, ctypes.POINTER(sz)]),
                            ("fa_kv4_reserve", [vp, vp, i, pg, vp, vp, sz, vp]),
                            ("fa_kv4_fork", [vp, vp, i, pg, vp, vp, sz, vp]), ("fa_kv4_release", [vp, i, pg, vp]),
                            ("fa_kv4_compact", [pg, vp, vp, sz, vp]),
-                           ("fa_kv4_pages_workspace", [i, i, ctypes.POINTER(sz)])):
+                           ("fa_kv4_pages_workspace", [i, i, ctypes.POINTER(sz)]),
+                           ("fa_rope", [vp, vp, i, i, i, i, i, vp, vp, ll, vp]),
+                           ("fa_rope_bwd", [vp, vp, i, i, i, i, i, vp, vp, ll, vp]),
+                           ("fa_kv16_append", [vp, vp, vp, vp, i, i, vp, vp, vp, vp]),
+                           ("fa_fwd_kv16", [vp, ll, ll, vp, vp, vp, i, i, i, vp, i, i, f, vp, vp, sz, vp]),
+                           ("fa_fwd_kv16_workspace", [i, i, i, i, ctypes.POINTER(sz)]),
+                           ("fa_kv16_keep", [vp, vp, vp, i, i, i, vp, vp, vp])):
             getattr(lib, name).restype = i
             getattr(lib, name).argtypes = args
         lib.fa_check.restype = i
@@ -1064,6 +1105,393 @@ def fa_kv4_compact(pool: torch.Tensor, table: torch.Tensor, seq_lens: torch.Tens
         return _on_stream(stream, refs, fa_kv4_compact, pool, table, seq_lens, refs, info, workspace=workspace)
     return _page_call("fa_kv4_compact", pool, None, table, seq_lens, refs, None, None, 0, info, workspace,
                       _refs_device(refs))
+
+
+# ------------------------------------------------------------- rotary positions and the 16-bit cache
+
+_pack_rope = struct.Struct("Piiif").pack       # struct fa_rope
+_pack_rows = struct.Struct("2P6qi4x").pack     # struct fa_rotary_rows
+_pack_kv16 = struct.Struct("4P6i").pack        # struct fa_kv16
+_PER_TURN = Fraction("0.159154943091895335768883763372514362034459645740456448747667344")  # 1 / (2 pi)
+
+
+class RopePlan:
+    """Frequencies of rotary positions on a device and how they are applied (see rope_plan)."""
+
+    __slots__ = ("freqs", "rot_dim", "start", "interleaved", "mscale", "_packed")
+
+    def __init__(self, freqs, start, interleaved, mscale):
+        self.freqs, self.rot_dim = freqs, 2 * freqs.numel()
+        self.start, self.interleaved, self.mscale = int(start), bool(interleaved), float(mscale)
+        self._packed = _pack_rope(freqs.data_ptr(), self.rot_dim, self.start, self.interleaved, self.mscale)
+
+
+def rope_plan(rot_dim: int | None = None, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+              original_length: int | None = None, inv_freq=None, mscale: float | None = None, start: int = 0,
+              interleaved: bool = False, device="cuda") -> RopePlan:
+    """The frequencies that fa_rope and fa_kv16_append take.  Pair c < rot_dim / 2 turns by w_c a position, w_c =
+    base ** (-2 c / rot_dim); it is made of dimensions start + c and start + c + rot_dim / 2, or with ``interleaved``
+    of start + 2 c and the next.  For a context stretched by ``factor``, ``scaling`` is
+
+    "linear"  w_c / factor,
+    "base"    the base times factor ** (rot_dim / (rot_dim - 2)),
+    "parts"   w_c / factor where a pair turns less than once in ``original_length`` positions, w_c where it turns more
+              than 32 times, linear in the turns between; and mscale 0.1 ln(factor) + 1 where none is given.
+
+    ``inv_freq`` (rot_dim / 2 numbers or a tensor, radians a position) replaces all that.  ``mscale`` multiplies the
+    turned dimensions (default 1).  Frequencies are kept to 2^-64 of a turn, so angles are exact at any position."""
+    if inv_freq is None:
+        if rot_dim is None or rot_dim <= 0 or rot_dim % 16:
+            raise ValueError(f"rot_dim must be a positive multiple of 16, got {rot_dim}")
+        if not base > 0 or not factor > 0 or math.isinf(base) or math.isinf(factor):
+            raise ValueError(f"base and factor must be positive and finite, got {base} and {factor}")
+        if scaling == "base":
+            base = base * factor ** (rot_dim / (rot_dim - 2))
+        w = [base ** (-2.0 * c / rot_dim) for c in range(rot_dim // 2)]
+        if scaling == "linear":
+            w = [x / factor for x in w]
+        elif scaling == "parts":
+            if not original_length or original_length <= 0:
+                raise ValueError("scaling 'parts' needs original_length")
+            own = [min(1.0, max(0.0, (original_length * x / (2 * math.pi) - 1) / 31)) for x in w]
+            w = [x * a + x / factor * (1 - a) for x, a in zip(w, own)]
+            mscale = 0.1 * math.log(factor) + 1.0 if mscale is None else mscale
+        elif scaling not in (None, "base"):
+            raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+    else:
+        if scaling is not None or factor != 1.0 or original_length is not None:
+            raise ValueError("inv_freq replaces scaling, factor and original_length")
+        w = [float(x) for x in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq)]
+        if not w or len(w) % 8 or (rot_dim is not None and rot_dim != 2 * len(w)):
+            raise ValueError(f"inv_freq must hold rot_dim / 2 frequencies, a multiple of 8, got {len(w)}")
+    if not all(math.isfinite(x) for x in w):
+        raise ValueError("frequencies must be finite")
+    mscale = 1.0 if mscale is None else float(mscale)
+    if not mscale > 0 or math.isinf(mscale):
+        raise ValueError(f"mscale must be positive and finite, got {mscale}")
+    if start < 0 or start % 16:
+        raise ValueError(f"start must be a multiple of 16, got {start}")
+    turns = [round(Fraction(x) * _PER_TURN * 2 ** 64) % 2 ** 64 for x in w]
+    freqs = torch.tensor([x - 2 ** 64 if x >> 63 else x for x in turns], dtype=torch.int64).to(device)
+    return RopePlan(freqs, start, interleaved, mscale)
+
+
+_ROPE_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _check_rows(t, name, ndim, dtype, device):
+    """Rows [..., D] of `dtype` on `device` whose D elements are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{max(device, 0)}, got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got shape {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+
+
+def _rotary_out(out, x, name, dtype):
+    """`out`, checked, or a new tensor of x's shape."""
+    if out is None:
+        return torch.empty(x.shape, dtype=dtype, device=x.device)
+    _check_rows(out, name, x.dim(), dtype, x.get_device())
+    if out.shape != x.shape:
+        raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(out.shape)}")
+    if out.data_ptr() == x.data_ptr() and out.dtype is x.dtype:
+        if out.stride() != x.stride():
+            raise ValueError(f"{name} in place must have its input's strides {x.stride()}, got {out.stride()}")
+    elif not out.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, or the input itself")
+    return out
+
+
+def _packed_rows(x, y):
+    """struct fa_rotary_rows of x (and y, or None): [T, heads, D] or [B, heads, L, D]."""
+    a, b = x.stride(), (0, 0, 0, 0) if y is None else y.stride()
+    to = 0 if y is None else y.data_ptr()
+    if x.dim() == 3:
+        return _pack_rows(x.data_ptr(), to, 0, a[0], a[1], 0, b[0], b[1], x.shape[1])
+    return _pack_rows(x.data_ptr(), to, a[0], a[2], a[1], b[0], b[2], b[1], x.shape[1])
+
+
+def _rope_call(name, q, k, rope, positions, dtype, q_out, k_out):
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if not isinstance(rope, RopePlan):
+        raise TypeError("rope must be a RopePlan (rope_plan)")
+    device, ndim, kind = q.get_device() if q.is_cuda else -1, q.dim(), q.dtype
+    if ndim not in (3, 4):
+        raise ValueError(f"q must be [T, H, D] or [B, H, L, D], got shape {tuple(q.shape)}")
+    if kind not in _ROPE_TYPES:
+        raise TypeError(f"q must be bfloat16 or float32, got {kind}")
+    if device < 0:
+        raise ValueError("q must be a CUDA tensor")
+    to = kind if dtype is None else dtype
+    if to not in _ROPE_TYPES or (kind is torch.bfloat16 and to is torch.float32):
+        raise TypeError(f"rows of {kind} can not become {to}")
+    _check_rows(q, "q", ndim, kind, device)
+    axis = 0 if ndim == 3 else 2  # of the tokens
+    B, T, D = (1 if ndim == 3 else q.shape[0]), q.shape[axis], q.shape[-1]
+    if rope.freqs.get_device() != device:
+        raise ValueError(f"rope must be on {q.device}, got {rope.freqs.device}")
+    if rope.start + rope.rot_dim > D:
+        raise ValueError(f"rope turns dimensions {rope.start} to {rope.start + rope.rot_dim} of {D}")
+    rows_k = None
+    if k is not None:
+        _check_rows(k, "k", ndim, kind, device)
+        if k.shape[axis] != T or k.shape[-1] != D or (ndim == 4 and k.shape[0] != B):
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
+        k_out = _rotary_out(k_out, k, "k_out", to)
+        rows_k = _packed_rows(k, k_out) if k.shape[1] else None
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    q_out = _rotary_out(q_out, q, "q_out", to)
+    at = step = 0
+    if positions is not None:
+        _want(positions, "positions", torch.int32, positions.dim() if isinstance(positions, torch.Tensor) else 1, device)
+        if positions.shape not in ((T,), (B, T)) or (positions.dim() == 2 and ndim == 3):
+            raise ValueError(f"positions must be {(T,)}{'' if ndim == 3 else f' or {(B, T)}'}, got {tuple(positions.shape)}")
+        at, step = positions.data_ptr(), T if positions.dim() == 2 else 0
+    lib = _lib or load_library()
+    st = _on_device(device, getattr(lib, name), _packed_rows(q, q_out), rows_k, B, T, D, kind is torch.float32,
+                    to is torch.float32, rope._packed, at or None, step, _raw_stream(device))
+    if st != FA_OK:
+        raise FAError(st, name)
+    return q_out, k_out
+
+
+def fa_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopePlan, positions: torch.Tensor | None = None,
+            dtype: torch.dtype | None = None, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+            stream=None):
+    """Turn the rows of q and k (which may be None) by their positions' angles.  q, k: packed [T,H,D] or dense
+    [B,H,L,D], bf16 or fp32, of any strides with contiguous rows (views of a fused projection, or of [B,L,H,D]);
+    positions int32 [T], [L] or [B,L] (default: the index along the tokens).  Returns (q_out, k_out), contiguous, of
+    ``dtype`` (default: the input's; fp32 rows may become bf16).  q_out may be q itself, and k_out k."""
+    if stream is not None:
+        return _on_stream(stream, q, fa_rope, q, k, rope, positions, dtype, q_out, k_out)
+    return _rope_call("fa_rope", q, k, rope, positions, dtype, q_out, k_out)
+
+
+def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, rope: RopePlan, positions: torch.Tensor | None = None,
+                dtype: torch.dtype | None = None, dq_out: torch.Tensor | None = None,
+                dk_out: torch.Tensor | None = None, stream=None):
+    """Backward of fa_rope: from the gradients of its outputs (fa_bwd's fp32 dq and dk, or bf16) those of its inputs.
+    Arguments as fa_rope.  Returns (dq_out, dk_out)."""
+    if stream is not None:
+        return _on_stream(stream, dq, fa_rope_bwd, dq, dk, rope, positions, dtype, dq_out, dk_out)
+    return _rope_call("fa_rope_bwd", dq, dk, rope, positions, dtype, dq_out, dk_out)
+
+
+def kv16_pool(num_pages: int, Hkv: int, page_size: int, D: int, layers: int | None = None,
+              device="cuda") -> torch.Tensor:
+    """An empty (all zero) pool of a paged bf16 KV cache: [num_pages, 2, Hkv, page_size, D], K then V, with ``layers`` in
+    front when given."""
+    if page_size not in (16, 32, 64, 128, 256) or D not in (64, 128):
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256 and D 64 or 128")
+    shape = (num_pages, 2, Hkv, page_size, D)
+    return torch.zeros(shape if layers is None else (layers, *shape), dtype=torch.bfloat16, device=device)
+
+
+def draft_mask(parents, cu_seqlens) -> tuple[torch.Tensor, torch.Tensor]:
+    """The mask of fa_fwd_kv16, int32 [T, words], and the depths, int32 [T], of drafted trees, on the host: parents[i]
+    is the parent of packed node i, an index in its own sequence in front of i's, or -1 for a child of the prefix's
+    last position.  A node sees its ancestors and itself; its position is the prefix length plus its depth."""
+    parents = parents.tolist() if isinstance(parents, torch.Tensor) else list(parents)
+    cu = cu_seqlens.tolist() if isinstance(cu_seqlens, torch.Tensor) else list(cu_seqlens)
+    if len(cu) < 2 or cu[0] != 0 or any(b < a for a, b in zip(cu, cu[1:])) or cu[-1] > len(parents):
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets of the nodes, from 0, not decreasing")
+    words = max(1, -(-max(b - a for a, b in zip(cu, cu[1:])) // 32))
+    seen, depth = [0] * len(parents), [0] * len(parents)
+    for a, b in zip(cu, cu[1:]):
+        for i in range(a, b):
+            p = parents[i]
+            if not -1 <= p < i - a:
+                raise ValueError(f"node {i - a} of a sequence has parent {p}")
+            seen[i] = (seen[a + p] if p >= 0 else 0) | 1 << (i - a)
+            depth[i] = depth[a + p] + 1 if p >= 0 else 0
+    bits = b"".join(x.to_bytes(4 * words, "little") for x in seen)
+    mask = torch.frombuffer(bytearray(bits or b"0000"), dtype=torch.int32)[:words * len(parents)]
+    return mask.reshape(len(parents), words).clone(), torch.tensor(depth, dtype=torch.int32)
+
+
+def _kv16(pool, table, seq_lens, seq_ids, num_seqs, layers=False):
+    """Checks the cache of a call with num_seqs sequences.  Returns (fa_kv16_t as bytes, device index, Hkv, D)."""
+    device = pool.get_device() if isinstance(pool, torch.Tensor) else -1
+    ndim = 6 if layers and isinstance(pool, torch.Tensor) and pool.dim() == 6 else 5
+    if not (device >= 0 and pool.dtype is torch.bfloat16 and pool.dim() == ndim and pool.is_contiguous()):
+        _check_tensor(pool, "pool", torch.bfloat16, ndim)
+    slots, width = _slots_of(table, seq_lens, device)
+    N, two, H, P, D = pool.shape[-5:]
+    if two != 2 or P not in (16, 32, 64, 128, 256) or D not in (64, 128):
+        raise ValueError(f"pool must be bfloat16 [..., pages, 2, Hkv, page_size, D], got {tuple(pool.shape)}")
+    ids = 0
+    if seq_ids is not None:
+        _want(seq_ids, "seq_ids", torch.int32, 1, device)
+        if seq_ids.shape[0] != num_seqs:
+            raise ValueError(f"seq_ids must name {num_seqs} slots")
+        ids = seq_ids.data_ptr()
+    elif num_seqs > slots:
+        raise ValueError(f"{num_seqs} sequences but {slots} slots")
+    return _pack_kv16(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ids, N, slots, width, P, H, D), device, H, D
+
+
+def fa_kv16_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
+                   table: torch.Tensor, seq_lens: torch.Tensor, seq_ids: torch.Tensor | None = None,
+                   rope: RopePlan | None = None, positions: torch.Tensor | None = None,
+                   q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
+    """Write packed rows k, v [T,Hkv,D] bf16 (of any strides with contiguous rows) into the cache, k turned by
+    ``rope``: the rows [cu_seqlens[s], cu_seqlens[s+1]) become the last positions of sequence s (slot seq_ids[s],
+    default s), which seq_lens already counts.  positions int32 [T] (default: the index in the cache).  q [T,Hq,D] is
+    turned alike; returns q_out (a new tensor, or q itself where given so), or None without q.  Rows of q behind the
+    last sequence are not written."""
+    if stream is not None:
+        return _on_stream(stream, pool, fa_kv16_append, k, v, cu_seqlens, pool, table, seq_lens, seq_ids, rope,
+                          positions, q, q_out)
+    n = _num_seqs(cu_seqlens)
+    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    _check_rows(k, "k", 3, torch.bfloat16, device)
+    _check_rows(v, "v", 3, torch.bfloat16, device)
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1:] != (H, D):
+        raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {H} heads of {D}")
+    packed = None
+    if rope is not None:
+        if not isinstance(rope, RopePlan):
+            raise TypeError("rope must be a RopePlan (rope_plan)")
+        if rope.freqs.get_device() != device or rope.start + rope.rot_dim > D:
+            raise ValueError(f"rope must be on {pool.device} and turn at most {D} dimensions")
+        packed = rope._packed
+    elif q is not None or positions is not None:
+        raise ValueError("q and positions need rope")
+    rows_q = None
+    if q is not None:
+        _check_rows(q, "q", 3, torch.bfloat16, device)
+        if q.shape[0] != T or q.shape[2] != D:
+            raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
+        q_out = _rotary_out(q_out, q, "q_out", torch.bfloat16)
+        rows_q = _packed_rows(q, q_out) if q.shape[1] else None
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    at = None
+    if positions is not None:
+        _want(positions, "positions", torch.int32, 1, device)
+        if positions.shape[0] != T:
+            raise ValueError(f"positions must hold {T} numbers, got {positions.shape[0]}")
+        at = positions.data_ptr() or None
+    lib = _lib or load_library()
+    st = _on_device(device, lib.fa_kv16_append, rows_q, _packed_rows(k, None), _packed_rows(v, None),
+                    cu_seqlens.data_ptr(), n, T, c, packed, at, _raw_stream(device))
+    if st != FA_OK:
+        raise FAError(st, "fa_kv16_append")
+    return q_out
+
+
+def kv16_workspace(total: int, Hq: int, Hkv: int, D: int) -> int:
+    """Workspace bytes fa_fwd_kv16 needs on the current device."""
+    nbytes = ctypes.c_size_t(0)
+    st = load_library().fa_fwd_kv16_workspace(total, Hq, Hkv, D, ctypes.byref(nbytes))
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_kv16_workspace")
+    return nbytes.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv16_workspace(device, total, Hq, Hkv, D):
+    """kv16_workspace on device `device`."""
+    return _on_device(device, kv16_workspace, total, Hq, Hkv, D)
+
+
+def fa_fwd_kv16(q: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor, table: torch.Tensor,
+                seq_lens: torch.Tensor, mask: torch.Tensor | None = None, causal: bool = False,
+                softmax_scale: float | None = None, seq_ids: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Attention of packed queries q [T,Hq,D] bf16 (contiguous rows) over a paged bf16 cache: the rows
+    [cu_seqlens[s], cu_seqlens[s+1]) are the last positions of sequence s (slot seq_ids[s], default s), whose keys the
+    cache already holds.  They see every position in front of the call's and, of the call's own, with ``mask`` (int32
+    [T,words], bit j % 32 of word j / 32 for position j of the sequence's rows; draft_mask) the marked ones, with
+    ``causal`` those up to their own, else all.  Returns (o [T,Hq,D] bf16, lse [Hq,T] fp32); rows behind the last
+    sequence are left as they were."""
+    if stream is not None:
+        return _on_stream(stream, pool, fa_fwd_kv16, q, cu_seqlens, pool, table, seq_lens, mask, causal, softmax_scale,
+                          seq_ids, out, lse, workspace=workspace)
+    n = _num_seqs(cu_seqlens)
+    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    _check_rows(q, "q", 3, torch.bfloat16, device)
+    T, Hq, Dq = q.shape
+    if Dq != D:
+        raise ValueError(f"q has head dimension {Dq} and the cache {D}")
+    if Hq % H or not Hq:
+        raise ValueError(f"{Hq} query heads over {H} KV heads")
+    words = 0
+    if mask is not None:
+        _want(mask, "mask", torch.int32, 2, device)
+        words = mask.shape[1]
+        if mask.shape[0] != T or words < 1:
+            raise ValueError(f"mask must be [{T}, words], got {tuple(mask.shape)}")
+        if causal:
+            raise ValueError("mask and causal exclude each other")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", torch.bfloat16, 3, device)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    else:
+        _want(lse, "lse", torch.float32, 2, device)
+    if out.shape != q.shape or lse.shape != (Hq, T):
+        raise ValueError("out/lse shape mismatch")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(D)
+    lib = _lib or load_library()
+    nbytes = _kv16_workspace(device, min(T, 129), Hq, H, D)  # more tokens need no more
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {q.device}, got {workspace.device}")
+    st = _on_device(device, lib.fa_fwd_kv16, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), lse.data_ptr(),
+                    cu_seqlens.data_ptr(), n, T, Hq, None if mask is None else mask.data_ptr(), words,
+                    1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(device))
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_kv16")
+    return out, lse
+
+
+def fa_kv16_keep(keep: torch.Tensor, counts: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
+                 table: torch.Tensor, seq_lens: torch.Tensor, seq_ids: torch.Tensor | None = None,
+                 new_tokens: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Keep the accepted nodes of drafted trees: of the last cu_seqlens[s+1] - cu_seqlens[s] positions of sequence s,
+    those named by keep[cu_seqlens[s] + j], j < counts[s] (int32, ascending, from 0), become the first, in order, in
+    every layer of pool (as for fa_kv16_append, or with the layers in front).  Returns new_tokens, int32 [num_seqs]:
+    counts[s] less the drafted ones, for fa_kv4_reserve, which takes the other positions back."""
+    if stream is not None:
+        return _on_stream(stream, pool, fa_kv16_keep, keep, counts, cu_seqlens, pool, table, seq_lens, seq_ids,
+                          new_tokens)
+    n = _num_seqs(cu_seqlens)
+    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n, layers=True)
+    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    _want(keep, "keep", torch.int32, 1, device)
+    _want(counts, "counts", torch.int32, 1, device)
+    if counts.shape[0] != n:
+        raise ValueError(f"counts must hold {n} numbers, got {counts.shape[0]}")
+    if new_tokens is None:
+        new_tokens = torch.empty(n, dtype=torch.int32, device=pool.device)
+    else:
+        _want(new_tokens, "new_tokens", torch.int32, 1, device)
+        if new_tokens.shape[0] != n:
+            raise ValueError(f"new_tokens must hold {n} numbers, got {new_tokens.shape[0]}")
+    lib = _lib or load_library()
+    st = _on_device(device, lib.fa_kv16_keep, keep.data_ptr() or counts.data_ptr(), counts.data_ptr(),
+                    cu_seqlens.data_ptr(), n, keep.shape[0], pool.shape[0] if pool.dim() == 6 else 1,
+                    new_tokens.data_ptr(), c, _raw_stream(device))
+    if st != FA_OK:
+        raise FAError(st, "fa_kv16_keep")
+    return new_tokens
 
 
 def fa_check(stream=None) -> int:

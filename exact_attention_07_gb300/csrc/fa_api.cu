@@ -13,6 +13,7 @@
 #include "fa_bwd.h"
 #include "fa_decode.h"
 #include "fa_fp8.h"
+#include "fa_kv16.h"
 #include "fa_kv4.h"
 #include "fa_launch.h"
 #include "fa_params.h"
@@ -1457,6 +1458,277 @@ extern "C" fa_status_t fa_kv4_compact(const fa_kv4_pages_t* pages, int* info, vo
     if (st != FA_OK) return st;
     if (launch_kv4_compact(p, ds->num_sms, stream) != cudaSuccess) return FA_ERR_CUDA;
     g_last_launches = 2;
+    return FA_OK;
+}
+
+// ------------------------------------------------------------- rotary positions and the 16-bit cache
+
+namespace {
+// Strides of rows, 0 where a dimension has one entry; false if one is not a multiple of 16 bytes.
+bool row_strides(long long b, long long t, long long h, int B, int T, int heads, int bytes, long long (&out)[3])
+{
+    const long long s[3] = {b, t, h};
+    const int n[3] = {B, T, heads};
+    for (int i = 0; i < 3; ++i) {
+        out[i] = n[i] > 1 ? s[i] : 0;
+        if (out[i] * bytes % 16 != 0) return false;
+    }
+    return true;
+}
+
+// Checks rows and fills the kernels' form of them; `write`: y is used.
+fa_status_t rotary_rows(const fa_rotary_rows_t* r, int B, int T, bool in_f32, bool out_f32, bool write, RotaryRows* out)
+{
+    if (!r->x || !aligned16(r->x) || r->heads <= 0) return FA_ERR_INVALID_ARG;
+    long long x[3], y[3] = {0, 0, 0};
+    if (!row_strides(r->x_batch, r->x_token, r->x_head, B, T, r->heads, in_f32 ? 4 : 2, x)) return FA_ERR_INVALID_ARG;
+    if (write) {
+        if (!r->y || !aligned16(r->y)) return FA_ERR_INVALID_ARG;
+        if (!row_strides(r->y_batch, r->y_token, r->y_head, B, T, r->heads, out_f32 ? 4 : 2, y)) return FA_ERR_INVALID_ARG;
+        // rows written must not coincide
+        if ((B > 1 && y[0] == 0) || (T > 1 && y[1] == 0) || (r->heads > 1 && y[2] == 0)) return FA_ERR_INVALID_ARG;
+        out->in_place = r->x == r->y && in_f32 == out_f32;
+        if (out->in_place && (x[0] != y[0] || x[1] != y[1] || x[2] != y[2])) return FA_ERR_INVALID_ARG;
+        if (r->x == r->y && in_f32 != out_f32) return FA_ERR_INVALID_ARG;
+    }
+    out->x = r->x;
+    out->y = write ? r->y : nullptr;
+    out->xb = x[0];
+    out->xt = x[1];
+    out->xh = x[2];
+    out->yb = y[0];
+    out->yt = y[1];
+    out->yh = y[2];
+    out->heads = r->heads;
+    return FA_OK;
+}
+
+fa_status_t rotary_plan(const fa_rope_t* rope, int D, RotaryParams* p)
+{
+    if (rope->rot_dim <= 0 || rope->start < 0 || rope->rot_dim > D || rope->start > D - rope->rot_dim ||
+        !(rope->mscale > 0.f) || !std::isfinite(rope->mscale) || !rope->freqs ||
+        (reinterpret_cast<uintptr_t>(rope->freqs) & 7u))
+        return FA_ERR_INVALID_ARG;
+    if (rope->rot_dim % 16 != 0 || rope->start % 16 != 0) return FA_ERR_UNSUPPORTED;
+    p->freqs = rope->freqs;
+    p->R = rope->rot_dim;
+    p->start = rope->start;
+    p->mscale = rope->mscale;
+    return FA_OK;
+}
+
+fa_status_t rope_call(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int B, int T, int D, int in_fp32,
+                      int out_fp32, const fa_rope_t* rope, const int* positions, long long position_batch_stride,
+                      bool backward, cudaStream_t stream)
+{
+    g_last_launches = 0;
+    if (!q || !rope || B < 0 || T < 0 || D <= 0 || !aligned4(positions)) return FA_ERR_INVALID_ARG;
+    if (D % 16 != 0 || D > 512 || (out_fp32 && !in_fp32)) return FA_ERR_UNSUPPORTED;
+    RotaryParams p{};
+    fa_status_t st = rotary_plan(rope, D, &p);
+    if (st != FA_OK) return st;
+    if (B == 0 || T == 0) return FA_OK;  // no rows: nothing to launch
+    if ((long long)B * T >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    st = rotary_rows(q, B, T, in_fp32 != 0, out_fp32 != 0, true, &p.r[0]);
+    if (st != FA_OK) return st;
+    if (k) {
+        st = rotary_rows(k, B, T, in_fp32 != 0, out_fp32 != 0, true, &p.r[1]);
+        if (st != FA_OK) return st;
+    }
+    if ((long long)p.r[0].heads + p.r[1].heads > 65535) return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    p.pos = positions;
+    p.pos_b = position_batch_stride;
+    p.B = B;
+    p.T = T;
+    p.D = D;
+    p.backward = backward;
+    if (launch_rope(in_fp32 != 0, out_fp32 != 0, rope->interleaved != 0, p, ds->num_sms, stream) != cudaSuccess)
+        return FA_ERR_CUDA;
+    g_last_launches = 1;
+    return FA_OK;
+}
+
+// Checks a cache description for a call of num_seqs sequences and fills the kernels' form of it.
+fa_status_t kv16_cache(const fa_kv16_t* c, int num_seqs, Kv16Cache* out)
+{
+    if (!c || !c->pool || !c->table || !c->seq_lens || num_seqs <= 0) return FA_ERR_INVALID_ARG;
+    if (!aligned16(c->pool) || !aligned4(c->table) || !aligned4(c->seq_lens) || !aligned4(c->seq_ids))
+        return FA_ERR_INVALID_ARG;
+    const fa_status_t st = kv4_geometry(c->num_pages, c->num_slots, c->table_width, c->page_size, c->Hkv, c->D,
+                                        &out->page_shift);
+    if (st != FA_OK) return st;
+    if ((long long)c->num_pages * 2 * c->Hkv >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    if (!c->seq_ids && num_seqs > c->num_slots) return FA_ERR_INVALID_ARG;
+    out->pool = static_cast<uint16_t*>(c->pool);
+    out->table = c->table;
+    out->lens = c->seq_lens;
+    out->ids = c->seq_ids;
+    out->num_pages = c->num_pages;
+    out->num_slots = c->num_slots;
+    out->table_width = c->table_width;
+    out->Hkv = c->Hkv;
+    return FA_OK;
+}
+
+fa_status_t kv16_attn_shape(int total, int Hq, int Hkv, int D, int* rows)
+{
+    if (total < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
+    if (total > (1 << 30)) return FA_ERR_INVALID_ARG;
+    *rows = kv16_attn_rows(total, Hq / Hkv);
+    return FA_OK;
+}
+}  // namespace
+
+extern "C" fa_status_t fa_rope(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int B, int T, int D, int in_fp32,
+                               int out_fp32, const fa_rope_t* rope, const int* positions,
+                               long long position_batch_stride, cudaStream_t stream)
+{
+    return rope_call(q, k, B, T, D, in_fp32, out_fp32, rope, positions, position_batch_stride, false, stream);
+}
+
+extern "C" fa_status_t fa_rope_bwd(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int B, int T, int D, int in_fp32,
+                                   int out_fp32, const fa_rope_t* rope, const int* positions,
+                                   long long position_batch_stride, cudaStream_t stream)
+{
+    return rope_call(q, k, B, T, D, in_fp32, out_fp32, rope, positions, position_batch_stride, true, stream);
+}
+
+extern "C" fa_status_t fa_kv16_append(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, const fa_rotary_rows_t* v,
+                                      const int* cu_seqlens, int num_seqs, int total, const fa_kv16_t* cache,
+                                      const fa_rope_t* rope, const int* positions, cudaStream_t stream)
+{
+    g_last_launches = 0;
+    RotaryParams p{};
+    fa_status_t st = kv16_cache(cache, num_seqs, &p.c);
+    if (st != FA_OK) return st;
+    if (!cu_seqlens || !aligned4(cu_seqlens) || !aligned4(positions) || total < 0 || total > (1 << 30))
+        return FA_ERR_INVALID_ARG;
+    if (q && !rope) return FA_ERR_INVALID_ARG;
+    if (rope) {
+        st = rotary_plan(rope, cache->D, &p);
+        if (st != FA_OK) return st;
+    }
+    if (total == 0) return FA_OK;  // no rows: nothing to launch
+    if (!k || !v || k->heads != cache->Hkv || v->heads != cache->Hkv) return FA_ERR_INVALID_ARG;
+    if (q && (st = rotary_rows(q, 1, total, false, false, true, &p.r[0])) != FA_OK) return st;
+    if ((st = rotary_rows(k, 1, total, false, false, false, &p.r[1])) != FA_OK) return st;
+    if ((st = rotary_rows(v, 1, total, false, false, false, &p.r[2])) != FA_OK) return st;
+    if ((long long)p.r[0].heads + 2ll * cache->Hkv > 65535) return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    p.pos = positions;
+    p.B = 1;
+    p.T = total;
+    p.D = cache->D;
+    p.cu = cu_seqlens;
+    p.num_seqs = num_seqs;
+    p.c.err = ds->err;
+    p.c.diag = ds->diag;
+    if (launch_kv16_append(rope && rope->interleaved, p, ds->num_sms, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 1;
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_fwd_kv16_workspace(int total, int Hq, int Hkv, int D, size_t* workspace_bytes)
+{
+    if (!workspace_bytes) return FA_ERR_INVALID_ARG;
+    int rows = 0;
+    fa_status_t st = kv16_attn_shape(total, Hq, Hkv, D, &rows);
+    if (st != FA_OK) return st;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    *workspace_bytes = kv16_attn_workspace(D, rows, ds->num_sms);
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_fwd_kv16(const void* q, long long q_token, long long q_head, void* o, float* lse,
+                                   const int* cu_seqlens, int num_seqs, int total, int Hq, const int* mask,
+                                   int mask_words, int causal, float softmax_scale, const fa_kv16_t* cache,
+                                   void* workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    g_last_launches = 0;
+    if (!cache) return FA_ERR_INVALID_ARG;
+    Kv16AttnParams p{};
+    fa_status_t st = kv16_attn_shape(total, Hq, cache->Hkv, cache->D, &p.rows);
+    if (st != FA_OK) return st;
+    st = kv16_cache(cache, num_seqs, &p.c);
+    if (st != FA_OK) return st;
+    if (!scale_ok(softmax_scale) || !cu_seqlens || !aligned4(cu_seqlens) || !aligned4(mask)) return FA_ERR_INVALID_ARG;
+    if (mask && (causal || mask_words <= 0)) return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    if (total == 0) return FA_OK;  // no rows: nothing to launch
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned16(lse)) return FA_ERR_INVALID_ARG;
+    const int D = cache->D;
+    if (Hq == 1) q_head = D;  // of one head, one token: any stride will do
+    if (total == 1) q_token = (long long)Hq * D;
+    if (q_token <= 0 || q_head <= 0 || q_token % 8 != 0 || q_head % 8 != 0 || q_token >= (1ll << 38) || q_head >= (1ll << 38))
+        return FA_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace) || workspace_bytes < kv16_attn_workspace(D, p.rows, ds->num_sms))
+        return FA_ERR_INVALID_ARG;
+    p.o = static_cast<uint16_t*>(o);
+    p.lse = lse;
+    p.part = static_cast<float*>(workspace);
+    p.cu = cu_seqlens;
+    p.mask = mask;
+    p.mask_words = mask_words;
+    p.B = num_seqs;
+    p.T = total;
+    p.Hq = Hq;
+    p.group = Hq / cache->Hkv;
+    p.npt = 128 / p.group;
+    p.causal = causal != 0;
+    p.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
+    p.c.err = ds->err;
+    p.c.diag = ds->diag;
+    p.fault = g_fault_next;
+    g_fault_next = 0;
+    CUtensorMap mq, mkv;
+    const uint64_t row = 2ull * D;
+    if (!encode_map(&mq, q, D, Hq, total, 2 * q_head, 2 * q_token, p.group, p.npt) ||
+        !encode_map(&mkv, cache->pool, D, cache->page_size, (uint64_t)cache->num_pages * 2 * cache->Hkv, row,
+                    row * cache->page_size, std::min(cache->page_size, 128), 1))
+        return FA_ERR_CUDA;
+    if (launch_kv16_attn(D, mq, mkv, p, ds->num_sms, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 2;
+    return FA_OK;
+}
+
+extern "C" fa_status_t fa_kv16_keep(const int* keep, const int* counts, const int* cu_seqlens, int num_seqs, int total,
+                                    int num_layers, int* new_tokens, const fa_kv16_t* cache, cudaStream_t stream)
+{
+    g_last_launches = 0;
+    Kv16KeepParams p{};
+    fa_status_t st = kv16_cache(cache, num_seqs, &p.c);
+    if (st != FA_OK) return st;
+    if (!keep || !counts || !cu_seqlens || !new_tokens || !aligned4(keep) || !aligned4(counts) || !aligned4(cu_seqlens) ||
+        !aligned4(new_tokens) || total < 0 || num_layers <= 0)
+        return FA_ERR_INVALID_ARG;
+    if ((long long)num_layers * 2 * cache->Hkv * (cache->D / 8) >= 256ll * 65535) return FA_ERR_INVALID_ARG;
+    DeviceState* ds = nullptr;
+    st = device_state(&ds);
+    if (st != FA_OK) return st;
+    p.keep = keep;
+    p.counts = counts;
+    p.cu = cu_seqlens;
+    p.back = new_tokens;
+    p.num_seqs = num_seqs;
+    p.total = total;
+    p.D = cache->D;
+    p.layers = num_layers;
+    p.layer_stride = (long long)cache->num_pages * 2 * cache->Hkv * cache->page_size * cache->D;
+    p.c.err = ds->err;
+    p.c.diag = ds->diag;
+    if (launch_kv16_keep(p, stream) != cudaSuccess) return FA_ERR_CUDA;
+    g_last_launches = 1;
     return FA_OK;
 }
 

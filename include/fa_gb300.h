@@ -566,6 +566,149 @@ fa_status_t fa_kv4_compact(const fa_kv4_pages_t* pages, int* info, void* workspa
 fa_status_t fa_kv4_pages_workspace(int num_pages, int n, size_t* workspace_bytes);
 
 /*
+ * Rotary positions (no counterpart on the pages).  Pair c of a row at position
+ * p turns by the angle p * w_c:
+ *
+ *   (y1, y2) = mscale * (cos x1 - sin x2, sin x1 + cos x2),  c = 0 .. rot_dim / 2 - 1
+ *
+ *   pair c is the dimensions (start + c, start + c + rot_dim / 2), or, with
+ *   interleaved != 0, (start + 2 c, start + 2 c + 1).  Dimensions outside
+ *   [start, start + rot_dim) are copied.
+ *   freqs: DEVICE uint64 [rot_dim / 2], turns per position times 2^64, i.e.
+ *     w_c / (2 pi) * 2^64 modulo 2^64.  Position times frequency modulo 2^64 is
+ *     the angle's part of a turn with no rounding, for any int32 position.
+ *   Scalings for long contexts are choices of w_c and mscale.
+ */
+typedef struct fa_rope {
+    const unsigned long long* freqs;
+    int rot_dim;
+    int start;
+    int interleaved;
+    float mscale;
+} fa_rope_t;
+
+/* Rows [B, T, heads, D] with strides in elements; the D elements of a row are
+ * contiguous.  x is read and y written; y may be x with the same strides (in
+ * place), else they must not overlap.  Addresses are multiples of 16 bytes, and
+ * so are the strides of dimensions of more than one entry.  A stride of x may be 0. */
+typedef struct fa_rotary_rows {
+    const void* x;
+    void* y;
+    long long x_batch, x_token, x_head;
+    long long y_batch, y_token, y_head;
+    int heads;
+} fa_rotary_rows_t;
+
+/*
+ * Turns the rows of q and, unless it is NULL, of k (HOST structs), each with
+ * its own heads.  positions: int32 DEVICE, position of token t of batch b at
+ * b * position_batch_stride + t, or NULL for t itself.  in_fp32, out_fp32: fp32
+ * rows in place of bf16; (0, 0), (1, 1) and (1, 0) are supported
+ * (FA_ERR_UNSUPPORTED otherwise).  D, rot_dim and start are multiples of 16, D
+ * at most 512.  Angles are exact to 2^-24 of a turn's half, sine, cosine and
+ * products in fp32, and the result is rounded once.
+ *
+ * fa_rope_bwd: the gradient, the same with the angles negated: x the gradients
+ * of the outputs, y those of the inputs (of fp32 gradients, as fa_bwd's, in
+ * fp32 or bf16).  1 kernel each; no rows, no kernel.
+ */
+fa_status_t fa_rope(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int B, int T, int D, int in_fp32, int out_fp32,
+                    const fa_rope_t* rope, const int* positions, long long position_batch_stride, cudaStream_t stream);
+fa_status_t fa_rope_bwd(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int B, int T, int D, int in_fp32,
+                        int out_fp32, const fa_rope_t* rope, const int* positions, long long position_batch_stride,
+                        cudaStream_t stream);
+
+/*
+ * Paged KV cache in bf16 ("kv16"; no counterpart on the pages).  Its table,
+ * lengths and slots are the 4-bit cache's (above), and fa_kv4_reserve and
+ * fa_kv4_release, which do not touch the pool, serve both.  The pool:
+ *
+ *   pool [num_pages][2][Hkv][page_size][D] bf16: K, then V
+ *
+ * fa_kv16_t is a HOST struct of DEVICE pointers as fa_kv4_t, with the same
+ * limits, checks on the device and rules for padded batches; num_pages * 2 *
+ * Hkv is below 2^31.
+ */
+typedef struct fa_kv16 {
+    void* pool;
+    const int* table;
+    const int* seq_lens;
+    const int* seq_ids;
+    int num_pages;
+    int num_slots;
+    int table_width;
+    int page_size;
+    int Hkv;
+    int D;
+} fa_kv16_t;
+
+/*
+ * Writes new rows into the cache, K turned on the way.  k, v: rows [1, total,
+ * Hkv, D] bf16 of which x is read (y is not used); q: NULL, or rows [1, total,
+ * heads, D] that are turned alike from x to y.  cu_seqlens as for fa_kv4_append:
+ * the rows become the LAST positions of their sequences, which seq_lens already
+ * counts.  positions: int32 DEVICE [total], or NULL for the index in the
+ * sequence's cache (a drafted tree's nodes have the prefix length plus their
+ * depth).  rope: HOST, or NULL (q too then): rows are copied.
+ * Bytes of other positions keep their values; rows behind cu_seqlens[num_seqs]
+ * are neither read into the cache nor turned.  A slot named twice (each time
+ * with rows) latches FA_ERR_INVALID_ARG.  1 kernel.
+ */
+fa_status_t fa_kv16_append(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, const fa_rotary_rows_t* v,
+                           const int* cu_seqlens, int num_seqs, int total, const fa_kv16_t* cache, const fa_rope_t* rope,
+                           const int* positions, cudaStream_t stream);
+
+/*
+ * Attention of packed queries over the cache: decode, drafted trees, and chunks
+ * of prompts.
+ *
+ *   q [total, Hq, D] bf16, the D elements contiguous, token and head strides in
+ *     elements (multiples of 8); o [total, Hq, D] bf16, lse [Hq, total] fp32
+ *   cu_seqlens int32 DEVICE [num_seqs + 1]: as for fa_kv16_append; sequence s's
+ *     rows are the last positions of its cache, which already holds their keys.
+ *     Rows behind cu_seqlens[num_seqs] are left as they were.
+ *   mask: int32 DEVICE [total][mask_words], or NULL.  Row i sees all positions in
+ *     front of the call's and, of its sequence's call positions j, those with bit
+ *     j % 32 of word j / 32 set.  A sequence with more than 32 * mask_words rows
+ *     latches FA_ERR_INVALID_ARG.  Without a mask a row sees, with causal != 0,
+ *     the positions up to its own, else all.  A mask and causal together are
+ *     refused.
+ *   Hq / Hkv at most 128 (FA_ERR_UNSUPPORTED otherwise); total at most 2^30.
+ *   workspace: DEVICE memory of at least fa_fwd_kv16_workspace bytes, 16-byte
+ *     aligned; calls that overlap on the GPU need separate workspaces.
+ *
+ * Scores, softmax statistics and O accumulate in fp32.  P enters P.V in bf16
+ * and O is rounded to bf16 once, so that O errs by up to a bf16 step of a row's
+ * largest |v| where many keys share the weight.  LSE comes from the fp32 P.
+ * A masked key contributes nothing whatever its bytes hold; a row without keys
+ * gets O = 0 and LSE = -inf.  The work is cut evenly over the GPU from the
+ * lengths on the device.  2 kernels; none for total = 0.
+ */
+fa_status_t fa_fwd_kv16(const void* q, long long q_token, long long q_head, void* o, float* lse, const int* cu_seqlens,
+                        int num_seqs, int total, int Hq, const int* mask, int mask_words, int causal,
+                        float softmax_scale, const fa_kv16_t* cache, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/* Workspace bytes of fa_fwd_kv16 on the CURRENT device, written to *workspace_bytes. */
+fa_status_t fa_fwd_kv16_workspace(int total, int Hq, int Hkv, int D, size_t* workspace_bytes);
+
+/*
+ * Keeps the accepted nodes of drafted trees: of the n = cu_seqlens[s + 1] -
+ * cu_seqlens[s] last positions of each sequence, keep[cu_seqlens[s] + j], j <
+ * counts[s] (int32 DEVICE, ascending, from 0), names those that become its
+ * first, in order: row len - n + j takes row len - n + keep[j], K and V, in each
+ * of num_layers pools that lie one after the other.  new_tokens (int32 DEVICE
+ * [num_seqs], output) receives counts[s] - n, which fa_kv4_reserve takes to give
+ * the other positions back.  Other rows, and seq_lens, keep their values.
+ * A list that does not ascend or leaves [0, n), or a count out of range, latches
+ * FA_ERR_INVALID_ARG; that sequence's rows are left as they were and its
+ * new_tokens are 0.  The pages written must be the sequence's own; a slot
+ * named twice as for fa_kv16_append.  1 kernel.
+ */
+fa_status_t fa_kv16_keep(const int* keep, const int* counts, const int* cu_seqlens, int num_seqs, int total,
+                         int num_layers, int* new_tokens, const fa_kv16_t* cache, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then returns and clears the device-side error latch
  * of the current device: FA_ERR_TIMEOUT or FA_ERR_INVALID_ARG from an earlier
  * launch, or FA_ERR_CUDA when a kernel found its launch configuration unusable
@@ -580,14 +723,14 @@ const char* fa_status_string(fa_status_t status);
  * Number of kernels the last successful forward call on this host thread
  * launched (1 for dense, 2 for varlen: schedule + attention; 1 or 2 for
  * split-KV: partials, then the merge when there is more than one partition;
- * 2 for backward; for the 4-bit cache's calls as documented with each, 0 for
- * an append or read of no rows).
+ * 2 for backward; for the caches' calls and fa_rope as documented with each, 0
+ * for an append or read of no rows).
  */
 int fa_last_launch_count(void);
 
 /*
  * Test hook (no counterpart on the pages).  kind = 1 makes the next fa_fwd
- * (or fa_fwd_splitkv, fa_bwd, fa_fwd_fp8 or fa_fwd_kv4) call on this host thread drop the first K
+ * (or fa_fwd_splitkv, fa_bwd, fa_fwd_fp8, fa_fwd_kv4 or fa_fwd_kv16) call on this host thread drop the first K
  * tile load (split-KV, backward: the first K/V tile) of every CTA (fa_fwd_kv4: of every warp): the bounded wait for it runs out (about 1 s), every thread of
  * the kernel retires, and fa_check then reports FA_ERR_TIMEOUT with the CUDA
  * context still usable.  kind = 0 clears a pending request.  Results of the faulted
