@@ -73,6 +73,24 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 __device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Three barrier phases tested by one thread back to back; true when all have completed.
+__device__ __forceinline__ bool mbar_try_wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred q0, q1, q2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q0, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q1, [%3], %4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q2, [%5], %6;\n\t"
+        "and.pred q0, q0, q1;\n\t"
+        "and.pred q0, q0, q2;\n\t"
+        "selp.u32 %0, 1, 0, q0;\n\t}\n"
+        : "=r"(ok)
+        : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const WaitFailure& wf,
                                           int site, int item)
 {
@@ -383,6 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool edge = key0 + kTile > v.clear;
                 if (!warp_wait(bar(L::bSFull + t), s_ph, abort_flag, wf, 80 + t, x.e)) goto done;
                 s_ph ^= 1;
+                // S1(j) is complete, and so is all that was issued before it: K(j)
+                // and V(j - 1) are no longer read
+                if (v.pair && t == 1 && row == 0) {
+                    mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)k_load(j)) % L::kStages));
+                    if (j > 0) mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)v_load(j - 1, x.n)) % L::kStages));
+                }
                 tc_fence_after_sync();
                 if (work) {
                     uint32_t sv[4][32];
@@ -649,6 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
         } else if (warp == 9) {
             // ============================================================ MMA issuer
+            // The whole warp runs this loop; lane 0 issues every MMA and commit (a
+            // commit tracks the MMAs of the thread that executes it).
             constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false), kIdescPV = idesc_bf16_f32(128, D, true);
             const bool leader = lane == 0;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -656,59 +682,137 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) tc_commit(bar(b));
                 __syncwarp();
             };
-            uint32_t ring = 0, q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {1, 1};
+            // S_t = Q_q K^T of the tile in a ring stage, and O_t (+)= P_t V
+            auto mma_s = [&](int t, int q, uint32_t stage) {
+                const uint64_t qd = smem_desc_sw128(sb + L::kQ + q * L::kTileBytes, 16, 1024);
+                const uint64_t kd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, 16, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
+                        mma_ss(tm + L::kColS + (uint32_t)(128 * t), qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+                    }
+                }
+                __syncwarp();
+            };
+            auto mma_pv = [&](int t, uint32_t stage, bool acc) {
+                const uint64_t vd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, kBox, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_ts(tm + L::kColO + (uint32_t)(D * t), tm + L::kColS + (uint32_t)(128 * t + 8 * kk),
+                               vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+                }
+                __syncwarp();
+            };
+            uint32_t stage = 0, ph = 0;  // of the next load in the ring
+            auto take = [&](uint32_t& st, uint32_t& p_) {
+                st = stage;
+                p_ = ph;
+                if (++stage == (uint32_t)L::kStages) {
+                    stage = 0;
+                    ph ^= 1u;
+                }
+            };
+            uint32_t q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {1, 1};
             bool ok = true, issued = false;
+            auto full = [&](uint32_t st, uint32_t p_, int site) {
+                return warp_wait(bar(L::bKVFull + st), p_, abort_flag, wf, site, x.e);
+            };
+            auto o_empty = [&](int t) {
+                const bool got = warp_wait(bar(L::bOEmpty + t), oe_ph[t], abort_flag, wf, 97, x.e);
+                oe_ph[t] ^= 1;
+                return got;
+            };
+            auto p_full = [&](int t) { return warp_wait(bar(L::bPFull + t), p_ph[t], abort_flag, wf, 96, x.e); };
             for (; more && ok; more = next_item(p, x)) {
                 const View v = view_of(p, x);
-                const int steps = v.pair ? 2 * x.n : x.n;
+                const int n = x.n;
                 if (!(ok = warp_wait(bar(L::bQFull), q_ph, abort_flag, wf, 93, x.e))) break;
                 q_ph ^= 1;
-                auto s_step = [&](int u) -> bool {
-                    const int t = u & 1, j = v.pair ? u >> 1 : u;
-                    const uint32_t n = ring + (uint32_t)k_load(j), stage = n % L::kStages;
-                    if (!warp_wait(bar(L::bKVFull + stage), (n / L::kStages) & 1u, abort_flag, wf, 94, x.e)) return false;
-                    tc_fence_after_sync();
-                    const uint64_t qd = smem_desc_sw128(sb + L::kQ + (v.pair ? t : 0) * L::kTileBytes, 16, 1024);
-                    const uint64_t kd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, 16, 1024);
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t off = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
-                            mma_ss(tm + L::kColS + (uint32_t)(128 * t), qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+                uint32_t ks, kp, vs, vp;
+                take(ks, kp);
+                if (!(ok = full(ks, kp, 94))) break;
+                tc_fence_after_sync();
+                mma_s(0, 0, ks);
+                issued = true;
+                commit(L::bSFull);
+                if (v.pair) {
+                    // Both streams read every tile.  A wait or a commit of this warp
+                    // idles the tensor core for some 100 cycles, so a tile takes two of
+                    // each: V(j), K(j + 1) and P0(j) are tested at once, and the second
+                    // softmax group frees the stages when it sees S1.
+                    mma_s(1, 1, ks);
+                    commit(L::bSFull + 1);
+                    if (n == 1) commit(L::bQEmpty);
+                    for (int j = 0; j < n; ++j) {
+                        const bool last = j + 1 == n;
+                        if (!last) take(ks, kp);
+                        take(vs, vp);
+                        if (j == 0 || !__all_sync(0xffffffffu,
+                                                  mbar_try_wait3(bar(L::bKVFull + vs), vp, bar(L::bKVFull + (last ? vs : ks)),
+                                                                 last ? vp : kp, bar(L::bPFull), p_ph[0]))) {
+                            if (!last && !(ok = full(ks, kp, 94))) break;
+                            if (!(ok = full(vs, vp, 95))) break;
+                            if (!(ok = p_full(0))) break;
+                        }
+                        p_ph[0] ^= 1;
+                        if (j == 0 && !(ok = o_empty(0))) break;
+                        tc_fence_after_sync();
+                        mma_pv(0, vs, j > 0);
+                        if (last) {
+                            commit(L::bOFull);
+                        } else {
+                            mma_s(0, 0, ks);
+                            commit(L::bSFull);
+                        }
+                        if (!(ok = p_full(1))) break;
+                        p_ph[1] ^= 1;
+                        if (j == 0 && !(ok = o_empty(1))) break;
+                        tc_fence_after_sync();
+                        mma_pv(1, vs, j > 0);
+                        if (last) {
+                            commit(L::bOFull + 1);
+                            commit(L::bKVEmpty + vs);
+                        } else {
+                            mma_s(1, 1, ks);
+                            commit(L::bSFull + 1);
+                            if (j + 2 == n) commit(L::bQEmpty);
                         }
                     }
-                    __syncwarp();
-                    issued = true;
-                    commit(L::bSFull + t);
-                    if (!v.pair || t == 1) commit(L::bKVEmpty + stage);
-                    if (u == steps - 1) commit(L::bQEmpty);
-                    return true;
-                };
-                ok = s_step(0) && (steps < 2 || s_step(1));
-                for (int u = 0; u < steps && ok; ++u) {
-                    const int t = u & 1, j = v.pair ? u >> 1 : u;
-                    const uint32_t n = ring + (uint32_t)v_load(j, x.n), stage = n % L::kStages;
-                    if (!(ok = warp_wait(bar(L::bKVFull + stage), (n / L::kStages) & 1u, abort_flag, wf, 95, x.e))) break;
-                    if (!(ok = warp_wait(bar(L::bPFull + t), p_ph[t], abort_flag, wf, 96, x.e))) break;
-                    p_ph[t] ^= 1;
-                    if (u < 2) {
-                        if (!(ok = warp_wait(bar(L::bOEmpty + t), oe_ph[t], abort_flag, wf, 97, x.e))) break;
-                        oe_ph[t] ^= 1;
+                } else {
+                    commit(L::bKVEmpty + ks);
+                    if (n > 1) {
+                        take(ks, kp);
+                        if (!(ok = full(ks, kp, 94))) break;
+                        tc_fence_after_sync();
+                        mma_s(1, 0, ks);
+                        commit(L::bSFull + 1);
+                        commit(L::bKVEmpty + ks);
                     }
-                    tc_fence_after_sync();
-                    const uint64_t vd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, kBox, 1024);
-                    if (leader) {
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ts(tm + L::kColO + (uint32_t)(D * t), tm + L::kColS + (uint32_t)(128 * t + 8 * kk),
-                                   vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV, (u >= 2 || kk > 0) ? 1u : 0u);
+                    if (n <= 2) commit(L::bQEmpty);
+                    for (int j = 0; j < n; ++j) {
+                        const int t = j & 1;
+                        take(vs, vp);
+                        if (!(ok = full(vs, vp, 95))) break;
+                        if (!(ok = p_full(t))) break;
+                        p_ph[t] ^= 1;
+                        if (j < 2 && !(ok = o_empty(t))) break;
+                        tc_fence_after_sync();
+                        mma_pv(t, vs, j >= 2);
+                        commit(L::bKVEmpty + vs);
+                        if (j >= n - 2) commit(L::bOFull + t);
+                        if (j + 2 < n) {
+                            take(ks, kp);
+                            if (!(ok = full(ks, kp, 94))) break;
+                            tc_fence_after_sync();
+                            mma_s(t, 0, ks);
+                            commit(L::bSFull + t);
+                            commit(L::bKVEmpty + ks);
+                            if (j + 3 == n) commit(L::bQEmpty);
+                        }
                     }
-                    __syncwarp();
-                    if (!v.pair || t == 1) commit(L::bKVEmpty + stage);
-                    if (u >= steps - 2) commit(L::bOFull + t);
-                    if (u + 2 < steps) ok = s_step(u + 2);
                 }
-                ring += 2u * (uint32_t)x.n;
             }
             if (issued) {
                 commit(L::bDrain);

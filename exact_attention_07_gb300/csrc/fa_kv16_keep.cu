@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(kThreads) fa_kv16_keep_kernel(const Kv16KeepPa
     __shared__ long long s_src[kThreads], s_dst[kThreads];
     const int s = blockIdx.x;
     if (s == p.num_seqs) {  // only this check
-        if (blockIdx.y == 0) kv16_check_slots<kThreads>(p.c, p.cu, p.num_seqs);
+        if (blockIdx.y == 0) kv16_check_slots(p.c, p.cu, p.num_seqs);
         return;
     }
     const Kv16Seq q = kv16_sequence(p.c, p.cu, p.total, s);

@@ -10,10 +10,10 @@
 // rounding at all; its top 32 bits go to sincospif.  Products and sums are in
 // fp32, rounded once to the output's type.
 //
-// Bound: HBM, each element read and written once.  A thread holds the cosines
-// and sines of 8 pairs (16 dimensions) of one token and takes its rows of
-// several heads, so that the angles' work (about 200 instructions) is shared,
-// with four rows' loads in flight.  Dimensions that do not turn are copied by
+// Bound: HBM, each element read and written once.  A block computes
+// the cosines and sines of its tokens once; a thread holds those of 8 pairs (16
+// dimensions) of one token and takes its rows of several heads, with four rows'
+// loads in flight.  Dimensions that do not turn are copied by
 // threads of the same kind.
 #include <cuda_bf16.h>
 
@@ -25,7 +25,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kMaxTokens = 8;
 
 template <typename T>
 struct Eight {  // 8 elements of a row
@@ -59,8 +59,8 @@ __device__ __forceinline__ void unpack8(const Eight<T>& x, float (&f)[8])
 
 __device__ __forceinline__ void store8(float* p, const float (&f)[8])
 {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8])
@@ -71,21 +71,17 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&f)[8])
         const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// m cos and m sin of the angles of 8 pairs from pair c0 on.
-__device__ __forceinline__ void angles(const RotaryParams& p, int pos, int c0, float (&c)[8], float (&s)[8])
+// m cos and m sin of pair c of a row at position pos.
+__device__ __forceinline__ float2 angle(const RotaryParams& p, int pos, int c)
 {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const unsigned long long turn = (unsigned long long)(long long)pos * __ldg(p.freqs + c0 + i);
-        const float x = (float)(int)(turn >> 32) * 4.656612873077393e-10f;  // half turns, -1 .. 1
-        float sn, cs;
-        sincospif(x, &sn, &cs);
-        c[i] = p.mscale * cs;
-        s[i] = p.mscale * (p.backward ? -sn : sn);
-    }
+    const unsigned long long turn = (unsigned long long)(long long)pos * __ldg(p.freqs + c);
+    const float x = (float)(int)(turn >> 32) * 4.656612873077393e-10f;  // half turns, -1 .. 1
+    float sn, cs;
+    sincospif(x, &sn, &cs);
+    return make_float2(p.mscale * cs, p.mscale * (p.backward ? -sn : sn));
 }
 
 template <bool INTER>
@@ -102,25 +98,27 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
 }
 
 // A block takes `tokens` tokens (blockIdx.x) and, with gridDim.y > 1, a share
-// of their heads.  Of a token's threads, neighbours take the D / 16 units of a
-// row: the first R / 16 turn, the others copy.
+// of their heads.  It computes the tokens' cosines and sines once, into shared
+// memory.  Of a token's threads, neighbours take the D / 16 units of a row: the
+// first R / 16 turn, the others copy.
 template <typename In, typename Out, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RotaryParams p, const int tokens)
+__global__ void __launch_bounds__(kThreads, 4) fa_rope_kernel(const RotaryParams p, const int tokens, const int slots)
 {
     constexpr int U = sizeof(In) == 2 ? 4 : 2;  // rows in flight
     if constexpr (APPEND) {
         if (p.c.ids && blockIdx.x == gridDim.x - 1) {  // the last blocks: only this check
-            if (blockIdx.y == 0) kv16_check_slots<kThreads>(p.c, p.cu, p.num_seqs);
+            if (blockIdx.y == 0) kv16_check_slots(p.c, p.cu, p.num_seqs);
             return;
         }
     }
-    __shared__ long long s_row[8];  // append: the token's K of head 0 in the pool, or -1
-    __shared__ int s_pos[8];
-    const int per = kThreads / tokens, units = p.D >> 4, slots = per / units;
-    const int tok = threadIdx.x / per, rest = threadIdx.x % per, slot = rest / units, unit = rest % units;
-    const long long t = (long long)blockIdx.x * tokens + tok;
-    const bool on = slot < slots && t < (long long)p.B * p.T;
-    const int b = on ? (int)(t / p.T) : 0, l = on ? (int)(t % p.T) : 0;
+    extern __shared__ __align__(16) float s_angle[];  // [tokens][R / 16][cosines 8, sines 8]
+    __shared__ long long s_row[kMaxTokens];  // append: the token's K of head 0 in the pool, or -1
+    __shared__ int s_pos[kMaxTokens];
+    const int units = p.D >> 4, slot = (int)threadIdx.x / units % slots, unit = (int)threadIdx.x % units;
+    const int tok = (int)threadIdx.x / (units * slots);
+    const long long t0 = (long long)blockIdx.x * tokens, t = t0 + tok;
+    const bool on = tok < tokens && t < (long long)p.B * p.T;  // threads behind the tokens' fill a warp
+    const int b = on ? (int)(t / p.T) : 0, l = on ? (int)(t - (long long)b * p.T) : 0;
 
     const int nturn = p.R >> 4;
     const bool turns = unit < nturn;
@@ -133,87 +131,130 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RotaryParams p,
         if (o1 >= p.start) o1 += p.R;
         o2 = o1 + 8;
     }
-    const int h1 = p.r[0].heads, h2 = h1 + p.r[1].heads, heads = h2 + p.r[2].heads;
+
+    // with few tokens (gridDim.y > 1) a thread has one row at most: it is on its
+    // way while the position is looked up
     const int step = slots * gridDim.y;
+    int h = slot + slots * blockIdx.y;  // of the rows of all kinds
+    const int h1 = p.r[0].heads, h2 = h1 + p.r[1].heads, heads_all = h2 + p.r[2].heads;
+    Eight<In> e1, e2;
+    const bool early = gridDim.y > 1 && on && h < heads_all;
+    if (early) {
+        const int kind = (h >= h1) + (h >= h2);
+        const RotaryRows& r = p.r[kind];
+        const In* x = static_cast<const In*>(r.x) + b * r.xb + l * r.xt + (h - (kind == 0 ? 0 : kind == 1 ? h1 : h2)) * r.xh;
+        e1 = load8(x + o1);
+        e2 = load8(x + o2);
+    }
 
-    Eight<In> x1[U], x2[U];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = h0 + i * step;
-            if (h >= heads) break;
-            const int kind = (h >= h1) + (h >= h2);
-            const RotaryRows& r = p.r[kind];
-            if (!turns && r.in_place) continue;
-            const In* x = static_cast<const In*>(r.x) + b * r.xb + l * r.xt +
-                          (h - (kind == 0 ? 0 : kind == 1 ? h1 : h2)) * r.xh;
-            x1[i] = load8(x + o1);
-            x2[i] = load8(x + o2);
-        }
-    };
-    int h0 = slot + slots * blockIdx.y;
-    if (on) load(h0);
-
-    int pos = 0;
-    long long row = 0;
     if constexpr (APPEND) {
-        if (threadIdx.x < tokens) {
-            const long long mine = (long long)blockIdx.x * tokens + threadIdx.x;
+        // the tokens' sequences, a warp a token: lanes look at 32 offsets at once
+        const int lane = threadIdx.x & 31;
+        for (int k = threadIdx.x >> 5; k < tokens; k += (int)blockDim.x >> 5) {
+            const long long mine = t0 + k;
             long long at = -1;
-            int ps = 0;
+            int pos = 0;
             if (mine < p.T) {
-                int s = 0, end = p.num_seqs - 1;  // the last sequence that begins at the token or before
-                while (s < end) {
-                    const int mid = (s + end + 1) >> 1;
-                    if (p.cu[mid] <= (int)mine)
-                        s = mid;
-                    else
-                        end = mid - 1;
+                int s = 0, n = p.num_seqs;  // the last sequence that begins at the token or before is in [s, s + n)
+                while (n > 1) {
+                    const int run = (n + 31) >> 5, i = s + lane * run;
+                    const int before = __popc(__ballot_sync(~0u, i < s + n && p.cu[min(i, s + n - 1)] <= (int)mine));
+                    const int skip = max(before - 1, 0) * run;
+                    s += skip;
+                    n = min(run, n - skip);
                 }
                 const Kv16Seq q = kv16_sequence(p.c, p.cu, p.T, s);
                 const int i = (int)mine - q.row0;
                 if (i >= 0 && i < q.n) {  // else a row behind the last sequence
-                    ps = q.len - q.n + i;
-                    at = kv16_row(p.c, p.D, q.pages, ps);
+                    pos = q.len - q.n + i;
+                    at = kv16_row(p.c, p.D, q.pages, pos);
                 }
+                if (p.pos) pos = __ldg(p.pos + mine);
             }
-            s_row[threadIdx.x] = at;
-            s_pos[threadIdx.x] = ps;
+            if (lane == 0) {
+                s_row[k] = at;
+                s_pos[k] = pos;
+            }
         }
         __syncthreads();
-        row = s_row[tok];
-        pos = s_pos[tok];
-        if (row < 0) return;
-        if (p.pos && on) pos = __ldg(p.pos + l);
-    } else {
-        pos = !on ? 0 : p.pos ? __ldg(p.pos + b * p.pos_b + l) : l;
     }
-    if (!on) return;
-    float c[8], s[8];
-    if (turns) angles(p, pos, 8 * unit, c, s);
-
-    while (h0 < heads) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = h0 + i * step;
-            if (h >= heads) break;
-            const int kind = (h >= h1) + (h >= h2), hh = h - (kind == 0 ? 0 : kind == 1 ? h1 : h2);
-            const RotaryRows& r = p.r[kind];
-            if (!turns && r.in_place) continue;
-            Out* y;
-            if (APPEND && kind > 0)
-                y = reinterpret_cast<Out*>(p.c.pool) + row + (hh + (kind == 2 ? p.c.Hkv : 0)) * kv16_head_stride(p.c, p.D);
-            else
-                y = static_cast<Out*>(r.y) + b * r.yb + l * r.yt + hh * r.yh;
-            float a[8], d[8];
-            unpack8<In>(x1[i], a);
-            unpack8<In>(x2[i], d);
-            if (turns && kind < 2) turn<INTER>(a, d, c, s);
-            store8(y + o1, a);
-            store8(y + o2, d);
+    for (int i = threadIdx.x; i < tokens * nturn * 8; i += blockDim.x) {
+        const int k = i / (nturn * 8), c = i - k * (nturn * 8);
+        int pos = 0;
+        if constexpr (APPEND) {
+            pos = s_pos[k];
+        } else {
+            const long long mine = min(t0 + k, (long long)p.B * p.T - 1);
+            const int mb = (int)(mine / p.T), ml = (int)(mine - (long long)mb * p.T);
+            pos = p.pos ? __ldg(p.pos + mb * p.pos_b + ml) : ml;
         }
-        h0 += U * step;
-        load(h0);
+        const float2 cs = angle(p, pos, c);
+        float* at = s_angle + (i & ~7) * 2 + (c & 7);
+        at[0] = cs.x;
+        at[8] = cs.y;
+    }
+    __syncthreads();
+    if (!on) return;
+    long long row = 0;
+    if constexpr (APPEND) {
+        row = s_row[tok];
+        if (row < 0) return;
+    }
+    float c[8], s[8];
+    if (turns) {
+        const float4* at = reinterpret_cast<const float4*>(s_angle + (tok * nturn + unit) * 16);
+        const float4 v[4] = {at[0], at[1], at[2], at[3]};
+        const float* f = &v[0].x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = f[i];
+            s[i] = f[8 + i];
+        }
+    }
+
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+        const RotaryRows& r = p.r[kind];
+        const int heads = r.heads;
+        const int mine = h;  // the slot's rows of this kind: every `step`-th from here
+        h = (mine - heads) % step;
+        if (h < 0) h += step;  // and the next kind's
+        if (mine >= heads || (!turns && r.in_place)) continue;
+        const In* x = static_cast<const In*>(r.x) + b * r.xb + l * r.xt + mine * r.xh;
+        Out* y;
+        long long ys;
+        if (APPEND && kind > 0) {
+            ys = kv16_head_stride(p.c, p.D);
+            y = reinterpret_cast<Out*>(p.c.pool) + row + (mine + (kind == 2 ? p.c.Hkv : 0)) * ys;
+        } else {
+            ys = r.yh;
+            y = static_cast<Out*>(r.y) + b * r.yb + l * r.yt + mine * ys;
+        }
+        const long long dx = r.xh * step, dy = ys * step;
+        const bool turning = turns && kind < 2;
+#pragma unroll 1
+        for (int k = mine; k < heads; k += U * step, x += U * dx, y += U * dy) {
+            Eight<In> x1[U], x2[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (i == 0 && early) {
+                    x1[0] = e1;
+                    x2[0] = e2;
+                } else if (k + i * step < heads) {
+                    x1[i] = load8(x + i * dx + o1);
+                    x2[i] = load8(x + i * dx + o2);
+                }
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                if (k + i * step < heads) {
+                    float a[8], d[8];
+                    unpack8<In>(x1[i], a);
+                    unpack8<In>(x2[i], d);
+                    if (turning) turn<INTER>(a, d, c, s);
+                    store8(y + i * dy + o1, a);
+                    store8(y + i * dy + o2, d);
+                }
+        }
     }
 }
 
@@ -222,7 +263,7 @@ __global__ void __launch_bounds__(kThreads) fa_rope_kernel(const RotaryParams p,
 // row; with many, eight tokens, and a thread takes all heads of its slot.
 struct RopeGrid {
     dim3 grid;
-    int tokens;
+    int threads, tokens, slots;
 };
 
 RopeGrid rope_grid(const RotaryParams& p, int num_sms, bool extra)
@@ -231,9 +272,10 @@ RopeGrid rope_grid(const RotaryParams& p, int num_sms, bool extra)
     const int units = p.D / 16, heads = p.r[0].heads + p.r[1].heads + p.r[2].heads;
     RopeGrid g;
     g.tokens = 1;
-    while (g.tokens < 8 && kThreads / (2 * g.tokens) >= units && n >= (long long)16 * num_sms * g.tokens) g.tokens *= 2;
-    const int slots = kThreads / g.tokens / units;
-    const int parts = n * heads / slots < 8ll * num_sms ? (heads + slots - 1) / slots : 1;
+    while (g.tokens < kMaxTokens && kThreads / (2 * g.tokens) >= units && n >= (long long)16 * num_sms * g.tokens) g.tokens *= 2;
+    g.slots = std::min(heads, kThreads / g.tokens / units);
+    g.threads = (g.tokens * g.slots * units + 31) / 32 * 32;  // whole warps: they look for sequences together
+    const int parts = n * heads / g.slots < 8ll * num_sms ? (heads + g.slots - 1) / g.slots : 1;
     g.grid = dim3((unsigned)((n + g.tokens - 1) / g.tokens + (extra ? 1 : 0)), (unsigned)parts);
     return g;
 }
@@ -242,7 +284,7 @@ template <typename In, typename Out, bool INTER, bool APPEND>
 cudaError_t launch(const RotaryParams& p, int num_sms, cudaStream_t stream)
 {
     const RopeGrid g = rope_grid(p, num_sms, APPEND && p.c.ids);
-    fa_rope_kernel<In, Out, INTER, APPEND><<<g.grid, kThreads, 0, stream>>>(p, g.tokens);
+    fa_rope_kernel<In, Out, INTER, APPEND><<<g.grid, g.threads, g.tokens * p.R * 4, stream>>>(p, g.tokens, g.slots);
     return cudaGetLastError();
 }
 

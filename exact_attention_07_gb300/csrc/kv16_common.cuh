@@ -48,14 +48,13 @@ __device__ __forceinline__ long long kv16_row(const Kv16Cache& c, int D, const i
 __device__ __forceinline__ long long kv16_head_stride(const Kv16Cache& c, int D) { return (long long)D << c.page_shift; }
 
 // One block looks for slots that a call names twice with rows.
-template <int THREADS>
 __device__ __forceinline__ void kv16_check_slots(const Kv16Cache& c, const int* cu, int num_seqs)
 {
     constexpr int kWords = 65536 / 32;  // FA_KV4_MAX_SLOTS
     __shared__ uint32_t seen[kWords];
-    for (int i = threadIdx.x; i < kWords; i += THREADS) seen[i] = 0;
+    for (int i = threadIdx.x; i < kWords; i += blockDim.x) seen[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < num_seqs; i += THREADS) {
+    for (int i = threadIdx.x; i < num_seqs; i += blockDim.x) {
         const int s = c.ids[i];
         if (s < 0 || s >= c.num_slots || cu[i + 1] <= cu[i]) continue;  // no rows: a padded batch
         const uint32_t bit = 1u << (s & 31);
