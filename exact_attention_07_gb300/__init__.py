@@ -1118,12 +1118,13 @@ _PER_TURN = Fraction("0.15915494309189533576888376337251436203445964574045644874
 class RopePlan:
     """Frequencies of rotary positions on a device and how they are applied (see rope_plan)."""
 
-    __slots__ = ("freqs", "rot_dim", "start", "interleaved", "mscale", "_packed")
+    __slots__ = ("freqs", "rot_dim", "start", "end", "interleaved", "mscale", "device", "packed")
 
     def __init__(self, freqs, start, interleaved, mscale):
         self.freqs, self.rot_dim = freqs, 2 * freqs.numel()
         self.start, self.interleaved, self.mscale = int(start), bool(interleaved), float(mscale)
-        self._packed = _pack_rope(freqs.data_ptr(), self.rot_dim, self.start, self.interleaved, self.mscale)
+        self.end, self.device = self.start + self.rot_dim, freqs.get_device()  # -1: not on a GPU
+        self.packed = _pack_rope(freqs.data_ptr(), self.rot_dim, self.start, self.interleaved, self.mscale)
 
 
 def rope_plan(rot_dim: int | None = None, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -1196,6 +1197,8 @@ def _check_rows(t, name, ndim, dtype, device):
 def _rotary_out(out, x, name, dtype):
     """`out`, checked, or a new tensor of x's shape."""
     if out is None:
+        if x.dtype is dtype and x.is_contiguous():
+            return torch.empty_like(x)
         return torch.empty(x.shape, dtype=dtype, device=x.device)
     _check_rows(out, name, x.dim(), dtype, x.get_device())
     if out.shape != x.shape:
@@ -1208,56 +1211,75 @@ def _rotary_out(out, x, name, dtype):
     return out
 
 
-def _packed_rows(x, y):
-    """struct fa_rotary_rows of x (and y, or None): [T, heads, D] or [B, heads, L, D]."""
-    a, b = x.stride(), (0, 0, 0, 0) if y is None else y.stride()
-    to = 0 if y is None else y.data_ptr()
-    if x.dim() == 3:
-        return _pack_rows(x.data_ptr(), to, 0, a[0], a[1], 0, b[0], b[1], x.shape[1])
-    return _pack_rows(x.data_ptr(), to, a[0], a[2], a[1], b[0], b[2], b[1], x.shape[1])
+def _rows_of(x, y, heads):
+    """struct fa_rotary_rows of packed rows x [T, heads, D] (and y, or None)."""
+    a0, a1, _ = x.stride()
+    if y is None:
+        return _pack_rows(x.data_ptr(), 0, 0, a0, a1, 0, 0, 0, heads)
+    b0, b1, _ = y.stride()
+    return _pack_rows(x.data_ptr(), y.data_ptr(), 0, a0, a1, 0, b0, b1, heads)
+
+
+def _dense_rows_of(x, y, heads):
+    """struct fa_rotary_rows of rows x and y [B, heads, L, D]."""
+    (a0, a1, a2, _), (b0, b1, b2, _) = x.stride(), y.stride()
+    return _pack_rows(x.data_ptr(), y.data_ptr(), a0, a2, a1, b0, b2, b1, heads)
 
 
 def _rope_call(name, q, k, rope, positions, dtype, q_out, k_out):
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _ROPE_TYPES and q.dim() in (3, 4) and q.stride(-1) == 1):
+        if not isinstance(q, torch.Tensor):
+            raise TypeError("q must be a torch.Tensor")
+        if q.dim() not in (3, 4):
+            raise ValueError(f"q must be [T, H, D] or [B, H, L, D], got shape {tuple(q.shape)}")
+        if q.dtype not in _ROPE_TYPES:
+            raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
+        if not q.is_cuda:
+            raise ValueError("q must be a CUDA tensor")
+        _check_rows(q, "q", q.dim(), q.dtype, q.get_device())
     if not isinstance(rope, RopePlan):
         raise TypeError("rope must be a RopePlan (rope_plan)")
-    device, ndim, kind = q.get_device() if q.is_cuda else -1, q.dim(), q.dtype
-    if ndim not in (3, 4):
-        raise ValueError(f"q must be [T, H, D] or [B, H, L, D], got shape {tuple(q.shape)}")
-    if kind not in _ROPE_TYPES:
-        raise TypeError(f"q must be bfloat16 or float32, got {kind}")
-    if device < 0:
-        raise ValueError("q must be a CUDA tensor")
-    to = kind if dtype is None else dtype
-    if to not in _ROPE_TYPES or (kind is torch.bfloat16 and to is torch.float32):
+    device, kind = q.get_device(), q.dtype
+    to = dtype or kind
+    if to is not kind and (to not in _ROPE_TYPES or kind is torch.bfloat16):
         raise TypeError(f"rows of {kind} can not become {to}")
-    _check_rows(q, "q", ndim, kind, device)
-    axis = 0 if ndim == 3 else 2  # of the tokens
-    B, T, D = (1 if ndim == 3 else q.shape[0]), q.shape[axis], q.shape[-1]
-    if rope.freqs.get_device() != device:
-        raise ValueError(f"rope must be on {q.device}, got {rope.freqs.device}")
-    if rope.start + rope.rot_dim > D:
-        raise ValueError(f"rope turns dimensions {rope.start} to {rope.start + rope.rot_dim} of {D}")
+    dense = q.dim() == 4
+    if dense:
+        B, Hq, T, D = q.shape
+    else:
+        B, (T, Hq, D) = 1, q.shape
+    if rope.device != device:
+        raise ValueError(f"rope must be on {q.device}, got cuda:{rope.device}")
+    if rope.end > D:
+        raise ValueError(f"rope turns dimensions {rope.start} to {rope.end} of {D}")
+    pack = _dense_rows_of if dense else _rows_of
     rows_k = None
     if k is not None:
-        _check_rows(k, "k", ndim, kind, device)
-        if k.shape[axis] != T or k.shape[-1] != D or (ndim == 4 and k.shape[0] != B):
+        if not (isinstance(k, torch.Tensor) and k.dtype is kind and k.dim() == q.dim() and k.get_device() == device
+                and k.stride(-1) == 1):
+            _check_rows(k, "k", q.dim(), kind, device)
+        Hk = k.shape[1]
+        if k.shape != ((B, Hk, T, D) if dense else (T, Hk, D)):
             raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
         k_out = _rotary_out(k_out, k, "k_out", to)
-        rows_k = _packed_rows(k, k_out) if k.shape[1] else None
+        if Hk:
+            rows_k = pack(k, k_out, Hk)
     elif k_out is not None:
         raise ValueError("k_out without k")
     q_out = _rotary_out(q_out, q, "q_out", to)
-    at = step = 0
+    at, step = None, 0
     if positions is not None:
-        _want(positions, "positions", torch.int32, positions.dim() if isinstance(positions, torch.Tensor) else 1, device)
-        if positions.shape not in ((T,), (B, T)) or (positions.dim() == 2 and ndim == 3):
-            raise ValueError(f"positions must be {(T,)}{'' if ndim == 3 else f' or {(B, T)}'}, got {tuple(positions.shape)}")
-        at, step = positions.data_ptr(), T if positions.dim() == 2 else 0
+        shape = positions.shape if isinstance(positions, torch.Tensor) else ()
+        _want(positions, "positions", torch.int32, len(shape) or 1, device)
+        if shape == (B, T) and dense:
+            step = T
+        elif shape != (T,):
+            raise ValueError(f"positions must be {(T,)}{f' or {(B, T)}' if dense else ''}, got {tuple(shape)}")
+        at = positions.data_ptr() or None
     lib = _lib or load_library()
-    st = _on_device(device, getattr(lib, name), _packed_rows(q, q_out), rows_k, B, T, D, kind is torch.float32,
-                    to is torch.float32, rope._packed, at or None, step, _raw_stream(device))
+    fp32 = kind is torch.float32
+    st = _on_device(device, lib.fa_rope if name == "fa_rope" else lib.fa_rope_bwd, pack(q, q_out, Hq), rows_k, B, T, D,
+                    fp32, fp32 and to is kind, rope.packed, at, step, _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, name)
     return q_out, k_out
@@ -1317,25 +1339,31 @@ def draft_mask(parents, cu_seqlens) -> tuple[torch.Tensor, torch.Tensor]:
     return mask.reshape(len(parents), words).clone(), torch.tensor(depth, dtype=torch.int32)
 
 
-def _kv16(pool, table, seq_lens, seq_ids, num_seqs, layers=False):
-    """Checks the cache of a call with num_seqs sequences.  Returns (fa_kv16_t as bytes, device index, Hkv, D)."""
+def _kv16(pool, table, seq_lens, seq_ids, cu_seqlens, layers=False):
+    """Checks the cache of a call and its packed sequences.  Returns (fa_kv16_t as bytes, device index, sequences, Hkv,
+    D)."""
     device = pool.get_device() if isinstance(pool, torch.Tensor) else -1
     ndim = 6 if layers and isinstance(pool, torch.Tensor) and pool.dim() == 6 else 5
     if not (device >= 0 and pool.dtype is torch.bfloat16 and pool.dim() == ndim and pool.is_contiguous()):
         _check_tensor(pool, "pool", torch.bfloat16, ndim)
+    if not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1
+            and cu_seqlens.get_device() == device and cu_seqlens.is_contiguous()):
+        _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    n = _num_seqs(cu_seqlens)
     slots, width = _slots_of(table, seq_lens, device)
-    N, two, H, P, D = pool.shape[-5:]
+    N, two, H, P, D = pool.shape[-5:] if layers else pool.shape
     if two != 2 or P not in (16, 32, 64, 128, 256) or D not in (64, 128):
         raise ValueError(f"pool must be bfloat16 [..., pages, 2, Hkv, page_size, D], got {tuple(pool.shape)}")
     ids = 0
     if seq_ids is not None:
         _want(seq_ids, "seq_ids", torch.int32, 1, device)
-        if seq_ids.shape[0] != num_seqs:
-            raise ValueError(f"seq_ids must name {num_seqs} slots")
+        if seq_ids.shape[0] != n:
+            raise ValueError(f"seq_ids must name {n} slots")
         ids = seq_ids.data_ptr()
-    elif num_seqs > slots:
-        raise ValueError(f"{num_seqs} sequences but {slots} slots")
-    return _pack_kv16(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ids, N, slots, width, P, H, D), device, H, D
+    elif n > slots:
+        raise ValueError(f"{n} sequences but {slots} slots")
+    return (_pack_kv16(pool.data_ptr(), table.data_ptr(), seq_lens.data_ptr(), ids, N, slots, width, P, H, D), device, n, H,
+            D)
 
 
 def fa_kv16_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor,
@@ -1350,30 +1378,33 @@ def fa_kv16_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, p
     if stream is not None:
         return _on_stream(stream, pool, fa_kv16_append, k, v, cu_seqlens, pool, table, seq_lens, seq_ids, rope,
                           positions, q, q_out)
-    n = _num_seqs(cu_seqlens)
-    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n)
-    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
-    _check_rows(k, "k", 3, torch.bfloat16, device)
-    _check_rows(v, "v", 3, torch.bfloat16, device)
+    c, device, n, H, D = _kv16(pool, table, seq_lens, seq_ids, cu_seqlens)
+    bf16 = torch.bfloat16
+    for t, name in ((k, "k"), (v, "v")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is bf16 and t.dim() == 3 and t.get_device() == device and t.stride(2) == 1):
+            _check_rows(t, name, 3, bf16, device)
     T = k.shape[0]
-    if k.shape != v.shape or k.shape[1:] != (H, D):
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
         raise ValueError(f"shape mismatch: k {tuple(k.shape)} v {tuple(v.shape)}, cache of {H} heads of {D}")
     packed = None
     if rope is not None:
         if not isinstance(rope, RopePlan):
             raise TypeError("rope must be a RopePlan (rope_plan)")
-        if rope.freqs.get_device() != device or rope.start + rope.rot_dim > D:
+        if rope.device != device or rope.end > D:
             raise ValueError(f"rope must be on {pool.device} and turn at most {D} dimensions")
-        packed = rope._packed
+        packed = rope.packed
     elif q is not None or positions is not None:
         raise ValueError("q and positions need rope")
     rows_q = None
     if q is not None:
-        _check_rows(q, "q", 3, torch.bfloat16, device)
-        if q.shape[0] != T or q.shape[2] != D:
+        if not (isinstance(q, torch.Tensor) and q.dtype is bf16 and q.dim() == 3 and q.get_device() == device and q.stride(2) == 1):
+            _check_rows(q, "q", 3, bf16, device)
+        Tq, Hq, Dq = q.shape
+        if Tq != T or Dq != D:
             raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
-        q_out = _rotary_out(q_out, q, "q_out", torch.bfloat16)
-        rows_q = _packed_rows(q, q_out) if q.shape[1] else None
+        q_out = _rotary_out(q_out, q, "q_out", bf16)
+        if Hq:
+            rows_q = _rows_of(q, q_out, Hq)
     elif q_out is not None:
         raise ValueError("q_out without q")
     at = None
@@ -1383,7 +1414,7 @@ def fa_kv16_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, p
             raise ValueError(f"positions must hold {T} numbers, got {positions.shape[0]}")
         at = positions.data_ptr() or None
     lib = _lib or load_library()
-    st = _on_device(device, lib.fa_kv16_append, rows_q, _packed_rows(k, None), _packed_rows(v, None),
+    st = _on_device(device, lib.fa_kv16_append, rows_q, _rows_of(k, None, H), _rows_of(v, None, H),
                     cu_seqlens.data_ptr(), n, T, c, packed, at, _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, "fa_kv16_append")
@@ -1419,33 +1450,36 @@ def fa_fwd_kv16(q: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor, t
     if stream is not None:
         return _on_stream(stream, pool, fa_fwd_kv16, q, cu_seqlens, pool, table, seq_lens, mask, causal, softmax_scale,
                           seq_ids, out, lse, workspace=workspace)
-    n = _num_seqs(cu_seqlens)
-    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n)
-    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
-    _check_rows(q, "q", 3, torch.bfloat16, device)
+    c, device, n, H, D = _kv16(pool, table, seq_lens, seq_ids, cu_seqlens)
+    if not (isinstance(q, torch.Tensor) and q.dtype is torch.bfloat16 and q.dim() == 3 and q.get_device() == device
+            and q.stride(2) == 1):
+        _check_rows(q, "q", 3, torch.bfloat16, device)
     T, Hq, Dq = q.shape
     if Dq != D:
         raise ValueError(f"q has head dimension {Dq} and the cache {D}")
     if Hq % H or not Hq:
         raise ValueError(f"{Hq} query heads over {H} KV heads")
-    words = 0
+    words, bits = 0, None
     if mask is not None:
         _want(mask, "mask", torch.int32, 2, device)
-        words = mask.shape[1]
-        if mask.shape[0] != T or words < 1:
+        rows, words = mask.shape
+        if rows != T or words < 1:
             raise ValueError(f"mask must be [{T}, words], got {tuple(mask.shape)}")
         if causal:
             raise ValueError("mask and causal exclude each other")
+        bits = mask.data_ptr()
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     else:
         _want(out, "out", torch.bfloat16, 3, device)
+        if out.shape != q.shape:
+            raise ValueError("out shape mismatch")
     if lse is None:
         lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
     else:
         _want(lse, "lse", torch.float32, 2, device)
-    if out.shape != q.shape or lse.shape != (Hq, T):
-        raise ValueError("out/lse shape mismatch")
+        if lse.shape != (Hq, T):
+            raise ValueError("lse shape mismatch")
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(D)
     lib = _lib or load_library()
@@ -1454,9 +1488,9 @@ def fa_fwd_kv16(q: torch.Tensor, cu_seqlens: torch.Tensor, pool: torch.Tensor, t
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {q.device}, got {workspace.device}")
-    st = _on_device(device, lib.fa_fwd_kv16, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), lse.data_ptr(),
-                    cu_seqlens.data_ptr(), n, T, Hq, None if mask is None else mask.data_ptr(), words,
-                    1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(device))
+    step, head, _ = q.stride()
+    st = _on_device(device, lib.fa_fwd_kv16, q.data_ptr(), step, head, out.data_ptr(), lse.data_ptr(),
+                    cu_seqlens.data_ptr(), n, T, Hq, bits, words, 1 if causal else 0, softmax_scale, c, workspace.data_ptr(), nbytes, _raw_stream(device))
     if st != FA_OK:
         raise FAError(st, "fa_fwd_kv16")
     return out, lse
@@ -1472,9 +1506,7 @@ def fa_kv16_keep(keep: torch.Tensor, counts: torch.Tensor, cu_seqlens: torch.Ten
     if stream is not None:
         return _on_stream(stream, pool, fa_kv16_keep, keep, counts, cu_seqlens, pool, table, seq_lens, seq_ids,
                           new_tokens)
-    n = _num_seqs(cu_seqlens)
-    c, device, H, D = _kv16(pool, table, seq_lens, seq_ids, n, layers=True)
-    _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
+    c, device, n, H, D = _kv16(pool, table, seq_lens, seq_ids, cu_seqlens, layers=True)
     _want(keep, "keep", torch.int32, 1, device)
     _want(counts, "counts", torch.int32, 1, device)
     if counts.shape[0] != n:

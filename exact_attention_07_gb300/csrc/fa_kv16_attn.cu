@@ -37,12 +37,14 @@ namespace fa {
 
 namespace {
 
-constexpr int kThreads = 384;  // 8 softmax warps, producer, MMA, 2 without work
+constexpr int kWarps = 12, kThreads = 32 * kWarps;  // 8 softmax warps, producer, MMA, 2 without work
 constexpr int kTile = 128;     // keys of a tile, rows of a stream
 constexpr int kBox = 128 * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds it by 2^8
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemCost = 2;     // what an item costs a block beside its tiles, in tiles
+
+constexpr int kItemBytes = 80;  // struct Item
 
 template <int D>
 struct Smem {
@@ -56,9 +58,10 @@ struct Smem {
                          bStEmpty = 11, bDrain = 12, bKVFull = 13, bKVEmpty = bKVFull + kStages,
                          kNumBars = bKVEmpty + kStages;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
-    static constexpr int kBytes = kMisc + 16;
-    static constexpr int kDynamic = kBytes + 1024;
-    static_assert(kDynamic + 192 <= 232448, "shared memory of one block");
+    static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the block's share
+    static constexpr int kItems = kSums + (kWarps + 2) * 8;  // Item [kWarps]
+    static constexpr int kBytes = kItems + kWarps * kItemBytes;
+    static_assert(kBytes <= 232448, "shared memory of one block");
     static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
 };
 
@@ -103,13 +106,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // A sequence's items: for every KV head, blocks of up to 2 npt of its query
 // tokens.  An item costs kItemCost and its tiles of keys.
 struct Item {
-    int s, e;       // sequence, item of it
-    int t, n;       // the block's part: tiles t .. t + n - 1
-    int nt;         // tiles of the item
-    int blocks;     // of the sequence's query tokens
-    long long left; // of the block's share, from tile t on
+    int s, e;        // sequence, item of it
+    int t, n;        // the block's part: tiles t .. t + n - 1
+    int nt;          // tiles of the item
+    int blocks;      // of the sequence's query tokens
+    long long left;  // of the block's share, from tile t on
     Kv16Seq q;
+    int h, tok0, ntok;  // KV head, first query token, and how many
+    int clear;          // keys in front of this are seen by every row
+    bool pair;          // two tiles of rows
 };
+static_assert(sizeof(Item) == kItemBytes, "shared memory layout");
 
 __device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
 {
@@ -140,23 +147,41 @@ __device__ __forceinline__ long long head_cost(const Kv16AttnParams& p, const Kv
     return sum;
 }
 
-__device__ __forceinline__ bool next_item(const Kv16AttnParams& p, Item& x)
+// Fills in what follows from the item: its KV head, query tokens and keys.
+__device__ __forceinline__ void open_item(const Kv16AttnParams& p, Item& x)
+{
+    x.h = x.e / x.blocks;
+    const int rb = x.e - x.h * x.blocks;
+    x.nt = tiles_of(p, x.q, rb);
+    x.tok0 = rb * 2 * p.npt;
+    x.ntok = min(x.q.n - x.tok0, 2 * p.npt);
+    x.pair = x.ntok > p.npt;
+    const int prefix = x.q.len - x.q.n;
+    x.clear = p.mask ? prefix : p.causal ? prefix + x.tok0 + 1 : x.q.len;
+}
+
+// The block's part of the next item; left <= 0 at the end of its share.  One
+// copy of this code serves all warps: a short call's time is largely that of
+// fetching code for the first time.
+__device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x)
 {
     x.left -= x.n;
-    if (x.left <= 0) return false;
+    if (x.left <= 0) return;
     if (++x.e == x.blocks * p.c.Hkv) {
         x.e = 0;
         do {
-            if (++x.s >= p.B) return false;
+            if (++x.s >= p.B) {
+                x.left = 0;
+                return;
+            }
             x.q = open_sequence(p, x.s);
             x.blocks = row_blocks(p, x.q.n);
         } while (x.blocks == 0);
     }
-    x.nt = tiles_of(p, x.q, x.e % x.blocks);
+    open_item(p, x);
     x.left -= kItemCost;
     x.t = 0;
     x.n = (int)min(x.left, (long long)x.nt);
-    return x.left > 0;
 }
 
 // The item that begins in a block and ends in a later one: its end in the
@@ -180,27 +205,6 @@ __host__ __device__ inline Parts parts_of(float* ws, int blocks, int rows)
     p.stat = reinterpret_cast<float4*>(p.join + ((blocks + 1) & ~1));
     p.o = p.stat + (size_t)blocks * 2 * rows;
     return p;
-}
-
-// What the rows of an item see.
-struct View {
-    int h, tok0, ntok;  // KV head, first query token of the item, and how many
-    bool pair;          // two tiles of rows
-    int prefix;         // positions in front of the call's
-    int clear;          // keys in front of this are seen by every row
-};
-
-__device__ __forceinline__ View view_of(const Kv16AttnParams& p, const Item& x)
-{
-    View v;
-    v.h = x.e / x.blocks;
-    const int rb = x.e - v.h * x.blocks;
-    v.tok0 = rb * 2 * p.npt;
-    v.ntok = min(x.q.n - v.tok0, 2 * p.npt);
-    v.pair = v.ntok > p.npt;
-    v.prefix = x.q.len - x.q.n;
-    v.clear = p.mask ? v.prefix : p.causal ? v.prefix + v.tok0 + 1 : x.q.len;
-    return v;
 }
 
 // Bits of the keys k0 .. k0 + 31 that query token i of the sequence may see.
@@ -239,11 +243,11 @@ __device__ __forceinline__ bool make_finite(uint4& x)
 
 // Adds to 32 columns of a row's sum what make_finite took out of the keys that
 // the row sees, of the part's tiles with masked keys.
-__device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, const View& v, int tok, int D, int c0,
+__device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, int tok, int D, int c0,
                                         float (&o)[32])
 {
     const int end = min(x.q.len, (x.t + x.n) * kTile);
-    const int from = max(x.t, v.clear / kTile) * kTile;  // the tile of the first masked key
+    const int from = max(x.t, x.clear / kTile) * kTile;  // the tile of the first masked key
     for (int k0 = from; k0 < end; k0 += 32) {
         uint32_t bits = seen_word(p, x.q, tok, k0);
         while (bits) {
@@ -252,7 +256,7 @@ __device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, 
             if (k >= end) break;
             const long long at = kv16_row(p.c, D, x.q.pages, k);
             if (at < 0) continue;
-            const uint16_t* val = p.c.pool + at + (long long)(p.c.Hkv + v.h) * kv16_head_stride(p.c, D) + c0;
+            const uint16_t* val = p.c.pool + at + (long long)(p.c.Hkv + x.h) * kv16_head_stride(p.c, D) + c0;
             for (int i = 0; i < 32; ++i) {
                 const uint32_t e = val[i];
                 if (not_finite(e)) o[i] += __uint_as_float(e << 16);
@@ -269,12 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const Kv16AttnParams p)
 {
     using L = Smem<D>;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ long long s_sum[kThreads / 32];
-    __shared__ Item s_first;
-    __shared__ long long s_share[2];  // end of the block's share, and its length
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
+    if (sb & 1023u) {  // the operands' swizzle needs it; the window begins so where a kernel has no other shared memory
+        if (threadIdx.x == 0) atomicOr(p.c.err, 4);
+        return;
+    }
+    long long* s_sum = reinterpret_cast<long long*>(smem + L::kSums);
+    long long* s_share = s_sum + kWarps;  // end of the block's share, and its length
+    Item* s_item = reinterpret_cast<Item*>(smem + L::kItems);  // each warp's part in hand: not in registers
     auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *poison = 0;
         mbar_init_fence();
         parts.join[blockIdx.x].e = -1;
-        s_first.left = 0;
+        for (int w = 0; w < kWarps; ++w) s_item[w].left = 0;
     }
     if (warp == 8 && lane == 0) {
         tma_prefetch_map(&tmQ);
@@ -356,13 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 at += one;
             }
             x.e = h * x.blocks + rb;
-            x.nt = tiles_of(p, x.q, rb);
+            open_item(p, x);
             x.left = last - first;
             const long long t = first - at - kItemCost;
             if (t < 0) x.left += t;
             x.t = t < 0 ? 0 : (int)t;
             x.n = (int)min(x.left, (long long)(x.nt - x.t));
-            s_first = x;
+            for (int w = 0; w < kWarps; ++w) s_item[w] = x;
             s_share[0] = last;
             s_share[1] = share;
         }
@@ -371,8 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    Item x = s_first;
-    bool more = x.left > 0;
+    Item& x = s_item[warp];
+    auto next = [&]() {
+        __syncwarp();
+        if (lane == 0) next_item(p, x);
+        __syncwarp();
+    };
 
     // K and V tiles of a part in the ring: K(0), then for each tile j K(j + 1)
     // and V(j), as the tensor core needs them.
@@ -388,24 +399,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s_ph = 0, st_ph = 0, o_ph[2] = {0, 0};
         uint32_t ring = 0;  // loads of the parts before
         const int tok_row = row / p.group, head_row = row - tok_row * p.group;
-        for (; more; more = next_item(p, x)) {
-            const View v = view_of(p, x);
-            const int rows_t = min(p.npt, v.ntok - (v.pair && t ? p.npt : 0)) * p.group;  // rows of this stream
-            const int tok = v.tok0 + (v.pair && t ? p.npt : 0) + tok_row;                 // of the sequence
+        for (; x.left > 0; next()) {
+            const int n = x.n, clear = x.clear;
+            const bool pair = x.pair;
+            const int key_first = x.t * kTile;
+            const int rows_t = min(p.npt, x.ntok - (pair && t ? p.npt : 0)) * p.group;  // rows of this stream
+            const int tok = x.tok0 + (pair && t ? p.npt : 0) + tok_row;                 // of the sequence
             const bool valid = row < rows_t;
             const bool work = (row & ~31) < rows_t;  // the warp has a row
-            const int step = v.pair ? 1 : 2;
+            const int step = pair ? 1 : 2;
             float r = -INFINITY, l = 0.f, l_rnd = 0.f;
-            for (int j = v.pair ? 0 : t; j < x.n; j += step) {
-                const int key0 = (x.t + j) * kTile;
-                const bool edge = key0 + kTile > v.clear;
+            for (int j = pair ? 0 : t; j < n; j += step) {
+                const int key0 = key_first + j * kTile;
+                const bool edge = key0 + kTile > clear;
                 if (!warp_wait(bar(L::bSFull + t), s_ph, abort_flag, wf, 80 + t, x.e)) goto done;
                 s_ph ^= 1;
                 // S1(j) is complete, and so is all that was issued before it: K(j)
                 // and V(j - 1) are no longer read
-                if (v.pair && t == 1 && row == 0) {
+                if (pair && t == 1 && row == 0) {
                     mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)k_load(j)) % L::kStages));
-                    if (j > 0) mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)v_load(j - 1, x.n)) % L::kStages));
+                    if (j > 0) mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)v_load(j - 1, n)) % L::kStages));
                 }
                 tc_fence_after_sync();
                 if (work) {
@@ -478,9 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 // V of a tile with masked keys (one stream: its reader, or the first of a pair)
-                if (edge && !(v.pair && t)) {
-                    const uint32_t n = ring + (uint32_t)v_load(j, x.n), stage = n % L::kStages;
-                    if (!warp_wait(bar(L::bKVFull + stage), (n / L::kStages) & 1u, abort_flag, wf, 82 + t, x.e)) goto done;
+                if (edge && !(pair && t)) {
+                    const uint32_t vl = ring + (uint32_t)v_load(j, n), stage = vl % L::kStages;
+                    if (!warp_wait(bar(L::bKVFull + stage), (vl / L::kStages) & 1u, abort_flag, wf, 82 + t, x.e)) goto done;
                     uint8_t* vrow = smem + L::kKV + stage * L::kTileBytes + row * 128;
                     const bool past = key0 + row >= x.q.len;
                     bool any = false;
@@ -503,12 +516,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before_sync();
                 mbar_arrive(bar(L::bPFull + t));
             }
-            ring += 2u * (uint32_t)x.n;
+            ring += 2u * (uint32_t)n;
 
             // ---- the part's end.  Each stream of a pair ends its own rows; else
             // stream 0 adds stream 1's, whose state it gets through shared memory.
-            const bool two = !v.pair && x.n > 1;
-            if (!v.pair && t == 1) {
+            const bool two = !pair && n > 1;
+            if (!pair && t == 1) {
                 if (two) {
                     if (!warp_wait(bar(L::bStEmpty), st_ph ^ 1u, abort_flag, wf, 84, x.e)) goto done;
                     stats[row] = r;
@@ -522,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!warp_wait(bar(L::bOFull + t), o_ph[t], abort_flag, wf, 85 + t, x.e)) goto done;
             o_ph[t] ^= 1;
-            if (v.pair && t == 0) o_ph[1] ^= 1;  // stream 1 waits for its own
+            if (pair && t == 0) o_ph[1] ^= 1;  // stream 1 waits for its own
             float w0 = 1.f, w1 = 0.f;
             if (two) {
                 if (!warp_wait(bar(L::bOFull + 1), o_ph[1], abort_flag, wf, 87, x.e)) goto done;
@@ -538,15 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(L::bStEmpty));
             }
             tc_fence_after_sync();
-            const bool whole = x.t == 0 && x.n == x.nt;
+            const bool whole = x.t == 0 && n == x.nt;
             const long long part = (long long)blockIdx.x * 2 + (x.t == 0 ? 1 : 0);
-            const long long prow = part * p.rows + (v.pair ? 128 * t : 0) + row;
+            const long long prow = part * p.rows + (pair ? 128 * t : 0) + row;
             const float inv = l > 0.f || l != l ? 1.f / (l + l_rnd) : 0.f;  // NaN stays
             const bool poisoned = *poison != 0;
             if (work) {
                 const uint32_t tO = lane_base + L::kColO;
                 const long long token = (long long)x.q.row0 + tok;
-                const int head = v.h * p.group + head_row;
+                const int head = x.h * p.group + head_row;
                 uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D);
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -563,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float fix[32];  // o itself stays in registers
 #pragma unroll
                         for (int i = 0; i < 32; ++i) fix[i] = o[i];
-                        add_poison(p, x, v, tok, D, 32 * c, fix);
+                        add_poison(p, x, tok, D, 32 * c, fix);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = fix[i];
                     }
@@ -575,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                     } else {
-                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + (v.pair ? 128 * t : 0) + row;
+                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + (pair ? 128 * t : 0) + row;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             to[(long long)i * p.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -606,26 +619,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool drop = p.fault == 1;
             bool ok = true;
             uint32_t armed = 0;  // loads whose stage was armed
-            for (; more && ok; more = next_item(p, x)) {
-                const View v = view_of(p, x);
+            for (; ok && x.left > 0; next()) {
+                const bool pair = x.pair;
+                const int row0 = x.q.row0 + x.tok0, h = x.h, n = x.n, t0 = x.t;
+                const int* pages = x.q.pages;
                 if (!(ok = warp_wait(bar(L::bQEmpty), qe_ph, abort_flag, wf, 89, x.e))) break;
                 qe_ph ^= 1;
-                const int q_tiles = v.pair ? 2 : 1;
+                const int q_tiles = pair ? 2 : 1;
                 if (lane == 0) mbar_arrive_expect_tx(bar(L::bQFull), q_tiles * boxes * p.npt * p.group * 128);
                 __syncwarp();
                 if (lane < q_tiles * boxes) {
                     const int tile = lane / boxes, half = lane % boxes;
                     tma_load_3d(sb + L::kQ + tile * L::kTileBytes + half * kBox, &tmQ, bar(L::bQFull), 64 * half,
-                                v.h * p.group, x.q.row0 + v.tok0 + tile * p.npt);
+                                h * p.group, row0 + tile * p.npt);
                 }
                 q_armed = (int)(qe_ph & 1u);
                 // lane i has the page of box i of a tile: those of K(j) are V(j)'s
                 const int pages_end = (x.q.len + page_rows - 1) / page_rows;  // boxes of the sequence
                 auto page_of = [&](int tile) {
-                    const int i = (x.t + tile) * per_tile + lane;  // box of the sequence
+                    const int i = (t0 + tile) * per_tile + lane;  // box of the sequence
                     int page = 0;
                     if (lane < per_tile && i < pages_end) {
-                        page = x.q.pages[(long long)i * page_rows >> shift];
+                        page = pages[(long long)i * page_rows >> shift];
                         if ((unsigned)page >= (unsigned)p.c.num_pages) {
                             atomicOr(p.c.err, 2);
                             page = 0;
@@ -637,16 +652,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t stage = ring % L::kStages;
                     if (!warp_wait(bar(L::bKVEmpty + stage), ((ring / L::kStages) & 1u) ^ 1u, abort_flag, wf, 90, x.e))
                         return false;
-                    const int i0 = (x.t + tile) * per_tile, n = min(per_tile, pages_end - i0);
+                    const int i0 = (t0 + tile) * per_tile, boxes_in = min(per_tile, pages_end - i0);
                     if (!drop) {
-                        if (lane == 0) mbar_arrive_expect_tx(bar(L::bKVFull + stage), n * boxes * page_rows * 128);
+                        if (lane == 0) mbar_arrive_expect_tx(bar(L::bKVFull + stage), boxes_in * boxes * page_rows * 128);
                         __syncwarp();
                         const int i = lane % per_tile, half = lane / per_tile;
                         const int pg = __shfl_sync(~0u, page, i);
-                        if (i < n && half < boxes)
+                        if (i < boxes_in && half < boxes)
                             tma_load_3d(sb + L::kKV + stage * L::kTileBytes + half * kBox + i * page_rows * 128, &tmKV,
                                         bar(L::bKVFull + stage), 64 * half, (i0 + i) * page_rows & ((1 << shift) - 1),
-                                        (pg * 2 + which) * p.c.Hkv + v.h);
+                                        (pg * 2 + which) * p.c.Hkv + h);
                         armed |= 1u << stage;
                     }
                     drop = false;
@@ -655,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 int page = page_of(0), page_k = page;
                 ok = load(0, page, 0);
-                for (int j = 0; j < x.n && ok; ++j) {
-                    if (j + 1 < x.n) {
+                for (int j = 0; j < n && ok; ++j) {
+                    if (j + 1 < n) {
                         page_k = page_of(j + 1);
                         ok = load(j + 1, page_k, 0);
                     }
@@ -725,9 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return got;
             };
             auto p_full = [&](int t) { return warp_wait(bar(L::bPFull + t), p_ph[t], abort_flag, wf, 96, x.e); };
-            for (; more && ok; more = next_item(p, x)) {
-                const View v = view_of(p, x);
+            for (; ok && x.left > 0; next()) {
                 const int n = x.n;
+                const bool pair = x.pair;
                 if (!(ok = warp_wait(bar(L::bQFull), q_ph, abort_flag, wf, 93, x.e))) break;
                 q_ph ^= 1;
                 uint32_t ks, kp, vs, vp;
@@ -737,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_s(0, 0, ks);
                 issued = true;
                 commit(L::bSFull);
-                if (v.pair) {
+                if (pair) {
                     // Both streams read every tile.  A wait or a commit of this warp
                     // idles the tensor core for some 100 cycles, so a tile takes two of
                     // each: V(j), K(j + 1) and P0(j) are tested at once, and the second
@@ -850,10 +865,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
     x.e = cut.e;
     x.q = open_sequence(p, x.s);
     x.blocks = row_blocks(p, x.q.n);
-    const View v = view_of(p, x);
-    const int t = v.pair ? blockIdx.y >> 2 : 0;  // tile of rows
+    open_item(p, x);
+    const bool pair = x.pair;
+    const int t = pair ? blockIdx.y >> 2 : 0;  // tile of rows
     const int row = 32 * blockIdx.y + lane - 128 * t;
-    const int rows_t = min(p.npt, v.ntok - t * p.npt) * p.group;
+    const int rows_t = min(p.npt, x.ntok - t * p.npt) * p.group;
     if (row - lane >= rows_t) return;
     const bool valid = row < rows_t;
     const int n = (int)((cut.end - 1) / cut.share) - (int)blockIdx.x + 1;
@@ -889,16 +905,16 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
         *reinterpret_cast<uint2*>(&s_o[lane][4 * (warp + 8 * i)]) =
             make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
     if (valid && warp == 0) {
-        const int head = v.h * p.group + row % p.group;
-        const long long token = (long long)x.q.row0 + v.tok0 + t * p.npt + row / p.group;
+        const int head = x.h * p.group + row % p.group;
+        const long long token = (long long)x.q.row0 + x.tok0 + t * p.npt + row / p.group;
         p.lse[(long long)head * p.T + token] = l == 0.f ? -INFINITY : (top + __log2f(l)) * kLn2;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * (D / 8); i += kJoinThreads) {
         const int rr = i / (D / 8), c = i % (D / 8), at = row - lane + rr;
         if (at >= rows_t) break;
-        const int head = v.h * p.group + at % p.group;
-        const long long token = (long long)x.q.row0 + v.tok0 + t * p.npt + at / p.group;
+        const int head = x.h * p.group + at % p.group;
+        const long long token = (long long)x.q.row0 + x.tok0 + t * p.npt + at / p.group;
         reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D)[c] = *reinterpret_cast<const uint4*>(&s_o[rr][8 * c]);
     }
 }
@@ -906,9 +922,9 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
 template <int D>
 cudaError_t launch(const CUtensorMap& q, const CUtensorMap& kv, const Kv16AttnParams& p, int blocks, cudaStream_t stream)
 {
-    const cudaError_t e = smem_limit_once<fa_kv16_attn_kernel<D>>(Smem<D>::kDynamic);
+    const cudaError_t e = smem_limit_once<fa_kv16_attn_kernel<D>>(Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    fa_kv16_attn_kernel<D><<<blocks, kThreads, Smem<D>::kDynamic, stream>>>(q, kv, p);
+    fa_kv16_attn_kernel<D><<<blocks, kThreads, Smem<D>::kBytes, stream>>>(q, kv, p);
     const cudaError_t f = cudaGetLastError();
     if (f != cudaSuccess) return f;
     cudaLaunchAttribute attr{};
