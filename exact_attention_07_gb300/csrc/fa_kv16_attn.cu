@@ -10,15 +10,18 @@
 // 4 D operations on it, so up to some 280 rows per KV head HBM bounds the call,
 // more (chunks of prompts) the tensor core.
 //
-// One persistent block per SM.  Two softmax warpgroups, "streams", each with
-// its own scores (128 columns of tensor memory, P over them) and its own
-// accumulator, take turns on the tensor core, so that one's exponentials
-// overlap the other's products.  With up to 128 rows the streams take
-// alternate tiles of 128 keys and are added at the end; with more they take
-// two tiles of rows over the same keys, which are then read once for 256 rows.
+// One persistent block per SM.  Its work is one sequence of steps, a tile of
+// rows against a tile of 128 keys each, that two softmax warpgroups take in
+// turn, each with its own scores (128 columns of tensor memory, P over them)
+// and its own accumulator: one's exponentials overlap the other's products.
+// With up to 128 rows the steps of an item are its tiles of keys, and what the
+// two accumulators hold is added at its end; with more they are two tiles of
+// rows for each tile of keys, which are then read once for 256 rows.  The
+// scores of a step are issued two steps ahead, over the ends of items too, so
+// that short sequences follow one another without a gap.
 //
-// K and V come by TMA, one box per page and 64 dimensions, into a ring of
-// tiles.  Positions behind the sequence's end, and what no row may see, can
+// K and V come by TMA, one box per page and 64 dimensions, each into a ring of
+// its own with a producer warp of its own.  Positions behind the sequence's end, and what no row may see, can
 // hold anything: scores are replaced where a key is masked, and in tiles with
 // masked keys V is looked over in shared memory first: rows behind the end
 // become zeros, and so do elements that are not finite, which are added to the
@@ -37,31 +40,44 @@ namespace fa {
 
 namespace {
 
-constexpr int kWarps = 12, kThreads = 32 * kWarps;  // 8 softmax warps, producer, MMA, 2 without work
-constexpr int kTile = 128;     // keys of a tile, rows of a stream
+constexpr int kWarps = 12, kThreads = 32 * kWarps;  // 8 softmax warps, K, MMA, V, one without work
+constexpr int kTile = 128;     // keys of a tile, rows of a tile
 constexpr int kBox = 128 * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds it by 2^8
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kItemCost = 2;     // what an item costs a block beside its tiles, in tiles
 
-constexpr int kItemBytes = 80;  // struct Item
+// A block's part of an item.  A sequence has, for every KV head, blocks of up
+// to 2 npt of its query tokens: the items of the list of work.
+struct Item {
+    long long left;  // of the block's share, from tile t on
+    Kv16Seq q;
+    int s, h, rb;       // sequence, KV head, block of query tokens
+    int blocks;         // of the sequence's query tokens
+    int t, n;           // the block's part: tiles t .. t + n - 1
+    int nt;             // tiles of the item
+    int tok0, ntok;     // first query token, and how many
+    int clear;          // keys in front of this are seen by every row
+    int pair;           // two tiles of rows
+    uint32_t step, tile, qtile;  // of the block's parts before: steps, tiles of keys, tiles of rows
+};
 
 template <int D>
 struct Smem {
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 12;
+    static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 8;  // tiles of the rings
     static constexpr int kQ = 0;  // [2] tiles
-    static constexpr int kKV = 2 * kTileBytes;
-    static constexpr int kStats = kKV + kStages * kTileBytes;  // float [3][128]: stream 1's r, l, l_rnd
+    static constexpr int kKRing = 2 * kTileBytes, kVRing = kKRing + kK * kTileBytes;
+    static constexpr int kStats = kVRing + kV * kTileBytes;  // float [3][128]: r, l, l_rnd of the group that does not end an item
     static constexpr int kBars = kStats + 3 * 128 * 4;
-    static constexpr int bQFull = 0, bQEmpty = 1, bSFull = 2, bPFull = 4, bOFull = 6, bOEmpty = 8, bStFull = 10,
-                         bStEmpty = 11, bDrain = 12, bKVFull = 13, bKVEmpty = bKVFull + kStages,
-                         kNumBars = bKVEmpty + kStages;
+    static constexpr int bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bOEmpty = 10, bStFull = 12,
+                         bStEmpty = 13, bDrain = 14, bKFull = 15, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK,
+                         bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
-    static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the block's share
-    static constexpr int kItems = kSums + (kWarps + 2) * 8;  // Item [kWarps]
-    static constexpr int kBytes = kItems + kWarps * kItemBytes;
-    static_assert(kBytes <= 232448, "shared memory of one block");
+    static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the blocks' share
+    static constexpr int kItems = kSums + (kWarps + 1) * 8;  // Item [kWarps]
+    static constexpr int kBytes = kItems + kWarps * (int)sizeof(Item);
+    static_assert(kBytes <= 232448 && kBars % 8 == 0, "shared memory of one block");
     static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
 };
 
@@ -103,21 +119,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // ------------------------------------------------------------------ the list of work
 
-// A sequence's items: for every KV head, blocks of up to 2 npt of its query
-// tokens.  An item costs kItemCost and its tiles of keys.
-struct Item {
-    int s, e;        // sequence, item of it
-    int t, n;        // the block's part: tiles t .. t + n - 1
-    int nt;          // tiles of the item
-    int blocks;      // of the sequence's query tokens
-    long long left;  // of the block's share, from tile t on
-    Kv16Seq q;
-    int h, tok0, ntok;  // KV head, first query token, and how many
-    int clear;          // keys in front of this are seen by every row
-    bool pair;          // two tiles of rows
-};
-static_assert(sizeof(Item) == kItemBytes, "shared memory layout");
-
 __device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
 {
     Kv16Seq q = kv16_sequence(p.c, p.cu, p.T, s);
@@ -128,7 +129,10 @@ __device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
     return q;
 }
 
-__device__ __forceinline__ int row_blocks(const Kv16AttnParams& p, int n) { return (n + 2 * p.npt - 1) / (2 * p.npt); }
+__device__ __forceinline__ int row_blocks(const Kv16AttnParams& p, int n)
+{
+    return n <= 2 * p.npt ? n > 0 : (n + 2 * p.npt - 1) / (2 * p.npt);
+}
 
 // Tiles of keys that block rb of a sequence's query tokens reads.
 __device__ __forceinline__ int tiles_of(const Kv16AttnParams& p, const Kv16Seq& q, int rb)
@@ -137,46 +141,49 @@ __device__ __forceinline__ int tiles_of(const Kv16AttnParams& p, const Kv16Seq& 
     return (keys + kTile - 1) / kTile;
 }
 
-// Cost of one KV head of a sequence.
+// Length in the list of one KV head of a sequence: its items' tiles, and
+// kItemCost in front of each item.
 __device__ __forceinline__ long long head_cost(const Kv16AttnParams& p, const Kv16Seq& q)
 {
     const int nb = row_blocks(p, q.n);
-    if (!p.causal) return (long long)nb * (kItemCost + tiles_of(p, q, 0));
+    if (!p.causal || nb <= 1) return (long long)nb * (kItemCost + tiles_of(p, q, 0));
     long long sum = 0;
     for (int rb = 0; rb < nb; ++rb) sum += kItemCost + tiles_of(p, q, rb);
     return sum;
 }
 
-// Fills in what follows from the item: its KV head, query tokens and keys.
+// Fills in what follows from the sequence, the head and the block of tokens.
 __device__ __forceinline__ void open_item(const Kv16AttnParams& p, Item& x)
 {
-    x.h = x.e / x.blocks;
-    const int rb = x.e - x.h * x.blocks;
-    x.nt = tiles_of(p, x.q, rb);
-    x.tok0 = rb * 2 * p.npt;
+    x.nt = tiles_of(p, x.q, x.rb);
+    x.tok0 = x.rb * 2 * p.npt;
     x.ntok = min(x.q.n - x.tok0, 2 * p.npt);
     x.pair = x.ntok > p.npt;
     const int prefix = x.q.len - x.q.n;
     x.clear = p.mask ? prefix : p.causal ? prefix + x.tok0 + 1 : x.q.len;
 }
 
-// The block's part of the next item; left <= 0 at the end of its share.  One
-// copy of this code serves all warps: a short call's time is largely that of
-// fetching code for the first time.
+// The block's part of the next item; left <= 0 at the end of its share.
 __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x)
 {
+    x.step += x.pair ? 2 * x.n : x.n;
+    x.tile += x.n;
+    x.qtile += x.pair ? 2 : 1;
     x.left -= x.n;
     if (x.left <= 0) return;
-    if (++x.e == x.blocks * p.c.Hkv) {
-        x.e = 0;
-        do {
-            if (++x.s >= p.B) {
-                x.left = 0;
-                return;
-            }
-            x.q = open_sequence(p, x.s);
-            x.blocks = row_blocks(p, x.q.n);
-        } while (x.blocks == 0);
+    if (++x.rb == x.blocks) {
+        x.rb = 0;
+        if (++x.h == p.c.Hkv) {
+            x.h = 0;
+            do {
+                if (++x.s >= p.B) {
+                    x.left = 0;
+                    return;
+                }
+                x.q = open_sequence(p, x.s);
+                x.blocks = row_blocks(p, x.q.n);
+            } while (x.blocks == 0);
+        }
     }
     open_item(p, x);
     x.left -= kItemCost;
@@ -184,11 +191,10 @@ __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x)
     x.n = (int)min(x.left, (long long)x.nt);
 }
 
-// The item that begins in a block and ends in a later one: its end in the
-// list and the blocks' share of that; e -1: none.
+// The item that begins in a block and ends in a later one, for the kernel that
+// joins its parts; parts 0: none.
 struct Cut {
-    int s, e;
-    long long end, share;
+    int parts, token, ntok, h;  // blocks that hold a part; first row of q, how many, KV head
 };
 
 // Where the kernels keep what they share in the workspace.
@@ -202,7 +208,7 @@ __host__ __device__ inline Parts parts_of(float* ws, int blocks, int rows)
 {
     Parts p;
     p.join = reinterpret_cast<Cut*>(ws);
-    p.stat = reinterpret_cast<float4*>(p.join + ((blocks + 1) & ~1));
+    p.stat = reinterpret_cast<float4*>(p.join + blocks);
     p.o = p.stat + (size_t)blocks * 2 * rows;
     return p;
 }
@@ -241,14 +247,13 @@ __device__ __forceinline__ bool make_finite(uint4& x)
     return any;
 }
 
-// Adds to 32 columns of a row's sum what make_finite took out of the keys that
-// the row sees, of the part's tiles with masked keys.
+// Adds to 32 columns of a row's sum what make_finite took out of the part's
+// keys that the row sees.
 __device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, int tok, int D, int c0,
                                         float (&o)[32])
 {
     const int end = min(x.q.len, (x.t + x.n) * kTile);
-    const int from = max(x.t, x.clear / kTile) * kTile;  // the tile of the first masked key
-    for (int k0 = from; k0 < end; k0 += 32) {
+    for (int k0 = max(x.t * kTile, x.clear); k0 < end; k0 += 32) {
         uint32_t bits = seen_word(p, x.q, tok, k0);
         while (bits) {
             const int k = k0 + __ffs(bits) - 1;
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const Kv16AttnParams p)
 {
     using L = Smem<D>;
+    constexpr uint32_t kK = L::kK, kV = L::kV;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
     if (sb & 1023u) {  // the operands' swizzle needs it; the window begins so where a kernel has no other shared memory
@@ -280,7 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     long long* s_sum = reinterpret_cast<long long*>(smem + L::kSums);
-    long long* s_share = s_sum + kWarps;  // end of the block's share, and its length
     Item* s_item = reinterpret_cast<Item*>(smem + L::kItems);  // each warp's part in hand: not in registers
     auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
@@ -292,10 +297,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
 
     let_dependents_launch();
+
+    // This block's share of the list: every thread sums a run of sequences.
+    const int run = (p.B + kThreads - 1) / kThreads;
+    const int run0 = min(p.B, (int)threadIdx.x * run), run1 = min(p.B, run0 + run);
+    Kv16Seq own{};  // the run's first
+    long long mine = 0;
+    if (run0 < run1) {
+        own = open_sequence(p, run0);
+        mine = p.c.Hkv * head_cost(p, own);
+    }
+    for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
+
     if (threadIdx.x == 0) {
-        mbar_init(bar(L::bQFull), 1);
-        mbar_init(bar(L::bQEmpty), 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(bar(L::bQFull + t), 1);
+            mbar_init(bar(L::bQEmpty + t), 1);
             mbar_init(bar(L::bSFull + t), 1);
             mbar_init(bar(L::bPFull + t), 128);
             mbar_init(bar(L::bOFull + t), 1);
@@ -304,30 +321,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(L::bStFull), 128);
         mbar_init(bar(L::bStEmpty), 128);
         mbar_init(bar(L::bDrain), 1);
-        for (int s = 0; s < L::kStages; ++s) {
-            mbar_init(bar(L::bKVFull + s), 1);
-            mbar_init(bar(L::bKVEmpty + s), 1);
-        }
+        for (uint32_t s = 0; s < 2 * (kK + kV); ++s) mbar_init(bar(L::bKFull + s), 1);
         *abort_flag = 0;
         *poison = 0;
         mbar_init_fence();
-        parts.join[blockIdx.x].e = -1;
-        for (int w = 0; w < kWarps; ++w) s_item[w].left = 0;
+        parts.join[blockIdx.x].parts = 0;
+        s_item[0].left = 0;
     }
-    if (warp == 8 && lane == 0) {
-        tma_prefetch_map(&tmQ);
-        tma_prefetch_map(&tmKV);
-    }
+    if (warp == 8 && lane == 0) tma_prefetch_map(&tmQ);
+    if (warp == 10 && lane == 0) tma_prefetch_map(&tmKV);
     if (warp == 9) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
-
-    // This block's share of the list: every thread sums a run of sequences.
     {
-        const int run = (p.B + kThreads - 1) / kThreads, run0 = min(p.B, (int)threadIdx.x * run), run1 = min(p.B, run0 + run);
-        long long mine = 0;
-        for (int s = run0; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
         long long upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -337,58 +344,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 31) s_sum[warp] = upto;
         __syncthreads();
         long long total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
             if (w == warp) upto += total;
             total += s_sum[w];
         }
-        const long long share = max((total + gridDim.x - 1) / gridDim.x, (long long)kItemCost + 1);
+        // ceil(total / blocks), or a little above
+        long long share = (long long)((float)total * (1.f / gridDim.x) * 1.000002f + 0.999f);
+        share += share * gridDim.x < total;
+        share = max(share, (long long)kItemCost + 1);
         const long long first = share * blockIdx.x, last = min(total, first + share);
         if (first < last && first < upto && first >= upto - mine) {
             long long at = upto - mine, cost;
             Item x;
             x.s = run0;
-            for (;; ++x.s) {
-                x.q = open_sequence(p, x.s);
-                cost = head_cost(p, x.q);
-                if (at + cost * p.c.Hkv > first) break;
+            x.q = own;
+            while (at + (cost = head_cost(p, x.q)) * p.c.Hkv <= first) {
                 at += cost * p.c.Hkv;
+                x.q = open_sequence(p, ++x.s);
             }
             x.blocks = row_blocks(p, x.q.n);
-            const int h = (int)((first - at) / cost);
-            at += h * cost;
-            int rb = 0;
-            for (;; ++rb) {
-                const int one = kItemCost + tiles_of(p, x.q, rb);
-                if (at + one > first) break;
-                at += one;
-            }
-            x.e = h * x.blocks + rb;
+            for (x.h = 0; at + cost <= first; ++x.h) at += cost;
+            int one;
+            for (x.rb = 0; at + (one = kItemCost + tiles_of(p, x.q, x.rb)) <= first; ++x.rb) at += one;
             open_item(p, x);
             x.left = last - first;
             const long long t = first - at - kItemCost;
             if (t < 0) x.left += t;
             x.t = t < 0 ? 0 : (int)t;
             x.n = (int)min(x.left, (long long)(x.nt - x.t));
-            for (int w = 0; w < kWarps; ++w) s_item[w] = x;
-            s_share[0] = last;
-            s_share[1] = share;
+            x.step = x.tile = x.qtile = 0;
+            s_item[0] = x;
+            s_sum[kWarps] = share;
         }
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (s_item[0].left <= 0) goto done;  // no work, for no warp
+    if (warp > 0) {
+        for (int i = lane; i < (int)sizeof(Item) / 4; i += 32)
+            reinterpret_cast<int*>(s_item + warp)[i] = reinterpret_cast<const int*>(s_item)[i];
+    }
+    __syncthreads();  // warp 0 changes its own from here
+    {
     Item& x = s_item[warp];
-    auto next = [&]() {
+    auto next = [&](Item& y) {
         __syncwarp();
-        if (lane == 0) next_item(p, x);
+        if (lane == 0) next_item(p, y);
         __syncwarp();
     };
-
-    // K and V tiles of a part in the ring: K(0), then for each tile j K(j + 1)
-    // and V(j), as the tensor core needs them.
-    auto k_load = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto v_load = [](int j, int n) { return j == n - 1 ? 2 * j + 1 : 2 * j + 2; };
+    auto wait = [&](int b, uint32_t parity, int site) -> bool {
+        return warp_wait(bar(b), parity & 1u, abort_flag, wf, site, blockIdx.x);
+    };
 
     if (warp < 8) {
         // ============================================================ softmax
@@ -396,29 +405,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const uint32_t tS = lane_base + L::kColS + (uint32_t)(128 * t);
-        uint32_t s_ph = 0, st_ph = 0, o_ph[2] = {0, 0};
-        uint32_t ring = 0;  // loads of the parts before
+        uint32_t st_ph = 0, o_ph = 0;  // o_ph: a bit per stream
         const int tok_row = row / p.group, head_row = row - tok_row * p.group;
-        for (; x.left > 0; next()) {
-            const int n = x.n, clear = x.clear;
+        for (; x.left > 0; next(x)) {
+            const int n = x.n, clear = x.clear, key_first = x.t * kTile;
             const bool pair = x.pair;
-            const int key_first = x.t * kTile;
-            const int rows_t = min(p.npt, x.ntok - (pair && t ? p.npt : 0)) * p.group;  // rows of this stream
-            const int tok = x.tok0 + (pair && t ? p.npt : 0) + tok_row;                 // of the sequence
+            const int u0 = (t ^ (int)x.step) & 1;  // the group's first step of the item; of a pair: its tile of rows
+            const int rt = pair ? u0 : 0;
+            const int rows_t = min(p.npt, x.ntok - rt * p.npt) * p.group;  // rows of the tile
+            const int tok = x.tok0 + rt * p.npt + tok_row;                 // of the sequence
             const bool valid = row < rows_t;
             const bool work = (row & ~31) < rows_t;  // the warp has a row
-            const int step = pair ? 1 : 2;
+            const int j0 = pair ? 0 : u0, dj = pair ? 1 : 2;
+            uint32_t s_ph = (x.step + u0) >> 1;  // the group's steps so far
+            const uint32_t tile0 = x.tile;
             float r = -INFINITY, l = 0.f, l_rnd = 0.f;
-            for (int j = pair ? 0 : t; j < n; j += step) {
+            for (int j = j0; j < n; j += dj, ++s_ph) {
                 const int key0 = key_first + j * kTile;
                 const bool edge = key0 + kTile > clear;
-                if (!warp_wait(bar(L::bSFull + t), s_ph, abort_flag, wf, 80 + t, x.e)) goto done;
-                s_ph ^= 1;
-                // S1(j) is complete, and so is all that was issued before it: K(j)
-                // and V(j - 1) are no longer read
-                if (pair && t == 1 && row == 0) {
-                    mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)k_load(j)) % L::kStages));
-                    if (j > 0) mbar_arrive(bar(L::bKVEmpty + (ring + (uint32_t)v_load(j - 1, n)) % L::kStages));
+                if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
+                // the second scores of a tile are complete, and so is all that was
+                // issued before them: K(j) and V(j - 1) are no longer read
+                if (pair && rt == 1 && row == 0) {
+                    const uint32_t T = tile0 + (uint32_t)j;
+                    mbar_arrive(bar(L::bKEmpty + T % kK));
+                    if (j > 0) mbar_arrive(bar(L::bVEmpty + (T - 1) % kV));
                 }
                 tc_fence_after_sync();
                 if (work) {
@@ -474,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = fmaf(l, alpha, a0 + a1);
                     const float pm = ex2_approx(fmaf(mraw, p.scale_log2, -r_use));
                     l_rnd = fmaf(l_rnd, alpha, __uint_as_float(pack_bf16x2(pm, 0.f) << 16) - pm);
-                    // the stream's last P.V was complete before this S was: O is idle
-                    if (j >= step && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    // the group's last P.V was complete before these scores were: O is idle
+                    if (j != j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         const uint32_t tO = lane_base + L::kColO + (uint32_t)(D * t);
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -490,57 +501,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r = r_new;
                     tmem_wait_st();
                 }
-                // V of a tile with masked keys (one stream: its reader, or the first of a pair)
-                if (edge && !(pair && t)) {
-                    const uint32_t vl = ring + (uint32_t)v_load(j, n), stage = vl % L::kStages;
-                    if (!warp_wait(bar(L::bKVFull + stage), (vl / L::kStages) & 1u, abort_flag, wf, 82 + t, x.e)) goto done;
-                    uint8_t* vrow = smem + L::kKV + stage * L::kTileBytes + row * 128;
-                    const bool past = key0 + row >= x.q.len;
-                    bool any = false;
+                // V of a tile with masked keys, before its first product
+                if (edge && rt == 0) {
+                    const uint32_t T = tile0 + (uint32_t)j, stage = T % kV;
+                    if (!wait(L::bVFull + stage, T / kV, 82 + t)) goto done;
+                    if (key0 + row >= clear) {
+                        uint8_t* vrow = smem + L::kVRing + stage * L::kTileBytes + row * 128;
+                        const bool past = key0 + row >= x.q.len;
+                        bool any = false;
 #pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
-                        uint4* at = reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
-                        if (past) {
-                            *at = make_uint4(0, 0, 0, 0);
-                        } else {
-                            uint4 e = *at;
-                            if (make_finite(e)) {
-                                *at = e;
-                                any = true;
+                        for (int i = 0; i < D / 8; ++i) {
+                            uint4* at = reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
+                            if (past) {
+                                *at = make_uint4(0, 0, 0, 0);
+                            } else {
+                                uint4 e = *at;
+                                if (make_finite(e)) {
+                                    *at = e;
+                                    any = true;
+                                }
                             }
                         }
+                        if (any) *poison = 1;
                     }
-                    if (any) *poison = 1;
                     fence_proxy_async_smem();
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar(L::bPFull + t));
             }
-            ring += 2u * (uint32_t)n;
 
-            // ---- the part's end.  Each stream of a pair ends its own rows; else
-            // stream 0 adds stream 1's, whose state it gets through shared memory.
+            // ---- the item's end.  Each group of a pair ends its own rows; else the
+            // group of the last step adds the other's, whose state it gets through
+            // shared memory, and the other goes on.
+            const int g = pair ? t : (int)(x.step + (uint32_t)n - 1u) & 1;
             const bool two = !pair && n > 1;
-            if (!pair && t == 1) {
+            const uint32_t o_now = o_ph;
+            o_ph ^= pair || two ? 3u : 1u << g;
+            if (g != t) {
                 if (two) {
-                    if (!warp_wait(bar(L::bStEmpty), st_ph ^ 1u, abort_flag, wf, 84, x.e)) goto done;
+                    if (!wait(L::bStEmpty, st_ph ^ 1u, 84)) goto done;
                     stats[row] = r;
                     stats[128 + row] = l;
                     stats[256 + row] = l_rnd;
                     mbar_arrive(bar(L::bStFull));
                     st_ph ^= 1;
-                    o_ph[1] ^= 1;
                 }
                 continue;
             }
-            if (!warp_wait(bar(L::bOFull + t), o_ph[t], abort_flag, wf, 85 + t, x.e)) goto done;
-            o_ph[t] ^= 1;
-            if (pair && t == 0) o_ph[1] ^= 1;  // stream 1 waits for its own
+            if (!wait(L::bOFull + t, o_now >> t, 85 + t)) goto done;
             float w0 = 1.f, w1 = 0.f;
             if (two) {
-                if (!warp_wait(bar(L::bOFull + 1), o_ph[1], abort_flag, wf, 87, x.e)) goto done;
-                o_ph[1] ^= 1;
-                if (!warp_wait(bar(L::bStFull), st_ph, abort_flag, wf, 88, x.e)) goto done;
+                if (!wait(L::bOFull + (t ^ 1), o_now >> (t ^ 1), 87)) goto done;
+                if (!wait(L::bStFull, st_ph, 88)) goto done;
                 st_ph ^= 1;
                 const float r1 = stats[row], top = fmaxf(r, r1), m = top == -INFINITY ? 0.f : top;
                 w0 = ex2_approx(r - m);
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after_sync();
             const bool whole = x.t == 0 && n == x.nt;
             const long long part = (long long)blockIdx.x * 2 + (x.t == 0 ? 1 : 0);
-            const long long prow = part * p.rows + (pair ? 128 * t : 0) + row;
+            const int prow = 128 * rt + row;
             const float inv = l > 0.f || l != l ? 1.f / (l + l_rnd) : 0.f;  // NaN stays
             const bool poisoned = *poison != 0;
             if (work) {
@@ -566,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t ov[32], o1[32];
                     float o[32];
                     tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov);
-                    if (two) tmem_ld32(tO + (uint32_t)(D + 32 * c), o1);
+                    if (two) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -588,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                         pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
                                                         pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
                     } else {
-                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + (pair ? 128 * t : 0) + row;
+                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + prow;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             to[(long long)i * p.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -598,48 +610,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (whole)
                         p.lse[(long long)head * p.T + token] = l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
                     else
-                        parts.stat[prow] = make_float4(r, l, l_rnd, 0.f);
+                        parts.stat[part * p.rows + prow] = make_float4(r, l, l_rnd, 0.f);
                 }
             }
             tc_fence_before_sync();
             mbar_arrive(bar(L::bOEmpty + t));
-            if (two) mbar_arrive(bar(L::bOEmpty + 1));
-            if (!whole && x.t == 0 && t == 0 && row == 0)
-                parts.join[blockIdx.x] = Cut{x.s, x.e, s_share[0] - x.left + x.nt, s_share[1]};
+            if (two) mbar_arrive(bar(L::bOEmpty + (t ^ 1)));
+            if (!whole && x.t == 0 && rt == 0 && row == 0) {
+                const int rest = x.nt - n, share = (int)min(s_sum[kWarps], 1ll << 30);
+                parts.join[blockIdx.x] = Cut{1 + (rest + share - 1) / share, x.q.row0 + x.tok0, x.ntok, x.h};
+            }
         }
     } else {
         regs_decrease<88>();
-        if (warp == 8) {
-            // ============================================================ TMA producer
-            const int shift = p.c.page_shift, page_rows = 1 << min(shift, 7), boxes = D / 64;
+        if (warp != 9 && warp < 11) {
+            // ============================================================ TMA producers: Q and K, V
+            const bool keys = warp == 8;
+            const uint32_t stages = keys ? kK : kV;
+            const int full = keys ? L::bKFull : L::bVFull, empty = keys ? L::bKEmpty : L::bVEmpty;
+            const uint32_t ring = sb + (keys ? L::kKRing : L::kVRing);
+            const int shift = p.c.page_shift, page_rows = 1 << min(shift, 7);
+            constexpr int boxes = D / 64;
             const int per_tile = kTile / page_rows;  // boxes of pages in a tile
-            uint32_t ring = 0;
-            int q_armed = -1;
-            uint32_t qe_ph = 1;
-            bool drop = p.fault == 1;
-            bool ok = true;
-            uint32_t armed = 0;  // loads whose stage was armed
-            for (; ok && x.left > 0; next()) {
-                const bool pair = x.pair;
-                const int row0 = x.q.row0 + x.tok0, h = x.h, n = x.n, t0 = x.t;
+            const int sub = lane & (per_tile - 1), half = lane / per_tile;  // this lane's box
+            uint32_t stage = 0, ph = 1;  // of the next tile in the ring, and the parity of its stage's release
+            uint32_t q_armed = 0, armed = 0;  // stages with a copy, and the parity of the last one
+            uint32_t q_par = 0, par = 0;
+            bool drop = keys && p.fault == 1, ok = true;
+            for (; ok && x.left > 0; next(x)) {
+                const int n = x.n, h = x.h, t0 = x.t;
                 const int* pages = x.q.pages;
-                if (!(ok = warp_wait(bar(L::bQEmpty), qe_ph, abort_flag, wf, 89, x.e))) break;
-                qe_ph ^= 1;
-                const int q_tiles = pair ? 2 : 1;
-                if (lane == 0) mbar_arrive_expect_tx(bar(L::bQFull), q_tiles * boxes * p.npt * p.group * 128);
-                __syncwarp();
-                if (lane < q_tiles * boxes) {
-                    const int tile = lane / boxes, half = lane % boxes;
-                    tma_load_3d(sb + L::kQ + tile * L::kTileBytes + half * kBox, &tmQ, bar(L::bQFull), 64 * half,
-                                h * p.group, row0 + tile * p.npt);
-                }
-                q_armed = (int)(qe_ph & 1u);
-                // lane i has the page of box i of a tile: those of K(j) are V(j)'s
                 const int pages_end = (x.q.len + page_rows - 1) / page_rows;  // boxes of the sequence
                 auto page_of = [&](int tile) {
-                    const int i = (t0 + tile) * per_tile + lane;  // box of the sequence
+                    const int i = (t0 + tile) * per_tile + sub;
                     int page = 0;
-                    if (lane < per_tile && i < pages_end) {
+                    if (half < boxes && i < pages_end) {
                         page = pages[(long long)i * page_rows >> shift];
                         if ((unsigned)page >= (unsigned)p.c.num_pages) {
                             atomicOr(p.c.err, 2);
@@ -648,44 +653,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     return page;
                 };
-                auto load = [&](int tile, int page, int which) -> bool {
-                    const uint32_t stage = ring % L::kStages;
-                    if (!warp_wait(bar(L::bKVEmpty + stage), ((ring / L::kStages) & 1u) ^ 1u, abort_flag, wf, 90, x.e))
-                        return false;
-                    const int i0 = (t0 + tile) * per_tile, boxes_in = min(per_tile, pages_end - i0);
-                    if (!drop) {
-                        if (lane == 0) mbar_arrive_expect_tx(bar(L::bKVFull + stage), boxes_in * boxes * page_rows * 128);
+                int page = page_of(0);
+                if (keys) {
+                    const int tiles = x.pair ? 2 : 1, row0 = x.q.row0 + x.tok0;
+                    for (int i = 0; i < tiles && ok; ++i) {
+                        const uint32_t qt = x.qtile + i, b = qt & 1u;
+                        if (!(ok = wait(L::bQEmpty + b, (qt >> 1) ^ 1u, 89))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(bar(L::bQFull + b), boxes * p.npt * p.group * 128);
                         __syncwarp();
-                        const int i = lane % per_tile, half = lane / per_tile;
-                        const int pg = __shfl_sync(~0u, page, i);
-                        if (i < boxes_in && half < boxes)
-                            tma_load_3d(sb + L::kKV + stage * L::kTileBytes + half * kBox + i * page_rows * 128, &tmKV,
-                                        bar(L::bKVFull + stage), 64 * half, (i0 + i) * page_rows & ((1 << shift) - 1),
-                                        (pg * 2 + which) * p.c.Hkv + h);
+                        if (lane < boxes)
+                            tma_load_3d(sb + L::kQ + b * L::kTileBytes + lane * kBox, &tmQ, bar(L::bQFull + b), 64 * lane,
+                                        h * p.group, row0 + i * p.npt);
+                        q_armed |= 1u << b;
+                        q_par = (q_par & ~(1u << b)) | (qt >> 1 & 1u) << b;
+                    }
+                    if (!ok) break;
+                }
+                for (int j = 0; j < n; ++j) {
+                    const int pg = page;
+                    if (j + 1 < n) page = page_of(j + 1);  // on its way while this tile's stage is awaited
+                    if (!(ok = wait(empty + stage, ph, 90))) break;
+                    const int i0 = (t0 + j) * per_tile, count = min(per_tile, pages_end - i0);
+                    if (!drop) {
+                        if (lane == 0) mbar_arrive_expect_tx(bar(full + stage), count * boxes * page_rows * 128);
+                        __syncwarp();
+                        if (sub < count && half < boxes)
+                            tma_load_3d(ring + stage * L::kTileBytes + half * kBox + sub * page_rows * 128, &tmKV,
+                                        bar(full + stage), 64 * half, (i0 + sub) * page_rows & ((1 << shift) - 1),
+                                        (pg * 2 + (keys ? 0 : 1)) * p.c.Hkv + h);
                         armed |= 1u << stage;
+                        par = (par & ~(1u << stage)) | (ph ^ 1u) << stage;
                     }
                     drop = false;
-                    ++ring;
-                    return true;
-                };
-                int page = page_of(0), page_k = page;
-                ok = load(0, page, 0);
-                for (int j = 0; j < n && ok; ++j) {
-                    if (j + 1 < n) {
-                        page_k = page_of(j + 1);
-                        ok = load(j + 1, page_k, 0);
+                    if (++stage == stages) {
+                        stage = 0;
+                        ph ^= 1u;
                     }
-                    if (ok) ok = load(j, page, 1);
-                    page = page_k;
                 }
             }
             // every copy that this warp started has landed before the block retires
-            if (q_armed >= 0) mbar_settle(bar(L::bQFull), (uint32_t)q_armed, wf, 91);
-            for (uint32_t s = 0; s < (uint32_t)L::kStages; ++s)
-                if (armed >> s & 1u) {
-                    const uint32_t last = (ring - 1 - s) / L::kStages;  // the stage's last load
-                    mbar_settle(bar(L::bKVFull + s), last & 1u, wf, 92);
-                }
+            for (uint32_t b = 0; b < 2; ++b)
+                if (q_armed >> b & 1u) mbar_settle(bar(L::bQFull + b), q_par >> b & 1u, wf, 91);
+            for (uint32_t s = 0; s < stages; ++s)
+                if (armed >> s & 1u) mbar_settle(bar(full + s), par >> s & 1u, wf, 92);
         } else if (warp == 9) {
             // ============================================================ MMA issuer
             // The whole warp runs this loop; lane 0 issues every MMA and commit (a
@@ -697,10 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) tc_commit(bar(b));
                 __syncwarp();
             };
-            // S_t = Q_q K^T of the tile in a ring stage, and O_t (+)= P_t V
-            auto mma_s = [&](int t, int q, uint32_t stage) {
+            // S of stream t = rows in buffer q times K in a stage; O of stream t (+)= P V
+            auto mma_s = [&](int t, uint32_t q, uint32_t stage) {
                 const uint64_t qd = smem_desc_sw128(sb + L::kQ + q * L::kTileBytes, 16, 1024);
-                const uint64_t kd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, 16, 1024);
+                const uint64_t kd = smem_desc_sw128(sb + L::kKRing + stage * L::kTileBytes, 16, 1024);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             };
             auto mma_pv = [&](int t, uint32_t stage, bool acc) {
-                const uint64_t vd = smem_desc_sw128(sb + L::kKV + stage * L::kTileBytes, kBox, 1024);
+                const uint64_t vd = smem_desc_sw128(sb + L::kVRing + stage * L::kTileBytes, kBox, 1024);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
@@ -720,114 +730,107 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            uint32_t stage = 0, ph = 0;  // of the next load in the ring
-            auto take = [&](uint32_t& st, uint32_t& p_) {
-                st = stage;
-                p_ = ph;
-                if (++stage == (uint32_t)L::kStages) {
-                    stage = 0;
-                    ph ^= 1u;
+            struct Slot {
+                uint32_t stage, ph;
+            } kt{0, 0}, vt{0, 0};  // tiles of the rings that the next scores and the next P.V read
+            auto advance = [](Slot& s, uint32_t stages) {
+                if (++s.stage == stages) {
+                    s.stage = 0;
+                    s.ph ^= 1u;
                 }
             };
-            uint32_t q_ph = 0, p_ph[2] = {0, 0}, oe_ph[2] = {1, 1};
-            bool ok = true, issued = false;
-            auto full = [&](uint32_t st, uint32_t p_, int site) {
-                return warp_wait(bar(L::bKVFull + st), p_, abort_flag, wf, site, x.e);
-            };
-            auto o_empty = [&](int t) {
-                const bool got = warp_wait(bar(L::bOEmpty + t), oe_ph[t], abort_flag, wf, 97, x.e);
-                oe_ph[t] ^= 1;
-                return got;
-            };
-            auto p_full = [&](int t) { return warp_wait(bar(L::bPFull + t), p_ph[t], abort_flag, wf, 96, x.e); };
-            for (; ok && x.left > 0; next()) {
-                const int n = x.n;
+            Item& y = s_item[11];  // the item of the next P.V; x: that of the next scores, up to two steps ahead
+            int su = 0;            // step of x
+            uint32_t s_step = 0, v_step = 0, oe_ph = 3;
+            bool issued = false;
+            // The scores of the next step, if there is one; false: a wait ran out.
+            auto scores = [&]() -> bool {
+                if (x.left <= 0) return true;
                 const bool pair = x.pair;
-                if (!(ok = warp_wait(bar(L::bQFull), q_ph, abort_flag, wf, 93, x.e))) break;
-                q_ph ^= 1;
-                uint32_t ks, kp, vs, vp;
-                take(ks, kp);
-                if (!(ok = full(ks, kp, 94))) break;
+                const int steps = pair ? 2 * x.n : x.n, t = (int)s_step & 1;
+                const uint32_t qt = x.qtile + (pair ? su & 1 : 0), b = qt & 1u;
+                if (su < (pair ? 2 : 1) && !wait(L::bQFull + b, qt >> 1, 93)) return false;
+                if (!(pair && (su & 1)) && !wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
                 tc_fence_after_sync();
-                mma_s(0, 0, ks);
+                mma_s(t, b, kt.stage);
                 issued = true;
-                commit(L::bSFull);
-                if (pair) {
-                    // Both streams read every tile.  A wait or a commit of this warp
-                    // idles the tensor core for some 100 cycles, so a tile takes two of
-                    // each: V(j), K(j + 1) and P0(j) are tested at once, and the second
-                    // softmax group frees the stages when it sees S1.
-                    mma_s(1, 1, ks);
-                    commit(L::bSFull + 1);
-                    if (n == 1) commit(L::bQEmpty);
-                    for (int j = 0; j < n; ++j) {
-                        const bool last = j + 1 == n;
-                        if (!last) take(ks, kp);
-                        take(vs, vp);
-                        if (j == 0 || !__all_sync(0xffffffffu,
-                                                  mbar_try_wait3(bar(L::bKVFull + vs), vp, bar(L::bKVFull + (last ? vs : ks)),
-                                                                 last ? vp : kp, bar(L::bPFull), p_ph[0]))) {
-                            if (!last && !(ok = full(ks, kp, 94))) break;
-                            if (!(ok = full(vs, vp, 95))) break;
-                            if (!(ok = p_full(0))) break;
-                        }
-                        p_ph[0] ^= 1;
-                        if (j == 0 && !(ok = o_empty(0))) break;
-                        tc_fence_after_sync();
-                        mma_pv(0, vs, j > 0);
-                        if (last) {
-                            commit(L::bOFull);
-                        } else {
-                            mma_s(0, 0, ks);
-                            commit(L::bSFull);
-                        }
-                        if (!(ok = p_full(1))) break;
-                        p_ph[1] ^= 1;
-                        if (j == 0 && !(ok = o_empty(1))) break;
-                        tc_fence_after_sync();
-                        mma_pv(1, vs, j > 0);
-                        if (last) {
-                            commit(L::bOFull + 1);
-                            commit(L::bKVEmpty + vs);
-                        } else {
-                            mma_s(1, 1, ks);
-                            commit(L::bSFull + 1);
-                            if (j + 2 == n) commit(L::bQEmpty);
-                        }
-                    }
-                } else {
-                    commit(L::bKVEmpty + ks);
-                    if (n > 1) {
-                        take(ks, kp);
-                        if (!(ok = full(ks, kp, 94))) break;
-                        tc_fence_after_sync();
-                        mma_s(1, 0, ks);
-                        commit(L::bSFull + 1);
-                        commit(L::bKVEmpty + ks);
-                    }
-                    if (n <= 2) commit(L::bQEmpty);
-                    for (int j = 0; j < n; ++j) {
-                        const int t = j & 1;
-                        take(vs, vp);
-                        if (!(ok = full(vs, vp, 95))) break;
-                        if (!(ok = p_full(t))) break;
-                        p_ph[t] ^= 1;
-                        if (j < 2 && !(ok = o_empty(t))) break;
-                        tc_fence_after_sync();
-                        mma_pv(t, vs, j >= 2);
-                        commit(L::bKVEmpty + vs);
-                        if (j >= n - 2) commit(L::bOFull + t);
-                        if (j + 2 < n) {
-                            take(ks, kp);
-                            if (!(ok = full(ks, kp, 94))) break;
-                            tc_fence_after_sync();
-                            mma_s(t, 0, ks);
-                            commit(L::bSFull + t);
-                            commit(L::bKVEmpty + ks);
-                            if (j + 3 == n) commit(L::bQEmpty);
-                        }
-                    }
+                commit(L::bSFull + t);
+                if (!pair) commit(L::bKEmpty + kt.stage);
+                if (su >= steps - (pair ? 2 : 1)) commit(L::bQEmpty + b);
+                if (!pair || (su & 1)) advance(kt, kK);
+                ++s_step;
+                if (++su == steps) {
+                    su = 0;
+                    next(x);
                 }
+                return true;
+            };
+            bool ok = scores() && scores();
+            for (; ok && y.left > 0; next(y)) {
+                const bool pair = y.pair;
+                const int steps = pair ? 2 * y.n : y.n;
+                int u = 0;
+                if (pair && y.n > 1) {
+                    // Two tiles of rows, and the scores ahead are the same item's.  A
+                    // wait or a commit of this warp idles the tensor core for some 100
+                    // cycles, so a tile takes two of each: V(j), K(j + 1) and P are
+                    // tested at once, and the second softmax group frees the stages.
+                    const int t = (int)v_step & 1;
+                    auto step = [&](int g, uint32_t q, bool first) -> bool {
+                        const uint32_t p_ph = v_step >> 1 & 1u;
+                        if (!__all_sync(0xffffffffu, mbar_try_wait3(bar(L::bVFull + vt.stage), vt.ph, bar(L::bKFull + kt.stage),
+                                                                    kt.ph, bar(L::bPFull + g), p_ph))) {
+                            if (!wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
+                            if (!wait(L::bVFull + vt.stage, vt.ph, 95)) return false;
+                            if (!wait(L::bPFull + g, p_ph, 96)) return false;
+                        }
+                        if (first) {
+                            if (!wait(L::bOEmpty + g, oe_ph >> g, 97)) return false;
+                            oe_ph ^= 1u << g;
+                        }
+                        tc_fence_after_sync();
+                        mma_pv(g, vt.stage, !first);
+                        mma_s(g, q, kt.stage);
+                        commit(L::bSFull + g);
+                        ++v_step;
+                        return true;
+                    };
+                    const uint32_t q0 = y.qtile & 1u;
+                    const int n = y.n;
+                    for (int j = 0; j + 1 < n; ++j) {
+                        if (!(ok = t ? step(1, q0, j == 0) : step(0, q0, j == 0))) break;
+                        if (!(ok = t ? step(0, q0 ^ 1u, j == 0) : step(1, q0 ^ 1u, j == 0))) break;
+                        advance(kt, kK);
+                        advance(vt, kV);
+                    }
+                    if (!ok) break;
+                    commit(L::bQEmpty);
+                    commit(L::bQEmpty + 1);
+                    u = steps - 2;
+                    s_step += (uint32_t)u;
+                    su = 0;
+                    next(x);
+                }
+                for (; u < steps; ++u) {
+                    const int t = (int)v_step & 1;
+                    const bool second = pair && (u & 1);
+                    if (!second && !(ok = wait(L::bVFull + vt.stage, vt.ph, 95))) break;
+                    if (!(ok = wait(L::bPFull + t, v_step >> 1, 96))) break;
+                    if (u < 2) {
+                        if (!(ok = wait(L::bOEmpty + t, oe_ph >> t, 97))) break;
+                        oe_ph ^= 1u << t;
+                    }
+                    tc_fence_after_sync();
+                    mma_pv(t, vt.stage, u >= 2);
+                    if (!pair || second) {
+                        commit(L::bVEmpty + vt.stage);
+                        advance(vt, kV);
+                    }
+                    if (u >= steps - 2) commit(L::bOFull + t);
+                    ++v_step;
+                    if (!(ok = scores())) break;
+                }
+                if (!ok) break;
             }
             if (issued) {
                 commit(L::bDrain);
@@ -835,6 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         }
+    }
     }
 done:
     __syncwarp();
@@ -855,67 +859,71 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16AttnParams p)
 {
     __shared__ __align__(16) uint16_t s_o[32][D + 8];
+    constexpr int V = D / 32, U = 4;  // runs of a warp; parts whose loads are in flight together
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
     wait_for_primary();
     const Cut cut = parts.join[blockIdx.x];
-    if (cut.e < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Item x;
-    x.s = cut.s;
-    x.e = cut.e;
-    x.q = open_sequence(p, x.s);
-    x.blocks = row_blocks(p, x.q.n);
-    open_item(p, x);
-    const bool pair = x.pair;
-    const int t = pair ? blockIdx.y >> 2 : 0;  // tile of rows
-    const int row = 32 * blockIdx.y + lane - 128 * t;
-    const int rows_t = min(p.npt, x.ntok - t * p.npt) * p.group;
-    if (row - lane >= rows_t) return;
+    const int rt = cut.ntok > p.npt ? (int)blockIdx.y >> 2 : 0;  // tile of rows
+    const int prow = 32 * blockIdx.y + lane, row = prow - 128 * rt;
+    const int rows_t = min(p.npt, cut.ntok - rt * p.npt) * p.group;
+    if (cut.parts == 0 || row - lane >= rows_t) return;
     const bool valid = row < rows_t;
-    const int n = (int)((cut.end - 1) / cut.share) - (int)blockIdx.x + 1;
-    auto part = [&](int k) { return (long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0); };
-    const int prow = 32 * blockIdx.y + lane;
-    float top = -INFINITY;
-    if (valid)
-        for (int k = 0; k < n; ++k) top = fmaxf(top, parts.stat[part(k) * p.rows + prow].x);
-    const float m = top == -INFINITY ? 0.f : top;
-    constexpr int V = D / 32;
+    float r = -INFINITY, l = 0.f, l_o = 0.f;
     float4 acc[V];
-    float l = 0.f, l_o = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (valid)
-        for (int k = 0; k < n; ++k) {
-            const float4 st = parts.stat[part(k) * p.rows + prow];
-            const float w = ex2_approx(st.x - m);
-            l = fmaf(w, st.y, l);
-            l_o = fmaf(w, st.y + st.z, l_o);
+        for (int k0 = 0; k0 < cut.parts; k0 += U) {
+            float4 st[U], o[U][V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float4 o = parts.o[(part(k) * (D / 4) + warp + 8 * i) * p.rows + prow];
-                acc[i].x = fmaf(w, o.x, acc[i].x);
-                acc[i].y = fmaf(w, o.y, acc[i].y);
-                acc[i].z = fmaf(w, o.z, acc[i].z);
-                acc[i].w = fmaf(w, o.w, acc[i].w);
+            for (int u = 0; u < U; ++u) {
+                st[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+                if (k0 + u < cut.parts) {
+                    const long long part = (long long)(blockIdx.x + k0 + u) * 2 + (k0 + u == 0 ? 1 : 0);
+                    st[u] = parts.stat[part * p.rows + prow];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[u][i] = parts.o[(part * (D / 4) + warp + 8 * i) * p.rows + prow];
+                }
             }
+            float top = r;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, st[u].x);
+            const float m = top == -INFINITY ? 0.f : top, down = ex2_approx(r - m);
+            r = top;
+            l *= down;
+            l_o *= down;
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] = make_float4(acc[i].x * down, acc[i].y * down, acc[i].z * down, acc[i].w * down);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < cut.parts) {
+                    const float w = ex2_approx(st[u].x - m);
+                    l = fmaf(w, st[u].y, l);
+                    l_o = fmaf(w, st[u].y + st[u].z, l_o);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        acc[i].x = fmaf(w, o[u][i].x, acc[i].x);
+                        acc[i].y = fmaf(w, o[u][i].y, acc[i].y);
+                        acc[i].z = fmaf(w, o[u][i].z, acc[i].z);
+                        acc[i].w = fmaf(w, o[u][i].w, acc[i].w);
+                    }
+                }
         }
     const float inv = l > 0.f || l != l ? 1.f / l_o : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i)
         *reinterpret_cast<uint2*>(&s_o[lane][4 * (warp + 8 * i)]) =
             make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
-    if (valid && warp == 0) {
-        const int head = x.h * p.group + row % p.group;
-        const long long token = (long long)x.q.row0 + x.tok0 + t * p.npt + row / p.group;
-        p.lse[(long long)head * p.T + token] = l == 0.f ? -INFINITY : (top + __log2f(l)) * kLn2;
-    }
+    const int token0 = cut.token + rt * p.npt, head0 = cut.h * p.group;
+    if (valid && warp == 0)
+        p.lse[(long long)(head0 + row % p.group) * p.T + token0 + row / p.group] = l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
     __syncthreads();
     for (int i = threadIdx.x; i < 32 * (D / 8); i += kJoinThreads) {
         const int rr = i / (D / 8), c = i % (D / 8), at = row - lane + rr;
         if (at >= rows_t) break;
-        const int head = x.h * p.group + at % p.group;
-        const long long token = (long long)x.q.row0 + x.tok0 + t * p.npt + at / p.group;
-        reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D)[c] = *reinterpret_cast<const uint4*>(&s_o[rr][8 * c]);
+        const long long to = (long long)(token0 + at / p.group) * p.Hq + head0 + at % p.group;
+        reinterpret_cast<uint4*>(p.o + to * D)[c] = *reinterpret_cast<const uint4*>(&s_o[rr][8 * c]);
     }
 }
 
@@ -950,7 +958,7 @@ int kv16_attn_rows(long long T, int group)
 
 size_t kv16_attn_workspace(int D, int rows, int num_sms)
 {
-    return (size_t)((num_sms + 1) & ~1) * sizeof(Cut) + (size_t)num_sms * 2 * rows * (sizeof(float4) + 4u * D);
+    return (size_t)num_sms * sizeof(Cut) + (size_t)num_sms * 2 * rows * (sizeof(float4) + 4u * D);
 }
 
 cudaError_t launch_kv16_attn(int D, const CUtensorMap& q, const CUtensorMap& kv, const Kv16AttnParams& p, int num_sms,
