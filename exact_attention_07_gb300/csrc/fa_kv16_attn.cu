@@ -62,25 +62,6 @@ struct Item {
     uint32_t step, tile, qtile;  // of the block's parts before: steps, tiles of keys, tiles of rows
 };
 
-template <int D>
-struct Smem {
-    static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 8;  // tiles of the rings
-    static constexpr int kQ = 0;  // [2] tiles
-    static constexpr int kKRing = 2 * kTileBytes, kVRing = kKRing + kK * kTileBytes;
-    static constexpr int kStats = kVRing + kV * kTileBytes;  // float [3][128]: r, l, l_rnd of the group that does not end an item
-    static constexpr int kBars = kStats + 3 * 128 * 4;
-    static constexpr int bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bOEmpty = 10, bStFull = 12,
-                         bStEmpty = 13, bDrain = 14, bKFull = 15, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK,
-                         bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
-    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
-    static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the blocks' share
-    static constexpr int kItems = kSums + (kWarps + 1) * 8;  // Item [kWarps]
-    static constexpr int kBytes = kItems + kWarps * (int)sizeof(Item);
-    static_assert(kBytes <= 232448 && kBars % 8 == 0, "shared memory of one block");
-    static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
-};
-
 __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
@@ -119,15 +100,49 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 
 // ------------------------------------------------------------------ the list of work
 
-__device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
+__device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s, const Kv16Raw& raw)
 {
-    Kv16Seq q = kv16_sequence(p.c, p.cu, p.T, s);
+    Kv16Seq q = kv16_checked(p.c, p.T, s, raw);
     if (p.mask && q.n > 32 * p.mask_words) {
         atomicOr(p.c.err, 2);
         q.n = 0;
     }
     return q;
 }
+
+__device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
+{
+    return open_sequence(p, s, kv16_raw(p.c, p.cu, s));
+}
+
+// The sequences behind a block's first one, in shared memory, so that they are
+// at hand when its warps get there; further ones are read where they lie.
+struct Window {
+    static constexpr int kSeqs = 12;
+    Kv16Raw raw[kSeqs];
+    int base;  // the first
+    int pad[3];
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kK = D == 128 ? 2 : 4, kV = D == 128 ? 3 : 8;  // tiles of the rings
+    static constexpr int kQ = 0;  // [2] tiles
+    static constexpr int kKRing = 2 * kTileBytes, kVRing = kKRing + kK * kTileBytes;
+    static constexpr int kStats = kVRing + kV * kTileBytes;  // float [3][128]: r, l, l_rnd of the group that does not end an item
+    static constexpr int kBars = kStats + 3 * 128 * 4;
+    static constexpr int bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bOEmpty = 10, bStFull = 12,
+                         bStEmpty = 13, bDrain = 14, bWindow = 15, bKFull = 16, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK,
+                         bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
+    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
+    static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the blocks' share
+    static constexpr int kWindow = (kSums + (kWarps + 1) * 8 + 15) / 16 * 16;
+    static constexpr int kItems = kWindow + (int)sizeof(Window);  // Item [10]: softmax warps, of the next scores, of the next P.V
+    static constexpr int kBytes = kItems + 10 * (int)sizeof(Item);
+    static_assert(kBytes <= 232448 && kBars % 8 == 0, "shared memory of one block");
+    static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
+};
 
 __device__ __forceinline__ int row_blocks(const Kv16AttnParams& p, int n)
 {
@@ -164,7 +179,8 @@ __device__ __forceinline__ void open_item(const Kv16AttnParams& p, Item& x)
 }
 
 // The block's part of the next item; left <= 0 at the end of its share.
-__device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x)
+template <typename Ready>
+__device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, const Window& w, const Ready& window_here)
 {
     x.step += x.pair ? 2 * x.n : x.n;
     x.tile += x.n;
@@ -175,12 +191,14 @@ __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x)
         x.rb = 0;
         if (++x.h == p.c.Hkv) {
             x.h = 0;
+            window_here();
             do {
                 if (++x.s >= p.B) {
                     x.left = 0;
                     return;
                 }
-                x.q = open_sequence(p, x.s);
+                const int i = x.s - w.base;
+                x.q = i < Window::kSeqs ? open_sequence(p, x.s, w.raw[i]) : open_sequence(p, x.s);
                 x.blocks = row_blocks(p, x.q.n);
             } while (x.blocks == 0);
         }
@@ -294,22 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* stats = reinterpret_cast<float*>(smem + L::kStats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitFailure wf{p.c.err, p.c.diag};
+    Window& window = *reinterpret_cast<Window*>(smem + L::kWindow);
+    Item first;  // the producers keep theirs in registers
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
 
     let_dependents_launch();
 
-    // This block's share of the list: every thread sums a run of sequences.
-    const int run = (p.B + kThreads - 1) / kThreads;
-    const int run0 = min(p.B, (int)threadIdx.x * run), run1 = min(p.B, run0 + run);
-    Kv16Seq own{};  // the run's first
-    long long mine = 0;
-    if (run0 < run1) {
-        own = open_sequence(p, run0);
-        mine = p.c.Hkv * head_cost(p, own);
-    }
-    for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
-
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == kThreads - 32) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(L::bQFull + t), 1);
             mbar_init(bar(L::bQEmpty + t), 1);
@@ -321,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(L::bStFull), 128);
         mbar_init(bar(L::bStEmpty), 128);
         mbar_init(bar(L::bDrain), 1);
+        mbar_init(bar(L::bWindow), 32);
         for (uint32_t s = 0; s < 2 * (kK + kV); ++s) mbar_init(bar(L::bKFull + s), 1);
         *abort_flag = 0;
         *poison = 0;
@@ -334,6 +344,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    // This block's share of the list: every thread sums a run of sequences.
+    const int run = (p.B + kThreads - 1) / kThreads;
+    const int run0 = min(p.B, (int)threadIdx.x * run), run1 = min(p.B, run0 + run);
+    Kv16Seq own{};  // the run's first
+    long long mine = 0, own_cost = 0;
+    if (run0 < run1) {
+        own = open_sequence(p, run0);
+        own_cost = head_cost(p, own);
+        mine = p.c.Hkv * own_cost;
+    }
+    for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
+
     {
         long long upto = mine;
 #pragma unroll
@@ -355,13 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         share = max(share, (long long)kItemCost + 1);
         const long long first = share * blockIdx.x, last = min(total, first + share);
         if (first < last && first < upto && first >= upto - mine) {
-            long long at = upto - mine, cost;
+            long long at = upto - mine, cost = own_cost;
             Item x;
             x.s = run0;
             x.q = own;
-            while (at + (cost = head_cost(p, x.q)) * p.c.Hkv <= first) {
+            while (at + cost * p.c.Hkv <= first) {
                 at += cost * p.c.Hkv;
                 x.q = open_sequence(p, ++x.s);
+                cost = head_cost(p, x.q);
             }
             x.blocks = row_blocks(p, x.q.n);
             for (x.h = 0; at + cost <= first; ++x.h) at += cost;
@@ -383,16 +406,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     if (s_item[0].left <= 0) goto done;  // no work, for no warp
-    if (warp > 0) {
+    if (warp == 8 || warp == 10) {
+        first = s_item[0];
+    } else if (warp > 0) {
+        // [0, 8): softmax warps, 8: scores, 9: P.V
+        Item* mine_of = s_item + (warp < 8 ? warp : warp == 9 ? 8 : 9);
         for (int i = lane; i < (int)sizeof(Item) / 4; i += 32)
-            reinterpret_cast<int*>(s_item + warp)[i] = reinterpret_cast<const int*>(s_item)[i];
+            reinterpret_cast<int*>(mine_of)[i] = reinterpret_cast<const int*>(s_item)[i];
+        if (warp == 11 && lane == 0) window.base = s_item[0].s + 1;
     }
     __syncthreads();  // warp 0 changes its own from here
     {
-    Item& x = s_item[warp];
+    Item& x = s_item[warp < 8 ? warp : 8];
+    // (a window that does not come ends the wait, and with it the block: what is read then is checked)
+    auto window_here = [&]() { mbar_wait(bar(L::bWindow), 0, abort_flag, wf, 79, blockIdx.x); };
     auto next = [&](Item& y) {
         __syncwarp();
-        if (lane == 0) next_item(p, y);
+        if (lane == 0) next_item(p, y, window, window_here);
         __syncwarp();
     };
     auto wait = [&](int b, uint32_t parity, int site) -> bool {
@@ -424,12 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = key_first + j * kTile;
                 const bool edge = key0 + kTile > clear;
                 if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
-                // the second scores of a tile are complete, and so is all that was
-                // issued before them: K(j) and V(j - 1) are no longer read
-                if (pair && rt == 1 && row == 0) {
+                // These scores are complete, and so is all that was issued before
+                // them: K(j) is no longer read (of a pair: when they are the second
+                // of the tile), and V of the step two before neither.  (V of an item's
+                // last steps is freed by the MMA warp.)
+                if ((!pair || rt == 1) && row == 0) {
                     const uint32_t T = tile0 + (uint32_t)j;
                     mbar_arrive(bar(L::bKEmpty + T % kK));
-                    if (j > 0) mbar_arrive(bar(L::bVEmpty + (T - 1) % kV));
+                    if (j >= dj) mbar_arrive(bar(L::bVEmpty + (T - dj) % kV));
                 }
                 tc_fence_after_sync();
                 if (work) {
@@ -441,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (edge) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t bits = seen_word(p, x.q, tok, key0 + 32 * c);
+                            const uint32_t seen = seen_word(p, x.q, tok, key0 + 32 * c);
                             mx[c] = -INFINITY;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (!(bits >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
+                                if (!(seen >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
                                 mx[c] = fmaxf(mx[c], __uint_as_float(sv[c][i]));
                             }
                         }
@@ -574,36 +606,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int head = x.h * p.group + head_row;
                 uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32], o1[32];
-                    float o[32];
-                    tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov);
-                    if (two) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
-                    tmem_wait_ld();
+                for (int c = 0; c < D / 32; c += 1) {
+                    float o[1][32];
+                    {
+                        uint32_t ov[1][32], o1[1][32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = two ? fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i])) : __uint_as_float(ov[i]);
-                    if (!valid) continue;
-                    if (poisoned) {
-                        float fix[32];  // o itself stays in registers
+                        for (int k = 0; k < 1; ++k) tmem_ld32(tO + (uint32_t)(D * t + 32 * (c + k)), ov[k]);
+                        if (two)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) fix[i] = o[i];
-                        add_poison(p, x, tok, D, 32 * c, fix);
+                            for (int k = 0; k < 1; ++k) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * (c + k)), o1[k]);
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = fix[i];
+                        for (int k = 0; k < 1; ++k)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[k][i] = two ? fmaf(w0, __uint_as_float(ov[k][i]), w1 * __uint_as_float(o1[k][i]))
+                                              : __uint_as_float(ov[k][i]);
                     }
-                    if (whole) {
+                    if (!valid) continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[4 * c + i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                                        pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                                        pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                                        pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-                    } else {
-                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + prow;
+                    for (int k = 0; k < 1; ++k) {
+                        if (poisoned) {
+                            float fix[32];  // o itself stays in registers
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            to[(long long)i * p.rows] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < 32; ++i) fix[i] = o[k][i];
+                            add_poison(p, x, tok, D, 32 * (c + k), fix);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[k][i] = fix[i];
+                        }
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[4 * (c + k) + i] = make_uint4(pack_bf16x2(o[k][8 * i] * inv, o[k][8 * i + 1] * inv),
+                                                                  pack_bf16x2(o[k][8 * i + 2] * inv, o[k][8 * i + 3] * inv),
+                                                                  pack_bf16x2(o[k][8 * i + 4] * inv, o[k][8 * i + 5] * inv),
+                                                                  pack_bf16x2(o[k][8 * i + 6] * inv, o[k][8 * i + 7] * inv));
+                        } else {
+                            float4* to = parts.o + (part * (D / 4) + 8 * (c + k)) * p.rows + prow;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i, to += p.rows)
+                                *to = make_float4(o[k][4 * i], o[k][4 * i + 1], o[k][4 * i + 2], o[k][4 * i + 3]);
+                        }
                     }
                 }
                 if (valid) {
@@ -637,27 +680,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t q_armed = 0, armed = 0;  // stages with a copy, and the parity of the last one
             uint32_t q_par = 0, par = 0;
             bool drop = keys && p.fault == 1, ok = true;
-            for (; ok && x.left > 0; next(x)) {
-                const int n = x.n, h = x.h, t0 = x.t;
-                const int* pages = x.q.pages;
-                const int pages_end = (x.q.len + page_rows - 1) / page_rows;  // boxes of the sequence
-                auto page_of = [&](int tile) {
-                    const int i = (t0 + tile) * per_tile + sub;
-                    int page = 0;
-                    if (half < boxes && i < pages_end) {
-                        page = pages[(long long)i * page_rows >> shift];
-                        if ((unsigned)page >= (unsigned)p.c.num_pages) {
-                            atomicOr(p.c.err, 2);
-                            page = 0;
-                        }
-                    }
-                    return page;
-                };
-                int page = page_of(0);
+            // the page of this lane's box in tile j of an item, as it lies in the table
+            auto page_of = [&](const Item& y, int j) {
+                const int i = (y.t + j) * per_tile + sub;
+                return half < boxes && (long long)i * page_rows < y.q.len ? y.q.pages[(long long)i * page_rows >> shift] : 0;
+            };
+            Item& y = first;  // and the next one, whose first page is asked for early
+            int page = page_of(y, 0);
+            while (ok && y.left > 0) {
+                const int n = y.n, h = y.h, t0 = y.t;
+                const int pages_end = (y.q.len + page_rows - 1) / page_rows;  // boxes of the sequence
                 if (keys) {
-                    const int tiles = x.pair ? 2 : 1, row0 = x.q.row0 + x.tok0;
+                    const int tiles = y.pair ? 2 : 1, row0 = y.q.row0 + y.tok0;
                     for (int i = 0; i < tiles && ok; ++i) {
-                        const uint32_t qt = x.qtile + i, b = qt & 1u;
+                        const uint32_t qt = y.qtile + i, b = qt & 1u;
                         if (!(ok = wait(L::bQEmpty + b, (qt >> 1) ^ 1u, 89))) break;
                         if (lane == 0) mbar_arrive_expect_tx(bar(L::bQFull + b), boxes * p.npt * p.group * 128);
                         __syncwarp();
@@ -669,11 +705,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                 }
+                Item z = y;
                 for (int j = 0; j < n; ++j) {
-                    const int pg = page;
-                    if (j + 1 < n) page = page_of(j + 1);  // on its way while this tile's stage is awaited
+                    int pg = page;
+                    if (j + 1 < n) page = page_of(y, j + 1);  // on its way while this tile's stage is awaited
                     if (!(ok = wait(empty + stage, ph, 90))) break;
                     const int i0 = (t0 + j) * per_tile, count = min(per_tile, pages_end - i0);
+                    if ((unsigned)pg >= (unsigned)p.c.num_pages) {
+                        atomicOr(p.c.err, 2);
+                        pg = 0;
+                    }
                     if (!drop) {
                         if (lane == 0) mbar_arrive_expect_tx(bar(full + stage), count * boxes * page_rows * 128);
                         __syncwarp();
@@ -689,7 +730,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stage = 0;
                         ph ^= 1u;
                     }
+                    if (j == 0) next_item(p, z, window, window_here);
                 }
+                if (z.left > 0) page = page_of(z, 0);
+                y = z;
             }
             // every copy that this warp started has landed before the block retires
             for (uint32_t b = 0; b < 2; ++b)
@@ -739,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s.ph ^= 1u;
                 }
             };
-            Item& y = s_item[11];  // the item of the next P.V; x: that of the next scores, up to two steps ahead
+            Item& y = s_item[9];  // the item of the next P.V; x: that of the next scores, up to two steps ahead
             int su = 0;            // step of x
             uint32_t s_step = 0, v_step = 0, oe_ph = 3;
             bool issued = false;
@@ -755,7 +799,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_s(t, b, kt.stage);
                 issued = true;
                 commit(L::bSFull + t);
-                if (!pair) commit(L::bKEmpty + kt.stage);
                 if (su >= steps - (pair ? 2 : 1)) commit(L::bQEmpty + b);
                 if (!pair || (su & 1)) advance(kt, kK);
                 ++s_step;
@@ -770,19 +813,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool pair = y.pair;
                 const int steps = pair ? 2 * y.n : y.n;
                 int u = 0;
-                if (pair && y.n > 1) {
-                    // Two tiles of rows, and the scores ahead are the same item's.  A
-                    // wait or a commit of this warp idles the tensor core for some 100
-                    // cycles, so a tile takes two of each: V(j), K(j + 1) and P are
-                    // tested at once, and the second softmax group frees the stages.
-                    const int t = (int)v_step & 1;
+                if (steps > 2) {
+                    // The scores ahead are the same item's.  A wait or a commit of this
+                    // warp idles the tensor core for some 100 cycles, so a step takes
+                    // one of each: V, K of the step two ahead and P are tested at once,
+                    // and the softmax groups free the stages.
                     auto step = [&](int g, uint32_t q, bool first) -> bool {
                         const uint32_t p_ph = v_step >> 1 & 1u;
                         if (!__all_sync(0xffffffffu, mbar_try_wait3(bar(L::bVFull + vt.stage), vt.ph, bar(L::bKFull + kt.stage),
                                                                     kt.ph, bar(L::bPFull + g), p_ph))) {
-                            if (!wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
                             if (!wait(L::bVFull + vt.stage, vt.ph, 95)) return false;
                             if (!wait(L::bPFull + g, p_ph, 96)) return false;
+                            if (!wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
                         }
                         if (first) {
                             if (!wait(L::bOEmpty + g, oe_ph >> g, 97)) return false;
@@ -797,15 +839,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
                     const uint32_t q0 = y.qtile & 1u;
                     const int n = y.n;
-                    for (int j = 0; j + 1 < n; ++j) {
-                        if (!(ok = t ? step(1, q0, j == 0) : step(0, q0, j == 0))) break;
-                        if (!(ok = t ? step(0, q0 ^ 1u, j == 0) : step(1, q0 ^ 1u, j == 0))) break;
-                        advance(kt, kK);
-                        advance(vt, kV);
+                    if (pair) {
+                        const int t = (int)v_step & 1;
+                        for (int j = 0; j + 1 < n; ++j) {
+                            if (!(ok = t ? step(1, q0, j == 0) : step(0, q0, j == 0))) break;
+                            if (!(ok = t ? step(0, q0 ^ 1u, j == 0) : step(1, q0 ^ 1u, j == 0))) break;
+                            advance(kt, kK);
+                            advance(vt, kV);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int j = 0; j + 2 < n; ++j) {
+                            if (!(ok = step((int)v_step & 1, q0, j < 2))) break;
+                            advance(kt, kK);
+                            advance(vt, kV);
+                        }
                     }
                     if (!ok) break;
-                    commit(L::bQEmpty);
-                    commit(L::bQEmpty + 1);
+                    commit(L::bQEmpty + q0);
+                    if (pair) commit(L::bQEmpty + (q0 ^ 1u));
                     u = steps - 2;
                     s_step += (uint32_t)u;
                     su = 0;
@@ -837,6 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_settle(bar(L::bDrain), 0, wf, 98);
             }
             __syncwarp();
+        } else {
+            const int s = window.base + lane;
+            if (lane < Window::kSeqs && s < p.B) window.raw[lane] = kv16_raw(p.c, p.cu, s);
+            mbar_arrive(bar(L::bWindow));
         }
     }
     }
@@ -863,9 +919,20 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
     wait_for_primary();
+    // the first parts are asked for together with the record that says whether there are any
+    const int prow = 32 * blockIdx.y + lane;
+    float4 st[U], o[U][V];
+    auto load = [&](int u, int k) {
+        const long long part = (long long)min(blockIdx.x + k, gridDim.x - 1) * 2 + (k == 0 ? 1 : 0);
+        st[u] = parts.stat[part * p.rows + prow];
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[u][i] = parts.o[(part * (D / 4) + warp + 8 * i) * p.rows + prow];
+    };
+#pragma unroll
+    for (int u = 0; u < 2; ++u) load(u, u);
     const Cut cut = parts.join[blockIdx.x];
     const int rt = cut.ntok > p.npt ? (int)blockIdx.y >> 2 : 0;  // tile of rows
-    const int prow = 32 * blockIdx.y + lane, row = prow - 128 * rt;
+    const int row = prow - 128 * rt;
     const int rows_t = min(p.npt, cut.ntok - rt * p.npt) * p.group;
     if (cut.parts == 0 || row - lane >= rows_t) return;
     const bool valid = row < rows_t;
@@ -875,20 +942,13 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
     for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (valid)
         for (int k0 = 0; k0 < cut.parts; k0 += U) {
-            float4 st[U], o[U][V];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                st[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-                if (k0 + u < cut.parts) {
-                    const long long part = (long long)(blockIdx.x + k0 + u) * 2 + (k0 + u == 0 ? 1 : 0);
-                    st[u] = parts.stat[part * p.rows + prow];
-#pragma unroll
-                    for (int i = 0; i < V; ++i) o[u][i] = parts.o[(part * (D / 4) + warp + 8 * i) * p.rows + prow];
-                }
-            }
+            for (int u = 0; u < U; ++u)
+                if ((k0 > 0 || u >= 2) && k0 + u < cut.parts) load(u, k0 + u);
             float top = r;
 #pragma unroll
-            for (int u = 0; u < U; ++u) top = fmaxf(top, st[u].x);
+            for (int u = 0; u < U; ++u)
+                if (k0 + u < cut.parts) top = fmaxf(top, st[u].x);
             const float m = top == -INFINITY ? 0.f : top, down = ex2_approx(r - m);
             r = top;
             l *= down;

@@ -13,24 +13,41 @@ struct Kv16Seq {
     const int* pages;  // its row of the table
 };
 
+// What describes sequence s, as it lies in memory.
+struct Kv16Raw {
+    int c0, c1, slot, len;
+};
+
+__device__ __forceinline__ Kv16Raw kv16_raw(const Kv16Cache& c, const int* cu, int s)
+{
+    Kv16Raw r;
+    r.c0 = cu[s];
+    r.c1 = cu[s + 1];
+    r.slot = c.ids ? c.ids[s] : s;
+    r.len = r.slot >= 0 && r.slot < c.num_slots ? c.lens[r.slot] : -1;
+    return r;
+}
+
 // Sequence s; one that is not sound is latched and counts as having no rows.
-__device__ __forceinline__ Kv16Seq kv16_sequence(const Kv16Cache& c, const int* cu, int total, int s)
+__device__ __forceinline__ Kv16Seq kv16_checked(const Kv16Cache& c, int total, int s, const Kv16Raw& r)
 {
     Kv16Seq q{};
-    const int c0 = cu[s], c1 = cu[s + 1], slot = c.ids ? c.ids[s] : s;
-    const bool slot_ok = slot >= 0 && slot < c.num_slots;
-    const int len = slot_ok ? c.lens[slot] : -1;
-    if (c0 < 0 || c1 < c0 || c1 > total || (s == 0 && c0 != 0) || len < c1 - c0 ||
-        (long long)len > ((long long)c.table_width << c.page_shift)) {
+    if (r.c0 < 0 || r.c1 < r.c0 || r.c1 > total || (s == 0 && r.c0 != 0) || r.len < r.c1 - r.c0 ||
+        (long long)r.len > ((long long)c.table_width << c.page_shift)) {
         atomicOr(c.err, 2);
         q.pages = c.table;
         return q;
     }
-    q.n = c1 - c0;
-    q.len = len;
-    q.row0 = c0;
-    q.pages = c.table + (long long)slot * c.table_width;
+    q.n = r.c1 - r.c0;
+    q.len = r.len;
+    q.row0 = r.c0;
+    q.pages = c.table + (long long)r.slot * c.table_width;
     return q;
+}
+
+__device__ __forceinline__ Kv16Seq kv16_sequence(const Kv16Cache& c, const int* cu, int total, int s)
+{
+    return kv16_checked(c, total, s, kv16_raw(c, cu, s));
 }
 
 // Element offset in the pool of K of head 0 at a position; -1 for a bad page.
