@@ -40,21 +40,22 @@ namespace fa {
 
 namespace {
 
-constexpr int kWarps = 12, kThreads = 32 * kWarps;  // 8 softmax warps, K, MMA, V, one without work
+constexpr int kWarps = 12, kThreads = 32 * kWarps;  // 8 softmax warps, K, MMA, V, list of work
 constexpr int kTile = 128;     // keys of a tile, rows of a tile
 constexpr int kBox = 128 * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds it by 2^8
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr int kAhead = 4;        // items that the list runs ahead
 constexpr int kItemCost = 2;     // what an item costs a block beside its tiles, in tiles
 
 // A block's part of an item.  A sequence has, for every KV head, blocks of up
 // to 2 npt of its query tokens: the items of the list of work.
 struct Item {
-    long long left;  // of the block's share, from tile t on
     Kv16Seq q;
+    long long left;  // of the block's share, from tile t on
     int s, h, rb;       // sequence, KV head, block of query tokens
     int blocks;         // of the sequence's query tokens
-    int t, n;           // the block's part: tiles t .. t + n - 1
+    int t, n;           // the block's part: tiles t .. t + n - 1; n 0: no more
     int nt;             // tiles of the item
     int tok0, ntok;     // first query token, and how many
     int clear;          // keys in front of this are seen by every row
@@ -91,11 +92,23 @@ __device__ __forceinline__ bool mbar_try_wait3(uint32_t b0, uint32_t p0, uint32_
     return ok != 0;
 }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const WaitFailure& wf,
-                                          int site, int item)
+// A bounded wait whose code is short (there are some thirty): false when the
+// block's abort flag is raised or the time limit passes, which raises it to
+// `site`; the block reports it at its end.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site)
 {
-    const bool ok = mbar_wait(bar, parity, abort_flag, wf, site, item);
-    return __all_sync(0xffffffffu, ok);
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+        if (n & 31u) continue;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = site;
+            return false;
+        }
+    }
+    return true;
 }
 
 // ------------------------------------------------------------------ the list of work
@@ -115,13 +128,25 @@ __device__ __forceinline__ Kv16Seq open_sequence(const Kv16AttnParams& p, int s)
     return open_sequence(p, s, kv16_raw(p.c, p.cu, s));
 }
 
-// The sequences behind a block's first one, in shared memory, so that they are
-// at hand when its warps get there; further ones are read where they lie.
+// The sequences to come, a lane each, so that one of them is at hand when the
+// warp of the list gets there.
 struct Window {
-    static constexpr int kSeqs = 12;
-    Kv16Raw raw[kSeqs];
-    int base;  // the first
-    int pad[3];
+    int base;
+    Kv16Raw raw;
+
+    __device__ __forceinline__ void fill(const Kv16AttnParams& p, int s, int lane)
+    {
+        base = s;
+        raw = Kv16Raw{0, 0, 0, 0};
+        if (s + lane < p.B) raw = kv16_raw(p.c, p.cu, s + lane);
+    }
+    __device__ __forceinline__ Kv16Seq open(const Kv16AttnParams& p, int s, int lane)
+    {
+        if (s - base >= 32) fill(p, s, lane);
+        const int i = s - base;
+        return open_sequence(p, s, Kv16Raw{__shfl_sync(~0u, raw.c0, i), __shfl_sync(~0u, raw.c1, i),
+                                           __shfl_sync(~0u, raw.slot, i), __shfl_sync(~0u, raw.len, i)});
+    }
 };
 
 template <int D>
@@ -133,13 +158,12 @@ struct Smem {
     static constexpr int kStats = kVRing + kV * kTileBytes;  // float [3][128]: r, l, l_rnd of the group that does not end an item
     static constexpr int kBars = kStats + 3 * 128 * 4;
     static constexpr int bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bOEmpty = 10, bStFull = 12,
-                         bStEmpty = 13, bDrain = 14, bWindow = 15, bKFull = 16, bKEmpty = bKFull + kK, bVFull = bKEmpty + kK,
-                         bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
+                         bStEmpty = 13, bDrain = 14, bItemFull = 15, bItemEmpty = bItemFull + kAhead, bKFull = bItemEmpty + kAhead,
+                         bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
     static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the blocks' share
-    static constexpr int kWindow = (kSums + (kWarps + 1) * 8 + 15) / 16 * 16;
-    static constexpr int kItems = kWindow + (int)sizeof(Window);  // Item [10]: softmax warps, of the next scores, of the next P.V
-    static constexpr int kBytes = kItems + 10 * (int)sizeof(Item);
+    static constexpr int kItems = kSums + (kWarps + 1) * 8;  // Item [kAhead]
+    static constexpr int kBytes = kItems + kAhead * (int)sizeof(Item);
     static_assert(kBytes <= 232448 && kBars % 8 == 0, "shared memory of one block");
     static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
 };
@@ -163,6 +187,7 @@ __device__ __forceinline__ long long head_cost(const Kv16AttnParams& p, const Kv
     const int nb = row_blocks(p, q.n);
     if (!p.causal || nb <= 1) return (long long)nb * (kItemCost + tiles_of(p, q, 0));
     long long sum = 0;
+#pragma unroll 1
     for (int rb = 0; rb < nb; ++rb) sum += kItemCost + tiles_of(p, q, rb);
     return sum;
 }
@@ -178,27 +203,23 @@ __device__ __forceinline__ void open_item(const Kv16AttnParams& p, Item& x)
     x.clear = p.mask ? prefix : p.causal ? prefix + x.tok0 + 1 : x.q.len;
 }
 
-// The block's part of the next item; left <= 0 at the end of its share.
-template <typename Ready>
-__device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, const Window& w, const Ready& window_here)
+// The block's part of the next item; n = 0 at the end of its share.  All lanes
+// of a warp compute it alike.
+__device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, Window& w, int lane)
 {
     x.step += x.pair ? 2 * x.n : x.n;
     x.tile += x.n;
     x.qtile += x.pair ? 2 : 1;
     x.left -= x.n;
+    x.n = 0;
     if (x.left <= 0) return;
     if (++x.rb == x.blocks) {
         x.rb = 0;
         if (++x.h == p.c.Hkv) {
             x.h = 0;
-            window_here();
             do {
-                if (++x.s >= p.B) {
-                    x.left = 0;
-                    return;
-                }
-                const int i = x.s - w.base;
-                x.q = i < Window::kSeqs ? open_sequence(p, x.s, w.raw[i]) : open_sequence(p, x.s);
+                if (++x.s >= p.B) return;
+                x.q = w.open(p, x.s, lane);
                 x.blocks = row_blocks(p, x.q.n);
             } while (x.blocks == 0);
         }
@@ -206,7 +227,7 @@ __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, cons
     open_item(p, x);
     x.left -= kItemCost;
     x.t = 0;
-    x.n = (int)min(x.left, (long long)x.nt);
+    x.n = (int)max(0ll, min(x.left, (long long)x.nt));
 }
 
 // The item that begins in a block and ends in a later one, for the kernel that
@@ -231,22 +252,34 @@ __host__ __device__ inline Parts parts_of(float* ws, int blocks, int rows)
     return p;
 }
 
-// Bits of the keys k0 .. k0 + 31 that query token i of the sequence may see.
-__device__ __forceinline__ uint32_t seen_word(const Kv16AttnParams& p, const Kv16Seq& q, int i, int k0)
+// A word whose low n bits are set (n any).
+__device__ __forceinline__ uint32_t low_bits(int n)
 {
-    const int prefix = q.len - q.n;
-    const auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-    if (!p.mask) return below((p.causal ? prefix + min(i, q.n - 1) + 1 : q.len) - k0);
-    uint32_t bits = below(prefix - k0);
-    const int j0 = k0 - prefix;  // of the call's positions
-    if (j0 > -32 && j0 < q.n) {
-        const int* row = p.mask + (long long)(q.row0 + min(i, q.n - 1)) * p.mask_words;
-        const int w = j0 >> 5;
-        const uint32_t lo = w >= 0 ? (uint32_t)__ldg(row + w) : 0u;
-        const uint32_t hi = w + 1 < p.mask_words ? (uint32_t)__ldg(row + w + 1) : 0u;
-        bits |= __funnelshift_r(lo, hi, (uint32_t)j0 & 31u) & below(q.n - j0);
+    uint32_t r;
+    asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(32 - n, 0)));  // 32 and more shift everything out
+    return r;
+}
+
+// Bits of the keys k0 .. k0 + 32 N - 1 that query token i of the sequence may see.
+template <int N>
+__device__ __forceinline__ void seen_words(const Kv16AttnParams& p, const Kv16Seq& q, int i, int k0, uint32_t (&w)[N])
+{
+    const int prefix = q.len - q.n, j0 = k0 - prefix;  // the first key among the call's positions
+    i = min(i, q.n - 1);
+    const int all = (p.mask ? prefix : p.causal ? prefix + i + 1 : q.len) - k0;
+    uint32_t m[N + 1];
+#pragma unroll
+    for (int c = 0; c <= N; ++c) m[c] = 0u;
+    if (p.mask) {
+        const int* row = p.mask + (long long)(q.row0 + i) * p.mask_words;
+#pragma unroll
+        for (int c = 0; c <= N; ++c) {
+            const int at = (j0 >> 5) + c;
+            if (at >= 0 && 32 * at < q.n) m[c] = (uint32_t)__ldg(row + at) & low_bits(q.n - 32 * at);
+        }
     }
-    return bits;
+#pragma unroll
+    for (int c = 0; c < N; ++c) w[c] = low_bits(all - 32 * c) | __funnelshift_r(m[c], m[c + 1], (uint32_t)j0 & 31u);
 }
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
@@ -272,8 +305,9 @@ __device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, 
 {
     const int end = min(x.q.len, (x.t + x.n) * kTile);
     for (int k0 = max(x.t * kTile, x.clear); k0 < end; k0 += 32) {
-        uint32_t bits = seen_word(p, x.q, tok, k0);
-        while (bits) {
+        uint32_t word[1];
+        seen_words(p, x.q, tok, k0, word);
+        for (uint32_t bits = word[0]; bits;) {
             const int k = k0 + __ffs(bits) - 1;
             bits &= bits - 1;
             if (k >= end) break;
@@ -304,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     long long* s_sum = reinterpret_cast<long long*>(smem + L::kSums);
-    Item* s_item = reinterpret_cast<Item*>(smem + L::kItems);  // each warp's part in hand: not in registers
+    Item* s_item = reinterpret_cast<Item*>(smem + L::kItems);  // the items in hand: not in registers
     auto bar = [&](int i) -> uint32_t { return sb + L::kBars + 8u * (uint32_t)i; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
@@ -312,8 +346,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* stats = reinterpret_cast<float*>(smem + L::kStats);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const WaitFailure wf{p.c.err, p.c.diag};
-    Window& window = *reinterpret_cast<Window*>(smem + L::kWindow);
-    Item first;  // the producers keep theirs in registers
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
 
     let_dependents_launch();
@@ -330,13 +362,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(L::bStFull), 128);
         mbar_init(bar(L::bStEmpty), 128);
         mbar_init(bar(L::bDrain), 1);
-        mbar_init(bar(L::bWindow), 32);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(bar(L::bItemFull + i), 1);
+            mbar_init(bar(L::bItemEmpty + i), 11);  // every warp but the list's
+        }
         for (uint32_t s = 0; s < 2 * (kK + kV); ++s) mbar_init(bar(L::bKFull + s), 1);
         *abort_flag = 0;
         *poison = 0;
         mbar_init_fence();
         parts.join[blockIdx.x].parts = 0;
-        s_item[0].left = 0;
+        s_item[0].n = 0;
     }
     if (warp == 8 && lane == 0) tma_prefetch_map(&tmQ);
     if (warp == 10 && lane == 0) tma_prefetch_map(&tmKV);
@@ -354,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         own_cost = head_cost(p, own);
         mine = p.c.Hkv * own_cost;
     }
+#pragma unroll 1
     for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
 
     {
@@ -381,14 +417,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item x;
             x.s = run0;
             x.q = own;
+#pragma unroll 1
             while (at + cost * p.c.Hkv <= first) {
                 at += cost * p.c.Hkv;
                 x.q = open_sequence(p, ++x.s);
                 cost = head_cost(p, x.q);
             }
             x.blocks = row_blocks(p, x.q.n);
+#pragma unroll 1
             for (x.h = 0; at + cost <= first; ++x.h) at += cost;
             int one;
+#pragma unroll 1
             for (x.rb = 0; at + (one = kItemCost + tiles_of(p, x.q, x.rb)) <= first; ++x.rb) at += one;
             open_item(p, x);
             x.left = last - first;
@@ -397,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             x.t = t < 0 ? 0 : (int)t;
             x.n = (int)min(x.left, (long long)(x.nt - x.t));
             x.step = x.tile = x.qtile = 0;
-            s_item[0] = x;
+            if (x.left > 0) s_item[0] = x;
             s_sum[kWarps] = share;
         }
     }
@@ -405,28 +444,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    if (s_item[0].left <= 0) goto done;  // no work, for no warp
-    if (warp == 8 || warp == 10) {
-        first = s_item[0];
-    } else if (warp > 0) {
-        // [0, 8): softmax warps, 8: scores, 9: P.V
-        Item* mine_of = s_item + (warp < 8 ? warp : warp == 9 ? 8 : 9);
-        for (int i = lane; i < (int)sizeof(Item) / 4; i += 32)
-            reinterpret_cast<int*>(mine_of)[i] = reinterpret_cast<const int*>(s_item)[i];
-        if (warp == 11 && lane == 0) window.base = s_item[0].s + 1;
-    }
-    __syncthreads();  // warp 0 changes its own from here
     {
-    Item& x = s_item[warp < 8 ? warp : 8];
-    // (a window that does not come ends the wait, and with it the block: what is read then is checked)
-    auto window_here = [&]() { mbar_wait(bar(L::bWindow), 0, abort_flag, wf, 79, blockIdx.x); };
-    auto next = [&](Item& y) {
-        __syncwarp();
-        if (lane == 0) next_item(p, y, window, window_here);
-        __syncwarp();
-    };
     auto wait = [&](int b, uint32_t parity, int site) -> bool {
-        return warp_wait(bar(b), parity & 1u, abort_flag, wf, site, blockIdx.x);
+        return __all_sync(0xffffffffu, wait_for(bar(b), parity & 1u, abort_flag, site));
+    };
+    // The k-th item; n = 0: no more, or a wait ran out.
+    auto item = [&](uint32_t k) -> const Item* { return s_item + k % kAhead; };
+    auto item_here = [&](uint32_t k) -> bool {
+        return wait(L::bItemFull + k % kAhead, k / kAhead, 79) && item(k)->n > 0;
+    };
+    auto item_done = [&](uint32_t k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::bItemEmpty + k % kAhead));
     };
 
     if (warp < 8) {
@@ -437,7 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tS = lane_base + L::kColS + (uint32_t)(128 * t);
         uint32_t st_ph = 0, o_ph = 0;  // o_ph: a bit per stream
         const int tok_row = row / p.group, head_row = row - tok_row * p.group;
-        for (; x.left > 0; next(x)) {
+#pragma unroll 1
+        for (uint32_t k = 0; item_here(k); ++k) {
+            const Item& x = *item(k);
             const int n = x.n, clear = x.clear, key_first = x.t * kTile;
             const bool pair = x.pair;
             const int u0 = (t ^ (int)x.step) & 1;  // the group's first step of the item; of a pair: its tile of rows
@@ -450,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t s_ph = (x.step + u0) >> 1;  // the group's steps so far
             const uint32_t tile0 = x.tile;
             float r = -INFINITY, l = 0.f, l_rnd = 0.f;
+#pragma unroll 1
             for (int j = j0; j < n; j += dj, ++s_ph) {
                 const int key0 = key_first + j * kTile;
                 const bool edge = key0 + kTile > clear;
@@ -471,13 +503,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32u * c, sv[c], mx[c]);
                     tmem_wait_ld();
                     if (edge) {
+                        uint32_t seen[4];
+                        seen_words(p, x.q, tok, key0, seen);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const uint32_t seen = seen_word(p, x.q, tok, key0 + 32 * c);
                             mx[c] = -INFINITY;
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                if (!(seen >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
+                                if (!(seen[c] >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
                                 mx[c] = fmaxf(mx[c], __uint_as_float(sv[c][i]));
                             }
                         }
@@ -541,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint8_t* vrow = smem + L::kVRing + stage * L::kTileBytes + row * 128;
                         const bool past = key0 + row >= x.q.len;
                         bool any = false;
-#pragma unroll 4
+#pragma unroll 2
                         for (int i = 0; i < D / 8; ++i) {
                             uint4* at = reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
                             if (past) {
@@ -578,6 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bar(L::bStFull));
                     st_ph ^= 1;
                 }
+                item_done(k);
                 continue;
             }
             if (!wait(L::bOFull + t, o_now >> t, 85 + t)) goto done;
@@ -606,47 +640,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int head = x.h * p.group + head_row;
                 uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; c += 1) {
-                    float o[1][32];
-                    {
-                        uint32_t ov[1][32], o1[1][32];
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32], o1[32];
+                    float o[32];
+                    tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov);
+                    if (two) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 1; ++k) tmem_ld32(tO + (uint32_t)(D * t + 32 * (c + k)), ov[k]);
-                        if (two)
-#pragma unroll
-                            for (int k = 0; k < 1; ++k) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * (c + k)), o1[k]);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 1; ++k)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[k][i] = two ? fmaf(w0, __uint_as_float(ov[k][i]), w1 * __uint_as_float(o1[k][i]))
-                                              : __uint_as_float(ov[k][i]);
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = two ? fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i])) : __uint_as_float(ov[i]);
                     if (!valid) continue;
+                    if (poisoned) {
+                        float fix[32];  // o itself stays in registers
 #pragma unroll
-                    for (int k = 0; k < 1; ++k) {
-                        if (poisoned) {
-                            float fix[32];  // o itself stays in registers
+                        for (int i = 0; i < 32; ++i) fix[i] = o[i];
+                        add_poison(p, x, tok, D, 32 * c, fix);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) fix[i] = o[k][i];
-                            add_poison(p, x, tok, D, 32 * (c + k), fix);
+                        for (int i = 0; i < 32; ++i) o[i] = fix[i];
+                    }
+                    if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[k][i] = fix[i];
-                        }
-                        if (whole) {
+                        for (int i = 0; i < 4; ++i)
+                            dst[4 * c + i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                                        pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                                        pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                                        pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    } else {
+                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + prow;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                dst[4 * (c + k) + i] = make_uint4(pack_bf16x2(o[k][8 * i] * inv, o[k][8 * i + 1] * inv),
-                                                                  pack_bf16x2(o[k][8 * i + 2] * inv, o[k][8 * i + 3] * inv),
-                                                                  pack_bf16x2(o[k][8 * i + 4] * inv, o[k][8 * i + 5] * inv),
-                                                                  pack_bf16x2(o[k][8 * i + 6] * inv, o[k][8 * i + 7] * inv));
-                        } else {
-                            float4* to = parts.o + (part * (D / 4) + 8 * (c + k)) * p.rows + prow;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i, to += p.rows)
-                                *to = make_float4(o[k][4 * i], o[k][4 * i + 1], o[k][4 * i + 2], o[k][4 * i + 3]);
-                        }
+                        for (int i = 0; i < 8; ++i, to += p.rows)
+                            *to = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
                 if (valid) {
@@ -663,6 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rest = x.nt - n, share = (int)min(s_sum[kWarps], 1ll << 30);
                 parts.join[blockIdx.x] = Cut{1 + (rest + share - 1) / share, x.q.row0 + x.tok0, x.ntok, x.h};
             }
+            item_done(k);
         }
     } else {
         regs_decrease<88>();
@@ -685,13 +709,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i = (y.t + j) * per_tile + sub;
                 return half < boxes && (long long)i * page_rows < y.q.len ? y.q.pages[(long long)i * page_rows >> shift] : 0;
             };
-            Item& y = first;  // and the next one, whose first page is asked for early
-            int page = page_of(y, 0);
-            while (ok && y.left > 0) {
+            uint32_t k = 0;
+            ok = item_here(0);
+            int page = ok ? page_of(*item(0), 0) : 0;
+#pragma unroll 1
+            while (ok) {
+                const Item& y = *item(k);
                 const int n = y.n, h = y.h, t0 = y.t;
                 const int pages_end = (y.q.len + page_rows - 1) / page_rows;  // boxes of the sequence
                 if (keys) {
                     const int tiles = y.pair ? 2 : 1, row0 = y.q.row0 + y.tok0;
+#pragma unroll 1
                     for (int i = 0; i < tiles && ok; ++i) {
                         const uint32_t qt = y.qtile + i, b = qt & 1u;
                         if (!(ok = wait(L::bQEmpty + b, (qt >> 1) ^ 1u, 89))) break;
@@ -705,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!ok) break;
                 }
-                Item z = y;
+#pragma unroll 1
                 for (int j = 0; j < n; ++j) {
                     int pg = page;
                     if (j + 1 < n) page = page_of(y, j + 1);  // on its way while this tile's stage is awaited
@@ -730,14 +758,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stage = 0;
                         ph ^= 1u;
                     }
-                    if (j == 0) next_item(p, z, window, window_here);
                 }
-                if (z.left > 0) page = page_of(z, 0);
-                y = z;
+                if (!ok) break;
+                item_done(k);
+                if (!item_here(++k)) break;
+                page = page_of(*item(k), 0);
             }
             // every copy that this warp started has landed before the block retires
+#pragma unroll 1
             for (uint32_t b = 0; b < 2; ++b)
                 if (q_armed >> b & 1u) mbar_settle(bar(L::bQFull + b), q_par >> b & 1u, wf, 91);
+#pragma unroll 1
             for (uint32_t s = 0; s < stages; ++s)
                 if (armed >> s & 1u) mbar_settle(bar(full + s), par >> s & 1u, wf, 92);
         } else if (warp == 9) {
@@ -783,42 +814,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s.ph ^= 1u;
                 }
             };
-            Item& y = s_item[9];  // the item of the next P.V; x: that of the next scores, up to two steps ahead
-            int su = 0;            // step of x
-            uint32_t s_step = 0, v_step = 0, oe_ph = 3;
-            bool issued = false;
-            // The scores of the next step, if there is one; false: a wait ran out.
-            auto scores = [&]() -> bool {
-                if (x.left <= 0) return true;
-                const bool pair = x.pair;
-                const int steps = pair ? 2 * x.n : x.n, t = (int)s_step & 1;
-                const uint32_t qt = x.qtile + (pair ? su & 1 : 0), b = qt & 1u;
-                if (su < (pair ? 2 : 1) && !wait(L::bQFull + b, qt >> 1, 93)) return false;
-                if (!(pair && (su & 1)) && !wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
-                tc_fence_after_sync();
-                mma_s(t, b, kt.stage);
-                issued = true;
-                commit(L::bSFull + t);
-                if (su >= steps - (pair ? 2 : 1)) commit(L::bQEmpty + b);
-                if (!pair || (su & 1)) advance(kt, kK);
-                ++s_step;
-                if (++su == steps) {
-                    su = 0;
-                    next(x);
-                }
-                return true;
-            };
-            bool ok = scores() && scores();
-            for (; ok && y.left > 0; next(y)) {
-                const bool pair = y.pair;
-                const int steps = pair ? 2 * y.n : y.n;
-                int u = 0;
-                if (steps > 2) {
-                    // The scores ahead are the same item's.  A wait or a commit of this
-                    // warp idles the tensor core for some 100 cycles, so a step takes
-                    // one of each: V, K of the step two ahead and P are tested at once,
-                    // and the softmax groups free the stages.
-                    auto step = [&](int g, uint32_t q, bool first) -> bool {
+            // The next scores, up to two steps ahead of the next P.V: item kx, step su
+            // of it; v_step and s_step count the steps, whose streams alternate.
+            uint32_t kx = 0, ky = 0, s_step = 0, v_step = 0, oe_ph = 3;
+            int su = 0, u = 0;
+            bool issued = false, ok = true;
+            const Item *x = item_here(0) ? item(0) : nullptr, *y = x;
+#pragma unroll 1
+            while (y && ok) {
+                const bool pv = s_step - v_step == 2 || !x;  // else: the first scores
+                const bool pair = y->pair;
+                const int steps = pair ? 2 * y->n : y->n;
+                if (pv && x == y && steps - u > 4) {
+                    // In the middle of an item.  A wait or a commit of this warp idles the
+                    // tensor core for some 100 cycles, so a step takes one of each: V, K of
+                    // the step two ahead and P are tested at once, and the softmax groups
+                    // free the stages.
+                    auto step = [&](int g, uint32_t q, bool last_of_tile) -> bool {
                         const uint32_t p_ph = v_step >> 1 & 1u;
                         if (!__all_sync(0xffffffffu, mbar_try_wait3(bar(L::bVFull + vt.stage), vt.ph, bar(L::bKFull + kt.stage),
                                                                     kt.ph, bar(L::bPFull + g), p_ph))) {
@@ -826,47 +838,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (!wait(L::bPFull + g, p_ph, 96)) return false;
                             if (!wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
                         }
-                        if (first) {
+                        if (u < 2) {
                             if (!wait(L::bOEmpty + g, oe_ph >> g, 97)) return false;
                             oe_ph ^= 1u << g;
                         }
                         tc_fence_after_sync();
-                        mma_pv(g, vt.stage, !first);
+                        mma_pv(g, vt.stage, u >= 2);
                         mma_s(g, q, kt.stage);
                         commit(L::bSFull + g);
                         ++v_step;
+                        ++u;
+                        if (last_of_tile) {
+                            advance(kt, kK);
+                            advance(vt, kV);
+                        }
                         return true;
                     };
-                    const uint32_t q0 = y.qtile & 1u;
-                    const int n = y.n;
-                    if (pair) {
-                        const int t = (int)v_step & 1;
-                        for (int j = 0; j + 1 < n; ++j) {
-                            if (!(ok = t ? step(1, q0, j == 0) : step(0, q0, j == 0))) break;
-                            if (!(ok = t ? step(0, q0 ^ 1u, j == 0) : step(1, q0 ^ 1u, j == 0))) break;
-                            advance(kt, kK);
-                            advance(vt, kV);
-                        }
-                    } else {
+                    const uint32_t q0 = y->qtile & 1u;
+                    const int g = (int)v_step & 1, u0 = u;
 #pragma unroll 1
-                        for (int j = 0; j + 2 < n; ++j) {
-                            if (!(ok = step((int)v_step & 1, q0, j < 2))) break;
-                            advance(kt, kK);
-                            advance(vt, kV);
-                        }
+                    while (steps - u > 4) {  // the last scores also free Q
+                        if (!(ok = step(g, q0, !pair))) break;
+                        if (!(ok = step(g ^ 1, pair ? q0 ^ 1u : q0, true))) break;
                     }
-                    if (!ok) break;
-                    commit(L::bQEmpty + q0);
-                    if (pair) commit(L::bQEmpty + (q0 ^ 1u));
-                    u = steps - 2;
-                    s_step += (uint32_t)u;
-                    su = 0;
-                    next(x);
+                    s_step += (uint32_t)(u - u0);
+                    su += u - u0;
+                    continue;
                 }
-                for (; u < steps; ++u) {
+                if (pv) {
                     const int t = (int)v_step & 1;
                     const bool second = pair && (u & 1);
-                    if (!second && !(ok = wait(L::bVFull + vt.stage, vt.ph, 95))) break;
+                    if (!(ok = wait(L::bVFull + vt.stage, vt.ph, 95))) break;
                     if (!(ok = wait(L::bPFull + t, v_step >> 1, 96))) break;
                     if (u < 2) {
                         if (!(ok = wait(L::bOEmpty + t, oe_ph >> t, 97))) break;
@@ -875,14 +877,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                     mma_pv(t, vt.stage, u >= 2);
                     if (!pair || second) {
-                        commit(L::bVEmpty + vt.stage);
+                        if (u >= steps - 2) commit(L::bVEmpty + vt.stage);  // else the softmax frees it
                         advance(vt, kV);
                     }
                     if (u >= steps - 2) commit(L::bOFull + t);
                     ++v_step;
-                    if (!(ok = scores())) break;
+                    if (++u == steps) {
+                        item_done(ky);
+                        u = 0;
+                        y = item_here(++ky) ? item(ky) : nullptr;
+                    }
                 }
-                if (!ok) break;
+                if (x) {
+                    const bool pr = x->pair;
+                    const int t = (int)s_step & 1, all = pr ? 2 * x->n : x->n;
+                    const uint32_t qt = x->qtile + (pr ? su & 1 : 0), b = qt & 1u;
+                    if (su < (pr ? 2 : 1) && !(ok = wait(L::bQFull + b, qt >> 1, 93))) break;
+                    if (!(ok = wait(L::bKFull + kt.stage, kt.ph, 94))) break;
+                    tc_fence_after_sync();
+                    mma_s(t, b, kt.stage);
+                    issued = true;
+                    commit(L::bSFull + t);
+                    if (su >= all - (pr ? 2 : 1)) commit(L::bQEmpty + b);
+                    if (!pr || (su & 1)) advance(kt, kK);
+                    ++s_step;
+                    if (++su == all) {
+                        su = 0;
+                        x = item_here(++kx) ? item(kx) : nullptr;
+                    }
+                }
             }
             if (issued) {
                 commit(L::bDrain);
@@ -890,9 +913,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         } else {
-            const int s = window.base + lane;
-            if (lane < Window::kSeqs && s < p.B) window.raw[lane] = kv16_raw(p.c, p.cu, s);
-            mbar_arrive(bar(L::bWindow));
+            // ============================================================ the list of work
+            Item y = s_item[0];
+            if (lane == 0) mbar_arrive(bar(L::bItemFull));
+            Window window;
+            if (y.n > 0) window.fill(p, y.s + 1, lane);  // else there is no item, and y holds nothing
+#pragma unroll 1
+            for (uint32_t k = 1; y.n > 0; ++k) {
+                next_item(p, y, window, lane);
+                if (!wait(L::bItemEmpty + k % kAhead, (k / kAhead) ^ 1u, 78)) break;
+                if (lane == 0) {
+                    s_item[k % kAhead] = y;
+                    mbar_arrive(bar(L::bItemFull + k % kAhead));
+                }
+                __syncwarp();
+            }
         }
     }
     }
@@ -900,6 +935,10 @@ done:
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && *abort_flag) {
+        atomicOr(p.c.err, 1);
+        if (atomicCAS(p.c.diag, 0, 1 + *abort_flag) == 0) p.c.diag[1] = (int)blockIdx.x;
+    }
     if (warp == 9) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 512);
