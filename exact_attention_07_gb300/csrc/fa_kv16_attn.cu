@@ -32,7 +32,7 @@
 // that lies in several blocks is joined by a second kernel.
 #include <cuda_bf16.h>
 
-#include <cfloat>
+#include <climits>
 
 #include "kv16_common.cuh"
 
@@ -74,6 +74,37 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 __device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The descriptors of smem_desc_sw128 with a stride of 1024 bytes differ in their
+// low word only (start address and leading dimension), and MMAs that take it
+// alone are a third of the code.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+
+// D[tmem] (+)= A[smem] * B[smem] and A[tmem] * B[smem] (kind::f16, bf16)
+__device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "n"(kDescHigh)
+        : "memory");
+}
+
 // Three barrier phases tested by one thread back to back; true when all have completed.
 __device__ __forceinline__ bool mbar_try_wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2)
 {
@@ -92,18 +123,25 @@ __device__ __forceinline__ bool mbar_try_wait3(uint32_t b0, uint32_t p0, uint32_
     return ok != 0;
 }
 
-// A bounded wait whose code is short (there are some thirty): false when the
-// block's abort flag is raised or the time limit passes, which raises it to
-// `site`; the block reports it at its end.
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, int site)
+__device__ __forceinline__ uint32_t timer_low_ns()
 {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+// A bounded wait for test() whose code is short (there are some twenty): false
+// when the block's abort flag is raised or the time limit passes, which raises
+// it to `site`; the block reports it at its end.
+template <typename Test>
+__device__ __forceinline__ bool wait_for(Test test, volatile int* abort_flag, int site)
+{
+    if (test()) return true;
+    const uint32_t t0 = timer_low_ns();
 #pragma unroll 1
-    for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
-        if (n & 31u) continue;
+    while (!test()) {
         if (*abort_flag) return false;
-        if (global_timer_ns() - t0 > kWaitLimitNs) {
+        if (timer_low_ns() - t0 > (uint32_t)kWaitLimitNs) {
             *abort_flag = site;
             return false;
         }
@@ -142,7 +180,7 @@ struct Window {
     }
     __device__ __forceinline__ Kv16Seq open(const Kv16AttnParams& p, int s, int lane)
     {
-        if (s - base >= 32) fill(p, s, lane);
+        if (s >= base + 32) fill(p, s, lane);
         const int i = s - base;
         return open_sequence(p, s, Kv16Raw{__shfl_sync(~0u, raw.c0, i), __shfl_sync(~0u, raw.c1, i),
                                            __shfl_sync(~0u, raw.slot, i), __shfl_sync(~0u, raw.len, i)});
@@ -298,26 +336,30 @@ __device__ __forceinline__ bool make_finite(uint4& x)
     return any;
 }
 
-// Adds to 32 columns of a row's sum what make_finite took out of the part's
-// keys that the row sees.
-__device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, int tok, int D, int c0,
-                                        float (&o)[32])
+// Adds to a row's D sums what make_finite took out of the part's keys that the
+// row sees: an infinity or a NaN swallows what it is added to, whether that is
+// normalised and rounded (o16) or not (o32, four sums in every `step` float4).
+__device__ __noinline__ void add_poison(const Kv16AttnParams& p, const Item& x, int tok, int D, uint16_t* o16, float* o32,
+                                        int step)
 {
     const int end = min(x.q.len, (x.t + x.n) * kTile);
-    for (int k0 = max(x.t * kTile, x.clear); k0 < end; k0 += 32) {
+#pragma unroll 1
+    for (int k = max(x.t * kTile, x.clear); k < end; ++k) {
         uint32_t word[1];
-        seen_words(p, x.q, tok, k0, word);
-        for (uint32_t bits = word[0]; bits;) {
-            const int k = k0 + __ffs(bits) - 1;
-            bits &= bits - 1;
-            if (k >= end) break;
-            const long long at = kv16_row(p.c, D, x.q.pages, k);
-            if (at < 0) continue;
-            const uint16_t* val = p.c.pool + at + (long long)(p.c.Hkv + x.h) * kv16_head_stride(p.c, D) + c0;
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t e = val[i];
-                if (not_finite(e)) o[i] += __uint_as_float(e << 16);
-            }
+        seen_words(p, x.q, tok, k, word);
+        const long long at = word[0] & 1u ? kv16_row(p.c, D, x.q.pages, k) : -1;
+        if (at < 0) continue;
+        const uint16_t* val = p.c.pool + at + (p.c.Hkv + x.h) * kv16_head_stride(p.c, D);
+#pragma unroll 1
+        for (int d = 0; d < D; ++d) {
+            const uint32_t v = val[d];
+            if (!not_finite(v)) continue;
+            float* sum = o32 + (long long)(d >> 2) * step * 4 + (d & 3);
+            const float old = o16 ? __uint_as_float((uint32_t)o16[d] << 16) : *sum, now = old + __uint_as_float(v << 16);
+            if (o16)
+                o16[d] = (uint16_t)pack_bf16x2(now, 0.f);
+            else
+                *sum = now;
         }
     }
 }
@@ -446,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     {
     auto wait = [&](int b, uint32_t parity, int site) -> bool {
-        return __all_sync(0xffffffffu, wait_for(bar(b), parity & 1u, abort_flag, site));
+        const uint32_t at = bar(b);
+        return __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait(at, parity & 1u); }, abort_flag, site));
     };
     // The k-th item; n = 0: no more, or a wait ran out.
     auto item = [&](uint32_t k) -> const Item* { return s_item + k % kAhead; };
@@ -633,7 +676,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const long long part = (long long)blockIdx.x * 2 + (x.t == 0 ? 1 : 0);
             const int prow = 128 * rt + row;
             const float inv = l > 0.f || l != l ? 1.f / (l + l_rnd) : 0.f;  // NaN stays
-            const bool poisoned = *poison != 0;
             if (work) {
                 const uint32_t tO = lane_base + L::kColO;
                 const long long token = (long long)x.q.row0 + tok;
@@ -650,14 +692,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 32; ++i)
                         o[i] = two ? fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i])) : __uint_as_float(ov[i]);
                     if (!valid) continue;
-                    if (poisoned) {
-                        float fix[32];  // o itself stays in registers
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) fix[i] = o[i];
-                        add_poison(p, x, tok, D, 32 * c, fix);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = fix[i];
-                    }
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -677,6 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         p.lse[(long long)head * p.T + token] = l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
                     else
                         parts.stat[part * p.rows + prow] = make_float4(r, l, l_rnd, 0.f);
+                    if (*poison)
+                        add_poison(p, x, tok, D, whole ? reinterpret_cast<uint16_t*>(dst) : nullptr,
+                                   reinterpret_cast<float*>(parts.o + part * (D / 4) * p.rows + prow), p.rows);
                 }
             }
             tc_fence_before_sync();
@@ -782,26 +819,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (leader) tc_commit(bar(b));
                 __syncwarp();
             };
+            auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
             // S of stream t = rows in buffer q times K in a stage; O of stream t (+)= P V
             auto mma_s = [&](int t, uint32_t q, uint32_t stage) {
-                const uint64_t qd = smem_desc_sw128(sb + L::kQ + q * L::kTileBytes, 16, 1024);
-                const uint64_t kd = smem_desc_sw128(sb + L::kKRing + stage * L::kTileBytes, 16, 1024);
+                const uint32_t qd = uniform(desc_low(sb + L::kQ + q * L::kTileBytes, 16));
+                const uint32_t kd = uniform(desc_low(sb + L::kKRing + stage * L::kTileBytes, 16));
+                const uint32_t d = uniform(tm + L::kColS + (uint32_t)(128 * t));
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
-                        mma_ss(tm + L::kColS + (uint32_t)(128 * t), qd + off, kd + off, kIdescS, kk > 0 ? 1u : 0u);
+                        const uint32_t off = (uint32_t)(((kk >> 2) * kBox + (kk & 3) * 32) >> 4);
+                        mma_ss_low(d, qd + off, kd + off, kIdescS, kk > 0);
                     }
                 }
                 __syncwarp();
             };
             auto mma_pv = [&](int t, uint32_t stage, bool acc) {
-                const uint64_t vd = smem_desc_sw128(sb + L::kVRing + stage * L::kTileBytes, kBox, 1024);
+                const uint32_t vd = uniform(desc_low(sb + L::kVRing + stage * L::kTileBytes, kBox));
+                const uint32_t d = uniform(tm + L::kColO + (uint32_t)(D * t)), pa = uniform(tm + L::kColS + (uint32_t)(128 * t));
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_ts(tm + L::kColO + (uint32_t)(D * t), tm + L::kColS + (uint32_t)(128 * t + 8 * kk),
-                               vd + (uint64_t)((kk * 16 * 128) >> 4), kIdescPV, (acc || kk > 0) ? 1u : 0u);
+                        mma_ts_low(d, pa + (uint32_t)(8 * kk), vd + (uint32_t)((kk * 16 * 128) >> 4), kIdescPV, acc || kk > 0);
                 }
                 __syncwarp();
             };
@@ -825,25 +864,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool pv = s_step - v_step == 2 || !x;  // else: the first scores
                 const bool pair = y->pair;
                 const int steps = pair ? 2 * y->n : y->n;
-                if (pv && x == y && steps - u > 4) {
+                if (pv && x == y && u >= 2 && steps - u > 4) {
                     // In the middle of an item.  A wait or a commit of this warp idles the
                     // tensor core for some 100 cycles, so a step takes one of each: V, K of
                     // the step two ahead and P are tested at once, and the softmax groups
                     // free the stages.
                     auto step = [&](int g, uint32_t q, bool last_of_tile) -> bool {
-                        const uint32_t p_ph = v_step >> 1 & 1u;
-                        if (!__all_sync(0xffffffffu, mbar_try_wait3(bar(L::bVFull + vt.stage), vt.ph, bar(L::bKFull + kt.stage),
-                                                                    kt.ph, bar(L::bPFull + g), p_ph))) {
-                            if (!wait(L::bVFull + vt.stage, vt.ph, 95)) return false;
-                            if (!wait(L::bPFull + g, p_ph, 96)) return false;
-                            if (!wait(L::bKFull + kt.stage, kt.ph, 94)) return false;
-                        }
-                        if (u < 2) {
-                            if (!wait(L::bOEmpty + g, oe_ph >> g, 97)) return false;
-                            oe_ph ^= 1u << g;
-                        }
+                        const uint32_t b0 = bar(L::bVFull + vt.stage), b1 = bar(L::bKFull + kt.stage), b2 = bar(L::bPFull + g);
+                        const uint32_t p2 = v_step >> 1 & 1u;
+                        if (!__all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait3(b0, vt.ph, b1, kt.ph, b2, p2); },
+                                                              abort_flag, 94)))
+                            return false;
                         tc_fence_after_sync();
-                        mma_pv(g, vt.stage, u >= 2);
+                        mma_pv(g, vt.stage, true);
                         mma_s(g, q, kt.stage);
                         commit(L::bSFull + g);
                         ++v_step;
@@ -917,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item y = s_item[0];
             if (lane == 0) mbar_arrive(bar(L::bItemFull));
             Window window;
-            if (y.n > 0) window.fill(p, y.s + 1, lane);  // else there is no item, and y holds nothing
+            window.base = INT_MIN;  // filled when the first sequence ends
 #pragma unroll 1
             for (uint32_t k = 1; y.n > 0; ++k) {
                 next_item(p, y, window, lane);
