@@ -322,18 +322,18 @@ __device__ __forceinline__ void seen_words(const Kv16AttnParams& p, const Kv16Se
 
 __device__ __forceinline__ bool not_finite(uint32_t half) { return (half & 0x7f80u) == 0x7f80u; }
 
-// 16 bytes of V with the elements that are not finite made 0; true if there were any.
-__device__ __forceinline__ bool make_finite(uint4& x)
+// Not 0 where one of two bf16 elements is not finite: an exponent of all ones
+// carries into the sign's place.
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// 16 bytes of V with the elements that are not finite made 0.
+__device__ __forceinline__ uint4 make_finite(uint4 x)
 {
     uint32_t* w = &x.x;
-    bool any = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bool lo = not_finite(w[i]), hi = not_finite(w[i] >> 16);
-        any |= lo | hi;
-        w[i] = (lo ? 0u : w[i] & 0xffffu) | (hi ? 0u : w[i] & 0xffff0000u);
-    }
-    return any;
+    for (int i = 0; i < 4; ++i)
+        w[i] = (not_finite(w[i]) ? 0u : w[i] & 0xffffu) | (not_finite(w[i] >> 16) ? 0u : w[i] & 0xffff0000u);
+    return x;
 }
 
 // Adds to a row's D sums what make_finite took out of the part's keys that the
@@ -528,6 +528,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = j0; j < n; j += dj, ++s_ph) {
                 const int key0 = key_first + j * kTile;
                 const bool edge = key0 + kTile > clear;
+                // V of a tile with masked keys, before its first product: rows behind
+                // the sequence's end become zeros, and so do elements of masked rows
+                // that are not finite
+                if (edge && rt == 0) {
+                    const uint32_t T = tile0 + (uint32_t)j, stage = T % kV;
+                    if (!wait(L::bVFull + stage, T / kV, 82 + t)) goto done;
+                    uint8_t* vrow = smem + L::kVRing + stage * L::kTileBytes + row * 128;
+                    const auto at = [&](int i) {  // the row's 16-byte pieces, lanes on different banks
+                        return reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
+                    };
+                    if (key0 + row >= x.q.len) {
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) *at(i) = make_uint4(0, 0, 0, 0);
+                    } else if (key0 + row >= clear) {
+                        uint32_t odd = 0;
+#pragma unroll 8
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint4 e = *at(i);
+                            odd |= odd_halves(e.x) | odd_halves(e.y) | odd_halves(e.z) | odd_halves(e.w);
+                        }
+                        if (odd) {
+                            *poison = 1;
+#pragma unroll 1
+                            for (int i = 0; i < D / 8; ++i) *at(i) = make_finite(*at(i));
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
                 if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
                 // These scores are complete, and so is all that was issued before
                 // them: K(j) is no longer read (of a pair: when they are the second
@@ -609,31 +637,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     r = r_new;
                     tmem_wait_st();
                 }
-                // V of a tile with masked keys, before its first product
-                if (edge && rt == 0) {
-                    const uint32_t T = tile0 + (uint32_t)j, stage = T % kV;
-                    if (!wait(L::bVFull + stage, T / kV, 82 + t)) goto done;
-                    if (key0 + row >= clear) {
-                        uint8_t* vrow = smem + L::kVRing + stage * L::kTileBytes + row * 128;
-                        const bool past = key0 + row >= x.q.len;
-                        bool any = false;
-#pragma unroll 2
-                        for (int i = 0; i < D / 8; ++i) {
-                            uint4* at = reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
-                            if (past) {
-                                *at = make_uint4(0, 0, 0, 0);
-                            } else {
-                                uint4 e = *at;
-                                if (make_finite(e)) {
-                                    *at = e;
-                                    any = true;
-                                }
-                            }
-                        }
-                        if (any) *poison = 1;
-                    }
-                    fence_proxy_async_smem();
-                }
                 tc_fence_before_sync();
                 mbar_arrive(bar(L::bPFull + t));
             }
@@ -677,48 +680,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int prow = 128 * rt + row;
             const float inv = l > 0.f || l != l ? 1.f / (l + l_rnd) : 0.f;  // NaN stays
             if (work) {
+                // O into registers first: the next item's products wait for its place
                 const uint32_t tO = lane_base + L::kColO;
-                const long long token = (long long)x.q.row0 + tok;
-                const int head = x.h * p.group + head_row;
-                uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D);
-#pragma unroll 1
+                float o[D / 32][32];
+#pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32], o1[32];
-                    float o[32];
+                    uint32_t ov[32];
                     tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov);
-                    if (two) tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
-                    tmem_wait_ld();
+                    if (two) {
+                        uint32_t o1[32];
+                        tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = two ? fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i])) : __uint_as_float(ov[i]);
-                    if (!valid) continue;
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[4 * c + i] = make_uint4(pack_bf16x2(o[8 * i] * inv, o[8 * i + 1] * inv),
-                                                        pack_bf16x2(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                                        pack_bf16x2(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                                        pack_bf16x2(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                        for (int i = 0; i < 32; ++i) o[c][i] = fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i]));
                     } else {
-                        float4* to = parts.o + (part * (D / 4) + 8 * c) * p.rows + prow;
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i, to += p.rows)
-                            *to = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 32; ++i) o[c][i] = __uint_as_float(ov[i]);
                     }
                 }
+                tc_fence_before_sync();
+                mbar_arrive(bar(L::bOEmpty + t));
+                if (two) mbar_arrive(bar(L::bOEmpty + (t ^ 1)));
                 if (valid) {
-                    if (whole)
+                    const long long token = (long long)x.q.row0 + tok;
+                    const int head = x.h * p.group + head_row;
+                    uint4* dst = reinterpret_cast<uint4*>(p.o + (token * p.Hq + head) * D);
+                    float4* to = parts.o + part * (D / 4) * p.rows + prow;
+                    if (whole) {
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            const float* f = &o[i >> 2][8 * (i & 3)];
+                            dst[i] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                                pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
+                        }
                         p.lse[(long long)head * p.T + token] = l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
-                    else
+                    } else {
+                        float4* at = to;
+#pragma unroll
+                        for (int i = 0; i < D / 4; ++i, at += p.rows) {
+                            const float* f = &o[i >> 3][4 * (i & 7)];
+                            *at = make_float4(f[0], f[1], f[2], f[3]);
+                        }
                         parts.stat[part * p.rows + prow] = make_float4(r, l, l_rnd, 0.f);
+                    }
                     if (*poison)
-                        add_poison(p, x, tok, D, whole ? reinterpret_cast<uint16_t*>(dst) : nullptr,
-                                   reinterpret_cast<float*>(parts.o + part * (D / 4) * p.rows + prow), p.rows);
+                        add_poison(p, x, tok, D, whole ? reinterpret_cast<uint16_t*>(dst) : nullptr, reinterpret_cast<float*>(to),
+                                   p.rows);
                 }
+            } else {
+                mbar_arrive(bar(L::bOEmpty + t));
+                if (two) mbar_arrive(bar(L::bOEmpty + (t ^ 1)));
             }
-            tc_fence_before_sync();
-            mbar_arrive(bar(L::bOEmpty + t));
-            if (two) mbar_arrive(bar(L::bOEmpty + (t ^ 1)));
             if (!whole && x.t == 0 && rt == 0 && row == 0) {
                 const int rest = x.nt - n, share = (int)min(s_sum[kWarps], 1ll << 30);
                 parts.join[blockIdx.x] = Cut{1 + (rest + share - 1) / share, x.q.row0 + x.tok0, x.ntok, x.h};
