@@ -105,7 +105,28 @@ __device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, u
         : "memory");
 }
 
-// Three barrier phases tested by one thread back to back; true when all have completed.
+// Five and three barrier phases tested by one thread back to back; true when all have completed.
+__device__ __forceinline__ bool mbar_try_wait5(const uint32_t (&b)[5], const uint32_t (&p)[5])
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred q0, q1, q2, q3, q4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q0, [%1], %6;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q1, [%2], %7;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q2, [%3], %8;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q3, [%4], %9;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q4, [%5], %10;\n\t"
+        "and.pred q0, q0, q1;\n\t"
+        "and.pred q2, q2, q3;\n\t"
+        "and.pred q0, q0, q4;\n\t"
+        "and.pred q0, q0, q2;\n\t"
+        "selp.u32 %0, 1, 0, q0;\n\t}\n"
+        : "=r"(ok)
+        : "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4])
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ bool mbar_try_wait3(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2)
 {
     uint32_t ok;
@@ -559,32 +580,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
                 // These scores are complete, and so is all that was issued before
                 // them: K(j) is no longer read (of a pair: when they are the second
-                // of the tile), and V of the step two before neither.  (V of an item's
-                // last steps is freed by the MMA warp.)
-                if ((!pair || rt == 1) && row == 0) {
+                // of the tile), V of the step two before neither, and the tile of
+                // rows when they are its last.
+                if (row == 0) {
                     const uint32_t T = tile0 + (uint32_t)j;
-                    mbar_arrive(bar(L::bKEmpty + T % kK));
-                    if (j >= dj) mbar_arrive(bar(L::bVEmpty + (T - dj) % kV));
+                    if (!pair || rt == 1) {
+                        mbar_arrive(bar(L::bKEmpty + T % kK));
+                        if (j >= dj) mbar_arrive(bar(L::bVEmpty + (T - dj) % kV));
+                    }
+                    if (j == n - 1) mbar_arrive(bar(L::bQEmpty + (int)((x.qtile + rt) & 1u)));
                 }
                 tc_fence_after_sync();
                 if (work) {
                     uint32_t sv[4][32];
                     float mx[4];
+                    bool upper = true;  // some row sees some of the tile's upper 64 keys
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32u * c, sv[c], mx[c]);
-                    tmem_wait_ld();
                     if (edge) {
                         uint32_t seen[4];
                         seen_words(p, x.q, tok, key0, seen);
+                        tmem_wait_ld();
+                        upper = __any_sync(0xffffffffu, (seen[2] | seen[3]) != 0u);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            mx[c] = -INFINITY;
+                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 if (!(seen[c] >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
-                                mx[c] = fmaxf(mx[c], __uint_as_float(sv[c][i]));
+                                m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[c][i]));
                             }
+                            mx[c] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                         }
+                    } else {
+                        tmem_wait_ld();
                     }
                     const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const float mrow = mraw * p.scale_log2;
@@ -602,6 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pk[32];
+                        if (c == 1 && !upper) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) pk[i] = 0u;
+                            tmem_st32(tS + 32u * c, pk);
+                            break;
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const int e = 64 * c + 2 * i;
@@ -641,11 +676,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(L::bPFull + t));
             }
 
-            // ---- the item's end.  Each group of a pair ends its own rows; else the
-            // group of the last step adds the other's, whose state it gets through
-            // shared memory, and the other goes on.
-            const int g = pair ? t : (int)(x.step + (uint32_t)n - 1u) & 1;
+            // ---- the item's end.  Each group of a pair ends its own rows; else one
+            // group, in turn, adds the other's, whose state it gets through shared
+            // memory, and the other goes on.
             const bool two = !pair && n > 1;
+            const int g = pair ? t : (int)(two ? k : x.step) & 1;
             const uint32_t o_now = o_ph;
             o_ph ^= pair || two ? 3u : 1u << g;
             if (g != t) {
@@ -675,6 +710,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bar(L::bStEmpty));
             }
             tc_fence_after_sync();
+            if (row == 0 && (!pair || rt == 1)) {  // V of the last steps
+                const uint32_t T = tile0 + (uint32_t)n - 1u;
+                mbar_arrive(bar(L::bVEmpty + T % kV));
+                if (two) mbar_arrive(bar(L::bVEmpty + (T - 1u) % kV));
+            }
             const bool whole = x.t == 0 && n == x.nt;
             const long long part = (long long)blockIdx.x * 2 + (x.t == 0 ? 1 : 0);
             const int prow = 128 * rt + row;
@@ -682,22 +722,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (work) {
                 // O into registers first: the next item's products wait for its place
                 const uint32_t tO = lane_base + L::kColO;
-                float o[D / 32][32];
+                uint32_t ov[D / 32][32];
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t ov[32];
-                    tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov);
-                    if (two) {
+                for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + (uint32_t)(D * t + 32 * c), ov[c]);
+                if (two) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
                         uint32_t o1[32];
                         tmem_ld32(tO + (uint32_t)(D * (t ^ 1) + 32 * c), o1);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[c][i] = fmaf(w0, __uint_as_float(ov[i]), w1 * __uint_as_float(o1[i]));
-                    } else {
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[c][i] = __uint_as_float(ov[i]);
+                        for (int i = 0; i < 32; ++i)
+                            ov[c][i] = __float_as_uint(fmaf(w0, __uint_as_float(ov[c][i]), w1 * __uint_as_float(o1[i])));
                     }
+                } else {
+                    tmem_wait_ld();
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar(L::bOEmpty + t));
@@ -710,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < D / 8; ++i) {
-                            const float* f = &o[i >> 2][8 * (i & 3)];
+                            const float* f = reinterpret_cast<const float*>(&ov[i >> 2][8 * (i & 3)]);
                             dst[i] = make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
                                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
                         }
@@ -719,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float4* at = to;
 #pragma unroll
                         for (int i = 0; i < D / 4; ++i, at += p.rows) {
-                            const float* f = &o[i >> 3][4 * (i & 7)];
+                            const float* f = reinterpret_cast<const float*>(&ov[i >> 3][4 * (i & 7)]);
                             *at = make_float4(f[0], f[1], f[2], f[3]);
                         }
                         parts.stat[part * p.rows + prow] = make_float4(r, l, l_rnd, 0.f);
@@ -903,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t q0 = y->qtile & 1u;
                     const int g = (int)v_step & 1, u0 = u;
 #pragma unroll 1
-                    while (steps - u > 4) {  // the last scores also free Q
+                    while (steps - u > 4) {
                         if (!(ok = step(g, q0, !pair))) break;
                         if (!(ok = step(g ^ 1, pair ? q0 ^ 1u : q0, true))) break;
                     }
@@ -911,40 +950,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                     su += u - u0;
                     continue;
                 }
+                // V, P and the accumulator's place for P.V, K and Q for the scores: what
+                // this step does not need is replaced by what it does
+                const int tv = (int)v_step & 1, ts = (int)s_step & 1;
+                const bool pr = x && x->pair;
+                const int all = !x ? 0 : pr ? 2 * x->n : x->n;
+                const uint32_t qt = !x ? 0u : x->qtile + (pr ? su & 1 : 0), qb = qt & 1u;
+                uint32_t wb[5], wp[5];
+                wb[0] = pv ? bar(L::bVFull + vt.stage) : bar(L::bKFull + kt.stage), wp[0] = pv ? vt.ph : kt.ph;
+                wb[1] = pv ? bar(L::bPFull + tv) : wb[0], wp[1] = pv ? v_step >> 1 & 1u : wp[0];
+                wb[2] = pv && u < 2 ? bar(L::bOEmpty + tv) : wb[0], wp[2] = pv && u < 2 ? oe_ph >> tv & 1u : wp[0];
+                wb[3] = x ? bar(L::bKFull + kt.stage) : wb[0], wp[3] = x ? kt.ph : wp[0];
+                const bool new_q = x && su < (pr ? 2 : 1);
+                wb[4] = new_q ? bar(L::bQFull + qb) : wb[0], wp[4] = new_q ? qt >> 1 & 1u : wp[0];
+                if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait5(wb, wp); }, abort_flag, 95)))) break;
+                tc_fence_after_sync();
+                issued = true;
                 if (pv) {
-                    const int t = (int)v_step & 1;
-                    const bool second = pair && (u & 1);
-                    if (!(ok = wait(L::bVFull + vt.stage, vt.ph, 95))) break;
-                    if (!(ok = wait(L::bPFull + t, v_step >> 1, 96))) break;
-                    if (u < 2) {
-                        if (!(ok = wait(L::bOEmpty + t, oe_ph >> t, 97))) break;
-                        oe_ph ^= 1u << t;
-                    }
-                    tc_fence_after_sync();
-                    mma_pv(t, vt.stage, u >= 2);
-                    if (!pair || second) {
-                        if (u >= steps - 2) commit(L::bVEmpty + vt.stage);  // else the softmax frees it
-                        advance(vt, kV);
-                    }
-                    if (u >= steps - 2) commit(L::bOFull + t);
+                    mma_pv(tv, vt.stage, u >= 2);
+                    if (u >= steps - 2) commit(L::bOFull + tv);
+                    if (u < 2) oe_ph ^= 1u << tv;
+                    if (!pair || (u & 1)) advance(vt, kV);
                     ++v_step;
                     if (++u == steps) {
                         item_done(ky);
                         u = 0;
-                        y = item_here(++ky) ? item(ky) : nullptr;
                     }
                 }
                 if (x) {
-                    const bool pr = x->pair;
-                    const int t = (int)s_step & 1, all = pr ? 2 * x->n : x->n;
-                    const uint32_t qt = x->qtile + (pr ? su & 1 : 0), b = qt & 1u;
-                    if (su < (pr ? 2 : 1) && !(ok = wait(L::bQFull + b, qt >> 1, 93))) break;
-                    if (!(ok = wait(L::bKFull + kt.stage, kt.ph, 94))) break;
-                    tc_fence_after_sync();
-                    mma_s(t, b, kt.stage);
-                    issued = true;
-                    commit(L::bSFull + t);
-                    if (su >= all - (pr ? 2 : 1)) commit(L::bQEmpty + b);
+                    mma_s(ts, qb, kt.stage);
+                    commit(L::bSFull + ts);
                     if (!pr || (su & 1)) advance(kt, kK);
                     ++s_step;
                     if (++su == all) {
@@ -952,6 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x = item_here(++kx) ? item(kx) : nullptr;
                     }
                 }
+                if (pv && u == 0) y = item_here(++ky) ? item(ky) : nullptr;
             }
             if (issued) {
                 commit(L::bDrain);
