@@ -592,29 +592,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_after_sync();
                 if (work) {
-                    uint32_t sv[4][32];
-                    float mx[4];
                     bool upper = true;  // some row sees some of the tile's upper 64 keys
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32u * c, sv[c], mx[c]);
                     if (edge) {
+                        // masked scores become -inf where they lie, 32 keys at a time
+                        // (rolled: a tile's code is long, and few tiles have masked keys)
                         uint32_t seen[4];
                         seen_words(p, x.q, tok, key0, seen);
-                        tmem_wait_ld();
                         upper = __any_sync(0xffffffffu, (seen[2] | seen[3]) != 0u);
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
-                            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            uint32_t v[32];
+                            tmem_ld32(tS + 32u * c, v);
+                            tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                if (!(seen[c] >> i & 1u)) sv[c][i] = __float_as_uint(-INFINITY);
-                                m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(sv[c][i]));
-                            }
-                            mx[c] = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen[0] >> i & 1u)) v[i] = __float_as_uint(-INFINITY);
+                            tmem_st32(tS + 32u * c, v);
+                            seen[0] = seen[1];
+                            seen[1] = seen[2];
+                            seen[2] = seen[3];
                         }
-                    } else {
-                        tmem_wait_ld();
+                        tmem_wait_st();
                     }
+                    uint32_t sv[4][32];
+                    float mx[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32u * c, sv[c], mx[c]);
+                    tmem_wait_ld();
                     const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const float mrow = mraw * p.scale_log2;
                     const float r_new = mrow - r > kTau ? mrow : r;
