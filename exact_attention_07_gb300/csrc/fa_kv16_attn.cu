@@ -46,7 +46,12 @@ constexpr int kBox = 128 * 128;  // bytes of 64 dimensions of 128 rows
 constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds it by 2^8
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAhead = 4;        // items that the list runs ahead
-constexpr int kItemCost = 2;     // what an item costs a block beside its tiles, in tiles
+// What an item costs a block beside its tiles, in tiles, and the least that a
+// block takes.  From sweeps over 1 .. 8 and 1 .. 4: 32 ragged sequences of up to
+// 8192 keys (D = 64) take 25.0, 23.5, 22.3, 22.2, 23.5 us with a cost of 1, 2, 3,
+// 4, 6, 64 such of up to 4096 (D = 128) 37.6, 39.3, 38.6, 40.3, 42.5; one of 777
+// keys 12.0, 12.0, 12.5 with a least of 1, 2, 3.
+constexpr int kItemCost = 3, kLeastShare = 2;
 
 // A block's part of an item.  A sequence has, for every KV head, blocks of up
 // to 2 npt of its query tokens: the items of the list of work.
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ceil(total / blocks), or a little above
         long long share = (long long)((float)total * (1.f / gridDim.x) * 1.000002f + 0.999f);
         share += share * gridDim.x < total;
-        share = max(share, (long long)kItemCost + 1);
+        share = max(share, (long long)kLeastShare);
         const long long first = share * blockIdx.x, last = min(total, first + share);
         if (first < last && first < upto && first >= upto - mine) {
             long long at = upto - mine, cost = own_cost;
