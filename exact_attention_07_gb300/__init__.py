@@ -761,9 +761,12 @@ def _want(t, name, dtype, ndim, device):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # not in a build without CUDA
+
+
 def _on_device(index, fn, *args):
     """fn(*args) with the device current."""
-    if torch._C._cuda_getDevice() == index:
+    if _current_device() == index:
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)
@@ -1194,12 +1197,8 @@ def _check_rows(t, name, ndim, dtype, device):
         raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
 
 
-def _rotary_out(out, x, name, dtype):
-    """`out`, checked, or a new tensor of x's shape."""
-    if out is None:
-        if x.dtype is dtype and x.is_contiguous():
-            return torch.empty_like(x)
-        return torch.empty(x.shape, dtype=dtype, device=x.device)
+def _check_out(out, x, name, dtype):
+    """`out` for the turned rows of x: a contiguous tensor, or x itself."""
     _check_rows(out, name, x.dim(), dtype, x.get_device())
     if out.shape != x.shape:
         raise ValueError(f"{name} must be {tuple(x.shape)}, got {tuple(out.shape)}")
@@ -1208,7 +1207,6 @@ def _rotary_out(out, x, name, dtype):
             raise ValueError(f"{name} in place must have its input's strides {x.stride()}, got {out.stride()}")
     elif not out.is_contiguous():
         raise ValueError(f"{name} must be contiguous, or the input itself")
-    return out
 
 
 def _rows_of(x, y, heads):
@@ -1226,62 +1224,76 @@ def _dense_rows_of(x, y, heads):
     return _pack_rows(x.data_ptr(), y.data_ptr(), a0, a2, a1, b0, b2, b1, heads)
 
 
-def _rope_call(name, q, k, rope, positions, dtype, q_out, k_out):
-    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _ROPE_TYPES and q.dim() in (3, 4) and q.stride(-1) == 1):
-        if not isinstance(q, torch.Tensor):
-            raise TypeError("q must be a torch.Tensor")
-        if q.dim() not in (3, 4):
-            raise ValueError(f"q must be [T, H, D] or [B, H, L, D], got shape {tuple(q.shape)}")
-        if q.dtype not in _ROPE_TYPES:
-            raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
-        if not q.is_cuda:
-            raise ValueError("q must be a CUDA tensor")
-        _check_rows(q, "q", q.dim(), q.dtype, q.get_device())
+def _refuse_rows(q, rope):
+    """Says what is wrong with the q or the rope of a rotary call, if anything is."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q must be [T, H, D] or [B, H, L, D], got shape {tuple(q.shape)}")
+    if q.dtype not in _ROPE_TYPES:
+        raise TypeError(f"q must be bfloat16 or float32, got {q.dtype}")
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    _check_rows(q, "q", q.dim(), q.dtype, q.get_device())
     if not isinstance(rope, RopePlan):
         raise TypeError("rope must be a RopePlan (rope_plan)")
-    device, kind = q.get_device(), q.dtype
+    if rope.device != q.get_device():
+        raise ValueError(f"rope must be on {q.device}, got cuda:{rope.device}")
+    if rope.end > q.shape[-1]:
+        raise ValueError(f"rope turns dimensions {rope.start} to {rope.end} of {q.shape[-1]}")
+
+
+def _rope_call(backward, q, k, rope, positions, dtype, q_out, k_out):
+    if not (isinstance(q, torch.Tensor) and isinstance(rope, RopePlan)):
+        _refuse_rows(q, rope)
+    device, kind, shape = q.get_device(), q.dtype, q.shape
+    if len(shape) == 3:
+        B, (T, Hq, D), dense, pack = 1, shape, False, _rows_of
+    elif len(shape) == 4:
+        (B, Hq, T, D), dense, pack = shape, True, _dense_rows_of
+    else:
+        return _refuse_rows(q, rope)
+    if kind not in _ROPE_TYPES or device < 0 or q.stride(-1) != 1 or rope.device != device or rope.end > D:
+        _refuse_rows(q, rope)
     to = dtype or kind
     if to is not kind and (to not in _ROPE_TYPES or kind is torch.bfloat16):
         raise TypeError(f"rows of {kind} can not become {to}")
-    dense = q.dim() == 4
-    if dense:
-        B, Hq, T, D = q.shape
-    else:
-        B, (T, Hq, D) = 1, q.shape
-    if rope.device != device:
-        raise ValueError(f"rope must be on {q.device}, got cuda:{rope.device}")
-    if rope.end > D:
-        raise ValueError(f"rope turns dimensions {rope.start} to {rope.end} of {D}")
-    pack = _dense_rows_of if dense else _rows_of
     rows_k = None
     if k is not None:
-        if not (isinstance(k, torch.Tensor) and k.dtype is kind and k.dim() == q.dim() and k.get_device() == device
+        if not (isinstance(k, torch.Tensor) and k.dtype is kind and k.get_device() == device and k.dim() == len(shape)
                 and k.stride(-1) == 1):
-            _check_rows(k, "k", q.dim(), kind, device)
+            _check_rows(k, "k", len(shape), kind, device)
         Hk = k.shape[1]
         if k.shape != ((B, Hk, T, D) if dense else (T, Hk, D)):
-            raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
-        k_out = _rotary_out(k_out, k, "k_out", to)
+            raise ValueError(f"shape mismatch: q {tuple(shape)} k {tuple(k.shape)}")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=to, device=k.device)
+        else:
+            _check_out(k_out, k, "k_out", to)
         if Hk:
             rows_k = pack(k, k_out, Hk)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    q_out = _rotary_out(q_out, q, "q_out", to)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=to, device=q.device)
+    else:
+        _check_out(q_out, q, "q_out", to)
     at, step = None, 0
     if positions is not None:
-        shape = positions.shape if isinstance(positions, torch.Tensor) else ()
-        _want(positions, "positions", torch.int32, len(shape) or 1, device)
-        if shape == (B, T) and dense:
+        if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.get_device() == device
+                and positions.is_contiguous()):
+            _want(positions, "positions", torch.int32, positions.dim() if isinstance(positions, torch.Tensor) else 1, device)
+        if positions.shape != (T,):
+            if positions.shape != (B, T) or not dense:
+                raise ValueError(f"positions must be {(T,)}{f' or {(B, T)}' if dense else ''}, got {tuple(positions.shape)}")
             step = T
-        elif shape != (T,):
-            raise ValueError(f"positions must be {(T,)}{f' or {(B, T)}' if dense else ''}, got {tuple(shape)}")
         at = positions.data_ptr() or None
     lib = _lib or load_library()
     fp32 = kind is torch.float32
-    st = _on_device(device, lib.fa_rope if name == "fa_rope" else lib.fa_rope_bwd, pack(q, q_out, Hq), rows_k, B, T, D,
-                    fp32, fp32 and to is kind, rope.packed, at, step, _raw_stream(device))
+    st = _on_device(device, lib.fa_rope_bwd if backward else lib.fa_rope, pack(q, q_out, Hq), rows_k, B, T, D, fp32,
+                    fp32 and to is kind, rope.packed, at, step, _raw_stream(device))
     if st != FA_OK:
-        raise FAError(st, name)
+        raise FAError(st, "fa_rope_bwd" if backward else "fa_rope")
     return q_out, k_out
 
 
@@ -1294,7 +1306,7 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopePlan, positions: 
     ``dtype`` (default: the input's; fp32 rows may become bf16).  q_out may be q itself, and k_out k."""
     if stream is not None:
         return _on_stream(stream, q, fa_rope, q, k, rope, positions, dtype, q_out, k_out)
-    return _rope_call("fa_rope", q, k, rope, positions, dtype, q_out, k_out)
+    return _rope_call(False, q, k, rope, positions, dtype, q_out, k_out)
 
 
 def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, rope: RopePlan, positions: torch.Tensor | None = None,
@@ -1304,7 +1316,7 @@ def fa_rope_bwd(dq: torch.Tensor, dk: torch.Tensor | None, rope: RopePlan, posit
     Arguments as fa_rope.  Returns (dq_out, dk_out)."""
     if stream is not None:
         return _on_stream(stream, dq, fa_rope_bwd, dq, dk, rope, positions, dtype, dq_out, dk_out)
-    return _rope_call("fa_rope_bwd", dq, dk, rope, positions, dtype, dq_out, dk_out)
+    return _rope_call(True, dq, dk, rope, positions, dtype, dq_out, dk_out)
 
 
 def kv16_pool(num_pages: int, Hkv: int, page_size: int, D: int, layers: int | None = None,
@@ -1402,7 +1414,10 @@ def fa_kv16_append(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, p
         Tq, Hq, Dq = q.shape
         if Tq != T or Dq != D:
             raise ValueError(f"shape mismatch: q {tuple(q.shape)} k {tuple(k.shape)}")
-        q_out = _rotary_out(q_out, q, "q_out", bf16)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=bf16, device=q.device)
+        else:
+            _check_out(q_out, q, "q_out", bf16)
         if Hq:
             rows_q = _rows_of(q, q_out, Hq)
     elif q_out is not None:
