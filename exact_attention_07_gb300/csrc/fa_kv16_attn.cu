@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The k-th item; n = 0: no more, or a wait ran out.
     auto item = [&](uint32_t k) -> const Item* { return s_item + k % kAhead; };
     auto item_here = [&](uint32_t k) -> bool {
-        return wait(L::bItemFull + k % kAhead, k / kAhead, 79) && item(k)->n > 0;
+        return (k == 0 || wait(L::bItemFull + k % kAhead, k / kAhead, 79)) && item(k)->n > 0;  // the first: from the start
     };
     auto item_done = [&](uint32_t k) {
         __syncwarp();

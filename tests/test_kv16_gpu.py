@@ -135,6 +135,38 @@ def test_attention_of_many_sequences(B, mode):
     run_attention(lens, new.tolist(), 2, 1, 64, 16, mode, seed=B)
 
 
+def test_attention_of_thousands_of_sequences():
+    """More sequences in every block's share than it looks ahead."""
+    rng = np.random.default_rng(9)
+    new = (rng.random(8000) < 0.9).astype(int)
+    run_attention([int(n + rng.integers(0, 4)) for n in new], new.tolist(), 1, 1, 64, 16, "causal", seed=9)
+
+
+def test_pools_beyond_32_bits():
+    """Rows whose element offsets in the pool pass 2^32: append, attention and keep (in the second of two layers)."""
+    H, Hq, D, P = 8, 8, 128, 256
+    per = 2 * H * P * D
+    pages = (1 << 32) // per + 3
+    pool = torch.empty(2, pages, 2, H, P, D, dtype=torch.bfloat16, device=DEV)
+    one = pool[1]
+    table, lens = i32([[pages - 1, pages - 2, -7]]), i32([300])
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn(300, h, D, generator=g).bfloat16().to(DEV) for h in (Hq, H, H))
+    for layer in pool:
+        fa.fa_kv16_append(k, v, i32([0, 300]), layer, table, lens)
+    o, lse = fa.fa_fwd_kv16(q[-5:], i32([0, 5]), one, table, lens, causal=True)
+    fa.fa_check()
+    ro, rl, mag = kv16.attention(f64(q[-5:]), f64(k), f64(v), D ** -0.5, visible("causal", 5))
+    to, tl = kv16.attention_tolerance(f64(q[-5:]), f64(k), D ** -0.5, ro, rl, mag)
+    assert (np.abs(f64(o) - ro) <= to).all() and np.abs(f64(lse) - rl).max() <= tl
+    fa.fa_kv16_keep(i32([1, 3, 4, 0, 0]), i32([3]), i32([0, 5]), pool, table, lens)
+    fa.fa_check()
+    for layer in pool:
+        got = torch.cat([layer[pages - 1, :, :, :], layer[pages - 2, :, :, :44]], 2)[:, :, 295:300]
+        want = torch.stack([k[[296, 298, 299, 298, 299]], v[[296, 298, 299, 298, 299]]]).transpose(1, 2)
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("mode", ["causal", "tree"])
 def test_attention_with_sharp_scores(mode):
     """Scores of tens: rows that one key dominates, references that move many times."""
