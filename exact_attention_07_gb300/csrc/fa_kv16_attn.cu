@@ -47,11 +47,18 @@ constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds i
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAhead = 4;        // items that the list runs ahead
 // What an item costs a block beside its tiles, in tiles, and the least that a
-// block takes.  From sweeps over 1 .. 8 and 1 .. 4: 32 ragged sequences of up to
-// 8192 keys (D = 64) take 25.0, 23.5, 22.3, 22.2, 23.5 us with a cost of 1, 2, 3,
-// 4, 6, 64 such of up to 4096 (D = 128) 37.6, 39.3, 38.6, 40.3, 42.5; one of 777
-// keys 12.0, 12.0, 12.5 with a least of 1, 2, 3.
-constexpr int kItemCost = 3, kLeastShare = 2;
+// block takes.  From sweeps of 0 .. 8 each: with one tile of rows and D = 128, 64
+// sequences of 1 .. 4096 keys (8 heads) take 45.8, 37.8, 39.4, 38.6, 40.0 us with
+// a cost of 0 .. 4; D = 64, 32 sequences of 1 .. 8192 keys (4 heads) 25.0, 23.4,
+// 22.2, 21.7 with 1 .. 4 and 64 of 1 .. 4096 (8 heads) 31.7, 30.6, 32.1 with 2 .. 4;
+// with two tiles of rows, 8 sequences of 32768 202.3, 200.5, 200.0 with 3 .. 5.  One
+// sequence of 777 keys takes 12.0, 12.0, 12.5 us with a least share of 1, 2, 3.
+template <int D>
+__host__ __device__ constexpr int item_cost(bool pair)
+{
+    return pair ? 5 : D == 64 ? 3 : 1;
+}
+constexpr int kLeastShare = 2;
 
 // A block's part of an item.  A sequence has, for every KV head, blocks of up
 // to 2 npt of its query tokens: the items of the list of work.
@@ -244,15 +251,22 @@ __device__ __forceinline__ int tiles_of(const Kv16AttnParams& p, const Kv16Seq& 
     return (keys + kTile - 1) / kTile;
 }
 
-// Length in the list of one KV head of a sequence: its items' tiles, and
-// kItemCost in front of each item.
+template <int D>
+__device__ __forceinline__ int item_cost(const Kv16AttnParams& p, const Kv16Seq& q, int rb)
+{
+    return item_cost<D>(q.n - rb * 2 * p.npt > p.npt);
+}
+
+// Length in the list of one KV head of a sequence: its items' tiles, and what
+// each item costs in front of them.
+template <int D>
 __device__ __forceinline__ long long head_cost(const Kv16AttnParams& p, const Kv16Seq& q)
 {
     const int nb = row_blocks(p, q.n);
-    if (!p.causal || nb <= 1) return (long long)nb * (kItemCost + tiles_of(p, q, 0));
     long long sum = 0;
+    if (!p.causal && nb > 1) sum = (long long)(nb - 1) * (item_cost<D>(true) + tiles_of(p, q, 0));
 #pragma unroll 1
-    for (int rb = 0; rb < nb; ++rb) sum += kItemCost + tiles_of(p, q, rb);
+    for (int rb = p.causal || nb == 0 ? 0 : nb - 1; rb < nb; ++rb) sum += item_cost<D>(p, q, rb) + tiles_of(p, q, rb);
     return sum;
 }
 
@@ -269,6 +283,7 @@ __device__ __forceinline__ void open_item(const Kv16AttnParams& p, Item& x)
 
 // The block's part of the next item; n = 0 at the end of its share.  All lanes
 // of a warp compute it alike.
+template <int D>
 __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, Window& w, int lane)
 {
     x.step += x.pair ? 2 * x.n : x.n;
@@ -289,7 +304,7 @@ __device__ __forceinline__ void next_item(const Kv16AttnParams& p, Item& x, Wind
         }
     }
     open_item(p, x);
-    x.left -= kItemCost;
+    x.left -= item_cost<D>(x.pair);
     x.t = 0;
     x.n = (int)max(0ll, min(x.left, (long long)x.nt));
 }
@@ -454,11 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long mine = 0, own_cost = 0;
     if (run0 < run1) {
         own = open_sequence(p, run0);
-        own_cost = head_cost(p, own);
+        own_cost = head_cost<D>(p, own);
         mine = p.c.Hkv * own_cost;
     }
 #pragma unroll 1
-    for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost(p, open_sequence(p, s));
+    for (int s = run0 + 1; s < run1; ++s) mine += p.c.Hkv * head_cost<D>(p, open_sequence(p, s));
 
     {
         long long upto = mine;
@@ -489,17 +504,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             while (at + cost * p.c.Hkv <= first) {
                 at += cost * p.c.Hkv;
                 x.q = open_sequence(p, ++x.s);
-                cost = head_cost(p, x.q);
+                cost = head_cost<D>(p, x.q);
             }
             x.blocks = row_blocks(p, x.q.n);
 #pragma unroll 1
             for (x.h = 0; at + cost <= first; ++x.h) at += cost;
             int one;
 #pragma unroll 1
-            for (x.rb = 0; at + (one = kItemCost + tiles_of(p, x.q, x.rb)) <= first; ++x.rb) at += one;
+            for (x.rb = 0; at + (one = item_cost<D>(p, x.q, x.rb) + tiles_of(p, x.q, x.rb)) <= first; ++x.rb) at += one;
             open_item(p, x);
             x.left = last - first;
-            const long long t = first - at - kItemCost;
+            const long long t = first - at - item_cost<D>(x.pair);
             if (t < 0) x.left += t;
             x.t = t < 0 ? 0 : (int)t;
             x.n = (int)min(x.left, (long long)(x.nt - x.t));
@@ -1011,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             window.base = INT_MIN;  // filled when the first sequence ends
 #pragma unroll 1
             for (uint32_t k = 1; y.n > 0; ++k) {
-                next_item(p, y, window, lane);
+                next_item<D>(p, y, window, lane);
                 if (!wait(L::bItemEmpty + k % kAhead, (k / kAhead) ^ 1u, 78)) break;
                 if (lane == 0) {
                     s_item[k % kAhead] = y;
