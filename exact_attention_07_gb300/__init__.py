@@ -1354,21 +1354,32 @@ def draft_mask(parents, cu_seqlens) -> tuple[torch.Tensor, torch.Tensor]:
 def _kv16(pool, table, seq_lens, seq_ids, cu_seqlens, layers=False):
     """Checks the cache of a call and its packed sequences.  Returns (fa_kv16_t as bytes, device index, sequences, Hkv,
     D)."""
-    device = pool.get_device() if isinstance(pool, torch.Tensor) else -1
-    ndim = 6 if layers and isinstance(pool, torch.Tensor) and pool.dim() == 6 else 5
-    if not (device >= 0 and pool.dtype is torch.bfloat16 and pool.dim() == ndim and pool.is_contiguous()):
-        _check_tensor(pool, "pool", torch.bfloat16, ndim)
-    if not (isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dtype is torch.int32 and cu_seqlens.dim() == 1
+    if not (isinstance(pool, torch.Tensor) and isinstance(table, torch.Tensor) and isinstance(seq_lens, torch.Tensor)
+            and isinstance(cu_seqlens, torch.Tensor)):
+        for t, name in ((pool, "pool"), (table, "table"), (seq_lens, "seq_lens"), (cu_seqlens, "cu_seqlens")):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+    device, shape, i32 = pool.get_device(), pool.shape, torch.int32
+    if not (device >= 0 and pool.dtype is torch.bfloat16 and (len(shape) == 5 or len(shape) == 6 and layers)
+            and pool.is_contiguous() and table.dtype is i32 and table.dim() == 2 and table.get_device() == device
+            and table.is_contiguous() and seq_lens.dtype is i32 and seq_lens.dim() == 1 and seq_lens.get_device() == device
+            and seq_lens.is_contiguous() and cu_seqlens.dtype is i32 and cu_seqlens.dim() == 1
             and cu_seqlens.get_device() == device and cu_seqlens.is_contiguous()):
-        _want(cu_seqlens, "cu_seqlens", torch.int32, 1, device)
-    n = _num_seqs(cu_seqlens)
-    slots, width = _slots_of(table, seq_lens, device)
-    N, two, H, P, D = pool.shape[-5:] if layers else pool.shape
+        _check_tensor(pool, "pool", torch.bfloat16, 6 if layers and len(shape) == 6 else 5)
+        _check_slots(table, seq_lens, device)
+        _want(cu_seqlens, "cu_seqlens", i32, 1, device)
+    n = cu_seqlens.shape[0] - 1
+    slots, width = table.shape
+    N, two, H, P, D = shape[-5:] if layers else shape
     if two != 2 or P not in (16, 32, 64, 128, 256) or D not in (64, 128):
-        raise ValueError(f"pool must be bfloat16 [..., pages, 2, Hkv, page_size, D], got {tuple(pool.shape)}")
+        raise ValueError(f"pool must be bfloat16 [..., pages, 2, Hkv, page_size, D], got {tuple(shape)}")
+    if n < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 >= 2 offsets")
+    if seq_lens.shape[0] != slots:
+        raise ValueError(f"table has {slots} slots and seq_lens {seq_lens.shape[0]}")
     ids = 0
     if seq_ids is not None:
-        _want(seq_ids, "seq_ids", torch.int32, 1, device)
+        _want(seq_ids, "seq_ids", i32, 1, device)
         if seq_ids.shape[0] != n:
             raise ValueError(f"seq_ids must name {n} slots")
         ids = seq_ids.data_ptr()

@@ -1068,6 +1068,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
     const int prow = 32 * blockIdx.y + lane;
     float4 st[U], o[U][V];
     auto load = [&](int u, int k) {
+        if (prow >= p.rows) return;
         const long long part = (long long)min(blockIdx.x + k, gridDim.x - 1) * 2 + (k == 0 ? 1 : 0);
         st[u] = parts.stat[part * p.rows + prow];
 #pragma unroll
@@ -1144,7 +1145,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& kv, const Kv16AttnPa
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)(p.rows / 32));
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)((p.rows + 31) / 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = &attr;
@@ -1158,7 +1159,7 @@ int kv16_attn_rows(long long T, int group)
 {
     const long long rows = T * group;  // of one sequence, at most
     if (rows > 128 / group * group) return 256;
-    return (int)((rows + 31) / 32 * 32);
+    return (int)((rows + 3) / 4 * 4);
 }
 
 size_t kv16_attn_workspace(int D, int rows, int num_sms)
