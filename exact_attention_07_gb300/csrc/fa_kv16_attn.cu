@@ -1052,8 +1052,9 @@ done:
 }
 
 // Joins the parts of the item that begins in block blockIdx.x and ends in a
-// later one: 32 rows a block (blockIdx.y), a lane a row, a warp every eighth
-// run of four columns.
+// later one: 32 rows a block (blockIdx.y), a warp every eighth run of four
+// columns.  A lane takes a row, or, where there are at most 4, 8 or 16 rows, every
+// eighth, fourth or second of its parts; the lanes of a row are added at the end.
 constexpr int kJoinThreads = 256;
 
 template <int D>
@@ -1064,71 +1065,85 @@ __global__ void __launch_bounds__(kJoinThreads) fa_kv16_join_kernel(const Kv16At
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Parts parts = parts_of(p.part, gridDim.x, p.rows);
     wait_for_primary();
-    // the first parts are asked for together with the record that says whether there are any
-    const int prow = 32 * blockIdx.y + lane;
-    float4 st[U], o[U][V];
-    auto load = [&](int u, int k) {
-        if (prow >= p.rows) return;
-        const long long part = (long long)min(blockIdx.x + k, gridDim.x - 1) * 2 + (k == 0 ? 1 : 0);
-        st[u] = parts.stat[part * p.rows + prow];
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[u][i] = parts.o[(part * (D / 4) + warp + 8 * i) * p.rows + prow];
-    };
-#pragma unroll
-    for (int u = 0; u < 2; ++u) load(u, u);
     const Cut cut = parts.join[blockIdx.x];
     const int rt = cut.ntok > p.npt ? (int)blockIdx.y >> 2 : 0;  // tile of rows
-    const int row = prow - 128 * rt;
-    const int rows_t = min(p.npt, cut.ntok - rt * p.npt) * p.group;
-    if (cut.parts == 0 || row - lane >= rows_t) return;
-    const bool valid = row < rows_t;
+    const int row0 = 32 * (int)blockIdx.y - 128 * rt;
+    const int nrows = min(32, min(p.npt, cut.ntok - rt * p.npt) * p.group - row0);
+    if (cut.parts == 0 || nrows <= 0) return;
+    const int shift = nrows <= 4 ? 2 : nrows <= 8 ? 3 : nrows <= 16 ? 4 : 5, lanes = 32 >> shift;
+    const int sub = lane & ((1 << shift) - 1), mine = lane >> shift;
     float r = -INFINITY, l = 0.f, l_o = 0.f;
     float4 acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (valid)
-        for (int k0 = 0; k0 < cut.parts; k0 += U) {
+    const auto times = [](float w, float4 a) { return make_float4(w * a.x, w * a.y, w * a.z, w * a.w); };
+    const auto plus = [](float w, float4 a, float4 b) {
+        return make_float4(fmaf(w, a.x, b.x), fmaf(w, a.y, b.y), fmaf(w, a.z, b.z), fmaf(w, a.w, b.w));
+    };
+    if (sub < nrows) {
+        const int prow = 32 * blockIdx.y + sub;
+#pragma unroll 1
+        for (int k0 = mine; k0 < cut.parts; k0 += U * lanes) {
+            float4 st[U], o[U][V];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if ((k0 > 0 || u >= 2) && k0 + u < cut.parts) load(u, k0 + u);
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + u * lanes;
+                if (k < cut.parts) {
+                    const long long part = (long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0);
+                    st[u] = parts.stat[part * p.rows + prow];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) o[u][i] = parts.o[(part * (D / 4) + warp + 8 * i) * p.rows + prow];
+                }
+            }
             float top = r;
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (k0 + u < cut.parts) top = fmaxf(top, st[u].x);
+                if (k0 + u * lanes < cut.parts) top = fmaxf(top, st[u].x);
             const float m = top == -INFINITY ? 0.f : top, down = ex2_approx(r - m);
             r = top;
             l *= down;
             l_o *= down;
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = make_float4(acc[i].x * down, acc[i].y * down, acc[i].z * down, acc[i].w * down);
+            for (int i = 0; i < V; ++i) acc[i] = times(down, acc[i]);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (k0 + u < cut.parts) {
+                if (k0 + u * lanes < cut.parts) {
                     const float w = ex2_approx(st[u].x - m);
                     l = fmaf(w, st[u].y, l);
                     l_o = fmaf(w, st[u].y + st[u].z, l_o);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        acc[i].x = fmaf(w, o[u][i].x, acc[i].x);
-                        acc[i].y = fmaf(w, o[u][i].y, acc[i].y);
-                        acc[i].z = fmaf(w, o[u][i].z, acc[i].z);
-                        acc[i].w = fmaf(w, o[u][i].w, acc[i].w);
-                    }
+                    for (int i = 0; i < V; ++i) acc[i] = plus(w, o[u][i], acc[i]);
                 }
         }
-    const float inv = l > 0.f || l != l ? 1.f / l_o : 0.f;
+    }
+#pragma unroll 1
+    for (int off = 1 << shift; off < 32; off <<= 1) {
+        const auto other = [&](float x) { return __shfl_xor_sync(~0u, x, off); };
+        const float r1 = other(r), top = fmaxf(r, r1), m = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2_approx(r - m), w1 = ex2_approx(r1 - m);
+        r = top;
+        l = fmaf(w1, other(l), w0 * l);
+        l_o = fmaf(w1, other(l_o), w0 * l_o);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        *reinterpret_cast<uint2*>(&s_o[lane][4 * (warp + 8 * i)]) =
-            make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+        for (int i = 0; i < V; ++i)
+            acc[i] = plus(w1, make_float4(other(acc[i].x), other(acc[i].y), other(acc[i].z), other(acc[i].w)), times(w0, acc[i]));
+    }
     const int token0 = cut.token + rt * p.npt, head0 = cut.h * p.group;
-    if (valid && warp == 0)
-        p.lse[(long long)(head0 + row % p.group) * p.T + token0 + row / p.group] = l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
+    if (mine == 0) {
+        const float inv = l > 0.f || l != l ? 1.f / l_o : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            *reinterpret_cast<uint2*>(&s_o[sub][4 * (warp + 8 * i)]) =
+                make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+        const int row = row0 + sub;
+        if (warp == 0 && sub < nrows)
+            p.lse[(long long)(head0 + row % p.group) * p.T + token0 + row / p.group] =
+                l == 0.f ? -INFINITY : (r + __log2f(l)) * kLn2;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 32 * (D / 8); i += kJoinThreads) {
-        const int rr = i / (D / 8), c = i % (D / 8), at = row - lane + rr;
-        if (at >= rows_t) break;
-        const long long to = (long long)(token0 + at / p.group) * p.Hq + head0 + at % p.group;
+    for (int i = threadIdx.x; i < nrows * (D / 8); i += kJoinThreads) {
+        const int rr = i / (D / 8), c = i % (D / 8), row = row0 + rr;
+        const long long to = (long long)(token0 + row / p.group) * p.Hq + head0 + row % p.group;
         reinterpret_cast<uint4*>(p.o + to * D)[c] = *reinterpret_cast<const uint4*>(&s_o[rr][8 * c]);
     }
 }
