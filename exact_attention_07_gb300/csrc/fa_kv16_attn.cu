@@ -117,24 +117,22 @@ __device__ __forceinline__ void mma_ts_low(uint32_t d, uint32_t a, uint32_t b, u
         : "memory");
 }
 
-// Five and three barrier phases tested by one thread back to back; true when all have completed.
-__device__ __forceinline__ bool mbar_try_wait5(const uint32_t (&b)[5], const uint32_t (&p)[5])
+// Four and three barrier phases tested by one thread back to back; true when all have completed.
+__device__ __forceinline__ bool mbar_try_wait4(const uint32_t (&b)[4], const uint32_t (&p)[4])
 {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred q0, q1, q2, q3, q4;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 q0, [%1], %6;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 q1, [%2], %7;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 q2, [%3], %8;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 q3, [%4], %9;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 q4, [%5], %10;\n\t"
+        "{\n\t.reg .pred q0, q1, q2, q3;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q0, [%1], %5;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q1, [%2], %6;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q2, [%3], %7;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q3, [%4], %8;\n\t"
         "and.pred q0, q0, q1;\n\t"
         "and.pred q2, q2, q3;\n\t"
-        "and.pred q0, q0, q4;\n\t"
         "and.pred q0, q0, q2;\n\t"
         "selp.u32 %0, 1, 0, q0;\n\t}\n"
         : "=r"(ok)
-        : "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4])
+        : "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3])
         : "memory");
     return ok != 0;
 }
@@ -974,24 +972,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     su += u - u0;
                     continue;
                 }
-                // V, P and the accumulator's place for P.V, K and Q for the scores: what
-                // this step does not need is replaced by what it does
+                // V, P and the accumulator's place for P.V, K and Q for the scores.  They are
+                // tested together only within an item: the next item's K and Q can wait for
+                // places that the softmax groups free after this P.V (the end of an item
+                // needs it, and a pair's two Q tiles need both buffers), so P.V never waits
+                // for them.
                 const int tv = (int)v_step & 1, ts = (int)s_step & 1;
                 const bool pr = x && x->pair;
                 const int all = !x ? 0 : pr ? 2 * x->n : x->n;
                 const uint32_t qt = !x ? 0u : x->qtile + (pr ? su & 1 : 0), qb = qt & 1u;
-                uint32_t wb[5], wp[5];
-                wb[0] = pv ? bar(L::bVFull + vt.stage) : bar(L::bKFull + kt.stage), wp[0] = pv ? vt.ph : kt.ph;
-                wb[1] = pv ? bar(L::bPFull + tv) : wb[0], wp[1] = pv ? v_step >> 1 & 1u : wp[0];
-                wb[2] = pv && u < 2 ? bar(L::bOEmpty + tv) : wb[0], wp[2] = pv && u < 2 ? oe_ph >> tv & 1u : wp[0];
-                wb[3] = x ? bar(L::bKFull + kt.stage) : wb[0], wp[3] = x ? kt.ph : wp[0];
-                const bool new_q = x && su < (pr ? 2 : 1);
-                wb[4] = new_q ? bar(L::bQFull + qb) : wb[0], wp[4] = new_q ? qt >> 1 & 1u : wp[0];
-                if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait5(wb, wp); }, abort_flag, 95)))) break;
-                tc_fence_after_sync();
-                issued = true;
+                const bool new_q = x && su < (pr ? 2 : 1), together = pv && x == y && !new_q;
+                const uint32_t bk = bar(L::bKFull + kt.stage);
                 if (pv) {
+                    // what this step does not need is replaced by what it does
+                    uint32_t wb[4], wp[4];
+                    wb[0] = bar(L::bVFull + vt.stage), wp[0] = vt.ph;
+                    wb[1] = bar(L::bPFull + tv), wp[1] = v_step >> 1 & 1u;
+                    wb[2] = u < 2 ? bar(L::bOEmpty + tv) : wb[0], wp[2] = u < 2 ? oe_ph >> tv & 1u : wp[0];
+                    wb[3] = together ? bk : wb[0], wp[3] = together ? kt.ph : wp[0];
+                    if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait4(wb, wp); }, abort_flag, 95)))) break;
+                    tc_fence_after_sync();
                     mma_pv(tv, vt.stage, u >= 2);
+                    issued = true;
                     if (u >= steps - 2) commit(L::bOFull + tv);
                     if (u < 2) oe_ph ^= 1u << tv;
                     if (!pair || (u & 1)) advance(vt, kV);
@@ -1001,8 +1003,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u = 0;
                     }
                 }
+                if (x && !together) {
+                    const uint32_t bq = new_q ? bar(L::bQFull + qb) : bk, pq = new_q ? qt >> 1 & 1u : kt.ph;
+                    if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait3(bk, kt.ph, bq, pq, bk, kt.ph); },
+                                                                abort_flag, 96))))
+                        break;
+                    tc_fence_after_sync();
+                }
                 if (x) {
                     mma_s(ts, qb, kt.stage);
+                    issued = true;
                     commit(L::bSFull + ts);
                     if (!pr || (su & 1)) advance(kt, kK);
                     ++s_step;

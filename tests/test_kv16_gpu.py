@@ -135,6 +135,17 @@ def test_attention_of_many_sequences(B, mode):
     run_attention(lens, new.tolist(), 2, 1, 64, 16, mode, seed=B)
 
 
+@pytest.mark.parametrize("D,mode,top", [(128, "tree", 40), (64, "causal", 24), (128, "full", 1), (64, "tree", 6)])
+def test_attention_of_mixed_sequences(D, mode, top):
+    """Blocks whose shares mix items of one and two tiles of rows, short ones and long ones, alone and cut."""
+    rng = np.random.default_rng(D + top)
+    B = 330
+    new = rng.integers(0, top + 1, B)
+    lens = [int(n + rng.choice([0, rng.integers(0, 130), rng.integers(0, 700), rng.integers(900, 2500)], p=[.1, .5, .3, .1]))
+            for n in new]
+    run_attention(lens, new.tolist(), 8, 1, D, 32, mode, seed=D + top)
+
+
 def test_attention_of_thousands_of_sequences():
     """More sequences in every block's share than it looks ahead."""
     rng = np.random.default_rng(9)
