@@ -761,12 +761,9 @@ def _want(t, name, dtype, ndim, device):
         raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
 
 
-_current_device = getattr(torch._C, "_cuda_getDevice", None)  # not in a build without CUDA
-
-
 def _on_device(index, fn, *args):
     """fn(*args) with the device current."""
-    if _current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         return fn(*args)
     with torch.cuda.device(index):
         return fn(*args)
