@@ -93,6 +93,15 @@ constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
 
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
 
+// One lane of the warp, always the same.  A branch on it costs its body some ten
+// percent less code than one on a lane number: operands stay warp-uniform.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(e));
+    return e != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem] and A[tmem] * B[smem] (kind::f16, bf16)
 __device__ __forceinline__ void mma_ss_low(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
 {
@@ -884,10 +893,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (armed >> s & 1u) mbar_settle(bar(full + s), par >> s & 1u, wf, 92);
         } else if (warp == 9) {
             // ============================================================ MMA issuer
-            // The whole warp runs this loop; lane 0 issues every MMA and commit (a
+            // The whole warp runs this loop; one lane issues every MMA and commit (a
             // commit tracks the MMAs of the thread that executes it).
             constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false), kIdescPV = idesc_bf16_f32(128, D, true);
-            const bool leader = lane == 0;
+            const bool leader = elect_one();
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
             auto commit = [&](int b) {
                 if (leader) tc_commit(bar(b));
