@@ -237,13 +237,19 @@ struct Smem {
     static constexpr int kBars = kStats + 3 * 128 * 4;
     static constexpr int bQFull = 0, bQEmpty = 2, bSFull = 4, bPFull = 6, bOFull = 8, bOEmpty = 10, bStFull = 12,
                          bStEmpty = 13, bDrain = 14, bItemFull = 15, bItemEmpty = bItemFull + kAhead, bKFull = bItemEmpty + kAhead,
-                         bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV, kNumBars = bVEmpty + kV;
+                         bKEmpty = bKFull + kK, bVFull = bKEmpty + kK, bVEmpty = bVFull + kV,
+                         bSRead = bVEmpty + kV, bPvDone = bSRead + 2, kNumBars = bPvDone + 2;  // the last two: kOwnP
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory base, abort flag, poison flag
     static constexpr int kSums = kMisc + 16;            // long long [kWarps], and the blocks' share
     static constexpr int kItems = kSums + (kWarps + 1) * 8;  // Item [kAhead]
     static constexpr int kBytes = kItems + kAhead * (int)sizeof(Item);
     static_assert(kBytes <= 232448 && kBars % 8 == 0, "shared memory of one block");
-    static constexpr uint32_t kColS = 0, kColO = 256;  // [2] of 128 columns, [2] of D
+    // [2] of 128 columns, [2] of D.  P of D = 64 has [2] of 64 columns of its own, so
+    // that a group's next scores need not wait for its P.V; else it lies over the scores.
+    static constexpr bool kOwnP = D == 64;
+    static constexpr uint32_t kColS = 0, kColO = 256, kColP = kOwnP ? kColO + 2 * D : kColS;
+    static constexpr uint32_t kPitchP = kOwnP ? 64 : 128;
+    static constexpr int kLead = kOwnP ? 3 : 2;  // steps that the scores run ahead of P.V within an item
 };
 
 __device__ __forceinline__ int row_blocks(const Kv16AttnParams& p, int n)
@@ -448,6 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(L::bPFull + t), 128);
             mbar_init(bar(L::bOFull + t), 1);
             mbar_init(bar(L::bOEmpty + t), 128);
+            mbar_init(bar(L::bSRead + t), 4);
+            mbar_init(bar(L::bPvDone + t), 1);
         }
         mbar_init(bar(L::bStFull), 128);
         mbar_init(bar(L::bStEmpty), 128);
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         regs_increase<208>();
         const int t = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t tS = lane_base + L::kColS + (uint32_t)(128 * t);
+        const uint32_t tS = lane_base + L::kColS + (uint32_t)(128 * t), tP = lane_base + L::kColP + L::kPitchP * (uint32_t)t;
         uint32_t st_ph = 0, o_ph = 0;  // o_ph: a bit per stream
         const int tok_row = row / p.group, head_row = row - tok_row * p.group;
 #pragma unroll 1
@@ -607,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
                 // These scores are complete, and so is all that was issued before
                 // them: K(j) is no longer read (of a pair: when they are the second
-                // of the tile), V of the step two before neither, and the tile of
-                // rows when they are its last.
+                // of the tile), V of the step two before neither (unless kOwnP), and
+                // the tile of rows when they are its last.
                 if (row == 0) {
                     const uint32_t T = tile0 + (uint32_t)j;
                     if (!pair || rt == 1) {
                         mbar_arrive(bar(L::bKEmpty + T % kK));
-                        if (j >= dj) mbar_arrive(bar(L::bVEmpty + (T - dj) % kV));
+                        if (!L::kOwnP && j >= dj) mbar_arrive(bar(L::bVEmpty + (T - dj) % kV));
                     }
                     if (j == n - 1) mbar_arrive(bar(L::bQEmpty + (int)((x.qtile + rt) & 1u)));
                 }
@@ -646,6 +654,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32_max(tS + 32u * c, sv[c], mx[c]);
                     tmem_wait_ld();
+                    if (L::kOwnP) {  // the next scores may come
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::bSRead + t));
+                    }
                     const float mraw = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                     const float mrow = mraw * p.scale_log2;
                     const float r_new = mrow - r > kTau ? mrow : r;
@@ -665,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (c == 1 && !upper) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) pk[i] = 0u;
-                            tmem_st32(tS + 32u * c, pk);
+                            tmem_st32(tP + 32u * c, pk);
                             break;
                         }
 #pragma unroll
@@ -680,14 +693,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
                             pk[i] = pack_bf16x2(e0, e1);
                         }
-                        tmem_st32(tS + 32u * c, pk);
+                        if (L::kOwnP && c == 0) {
+                            // the group's P.V before this one has read P and left O
+                            if (!wait(L::bPvDone + t, s_ph ^ 1u, 83)) goto done;
+                            tc_fence_after_sync();
+                            if (row == 0 && j >= dj && (!pair || rt == 1))
+                                mbar_arrive(bar(L::bVEmpty + (tile0 + (uint32_t)(j - dj)) % kV));
+                        }
+                        tmem_st32(tP + 32u * c, pk);
                     }
                     float a0, a1;
                     f2_unpack(f2_add(sum[0], sum[1]), a0, a1);
                     l = fmaf(l, alpha, a0 + a1);
                     const float pm = ex2_approx(fmaf(mraw, p.scale_log2, -r_use));
                     l_rnd = fmaf(l_rnd, alpha, __uint_as_float(pack_bf16x2(pm, 0.f) << 16) - pm);
-                    // the group's last P.V was complete before these scores were: O is idle
+                    // the group's last P.V is complete: O is idle
                     if (j != j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                         const uint32_t tO = lane_base + L::kColO + (uint32_t)(D * t);
 #pragma unroll 1
@@ -702,6 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     r = r_new;
                     tmem_wait_st();
+                } else if (L::kOwnP) {
+                    // a warp without rows keeps step: it must not arrive for two steps at once
+                    if (lane == 0) mbar_arrive(bar(L::bSRead + t));
+                    if (!wait(L::bPvDone + t, s_ph ^ 1u, 83)) goto done;
                 }
                 tc_fence_before_sync();
                 mbar_arrive(bar(L::bPFull + t));
@@ -919,7 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto mma_pv = [&](int t, uint32_t stage, bool acc) {
                 const uint32_t vd = uniform(desc_low(sb + L::kVRing + stage * L::kTileBytes, kBox));
-                const uint32_t d = uniform(tm + L::kColO + (uint32_t)(D * t)), pa = uniform(tm + L::kColS + (uint32_t)(128 * t));
+                const uint32_t d = uniform(tm + L::kColO + (uint32_t)(D * t)), pa = uniform(tm + L::kColP + L::kPitchP * (uint32_t)t);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
@@ -936,46 +960,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     s.ph ^= 1u;
                 }
             };
-            // The next scores, up to two steps ahead of the next P.V: item kx, step su
-            // of it; v_step and s_step count the steps, whose streams alternate.
+            // The next scores are step su of item kx, up to kLead steps ahead of the next
+            // P.V: two over the ends of items.  v_step and s_step count the steps, whose
+            // streams alternate.
             uint32_t kx = 0, ky = 0, s_step = 0, v_step = 0, oe_ph = 3;
             int su = 0, u = 0;
             bool issued = false, ok = true;
             const Item *x = item_here(0) ? item(0) : nullptr, *y = x;
 #pragma unroll 1
             while (y && ok) {
-                const bool pv = s_step - v_step == 2 || !x;  // else: the first scores
+                const bool pr = x && x->pair;
+                const bool new_q = x && su < (pr ? 2 : 1), same = x == y && !new_q;
+                const uint32_t ahead = s_step - v_step;
+                const bool pv = !x || ahead >= (same ? L::kLead : 2u);
+                const bool sc = x && (same || ahead <= 2u);
                 const bool pair = y->pair;
                 const int steps = pair ? 2 * y->n : y->n;
-                if (pv && x == y && u >= 2 && steps - u > 4) {
+                if (pv && same && u >= 2 && steps - u > L::kLead + 2) {
                     // In the middle of an item.  A wait or a commit of this warp idles the
-                    // tensor core for some 100 cycles, so a step takes one of each: V, K of
-                    // the step two ahead and P are tested at once, and the softmax groups
-                    // free the stages.
-                    auto step = [&](int g, uint32_t q, bool last_of_tile) -> bool {
-                        const uint32_t b0 = bar(L::bVFull + vt.stage), b1 = bar(L::bKFull + kt.stage), b2 = bar(L::bPFull + g);
-                        const uint32_t p2 = v_step >> 1 & 1u;
-                        if (!__all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait3(b0, vt.ph, b1, kt.ph, b2, p2); },
+                    // tensor core for some 100 cycles, so a step tests V, P and what the
+                    // scores kLead steps ahead need at once, and the softmax groups free
+                    // the stages.
+                    auto step = [&](int g, uint32_t q, bool k_done, bool v_done) -> bool {
+                        const int gs = L::kOwnP ? g ^ 1 : g;
+                        uint32_t wb[4], wp[4];
+                        wb[0] = bar(L::bVFull + vt.stage), wp[0] = vt.ph;
+                        wb[1] = bar(L::bKFull + kt.stage), wp[1] = kt.ph;
+                        wb[2] = bar(L::bPFull + g), wp[2] = v_step >> 1 & 1u;
+                        wb[3] = bar(L::bSRead + gs), wp[3] = (v_step + 1u) >> 1 & 1u;
+                        if (!__all_sync(0xffffffffu, wait_for([&]() {
+                                            return L::kOwnP ? mbar_try_wait4(wb, wp)
+                                                            : mbar_try_wait3(wb[0], wp[0], wb[1], wp[1], wb[2], wp[2]);
+                                        },
                                                               abort_flag, 94)))
                             return false;
                         tc_fence_after_sync();
                         mma_pv(g, vt.stage, true);
-                        mma_s(g, q, kt.stage);
-                        commit(L::bSFull + g);
+                        if (L::kOwnP) commit(L::bPvDone + g);
+                        mma_s(gs, q, kt.stage);
+                        commit(L::bSFull + gs);
                         ++v_step;
                         ++u;
-                        if (last_of_tile) {
-                            advance(kt, kK);
-                            advance(vt, kV);
-                        }
+                        if (k_done) advance(kt, kK);
+                        if (v_done) advance(vt, kV);
                         return true;
                     };
-                    const uint32_t q0 = y->qtile & 1u;
-                    const int g = (int)v_step & 1, u0 = u;
+                    const uint32_t q0 = y->qtile & 1u, q1 = pair ? q0 ^ 1u : q0;
+                    const int g = (int)v_step & 1, u0 = u;  // of a pair: u is even
 #pragma unroll 1
-                    while (steps - u > 4) {
-                        if (!(ok = step(g, q0, !pair))) break;
-                        if (!(ok = step(g ^ 1, pair ? q0 ^ 1u : q0, true))) break;
+                    while (steps - u > L::kLead + 2) {
+                        if (!(ok = step(g, L::kOwnP ? q1 : q0, !pair || L::kOwnP, !pair))) break;
+                        if (!(ok = step(g ^ 1, L::kOwnP ? q0 : q1, !pair || !L::kOwnP, true))) break;
                     }
                     s_step += (uint32_t)(u - u0);
                     su += u - u0;
@@ -987,14 +1022,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // needs it, and a pair's two Q tiles need both buffers), so P.V never waits
                 // for them.
                 const int tv = (int)v_step & 1, ts = (int)s_step & 1;
-                const bool pr = x && x->pair;
                 const int all = !x ? 0 : pr ? 2 * x->n : x->n;
                 const uint32_t qt = !x ? 0u : x->qtile + (pr ? su & 1 : 0), qb = qt & 1u;
-                const bool new_q = x && su < (pr ? 2 : 1), together = pv && x == y && !new_q;
+                const bool together = !L::kOwnP && pv && same;
                 const uint32_t bk = bar(L::bKFull + kt.stage);
+                uint32_t wb[4], wp[4];  // what a step does not need is replaced by what it does
                 if (pv) {
-                    // what this step does not need is replaced by what it does
-                    uint32_t wb[4], wp[4];
                     wb[0] = bar(L::bVFull + vt.stage), wp[0] = vt.ph;
                     wb[1] = bar(L::bPFull + tv), wp[1] = v_step >> 1 & 1u;
                     wb[2] = u < 2 ? bar(L::bOEmpty + tv) : wb[0], wp[2] = u < 2 ? oe_ph >> tv & 1u : wp[0];
@@ -1003,6 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after_sync();
                     mma_pv(tv, vt.stage, u >= 2);
                     issued = true;
+                    if (L::kOwnP) commit(L::bPvDone + tv);
                     if (u >= steps - 2) commit(L::bOFull + tv);
                     if (u < 2) oe_ph ^= 1u << tv;
                     if (!pair || (u & 1)) advance(vt, kV);
@@ -1012,14 +1046,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         u = 0;
                     }
                 }
-                if (x && !together) {
-                    const uint32_t bq = new_q ? bar(L::bQFull + qb) : bk, pq = new_q ? qt >> 1 & 1u : kt.ph;
-                    if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait3(bk, kt.ph, bq, pq, bk, kt.ph); },
-                                                                abort_flag, 96))))
-                        break;
+                if (sc && !together) {
+                    wb[0] = wb[1] = wb[2] = wb[3] = bk, wp[0] = wp[1] = wp[2] = wp[3] = kt.ph;
+                    if (new_q) wb[1] = bar(L::bQFull + qb), wp[1] = qt >> 1 & 1u;
+                    if (L::kOwnP) wb[2] = bar(L::bSRead + ts), wp[2] = (s_step >> 1 & 1u) ^ 1u;
+                    if (!(ok = __all_sync(0xffffffffu, wait_for([&]() { return mbar_try_wait4(wb, wp); }, abort_flag, 96)))) break;
                     tc_fence_after_sync();
                 }
-                if (x) {
+                if (sc) {
                     mma_s(ts, qb, kt.stage);
                     issued = true;
                     commit(L::bSFull + ts);
