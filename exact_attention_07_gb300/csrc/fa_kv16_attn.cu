@@ -12,20 +12,29 @@
 //
 // One persistent block per SM.  Its work is one sequence of steps, a tile of
 // rows against a tile of 128 keys each, that two softmax warpgroups take in
-// turn, each with its own scores (128 columns of tensor memory, P over them)
-// and its own accumulator: one's exponentials overlap the other's products.
-// With up to 128 rows the steps of an item are its tiles of keys, and what the
-// two accumulators hold is added at its end; with more they are two tiles of
-// rows for each tile of keys, which are then read once for 256 rows.  The
-// scores of a step are issued two steps ahead, over the ends of items too, so
-// that short sequences follow one another without a gap.
+// turn, each with its own scores (128 columns of tensor memory) and its own
+// accumulator: one's exponentials overlap the other's products.  With up to 128
+// rows the steps of an item are its tiles of keys, and what the two accumulators
+// hold is added at its end; with more they are two tiles of rows for each tile of
+// keys, which are then read once for 256 rows.  The scores of a step are issued
+// two steps ahead, over the ends of items too, so that short sequences follow one
+// another without a gap.  At D = 128 P lies over the scores.  At D = 64 it has 64
+// columns of its own, and within an item the scores run three steps ahead: chunks
+// of 1024 tokens over 8192 keys take 250 us (1030 TFLOP/s), 280 with P over S.
+//
+// The warp that issues the MMAs paces the kernel where there are many rows: a
+// step is its wait, P.V, a commit, S and a commit, 1560 cycles at D = 128 for 1024
+// of products.  So it branches on an elected lane, which keeps its operands in
+// uniform registers (a rolled loop of MMAs is 15 % slower), and a step tests all
+// its barriers at once.
 //
 // K and V come by TMA, one box per page and 64 dimensions, each into a ring of
-// its own with a producer warp of its own.  Positions behind the sequence's end, and what no row may see, can
-// hold anything: scores are replaced where a key is masked, and in tiles with
-// masked keys V is looked over in shared memory first: rows behind the end
-// become zeros, and so do elements that are not finite, which are added to the
-// rows that may see them at the end (0 * inf would be NaN in the others).
+// its own with a producer warp of its own.  Positions behind the sequence's end,
+// and what no row may see, can hold anything: scores are replaced where a key is
+// masked, and in tiles with masked keys V is looked over in shared memory first:
+// rows behind the end become zeros, and so do elements that are not finite, which
+// are added to the rows that may see them at the end (0 * inf would be NaN in the
+// others).
 //
 // The work of all sequences is one list of (sequence, KV head, tile of rows)
 // items, cut evenly over the blocks from the lengths on the device; an item
@@ -47,18 +56,19 @@ constexpr float kTau = 8.f;      // the reference moves when a maximum exceeds i
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kAhead = 4;        // items that the list runs ahead
 // What an item costs a block beside its tiles, in tiles, and the least that a
-// block takes.  From sweeps of 0 .. 8 each: with one tile of rows and D = 128, 64
-// sequences of 1 .. 4096 keys (8 heads) take 45.8, 37.8, 39.4, 38.6, 40.0 us with
-// a cost of 0 .. 4; D = 64, 32 sequences of 1 .. 8192 keys (4 heads) 25.0, 23.4,
-// 22.2, 21.7 with 1 .. 4 and 64 of 1 .. 4096 (8 heads) 31.7, 30.6, 32.1 with 2 .. 4;
-// with two tiles of rows, 8 sequences of 32768 202.3, 200.5, 200.0 with 3 .. 5.  One
-// sequence of 777 keys takes 12.0, 12.0, 12.5 us with a least share of 1, 2, 3.
+// block takes.  With one tile of rows and D = 128, 64 sequences of 1 .. 4096 keys
+// (8 heads) take 43.5, 36.3, 37.4 us with a cost of 0, 1, 2; with D = 64, 32 of
+// 1 .. 8192 keys (4 heads) 23.5, 22.5, 22.1 and 64 of 1 .. 4096 (8 heads) 31.8,
+// 29.7, 30.2 with 2, 3, 4; with two tiles of rows, 8 sequences of up to 9000 30.9,
+// 30.9, 30.3 and 8 of 32768 202.8, 202.9, 204.5 with 4, 5, 7.  One sequence of 777
+// keys takes 11.0, 11.7, 12.7 us with a least share of 1, 2, 3, one of 100 keys
+// 9.7 and 9.0 with 1 and 2.
 template <int D>
 __host__ __device__ constexpr int item_cost(bool pair)
 {
     return pair ? 5 : D == 64 ? 3 : 1;
 }
-constexpr int kLeastShare = 2;
+constexpr int kLeastShare = 1;
 
 // A block's part of an item.  A sequence has, for every KV head, blocks of up
 // to 2 npt of its query tokens: the items of the list of work.

@@ -135,7 +135,8 @@ def test_attention_of_many_sequences(B, mode):
     run_attention(lens, new.tolist(), 2, 1, 64, 16, mode, seed=B)
 
 
-@pytest.mark.parametrize("D,mode,top", [(128, "tree", 40), (64, "causal", 24), (128, "full", 1), (64, "tree", 6)])
+@pytest.mark.parametrize("D,mode,top", [(128, "tree", 40), (64, "causal", 24), (128, "full", 1), (64, "tree", 6),
+                                        (64, "full", 40), (128, "causal", 70)])
 def test_attention_of_mixed_sequences(D, mode, top):
     """Blocks whose shares mix items of one and two tiles of rows, short ones and long ones, alone and cut."""
     rng = np.random.default_rng(D + top)
