@@ -7,11 +7,11 @@
 // dependent loads (offsets, slot, length, table, row) in each block.  So that
 // most blocks run at once (32 registers, 8 an SM) a thread has four rows in
 // flight and takes two columns: 64 sequences of 32 layers, 8 heads, D = 128, 34
-// MB moved, 8.2 us (11.2 with eight rows and one column, 9.0 with four columns).
-// The
-// accepted nodes ascend, keep[j] >= j, so a thread that takes one 16-byte
-// column of all the moves, in order, needs no buffer: what it writes lies in
-// front of all that it has yet to read.
+// MB moved, 8.2 us (11.2 with eight rows and one column, 9.0 with four columns;
+// 11.0 where three such caches take turns).  The accepted nodes ascend,
+// keep[j] >= j, so a thread that takes one 16-byte column of all the moves, in
+// order, needs no buffer: what it writes lies in front of all that it has yet to
+// read.
 #include "kv16_common.cuh"
 
 namespace fa {

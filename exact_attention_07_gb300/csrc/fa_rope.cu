@@ -10,11 +10,14 @@
 // rounding at all; its top 32 bits go to sincospif.  Products and sums are in
 // fp32, rounded once to the output's type.
 //
-// Bound: HBM, each element read and written once.  A block computes
-// the cosines and sines of its tokens once; a thread holds those of 8 pairs (16
+// Bound: HBM, each element read and written once.  A block computes the cosines
+// and sines of its tokens once, into shared memory (a thread that computes its
+// own takes 145 us where this takes 126); a thread holds those of 8 pairs (16
 // dimensions) of one token and takes its rows of several heads, with four rows'
-// loads in flight.  Dimensions that do not turn are copied by
-// threads of the same kind.
+// loads in flight.  Dimensions that do not turn are copied by threads of the same
+// kind.  Measured: 39235 tokens, 40 heads, D = 128, bf16 (804 MB) 126 us, 6380
+// GB/s; their gradients, fp32 to bf16, 183 us, 6600 GB/s; 26600 tokens' K and V
+// (8 heads each) into the cache, 32 heads of q turned alike (653 MB), 107 us, 6100.
 #include <cuda_bf16.h>
 
 #include <algorithm>
