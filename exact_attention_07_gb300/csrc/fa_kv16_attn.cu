@@ -596,10 +596,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool edge = key0 + kTile > clear;
                 // V of a tile with masked keys, before its first product: rows behind
                 // the sequence's end become zeros, and so do elements of masked rows
-                // that are not finite
-                if (edge && rt == 0) {
+                // that are not finite.  A wait by parity needs the phase before to be
+                // over: the tile three before (kV at D = 128) has landed only when these
+                // scores are complete, which come after its P.V; the one eight before (D =
+                // 64) when the group's last ones were.
+                const auto look_over_v = [&]() -> bool {
+                    if (!edge || rt != 0) return true;
                     const uint32_t T = tile0 + (uint32_t)j, stage = T % kV;
-                    if (!wait(L::bVFull + stage, T / kV, 82 + t)) goto done;
+                    if (!wait(L::bVFull + stage, T / kV, 82 + t)) return false;
                     uint8_t* vrow = smem + L::kVRing + stage * L::kTileBytes + row * 128;
                     const auto at = [&](int i) {  // the row's 16-byte pieces, lanes on different banks
                         return reinterpret_cast<uint4*>(vrow + (i >> 3) * kBox + (((i & 7) ^ (lane & 7)) << 4));
@@ -621,7 +625,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     fence_proxy_async_smem();
-                }
+                    return true;
+                };
+                if (kV == 8 && !look_over_v()) goto done;
                 if (!wait(L::bSFull + t, s_ph, 80 + t)) goto done;
                 // These scores are complete, and so is all that was issued before
                 // them: K(j) is no longer read (of a pair: when they are the second
@@ -635,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (j == n - 1) mbar_arrive(bar(L::bQEmpty + (int)((x.qtile + rt) & 1u)));
                 }
+                if (kV != 8 && !look_over_v()) goto done;
                 tc_fence_after_sync();
                 if (work) {
                     bool upper = true;  // some row sees some of the tile's upper 64 keys

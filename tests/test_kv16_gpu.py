@@ -147,6 +147,25 @@ def test_attention_of_mixed_sequences(D, mode, top):
     run_attention(lens, new.tolist(), 8, 1, D, 32, mode, seed=D + top)
 
 
+def test_a_call_gives_the_same_bits_every_time():
+    """Many items of a few tiles, the last of them partly masked: V of a tile must not be looked over while the stage
+    still waits for an earlier one."""
+    rng = np.random.default_rng(12)
+    B, H, P = 150, 8, 16
+    lens = [int(n) for n in rng.integers(385, 520, B)]
+    pool, table, tl = cache(lens, H, 128, P, 12)
+    q = torch.randn(B, 4 * H, 128, generator=torch.Generator().manual_seed(13)).bfloat16().to(DEV)
+    cu = i32(range(B + 1))
+    first = fa.fa_fwd_kv16(q, cu, pool, table, tl, causal=True)
+    other = torch.zeros((), dtype=torch.bool, device=DEV)
+    for _ in range(1500):
+        o, lse = fa.fa_fwd_kv16(q, cu, pool, table, tl, causal=True)
+        other |= (o != first[0]).any() | (lse != first[1]).any()
+    fa.fa_check()
+    assert not other.item()
+    check_attention(q, *first, range(B + 1), pool, table, range(B), lens, 128 ** -0.5, [visible("causal", 1)] * B)
+
+
 def test_attention_of_thousands_of_sequences():
     """More sequences in every block's share than it looks ahead."""
     rng = np.random.default_rng(9)
