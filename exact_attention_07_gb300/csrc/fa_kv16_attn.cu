@@ -20,7 +20,7 @@
 // two steps ahead, over the ends of items too, so that short sequences follow one
 // another without a gap.  At D = 128 P lies over the scores.  At D = 64 it has 64
 // columns of its own, and within an item the scores run three steps ahead: chunks
-// of 1024 tokens over 8192 keys take 250 us (1030 TFLOP/s), 280 with P over S.
+// of 1024 tokens over 8192 keys take 246 us (1050 TFLOP/s), 280 with P over S.
 //
 // The warp that issues the MMAs paces the kernel where there are many rows: a
 // step is its wait, P.V, a commit, S and a commit, 1560 cycles at D = 128 for 1024
