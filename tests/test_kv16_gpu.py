@@ -535,6 +535,18 @@ def test_a_lost_copy_ends_the_kernel():
     run_attention([300], [1], 1, 1, 128, 64, "causal")
 
 
+@pytest.mark.parametrize("lens,new,Hq,D", [([3000, 40], [40, 3], 8, 64), ([3000, 40], [40, 3], 8, 128), ([700], [1], 4, 64)])
+def test_a_lost_copy_ends_a_long_call(lens, new, Hq, D):
+    pool, table, tl = cache(lens, 1, D, 16, 1)
+    q = torch.randn(sum(new), Hq, D, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    fa.load_library().fa_test_inject_fault(1)
+    fa.fa_fwd_kv16(q, i32(prefix(new)), pool, table, tl, causal=True)
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_check()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    run_attention(lens, new, Hq, 1, D, 16, "causal")
+
+
 def test_two_graphs_replayed_with_other_lengths():
     """Two captured steps with workspaces of their own, replayed in turn and at once on two streams."""
     H, Hq, D, P = 2, 8, 128, 32
