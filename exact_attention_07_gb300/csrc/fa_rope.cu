@@ -103,14 +103,20 @@ __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (
 // A block takes `tokens` tokens (blockIdx.x) and, with gridDim.y > 1, a share
 // of their heads.  It computes the tokens' cosines and sines once, into shared
 // memory.  Of a token's threads, neighbours take the D / 16 units of a row: the
-// first R / 16 turn, the others copy.
+// first R / 16 turn, the others copy.  Append: the last `checks` blocks look at
+// the sequences, each for itself, as tokens lead only to those that have some.
 template <typename In, typename Out, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(kThreads, 4) fa_rope_kernel(const RotaryParams p, const int tokens, const int slots)
+__global__ void __launch_bounds__(kThreads, 4)
+    fa_rope_kernel(const RotaryParams p, const int tokens, const int slots, const int checks)
 {
     constexpr int U = sizeof(In) == 2 ? 4 : 2;  // rows in flight
     if constexpr (APPEND) {
-        if (p.c.ids && blockIdx.x == gridDim.x - 1) {  // the last blocks: only this check
-            if (blockIdx.y == 0) kv16_check_slots(p.c, p.cu, p.num_seqs);
+        const int check = (int)(blockIdx.x - (gridDim.x - checks));
+        if (check >= 0) {
+            if (blockIdx.y != 0) return;
+            for (long long s = (long long)check * blockDim.x + threadIdx.x; s < p.num_seqs; s += (long long)checks * blockDim.x)
+                kv16_sequence(p.c, p.cu, p.T, (int)s);  // latches one that is not sound
+            if (p.c.ids && check == 0) kv16_check_slots(p.c, p.cu, p.num_seqs);
             return;
         }
     }
@@ -266,10 +272,10 @@ __global__ void __launch_bounds__(kThreads, 4) fa_rope_kernel(const RotaryParams
 // row; with many, eight tokens, and a thread takes all heads of its slot.
 struct RopeGrid {
     dim3 grid;
-    int threads, tokens, slots;
+    int threads, tokens, slots, checks;
 };
 
-RopeGrid rope_grid(const RotaryParams& p, int num_sms, bool extra)
+RopeGrid rope_grid(const RotaryParams& p, int num_sms, bool append)
 {
     const long long n = (long long)p.B * p.T;
     const int units = p.D / 16, heads = p.r[0].heads + p.r[1].heads + p.r[2].heads;
@@ -279,15 +285,17 @@ RopeGrid rope_grid(const RotaryParams& p, int num_sms, bool extra)
     g.slots = std::min(heads, kThreads / g.tokens / units);
     g.threads = (g.tokens * g.slots * units + 31) / 32 * 32;  // whole warps: they look for sequences together
     const int parts = n * heads / g.slots < 8ll * num_sms ? (heads + g.slots - 1) / g.slots : 1;
-    g.grid = dim3((unsigned)((n + g.tokens - 1) / g.tokens + (extra ? 1 : 0)), (unsigned)parts);
+    g.checks = append ? std::min((p.num_seqs - 1) / g.threads + 1, num_sms) : 0;  // a sequence a thread
+    g.grid = dim3((unsigned)((n + g.tokens - 1) / g.tokens + g.checks), (unsigned)parts);
     return g;
 }
 
 template <typename In, typename Out, bool INTER, bool APPEND>
 cudaError_t launch(const RotaryParams& p, int num_sms, cudaStream_t stream)
 {
-    const RopeGrid g = rope_grid(p, num_sms, APPEND && p.c.ids);
-    fa_rope_kernel<In, Out, INTER, APPEND><<<g.grid, g.threads, g.tokens * p.R * 4, stream>>>(p, g.tokens, g.slots);
+    const RopeGrid g = rope_grid(p, num_sms, APPEND);
+    fa_rope_kernel<In, Out, INTER, APPEND>
+        <<<g.grid, g.threads, g.tokens * p.R * 4, stream>>>(p, g.tokens, g.slots, g.checks);
     return cudaGetLastError();
 }
 

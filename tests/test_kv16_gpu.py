@@ -615,3 +615,47 @@ def test_no_rows():
     back = fa.fa_kv16_keep(i32([]), i32([0]), i32([0, 0]), pool, table, tl)
     fa.fa_check()
     assert back.tolist() == [0]
+
+
+# cu, slots, lens: a sequence that is not sound and has no token in front of the call's end
+UNSOUND = [((0, 4, 9), None, None), ((0, 4, 2), None, None), ((0, 4, 4), [0, 2], None), ((0, 4, 4), [0, -1], None),
+           ((0, 4, 4), None, [40, -1]), ((0, 4, 4), [0, 1], [40, 1 << 20])]
+
+
+@pytest.mark.parametrize("call", ["append", "attention", "keep"])
+@pytest.mark.parametrize("cu,ids,lens", UNSOUND)
+def test_sequences_without_tokens_are_checked(cu, ids, lens, call):
+    D = 64
+    pool, table, tl = cache([40, 20], 1, D, 16, 1)
+    q = torch.randn(4, 2, D, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    k = q[:, :1].contiguous()
+    tl, cu, ids = tl if lens is None else i32(lens), i32(cu), None if ids is None else i32(ids)
+    if call == "append":
+        latched(lambda: fa.fa_kv16_append(k, k, cu, pool, table, tl, seq_ids=ids, rope=fa.rope_plan(D), q=q))
+    elif call == "attention":
+        latched(lambda: fa.fa_fwd_kv16(q, cu, pool, table, tl, causal=True, seq_ids=ids))
+    else:
+        latched(lambda: fa.fa_kv16_keep(i32([0, 1, 0, 0]), i32([2, 0]), cu, pool, table, tl, seq_ids=ids))
+
+
+@pytest.mark.parametrize("at", [0, 127, 128, 2999, 25000])
+@pytest.mark.parametrize("named", [False, True])
+def test_append_checks_every_sequence_of_a_large_batch(at, named):
+    """One slot of a batch of empty ones has a length that is none; the rows of the others are written."""
+    B, D, P = 25001, 64, 16
+    pool, table, tl = cache([9] + [0] * (B - 1), 1, D, P, 2)
+    lens = tl.clone()
+    first = 1 if at == 0 else 0  # the sequence with the rows
+    if at == 0:
+        table, lens = table.roll(1, 0), lens.roll(1)
+    lens[at] = -3
+    cu = torch.full((B + 1,), 5, dtype=torch.int32, device=DEV)
+    cu[:first + 1] = 0
+    k, v = torch.randn(2, 5, 1, D, generator=torch.Generator().manual_seed(3)).bfloat16().to(DEV)
+    ids = torch.arange(B, dtype=torch.int32, device=DEV) if named else None
+    latched(lambda: fa.fa_kv16_append(k, v, cu, pool, table, lens, seq_ids=ids))
+    got = pool[int(table[first, 0]), :, 0, 4:9]
+    assert torch.equal(got[0], k[:, 0]) and torch.equal(got[1], v[:, 0])
+    lens[at] = 0
+    fa.fa_kv16_append(k, v, cu, pool, table, lens, seq_ids=ids)
+    fa.fa_check()
