@@ -659,3 +659,68 @@ def test_append_checks_every_sequence_of_a_large_batch(at, named):
     lens[at] = 0
     fa.fa_kv16_append(k, v, cu, pool, table, lens, seq_ids=ids)
     fa.fa_check()
+
+
+@pytest.mark.parametrize("B", [32, 33, 64, 65, 1024, 1025, 4000])
+@pytest.mark.parametrize("empty", ["some", "first", "middle", "last", "most"])
+@pytest.mark.parametrize("named", [False, True])
+def test_append_to_many_sequences(B, empty, named):
+    """A token's sequence among many, with runs of empty ones: rows of k, v bit for bit, q turned at its index in the
+    cache, all else untouched (rows behind the last sequence too)."""
+    rng = np.random.default_rng(B + 7 * len(empty) + named)
+    new = rng.integers(0, 4, B)
+    third = B // 3
+    if empty == "first":
+        new[:2 * third] = 0
+    elif empty == "middle":
+        new[third:2 * third] = 0
+    elif empty == "last":
+        new[third:] = 0
+    elif empty == "most":
+        new[rng.random(B) < 0.95] = 0
+    new[rng.integers(third)] = 40  # more rows than a block has tokens
+    slots = rng.permutation(B) if named else np.arange(B)
+    old = rng.integers(0, 30, B)
+    lens = np.zeros(B, int)
+    lens[slots] = old + new
+    H, Hq, D, P, behind = 1, 2, 64, 16, 3
+    pool, table, tl = cache(lens.tolist(), H, D, P, B)
+    cu = prefix(new)
+    T = int(cu[-1])
+    x = torch.randn(T + behind, Hq + 2 * H, D, generator=torch.Generator().manual_seed(B)).bfloat16().to(DEV)
+    q, k, v = x.split([Hq, H, H], 1)
+    at = np.concatenate([np.arange(a, a + n) for a, n in zip(old, new)])
+    slot = np.repeat(slots, new)
+    page, row = torch.from_numpy(table.cpu().numpy()[slot, at // P]).long(), torch.from_numpy(at % P)
+    want = pool.clone()
+    y = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    ids = i32(slots) if named else None
+    fa.fa_kv16_append(k, v, i32(cu), pool, table, tl, seq_ids=ids)
+    fa.fa_check()
+    want[page, 0, :, row], want[page, 1, :, row] = k[:T], v[:T]
+    assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
+    rope, w = fa.rope_plan(D), [10000.0 ** (-2 * c / D) for c in range(D // 2)]
+    fa.fa_kv16_append(k, v, i32(cu), pool, table, tl, seq_ids=ids, rope=rope, q=q, q_out=y)
+    fa.fa_check()
+    assert (y[T:] == 7).all()
+    for got, src in ((y[:T], q[:T]), (pool[page, 0, :, row], k[:T])):
+        turned = kv16.turn(f64(src), at, w)
+        assert (np.abs(f64(got) - turned) <= kv16.turn_tolerance(f64(src), turned, 1.0, D // 2, True)).all()
+    want[page, 0, :, row] = pool[page, 0, :, row]
+    assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
+
+
+def test_append_of_a_padded_batch_writes_the_rows():
+    """Sequences of a batch padded with an empty slot, named out of order: each row at its place, bit for bit."""
+    H, D, P, lens = 2, 64, 16, [50, 0, 70]
+    pool, table, tl = cache(lens, H, D, P, 31)
+    ids, new = [2, 1, 0, 1, 1], [4, 0, 2, 0, 0]
+    k, v = torch.randn(2, 9, H, D, generator=torch.Generator().manual_seed(2)).bfloat16().to(DEV)
+    want = pool.clone()
+    tab = table.cpu()
+    for s, first, n in ((2, 0, 4), (0, 4, 2)):
+        p = torch.arange(lens[s] - n, lens[s])
+        want[tab[s, p // P].long(), 0, :, p % P], want[tab[s, p // P].long(), 1, :, p % P] = k[first:first + n], v[first:first + n]
+    fa.fa_kv16_append(k, v, i32(prefix(new)), pool, table, tl, seq_ids=i32(ids))
+    fa.fa_check()
+    assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
