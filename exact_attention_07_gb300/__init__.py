@@ -1524,8 +1524,9 @@ def fa_kv16_keep(keep: torch.Tensor, counts: torch.Tensor, cu_seqlens: torch.Ten
                  new_tokens: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Keep the accepted nodes of drafted trees: of the last cu_seqlens[s+1] - cu_seqlens[s] positions of sequence s,
     those named by keep[cu_seqlens[s] + j], j < counts[s] (int32, ascending, from 0), become the first, in order, in
-    every layer of pool (as for fa_kv16_append, or with the layers in front).  Returns new_tokens, int32 [num_seqs]:
-    counts[s] less the drafted ones, for fa_kv4_reserve, which takes the other positions back."""
+    every layer of pool (as for fa_kv16_append, or with the layers in front).  Returns new_tokens, int32 [num_seqs] (a
+    tensor of its own, not counts): counts[s] less the drafted ones, for fa_kv4_reserve, which takes the other positions
+    back."""
     if stream is not None:
         return _on_stream(stream, pool, fa_kv16_keep, keep, counts, cu_seqlens, pool, table, seq_lens, seq_ids,
                           new_tokens)

@@ -1573,6 +1573,13 @@ fa_status_t kv16_cache(const fa_kv16_t* c, int num_seqs, Kv16Cache* out)
     return FA_OK;
 }
 
+// Whether `a` bytes at x and `b` bytes at y have one in common.
+bool overlap(const void* x, size_t a, const void* y, size_t b)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x), q = reinterpret_cast<uintptr_t>(y);
+    return a && b && p < q + b && q < p + a;
+}
+
 fa_status_t kv16_attn_shape(int total, int Hq, int Hkv, int D, int* rows)
 {
     if (total < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
@@ -1712,6 +1719,15 @@ extern "C" fa_status_t fa_kv16_keep(const int* keep, const int* counts, const in
     if (!keep || !counts || !cu_seqlens || !new_tokens || !aligned4(keep) || !aligned4(counts) || !aligned4(cu_seqlens) ||
         !aligned4(new_tokens) || total < 0 || num_layers <= 0)
         return FA_ERR_INVALID_ARG;
+    // a sequence's blocks read these while one of them writes its new_tokens
+    const size_t n = num_seqs, slots = cache->num_slots;
+    const struct {
+        const void* p;
+        size_t ints;
+    } in[] = {{keep, (size_t)total}, {counts, n}, {cu_seqlens, n + 1}, {cache->seq_ids, cache->seq_ids ? n : 0},
+              {cache->seq_lens, slots}, {cache->table, slots * cache->table_width}};
+    for (const auto& x : in)
+        if (overlap(new_tokens, 4 * n, x.p, 4 * x.ints)) return FA_ERR_INVALID_ARG;
     if ((long long)num_layers * 2 * cache->Hkv * (cache->D / 8) >= 256ll * 65535) return FA_ERR_INVALID_ARG;
     DeviceState* ds = nullptr;
     st = device_state(&ds);

@@ -699,7 +699,9 @@ fa_status_t fa_fwd_kv16_workspace(int total, int Hq, int Hkv, int D, size_t* wor
  * first, in order: row len - n + j takes row len - n + keep[j], K and V, in each
  * of num_layers pools that lie one after the other.  new_tokens (int32 DEVICE
  * [num_seqs], output) receives counts[s] - n, which fa_kv4_reserve takes to give
- * the other positions back.  Other rows, and seq_lens, keep their values.
+ * the other positions back; it must not overlap what the call reads (counts,
+ * keep, cu_seqlens, the cache's slots, lengths and table): FA_ERR_INVALID_ARG.
+ * Other rows, and seq_lens, keep their values.
  * A list that does not ascend or leaves [0, n), or a count out of range, latches
  * FA_ERR_INVALID_ARG; that sequence's rows are left as they were and its
  * new_tokens are 0.  The pages written must be the sequence's own; a slot

@@ -724,3 +724,25 @@ def test_append_of_a_padded_batch_writes_the_rows():
     fa.fa_kv16_append(k, v, i32(prefix(new)), pool, table, tl, seq_ids=i32(ids))
     fa.fa_check()
     assert torch.equal(pool.view(torch.int16), want.view(torch.int16))
+
+
+def test_keep_refuses_counts_as_its_output():
+    """512 columns and more take several blocks a sequence, which all read counts.  Beside it is well."""
+    lens, n, layers = [60, 40], [5, 3], 9
+    pool, table, tl = cache(lens, 4, 64, 16, 9, layers=layers)
+    assert layers * 2 * 4 * 8 > 512
+    ints = i32([1, 2, 0, 0])
+    counts, beside = ints[:2], ints[2:]
+    before = pool.clone()
+    with pytest.raises(fa.FAError, match="invalid"):
+        fa.fa_kv16_keep(i32([1, 0, 0, 0, 0, 0, 2, 0]), counts, i32(prefix(n)), pool, table, tl, new_tokens=counts)
+    fa.fa_check()
+    assert torch.equal(pool.view(torch.int16), before.view(torch.int16)) and ints.tolist() == [1, 2, 0, 0]
+    back = fa.fa_kv16_keep(i32([1, 0, 0, 0, 0, 0, 2, 0]), counts, i32(prefix(n)), pool, table, tl, new_tokens=beside)
+    fa.fa_check()
+    assert back is beside and ints.tolist() == [1, 2, -4, -1]
+    for s, moves in enumerate(([(0, 1)], [(1, 2)])):
+        for to, of in moves:
+            p, o = lens[s] - n[s] + to, lens[s] - n[s] + of
+            before[:, int(table[s, p // 16]), :, :, p % 16] = before[:, int(table[s, o // 16]), :, :, o % 16].clone()
+    assert torch.equal(pool.view(torch.int16), before.view(torch.int16))

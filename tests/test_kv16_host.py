@@ -251,3 +251,19 @@ def test_oracle_attends_what_rows_see():
             assert np.allclose(o[i, h], p @ v[keys, h // 2]) and np.isclose(lse[h, i], np.log(np.exp(s).sum()))
     o, lse, _ = kv16.attention(q, k[4:], v[4:], 0.5, np.zeros((3, 3), bool))
     assert not o.any() and np.isneginf(lse).all()
+
+
+# Where the call's inputs begin: keep [4], counts [2], cu_seqlens [3], slots [2], lengths [3], table [3][2], 4 bytes each
+KEEP_INPUTS = dict(keep=(0x1000, 4), counts=(0x2000, 2), cu=(0x3000, 3), seq_ids=(0x4000, 2), seq_lens=(0x5000, 3),
+                   table=(0x6000, 6))
+
+
+@pytest.mark.parametrize("name", KEEP_INPUTS)
+def test_keep_refuses_new_tokens_over_its_inputs(lib, name):
+    """One block of a sequence writes its new_tokens while others may not have read the inputs yet."""
+    at, n = KEEP_INPUTS[name]
+    a = {k: v[0] for k, v in KEEP_INPUTS.items()}
+
+    c = cache(seq_ids=a["seq_ids"], seq_lens=a["seq_lens"], table=a["table"], num_slots=3, table_width=2)
+    for new in (at, at + 4, at - 4, at + 4 * (n - 1)):
+        assert lib.fa_kv16_keep(a["keep"], a["counts"], a["cu"], 2, 4, 1, new, c, None) == INV
