@@ -439,8 +439,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kK = L::kK, kV = L::kV;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sb = smem_u32(smem);
-    if (sb & 1023u) {  // the operands' swizzle needs it; the window begins so where a kernel has no other shared memory
-        if (threadIdx.x == 0) atomicOr(p.c.err, 4);
+    // The operands' swizzle needs an aligned base; the window begins so where a
+    // kernel has no other shared memory.  The second kernel runs all the same, and
+    // the workspace can hold anything: nothing to join.
+    if (sb & 1023u) {
+        if (threadIdx.x == 0) {
+            parts_of(p.part, gridDim.x, p.rows).join[blockIdx.x].parts = 0;
+            atomicOr(p.c.err, 4);
+        }
         return;
     }
     long long* s_sum = reinterpret_cast<long long*>(smem + L::kSums);

@@ -267,3 +267,25 @@ def test_keep_refuses_new_tokens_over_its_inputs(lib, name):
     c = cache(seq_ids=a["seq_ids"], seq_lens=a["seq_lens"], table=a["table"], num_slots=3, table_width=2)
     for new in (at, at + 4, at - 4, at + 4 * (n - 1)):
         assert lib.fa_kv16_keep(a["keep"], a["counts"], a["cu"], 2, 4, 1, new, c, None) == INV
+
+
+def test_early_ways_out_of_the_attention_leave_nothing_to_join():
+    """The second kernel runs whatever becomes of the first and takes its blocks' parts from the workspace, which can
+    hold anything: a block that returns before it has said that there are none says so on its way out.  No launch gets
+    there (the address that the branch looks at is always aligned), so the source is what can be looked at."""
+    import os
+    import re
+
+    path = os.path.join(os.path.dirname(fa.__file__), "csrc", "fa_kv16_attn.cu")
+    with open(path) as f:
+        text = f.read()
+    head = text[text.index("fa_kv16_attn_kernel(const"):]
+    head = head[:head.index("__syncthreads()")]
+    exits = [m.start() for m in re.finditer(r"\breturn;", head)]
+    assert len(exits) == 1
+    for at in exits:
+        depth, begin = 0, at  # the branch that returns: back to the brace that opens it
+        while depth >= 0:
+            begin -= 1
+            depth += {"}": 1, "{": -1}.get(head[begin], 0)
+        assert "join[blockIdx.x].parts = 0;" in head[begin:at]
