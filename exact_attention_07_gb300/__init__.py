@@ -1126,6 +1126,9 @@ class RopePlan:
         self.end, self.device = self.start + self.rot_dim, freqs.get_device()  # -1: not on a GPU
         self.packed = _pack_rope(freqs.data_ptr(), self.rot_dim, self.start, self.interleaved, self.mscale)
 
+    def __reduce__(self):  # a copy packs the address of its own frequencies
+        return RopePlan, (self.freqs, self.start, self.interleaved, self.mscale)
+
 
 def rope_plan(rot_dim: int | None = None, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
               original_length: int | None = None, inv_freq=None, mscale: float | None = None, start: int = 0,

@@ -289,3 +289,27 @@ def test_early_ways_out_of_the_attention_leave_nothing_to_join():
             begin -= 1
             depth += {"}": 1, "{": -1}.get(head[begin], 0)
         assert "join[blockIdx.x].parts = 0;" in head[begin:at]
+
+
+def held(plan):
+    """What a call hands to the library: address of the frequencies, dimensions, start, order, factor."""
+    p = fa._Rope.from_buffer_copy(plan.packed)
+    return p.freqs, p.rot_dim, p.start, p.interleaved, p.mscale
+
+
+@pytest.mark.parametrize("way", ["copy", "deepcopy", "pickle", "module"])
+def test_copies_of_plans_hold_frequencies_of_their_own(way):
+    """A copied plan must not hand over the address of the original's frequencies, which may be gone by then."""
+    import copy
+    import pickle
+
+    plan = fa.rope_plan(32, base=500.0, start=16, interleaved=True, mscale=0.5, device="cpu")
+    if way == "module":
+        m = torch.nn.Linear(1, 1)
+        m.rope = plan
+        other = copy.deepcopy(m).rope
+    else:
+        other = pickle.loads(pickle.dumps(plan)) if way == "pickle" else getattr(copy, way)(plan)
+    assert torch.equal(other.freqs, plan.freqs) and (other.freqs is plan.freqs) == (way == "copy")
+    assert held(other) == (other.freqs.data_ptr(), 32, 16, 1, 0.5)
+    assert (other.end, other.device, other.interleaved) == (48, -1, True)
