@@ -1121,6 +1121,14 @@ class RopePlan:
     __slots__ = ("freqs", "rot_dim", "start", "end", "interleaved", "mscale", "device", "packed")
 
     def __init__(self, freqs, start, interleaved, mscale):
+        """freqs: int64 [rot_dim / 2], turns per position times 2^64 modulo 2^64."""
+        _check_tensor(freqs, "freqs", torch.int64, 1, on_device=False)
+        if freqs.numel() == 0 or freqs.numel() % 8:
+            raise ValueError(f"freqs must hold rot_dim / 2 frequencies, a multiple of 8, got {freqs.numel()}")
+        if start < 0 or start % 16:
+            raise ValueError(f"start must be a multiple of 16, got {start}")
+        if not mscale > 0 or math.isinf(mscale):
+            raise ValueError(f"mscale must be positive and finite, got {mscale}")
         self.freqs, self.rot_dim = freqs, 2 * freqs.numel()
         self.start, self.interleaved, self.mscale = int(start), bool(interleaved), float(mscale)
         self.end, self.device = self.start + self.rot_dim, freqs.get_device()  # -1: not on a GPU
@@ -1171,10 +1179,6 @@ def rope_plan(rot_dim: int | None = None, base: float = 10000.0, scaling: str | 
     if not all(math.isfinite(x) for x in w):
         raise ValueError("frequencies must be finite")
     mscale = 1.0 if mscale is None else float(mscale)
-    if not mscale > 0 or math.isinf(mscale):
-        raise ValueError(f"mscale must be positive and finite, got {mscale}")
-    if start < 0 or start % 16:
-        raise ValueError(f"start must be a multiple of 16, got {start}")
     turns = [round(Fraction(x) * _PER_TURN * 2 ** 64) % 2 ** 64 for x in w]
     freqs = torch.tensor([x - 2 ** 64 if x >> 63 else x for x in turns], dtype=torch.int64).to(device)
     return RopePlan(freqs, start, interleaved, mscale)

@@ -313,3 +313,16 @@ def test_copies_of_plans_hold_frequencies_of_their_own(way):
     assert torch.equal(other.freqs, plan.freqs) and (other.freqs is plan.freqs) == (way == "copy")
     assert held(other) == (other.freqs.data_ptr(), 32, 16, 1, 0.5)
     assert (other.end, other.device, other.interleaved) == (48, -1, True)
+
+
+@pytest.mark.parametrize("bad", [dict(freqs=[1] * 8), dict(freqs=torch.zeros(8)), dict(freqs=torch.zeros(8, dtype=torch.int32)),
+                                 dict(freqs=torch.zeros(0, dtype=torch.int64)), dict(freqs=torch.zeros(12, dtype=torch.int64)),
+                                 dict(freqs=torch.zeros(2, 8, dtype=torch.int64)),
+                                 dict(freqs=torch.zeros(16, dtype=torch.int64)[::2]), dict(start=8), dict(start=-16),
+                                 dict(mscale=0.0), dict(mscale=math.nan), dict(mscale=math.inf)])
+def test_plans_of_other_frequencies_are_refused(bad):
+    """The kernels read rot_dim / 2 numbers of 64 bits where the plan says that they are."""
+    args = dict(freqs=torch.zeros(8, dtype=torch.int64), start=0, interleaved=False, mscale=1.0)
+    assert held(fa.RopePlan(**args))[1:] == (16, 0, 0, 1.0)
+    with pytest.raises((TypeError, ValueError)):
+        fa.RopePlan(**{**args, **bad})
