@@ -1129,10 +1129,18 @@ class RopePlan:
             raise ValueError(f"start must be a multiple of 16, got {start}")
         if not mscale > 0 or math.isinf(mscale):
             raise ValueError(f"mscale must be positive and finite, got {mscale}")
-        self.freqs, self.rot_dim = freqs, 2 * freqs.numel()
-        self.start, self.interleaved, self.mscale = int(start), bool(interleaved), float(mscale)
-        self.end, self.device = self.start + self.rot_dim, freqs.get_device()  # -1: not on a GPU
-        self.packed = _pack_rope(freqs.data_ptr(), self.rot_dim, self.start, self.interleaved, self.mscale)
+        rot_dim, start, interleaved, mscale = 2 * freqs.numel(), int(start), bool(interleaved), float(mscale)
+        packed = _pack_rope(freqs.data_ptr(), rot_dim, start, interleaved, mscale)
+        for name, value in (("freqs", freqs), ("rot_dim", rot_dim), ("start", start), ("end", start + rot_dim),
+                            ("interleaved", interleaved), ("mscale", mscale), ("packed", packed),
+                            ("device", freqs.get_device())):  # -1: not on a GPU
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):  # calls take what is packed
+        raise AttributeError(f"a RopePlan stays as it was made: make another for another {name}")
+
+    def __delattr__(self, name):
+        raise AttributeError("a RopePlan stays as it was made")
 
     def __reduce__(self):  # a copy packs the address of its own frequencies
         return RopePlan, (self.freqs, self.start, self.interleaved, self.mscale)

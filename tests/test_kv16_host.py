@@ -315,6 +315,17 @@ def test_copies_of_plans_hold_frequencies_of_their_own(way):
     assert (other.end, other.device, other.interleaved) == (48, -1, True)
 
 
+def test_plans_stay_as_they_are():
+    """The library gets what a plan was made with: a changed attribute would say otherwise."""
+    plan = fa.rope_plan(32, device="cpu")
+    for name, value in (("mscale", 2.0), ("start", 16), ("interleaved", True), ("freqs", plan.freqs + 1), ("rot_dim", 16)):
+        with pytest.raises(AttributeError):
+            setattr(plan, name, value)
+        with pytest.raises(AttributeError):
+            delattr(plan, name)
+    assert held(plan) == (plan.freqs.data_ptr(), 32, 0, 0, 1.0)
+
+
 @pytest.mark.parametrize("bad", [dict(freqs=[1] * 8), dict(freqs=torch.zeros(8)), dict(freqs=torch.zeros(8, dtype=torch.int32)),
                                  dict(freqs=torch.zeros(0, dtype=torch.int64)), dict(freqs=torch.zeros(12, dtype=torch.int64)),
                                  dict(freqs=torch.zeros(2, 8, dtype=torch.int64)),
