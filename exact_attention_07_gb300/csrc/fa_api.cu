@@ -1534,6 +1534,8 @@ fa_status_t rope_call(const fa_rotary_rows_t* q, const fa_rotary_rows_t* k, int 
     if (k) {
         st = rotary_rows(k, B, T, in_fp32 != 0, out_fp32 != 0, true, &p.r[1]);
         if (st != FA_OK) return st;
+        // written while the other rows are read, or by both
+        if (q->y == k->x || k->y == q->x || q->y == k->y) return FA_ERR_INVALID_ARG;
     }
     if ((long long)p.r[0].heads + p.r[1].heads > 65535) return FA_ERR_INVALID_ARG;
     DeviceState* ds = nullptr;
@@ -1625,6 +1627,7 @@ extern "C" fa_status_t fa_kv16_append(const fa_rotary_rows_t* q, const fa_rotary
     if (q && (st = rotary_rows(q, 1, total, false, false, true, &p.r[0])) != FA_OK) return st;
     if ((st = rotary_rows(k, 1, total, false, false, false, &p.r[1])) != FA_OK) return st;
     if ((st = rotary_rows(v, 1, total, false, false, false, &p.r[2])) != FA_OK) return st;
+    if (q && (q->y == k->x || q->y == v->x)) return FA_ERR_INVALID_ARG;  // written while they are read
     if ((long long)p.r[0].heads + 2ll * cache->Hkv > 65535) return FA_ERR_INVALID_ARG;
     DeviceState* ds = nullptr;
     st = device_state(&ds);

@@ -589,7 +589,8 @@ typedef struct fa_rope {
 
 /* Rows [B, T, heads, D] with strides in elements; the D elements of a row are
  * contiguous.  x is read and y written; y may be x with the same strides (in
- * place), else they must not overlap.  Addresses are multiples of 16 bytes, and
+ * place), else they must not overlap, and y overlaps no other rows of the call
+ * (FA_ERR_INVALID_ARG where it is another's x or y).  Addresses are multiples of 16 bytes, and
  * so are the strides of dimensions of more than one entry.  A stride of x may be 0. */
 typedef struct fa_rotary_rows {
     const void* x;

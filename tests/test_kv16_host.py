@@ -337,3 +337,13 @@ def test_plans_of_other_frequencies_are_refused(bad):
     assert held(fa.RopePlan(**args))[1:] == (16, 0, 0, 1.0)
     with pytest.raises((TypeError, ValueError)):
         fa.RopePlan(**{**args, **bad})
+
+
+def test_rows_written_are_no_other_rows(lib):
+    """One block turns q in place while another reads it as k, or both write the same rows."""
+    x, y, z = 0x1000, 0x2000, 0x3000
+    for fn in (lib.fa_rope, lib.fa_rope_bwd):
+        for q, k in (((x, x), (x, y)), ((x, y), (y, z)), ((x, y), (y, y)), ((x, y), (z, x)), ((x, y), (z, y)), ((x, x), (x, x))):
+            assert fn(rows(x=q[0], y=q[1]), rows(x=k[0], y=k[1]), 1, 4, 128, 0, 0, rope(), None, 0, None) == INV
+    for k, v in ((y, z), (z, y), (y, y)):
+        assert lib.fa_kv16_append(rows(x=x, y=y), rows(x=k), rows(x=v), 16, 2, 4, cache(), rope(), None, None) == INV
