@@ -347,3 +347,22 @@ def test_rows_written_are_no_other_rows(lib):
             assert fn(rows(x=q[0], y=q[1]), rows(x=k[0], y=k[1]), 1, 4, 128, 0, 0, rope(), None, 0, None) == INV
     for k, v in ((y, z), (z, y), (y, y)):
         assert lib.fa_kv16_append(rows(x=x, y=y), rows(x=k), rows(x=v), 16, 2, 4, cache(), rope(), None, None) == INV
+
+
+@pytest.mark.parametrize("gpu", [False, True])
+def test_calls_that_would_launch_on_nothing_stay_off_a_gpu(gpu, monkeypatch, request):
+    """test_rope_calls_are_refused makes one call that is sound but for its made-up addresses: it ends for want of a
+    device, and with one it would read them."""
+    class Item:
+        def __init__(self, name):
+            self.name, self.marks = name, []
+
+        def add_marker(self, mark):
+            self.marks.append(mark.name)
+
+    conftest = [p for p in request.config.pluginmanager.get_plugins() if hasattr(p, "NEEDS_NO_GPU")]
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: gpu)
+    items = [Item("test_rope_calls_are_refused"), Item("test_keep_calls_are_refused")]
+    assert conftest, "no list of such tests"
+    conftest[0].pytest_collection_modifyitems(items)
+    assert [i.marks for i in items] == [["skip"] if gpu else [], []]
