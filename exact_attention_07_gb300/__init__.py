@@ -1314,9 +1314,9 @@ def fa_rope(q: torch.Tensor, k: torch.Tensor | None, rope: RopePlan, positions: 
             stream=None):
     """Turn the rows of q and k (which may be None) by their positions' angles.  q, k: packed [T,H,D] or dense
     [B,H,L,D], bf16 or fp32, of any strides with contiguous rows (views of a fused projection, or of [B,L,H,D]);
-    positions int32 [T], [L] or [B,L] (default: the index along the tokens).  Returns (q_out, k_out), contiguous, of
-    ``dtype`` (default: the input's; fp32 rows may become bf16).  q_out may be q itself, and k_out k, but neither the
-    other's."""
+    positions int32 [T], [L] or [B,L] (default: the index along the tokens; packed rows of several sequences need
+    theirs, as the call does not know where one begins).  Returns (q_out, k_out), contiguous, of ``dtype`` (default: the
+    input's; fp32 rows may become bf16).  q_out may be q itself, and k_out k, but neither the other's."""
     if stream is not None:
         return _on_stream(stream, q, fa_rope, q, k, rope, positions, dtype, q_out, k_out)
     return _rope_call(False, q, k, rope, positions, dtype, q_out, k_out)

@@ -23,8 +23,8 @@
 // of 1024 tokens over 8192 keys take 246 us (1050 TFLOP/s), 280 with P over S.
 //
 // The warp that issues the MMAs paces the kernel where there are many rows: a
-// step is its wait, P.V, a commit, S and a commit, 1560 cycles at D = 128 for 1024
-// of products.  So it branches on an elected lane, which keeps its operands in
+// step is its wait, P.V, S and a commit (at D = 64 one behind P.V too), 1560 cycles
+// at D = 128 for 1024 of products.  So it branches on an elected lane, which keeps its operands in
 // uniform registers (a rolled loop of MMAs is 15 % slower), and a step tests all
 // its barriers at once.
 //
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // fp32 p.  O is divided by that sum plus the rounding error of
                     // each tile's largest p, so that a row which one key dominates
                     // (some tile's largest) weighs it alike above and below; the
-                    // other errors, at most 2^-9 of a key's weight, average out
+                    // other errors, at most 2^-8 of a key's weight, average out
                     // against O's own rounding to bf16.
                     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nr2 = f2_pack(-r_use, -r_use);
                     uint64_t sum[2] = {0ull, 0ull};

@@ -603,8 +603,9 @@ typedef struct fa_rotary_rows {
 /*
  * Turns the rows of q and, unless it is NULL, of k (HOST structs), each with
  * its own heads.  positions: int32 DEVICE, position of token t of batch b at
- * b * position_batch_stride + t, or NULL for t itself.  in_fp32, out_fp32: fp32
- * rows in place of bf16; (0, 0), (1, 1) and (1, 0) are supported
+ * b * position_batch_stride + t, or NULL for t itself (packed rows of several
+ * sequences need theirs: the call does not know where one begins).  in_fp32,
+ * out_fp32: fp32 rows in place of bf16; (0, 0), (1, 1) and (1, 0) are supported
  * (FA_ERR_UNSUPPORTED otherwise).  D, rot_dim and start are multiples of 16, D
  * at most 512.  Angles are exact to 2^-24 of a turn's half, sine, cosine and
  * products in fp32, and the result is rounded once.
